@@ -25,10 +25,17 @@
  *   qmv_wide          the same product for wide blocks (M = 17..128, e.g. the
  *                     verify blocks of 32 sequences against one LM head) on
  *                     the tcgen05 tensor cores
+ *   kv_pages_step     a paged cache's bookkeeping of one step: commit, pages,
+ *                     slots and positions of the new tokens
+ *   rope_kv_append    head norms and rotary positions of a step's queries and
+ *                     keys; keys and values into the paged cache
+ *   paged_attention   attention of a step's new tokens (one, a verify block,
+ *                     or a chunk of a prompt) over the paged cache
  *
  * Conventions (all entry points):
  *  - Every tensor argument is a DEVICE pointer owned by the caller, to
- *    contiguous row-major memory.  The library allocates no device memory and
+ *    contiguous row-major memory (rope_kv_append and paged_attention take a
+ *    row stride for their packed rows).  The library allocates no device memory and
  *    keeps no pointer after a call returns, except a qmv plan (below), which
  *    holds the pointers it was created with.
  *  - Calls are asynchronous on `stream` (NULL = the legacy default stream) and
@@ -75,7 +82,11 @@ typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_FLAG_DRAFT_ZERO_Q 2       /* q(d) == 0, the draft could not have been drawn */
 #define SV_FLAG_NONFINITE_LOGIT 4    /* a NaN or +inf logit in a row that was used   */
 #define SV_FLAG_EMPTY_DIST 8         /* nothing to sample from: token -1 emitted     */
-#define SV_FLAG_REPLAY_RANGE 16      /* gdn_tape_replay: record count clamped to [0,T] */
+#define SV_FLAG_REPLAY_RANGE 16      /* gdn_tape_replay: record count clamped to [0,T];
+                                      * kv_pages_step: committed length clamped to its pages */
+#define SV_FLAG_NO_PAGES 32          /* kv_pages_step: too few pages, the request is refused */
+#define SV_FLAG_ROWS 64              /* kv_pages_step: past the step's rows, refused        */
+#define SV_FLAG_PAGE_STATE 128       /* kv_pages_step: the page state contradicts itself    */
 
 int sv_abi_version(void);
 const char *sv_status_string(int status);
@@ -487,6 +498,119 @@ sv_status conv_window_capture(const float *window, const float *x, const float *
 sv_status conv_window_replay(float *window, const float *x, const int32_t *n_replay,
                              int n_replay_count, int n_replay_bias, int B, int T, int C, int W,
                              int32_t *err_flags, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention layers: a paged cache, and attention of the new tokens over it. */
+/* ------------------------------------------------------------------------ */
+/* The attention layers of the target model run between the projections that
+ * qmv_smallm computes.  Their keys and values live in pages of page_size
+ * tokens shared by all requests; a step's new tokens (single tokens, verify
+ * blocks of K + 1 rows, chunks of prompts) are packed rows, request b's at
+ * q_start[b] .. q_start[b+1].  A rejected draft needs no rollback: only the
+ * committed length decides what the next step attends and overwrites.
+ * page_size is 16, 32, 64, 128 or 256 in all three calls.
+ *
+ * kv_pages_step: one step's bookkeeping, on the device, in one launch.
+ * State: length [B] (committed tokens), held [B] (pages in the request's row
+ * of block_table int32 [B][max_pages]), and the free pages, the `cursor[1]`
+ * entries of ring int32 [num_pages] from cursor[0] on, wrapping.  Per request:
+ *   L = length + n_commit[b % n_commit_count] + n_commit_bias   (n_commit may
+ *       be NULL: L = length); clamped to [0, held * page_size], a clamp sets
+ *       SV_FLAG_REPLAY_RANGE.  spec_accept's n_accepted feeds it directly,
+ *       bias 1 when the last committed token is among the verify rows.
+ *   n_new < 0: the request has ended; its pages go back to the ring (to be
+ *       given out from the next step on), and length, held and kv_len are 0.
+ *   else n_new rows are packed after those of the requests before it, pages
+ *       for L + n_new tokens are taken from the ring in request order, and
+ *       kv_len = L + n_new.  A request is refused when it would pass max_pages
+ *       or the free pages left by the requests before it, those refused for
+ *       want of free pages included (SV_FLAG_NO_PAGES), or when its rows
+ *       would pass `rows` (SV_FLAG_ROWS): it takes no page, its rows stay (as
+ *       far as they fit) with slot -1, and kv_len is 0, so paged_attention
+ *       gives zeros for them.
+ * Outputs: length_out, held_out, cursor_out (may be the inputs' own buffers),
+ * block_table and ring (in place), q_start [B+1], kv_len [B], and for each of
+ * the `rows` rows its slot (page * page_size + offset; -1 for a refused
+ * request's row, a page id outside [0, num_pages) and rows past the last) and
+ * its position L + t (0 past the last).  err_flags [B] may be NULL.
+ * SV_FLAG_PAGE_STATE: held or the cursor out of range (clamped), or more
+ * pages given back than the ring has room for (the rest is dropped).
+ * Requires B <= 4096 (0: no-op), rows >= 0, max_pages * page_size + rows and
+ * num_pages * page_size below 2^31; 4-byte aligned pointers; apart from the
+ * three in-place pairs no output overlaps an input or another output. */
+sv_status kv_pages_step(const int32_t *length, const int32_t *held, const int32_t *cursor,
+                        const int32_t *n_new, const int32_t *n_commit, int n_commit_count,
+                        int n_commit_bias, int B, int page_size, int max_pages, int num_pages,
+                        int rows, int32_t *block_table, int32_t *ring, int32_t *length_out,
+                        int32_t *held_out, int32_t *cursor_out, int32_t *q_start,
+                        int32_t *kv_len, int32_t *slots, int32_t *positions,
+                        int32_t *err_flags, sv_stream_t stream);
+
+/* rope_kv_append: per packed row, q [Hq][D], k and v [Hkv][D] (fp32 or bf16,
+ * rows q_row_stride etc. elements apart, so the three may be slices of one
+ * projection's rows):
+ *   q and k heads, when q_weight / k_weight fp32 [D] are given, are scaled to
+ *     x_e w_e / sqrt(mean(x^2) + eps);
+ *   their first rotary_dim elements are turned: pair f of rotary_dim / 2, the
+ *     elements (f, f + rotary_dim / 2), or (2f, 2f + 1) when interleaved, by
+ *     the angle  2 pi 2^-64 freqs[f] * positions[row][axis[f]]  (modulo a
+ *     turn, exact to 2^-34 turns at any 31-bit position);
+ *   q goes to q_out bf16 [rows][Hq][D], k and v to slot slots[row] of the
+ *     caches bf16 [num_pages][Hkv][page_size][D]; a slot outside
+ *     [0, num_pages * page_size) writes nothing to the caches.
+ * Arithmetic is fp32, rounded once to bf16.  Two rows with the same slot leave
+ * either one's values there.  positions int32 [rows][axes]; freqs uint64
+ * [rotary_dim / 2] (turns per position in units of 2^-64); axis uint8
+ * [rotary_dim / 2] (NULL with one axis; values past axes - 1 count as that).
+ * Requires D 64, 128 or 256; rotary_dim a multiple of 16 in [0, D]; axes 1..4;
+ * q, k, v, q_out and the caches 16-byte aligned, row strides multiples of 16
+ * bytes; no output overlaps an input or another output. */
+sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x_dtype,
+                         long long q_row_stride, long long k_row_stride, long long v_row_stride,
+                         const int32_t *positions, int axes, const int32_t *slots,
+                         const uint64_t *freqs, const uint8_t *axis, const float *q_weight,
+                         const float *k_weight, float eps, int rows, int Hq, int Hkv, int D,
+                         int rotary_dim, int interleaved, int page_size, int num_pages,
+                         uint16_t *q_out, uint16_t *k_cache, uint16_t *v_cache,
+                         sv_stream_t stream);
+
+/* paged_attention: causal attention of packed rows over the paged cache.
+ * Row t of request b (n = q_start[b+1] - q_start[b] rows) stands at position
+ * p = kv_len[b] - n + t and attends positions max(0, p - window + 1) .. p of
+ * the request (from 0 when window is 0); its query heads h G .. h G + G - 1
+ * (G = Hq / Hkv) read kv head h:
+ *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)
+ * A row that attends nothing (p < 0) is zero with lse -inf, and so are rows
+ * from q_start[B] on.  Positions j come from page block_table[b][j / page_size];
+ * a page id outside [0, num_pages) reads as zeros.  What no row attends is not
+ * read, or has no effect whatever it holds: slots past kv_len, pages before
+ * the window, later tokens of a chunk, NaN and infinities included.
+ * q bf16 [rows][Hq][D] and out bf16 [rows][Hq][D] with their rows
+ * q_row_stride and out_row_stride elements apart; caches bf16
+ * [num_pages][Hkv][page_size][D]; block_table int32 [B][max_pages]; q_start
+ * int32 [B+1], ascending from 0 and clamped to [0, rows]; kv_len int32 [B],
+ * clamped to [0, max_pages * page_size]; lse fp32 [rows][Hq] or NULL.
+ * max_new: the caller's bound on n, which picks the kernel; a request with
+ * more rows is still computed.  Scores, sums and outputs are fp32, weights
+ * are rounded to bf16 before they multiply the values, out once at the end.
+ * Results do not depend on the run (no floating-point atomics).
+ * Requires Hq a multiple of Hkv; D 64, 128 or 256; scale positive and finite;
+ * window >= 0; (num_pages + 1) * Hkv * page_size below 2^31; q, out and the
+ * caches 16-byte aligned, row strides multiples of 8 elements; no output
+ * overlaps an input.
+ * workspace: paged_attention_workspace_bytes(D) bytes on the current device
+ * (0 on an unsupported D), 256-byte aligned, zero-filled once by the caller;
+ * every call leaves its counters (the first 4096 bytes) at zero for the next,
+ * of any shape with this D.  Calls that run concurrently need workspaces of
+ * their own.  One launch on `stream`. */
+size_t paged_attention_workspace_bytes(int D);
+sv_status paged_attention(const uint16_t *q, long long q_row_stride, const uint16_t *k_cache,
+                          const uint16_t *v_cache, const int32_t *block_table,
+                          const int32_t *q_start, const int32_t *kv_len, int B, int rows,
+                          int max_new, int Hq, int Hkv, int D, int page_size, int num_pages,
+                          int max_pages, float scale, int window, uint16_t *out,
+                          long long out_row_stride, float *lse, void *workspace,
+                          size_t workspace_bytes, sv_stream_t stream);
 
 #ifdef __cplusplus
 }

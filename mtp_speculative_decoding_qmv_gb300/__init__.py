@@ -10,11 +10,16 @@ the library is missing, every call raises -- there is no fallback.
   spec_accept       fp32 probability-ratio acceptance, residual, bonus token
   gdn_tape_capture  GatedDeltaNet recurrence + innovation tape
   gdn_tape_replay   rebuild the recurrent state over an accepted prefix
+  kv_pages_step     a paged cache's bookkeeping of one step
+  rope_kv_append    rotary positions; keys and values into the paged cache
+  paged_attention   a step's new tokens over the paged cache
 """
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
@@ -23,6 +28,8 @@ __all__ = [
     "make_accept_workspace", "gdn_tape_bytes", "gdn_tape_capture", "gdn_tape_replay",
     "set_pdl", "get_pdl", "device_status", "FLAGS", "QmvPlan", "spec_accept_noalloc",
     "spec_accept_noalloc_scratch_bytes", "conv_window_capture", "conv_window_replay",
+    "KvStep", "kv_pages_step", "rope_freqs", "rope_kv_append", "paged_attention",
+    "make_attention_workspace", "paged_attention_workspace_bytes",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
@@ -30,7 +37,7 @@ _LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_DEVICE_FLAG = range(5)
 SV_F32, SV_BF16 = 0, 1
 FLAGS = {"draft_out_of_range": 1, "draft_zero_q": 2, "nonfinite_logit": 4, "empty_dist": 8,
-         "replay_range": 16}
+         "replay_range": 16, "no_pages": 32, "rows": 64, "page_state": 128}
 
 
 class SvError(RuntimeError):
@@ -122,6 +129,18 @@ def lib() -> ctypes.CDLL:
         L.gdn_tape_capture.restype = I
         L.gdn_tape_replay.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P]
         L.gdn_tape_replay.restype = I
+        LL, F = ctypes.c_longlong, ctypes.c_float
+        L.kv_pages_step.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, P,
+                                    P, P, P]
+        L.kv_pages_step.restype = I
+        L.rope_kv_append.argtypes = [P, P, P, I, LL, LL, LL, P, I, P, P, P, P, P, F, I, I, I, I,
+                                     I, I, I, I, P, P, P, P]
+        L.rope_kv_append.restype = I
+        L.paged_attention_workspace_bytes.argtypes = [I]
+        L.paged_attention_workspace_bytes.restype = Z
+        L.paged_attention.argtypes = [P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P,
+                                      LL, P, P, Z, P]
+        L.paged_attention.restype = I
         _lib = L
     return _lib
 
@@ -616,3 +635,220 @@ def conv_window_replay(window: torch.Tensor, x: torch.Tensor, n_replay: torch.Te
     _check(lib().conv_window_replay(_ptr(window), _ptr(x), _ptr(n_replay), n_replay.numel(),
                                     int(n_replay_bias), B, T, C, W, _ptr(err_flags),
                                     _stream(dev)), "conv_window_replay")
+
+
+# ----------------------------------------------------------------------------
+class KvStep(NamedTuple):
+    """What :func:`kv_pages_step` writes (block_table and ring are updated in place)."""
+    length: torch.Tensor     # [B] committed tokens
+    held: torch.Tensor       # [B] pages in the table's row
+    cursor: torch.Tensor     # [2] first free entry of the ring, free pages
+    q_start: torch.Tensor    # [B + 1] packed rows of each request
+    kv_len: torch.Tensor     # [B] positions after the step's new tokens
+    slots: torch.Tensor      # [rows]
+    positions: torch.Tensor  # [rows]
+    err_flags: torch.Tensor  # [B]
+
+
+def _out(t, name, dtype, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, shape, dev)
+    return t
+
+
+def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor,
+                  ring: torch.Tensor, block_table: torch.Tensor, n_new: torch.Tensor,
+                  page_size: int, rows: int, *, n_commit: torch.Tensor | None = None,
+                  n_commit_bias: int = 0, length_out: torch.Tensor | None = None,
+                  held_out: torch.Tensor | None = None, cursor_out: torch.Tensor | None = None,
+                  q_start: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
+                  slots: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                  err_flags: torch.Tensor | None = None) -> KvStep:
+    """Commits ``n_commit`` tokens of the previous step, gives every request
+    pages for its ``n_new`` tokens (-1: it ended, its pages return to the
+    ring) and writes the step's packed rows: slots and positions.  All int32.
+    ``length_out=length`` and so on update the state in place."""
+    dev, i32 = length.device, torch.int32
+    B, max_pages = block_table.shape
+    _need(length, "length", i32, (B,), dev)
+    _need(held, "held", i32, (B,), dev)
+    _need(cursor, "cursor", i32, (2,), dev)
+    _need(ring, "ring", i32, None, dev)
+    _need(block_table, "block_table", i32, None, dev)
+    _need(n_new, "n_new", i32, (B,), dev)
+    if n_commit is not None:
+        _need(n_commit, "n_commit", i32, None, dev)
+    rows = int(rows)
+    step = KvStep(_out(length_out, "length_out", i32, (B,), dev),
+                  _out(held_out, "held_out", i32, (B,), dev),
+                  _out(cursor_out, "cursor_out", i32, (2,), dev),
+                  _out(q_start, "q_start", i32, (B + 1,), dev),
+                  _out(kv_len, "kv_len", i32, (B,), dev),
+                  _out(slots, "slots", i32, (max(rows, 0),), dev),
+                  _out(positions, "positions", i32, (max(rows, 0),), dev),
+                  _out(err_flags, "err_flags", i32, (B,), dev))
+    with torch.cuda.device(dev):
+        st = lib().kv_pages_step(
+            length.data_ptr(), held.data_ptr(), cursor.data_ptr(), n_new.data_ptr(),
+            None if n_commit is None else n_commit.data_ptr(),
+            0 if n_commit is None else n_commit.numel(), int(n_commit_bias), B, int(page_size),
+            max_pages, ring.numel(), rows, block_table.data_ptr(), ring.data_ptr(),
+            step.length.data_ptr(), step.held.data_ptr(), step.cursor.data_ptr(),
+            step.q_start.data_ptr(), step.kv_len.data_ptr(), step.slots.data_ptr(),
+            step.positions.data_ptr(), step.err_flags.data_ptr(), _stream(dev))
+    _check(st, "kv_pages_step")
+    return step
+
+
+def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:
+    """Rotary frequencies for :func:`rope_kv_append`: ``inv_freq`` float64
+    [rotary_dim / 2], radians per position, as int64 words of 2^-64 turns."""
+    if inv_freq.dtype != torch.float64:
+        raise TypeError(f"inv_freq must be torch.float64, got {inv_freq.dtype}")
+    turns = inv_freq / (2.0 * math.pi)
+    turns = (turns - torch.floor(turns)) * 2.0 ** 32
+    high = torch.floor(turns)
+    low = torch.floor((turns - high) * 2.0 ** 32 + 0.5)
+    # the sum wraps modulo 2^64, as angles wrap modulo one turn
+    return (high.to(torch.int64) << 32) + low.to(torch.int64)
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, heads: int, D: int, dev) -> int:
+    """Packed rows [rows, heads, D] with contiguous heads; returns the row stride."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads}, {D})")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if t.shape[0] > 1 else heads * D
+
+
+def _need_cache(t: torch.Tensor, name: str, shape, dev) -> None:
+    _need(t, name, torch.bfloat16, shape, dev)
+
+
+def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                   slots: torch.Tensor, freqs: torch.Tensor | None, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, *, axis: torch.Tensor | None = None,
+                   q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                   eps: float = 1e-6, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Turns q [rows, Hq, D] and k [rows, Hkv, D] (fp32 or bf16; row slices of
+    one projection's output will do) by their positions [rows] or [rows, axes],
+    after the norm of each head where a weight fp32 [D] is given; writes q to
+    ``q_out`` bf16 and k, v to ``slots`` of the caches bf16
+    [pages, Hkv, page_size, D] in place.  Returns q_out."""
+    dev = q.device
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [rows, Hq, D] and the caches [pages, Hkv, page_size, D]")
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    rows, Hq, D = q.shape
+    pages, Hkv, page_size, _ = k_cache.shape
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("q, k and v must be float32 or bfloat16")
+    qs = _need_rows(q, "q", q.dtype, Hq, D, dev)
+    ks = _need_rows(k, "k", q.dtype, Hkv, D, dev)
+    vs = _need_rows(v, "v", q.dtype, Hkv, D, dev)
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError("q, k and v must have the same rows")
+    _need_cache(k_cache, "k_cache", (pages, Hkv, page_size, D), dev)
+    _need_cache(v_cache, "v_cache", (pages, Hkv, page_size, D), dev)
+    axes = 1 if positions.dim() == 1 else positions.shape[-1]
+    _need(positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes),
+          dev)
+    _need(slots, "slots", torch.int32, (rows,), dev)
+    half = 0
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [rotary_dim / 2]")
+        _need(freqs, "freqs", torch.int64, None, dev)
+        half = freqs.numel()
+    if axis is not None:
+        _need(axis, "axis", torch.uint8, (half,), dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, (D,), dev)
+    if q_out is None:
+        q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
+    _need(q_out, "q_out", torch.bfloat16, (rows, Hq, D), dev)
+    with torch.cuda.device(dev):
+        st = lib().rope_kv_append(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            SV_BF16 if q.dtype == torch.bfloat16 else SV_F32, qs, ks, vs, positions.data_ptr(),
+            axes, slots.data_ptr(), None if freqs is None else freqs.data_ptr(),
+            None if axis is None else axis.data_ptr(),
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), float(eps), rows, Hq, Hkv, D,
+            2 * half, 1 if interleaved else 0, page_size, pages, q_out.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), _stream(dev))
+    _check(st, "rope_kv_append")
+    return q_out
+
+
+def paged_attention_workspace_bytes(D: int) -> int:
+    return int(lib().paged_attention_workspace_bytes(int(D)))
+
+
+def make_attention_workspace(D: int, device) -> torch.Tensor:
+    """A workspace (uint8) for paged_attention with head dim D, its counters zero."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = paged_attention_workspace_bytes(D)
+        if n == 0:
+            _check(SV_ERR_UNSUPPORTED, "paged_attention_workspace_bytes")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:4096].zero_()
+    return ws
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                    max_new: int, *, scale: float | None = None, window: int = 0,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None):
+    """Causal attention of packed rows q bf16 [rows, Hq, D] over caches bf16
+    [pages, Hkv, page_size, D]: request b's rows q_start[b]:q_start[b+1] are
+    its last positions of kv_len[b].  ``max_new``: a bound on a request's rows;
+    ``scale``: 1 / sqrt(D) when omitted.  Returns (out bf16 [rows, Hq, D],
+    lse); lse fp32 [rows, Hq] is written when given.  ``workspace`` (from
+    make_attention_workspace) is made per call when omitted."""
+    dev = q.device
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [rows, Hq, D], the caches [pages, Hkv, page_size, D] and "
+                         "block_table [B, max_pages]")
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    rows, Hq, D = q.shape
+    pages, Hkv, page_size, _ = k_cache.shape
+    B, max_pages = block_table.shape
+    qs = _need_rows(q, "q", torch.bfloat16, Hq, D, dev)
+    _need_cache(k_cache, "k_cache", (pages, Hkv, page_size, D), dev)
+    _need_cache(v_cache, "v_cache", (pages, Hkv, page_size, D), dev)
+    _need(block_table, "block_table", torch.int32, None, dev)
+    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
+    os_ = _need_rows(out, "out", torch.bfloat16, Hq, D, dev)
+    if out.shape[0] != rows:
+        raise ValueError("q and out must have the same rows")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (rows, Hq), dev)
+    if workspace is None:
+        workspace = make_attention_workspace(D, dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    with torch.cuda.device(dev):
+        st = lib().paged_attention(
+            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            q_start.data_ptr(), kv_len.data_ptr(), B, rows, int(max_new), Hq, Hkv, D, page_size,
+            pages, max_pages, 1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
+            out.data_ptr(), os_, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream(dev))
+    _check(st, "paged_attention")
+    return out, lse

@@ -1,0 +1,225 @@
+// attn_common.cuh -- shared by the two paged-attention kernels: the call's
+// arguments, which keys each packed query row may attend, how the work is cut
+// into equal runs of key tiles, the joining of split results, and the plain
+// row-by-row path for non-finite values in masked places.
+//
+// Row r = t G + g of request b and kv head h is token t (of n_b) under query
+// head h G + g (G = Hq / Hkv query heads share a kv head), so all rows of
+// (b, h) read the same keys.  Token t stands at position p = kv_len_b - n_b + t
+// and attends positions max(0, p - window + 1) .. p (from 0 when window is 0):
+//   out_r = sum_j softmax_j(scale q_r . k_j) v_j
+// and a row with no position (p < 0) is zero, its log-sum-exp -inf.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sv_device.cuh"
+
+namespace sv {
+namespace attn {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kMaxCtas = 1024;  // join counters at the start of the workspace
+constexpr size_t kCounterBytes = kMaxCtas * 4;
+
+struct Args {
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_stride, out_stride;  // elements from a row to the next
+  __nv_bfloat16 *out;
+  float *lse;  // [rows][Hq] or null
+  const int32_t *table, *q_start, *kv_len;
+  int B, rows, Hq, Hkv, G;
+  int num_pages, max_pages, page_shift, window;
+  float scale, scale_log2;  // scale, scale * log2(e)
+  unsigned *counters;       // [kMaxCtas], zero between calls
+  float *partials;
+};
+
+struct Request {
+  int q0, n, len;  // first packed row, new tokens, positions in the cache
+};
+__device__ __forceinline__ Request load_request(const Args &a, int b) {
+  Request r;
+  r.q0 = min(max(__ldg(a.q_start + b), 0), a.rows);
+  r.n = min(max(__ldg(a.q_start + b + 1), r.q0), a.rows) - r.q0;
+  const long long most = (long long)a.max_pages << a.page_shift;
+  r.len = (int)min((long long)max(__ldg(a.kv_len + b), 0), most);
+  return r;
+}
+// Rows [r0, r0 + count) of a request: positions [lo, hi) hold every key that
+// one of them attends; [all_lo, all_hi) the keys that all of them attend.
+struct Span {
+  int lo, hi, all_lo, all_hi;
+};
+__device__ __forceinline__ Span rows_span(const Args &a, const Request &q, int r0, int count) {
+  const int t0 = r0 / a.G, t1 = (r0 + count - 1) / a.G;
+  const int p0 = q.len - q.n + t0, p1 = q.len - q.n + t1;
+  Span s;
+  s.hi = max(p1 + 1, 0);
+  s.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), s.hi) : 0;
+  s.all_lo = a.window > 0 ? max(p1 - a.window + 1, 0) : 0;
+  s.all_hi = max(p0 + 1, 0);
+  return s;
+}
+
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                              uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ bool has_nonfinite_bf16x2(uint32_t u) {
+  return (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// log-sum-exp of a row from its sum l and the maximum m of its raw scores
+__device__ __forceinline__ float row_lse(const Args &a, float m, float l) {
+  return l > 0.f || l != l ? fmaf(m, a.scale, logf(l)) : kNegInf;
+}
+
+// The first tensor-map row of page `idx` of request b under head h, or the row
+// past the last (read as zeros) when the page holds no key in [lo, hi) or its
+// id is out of range.
+__device__ __forceinline__ int page_row(const Args &a, int b, int h, int idx, int lo, int hi) {
+  int page = a.num_pages;
+  const long long first = (long long)idx << a.page_shift;
+  if (first < hi && first + (1 << a.page_shift) > lo && idx < a.max_pages) {
+    page = __ldg(a.table + (size_t)b * a.max_pages + idx);
+    if ((unsigned)page >= (unsigned)a.num_pages) page = a.num_pages;
+  }
+  return (page * a.Hkv + (page < a.num_pages ? h : 0)) << a.page_shift;
+}
+
+// One row by a whole warp, straight from memory, over its keys in [j0, j1):
+// only keys that the row attends are read.  Lane l returns elements
+// l D / 32 .. of the unnormalised sum, with the row's maximum raw score and
+// sum.  Taken where a masked place holds an infinity or NaN value, which a
+// tile's product would multiply by a weight of zero.
+template <int D>
+__device__ __noinline__ void attend_row(const Args &a, int b, int h, const Request &rq, int r,
+                                        int j0, int j1, float (&o)[D / 32], float &m, float &l) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int t = r / a.G, g = r - t * a.G;
+  const int p = rq.len - rq.n + t;
+  if (a.window > 0) j0 = max(j0, p - a.window + 1);
+  j1 = min(j1, p + 1);
+  const __nv_bfloat16 *q =
+      a.q + (long long)(rq.q0 + t) * a.q_stride + (long long)(h * a.G + g) * D + lane * E;
+  float qv[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = __bfloat162float(q[e]);
+    o[e] = 0.f;
+  }
+  m = kNegInf;
+  l = 0.f;
+  for (int j = max(j0, 0); j < j1; ++j) {
+    const int page = __ldg(a.table + (size_t)b * a.max_pages + (j >> a.page_shift));
+    const bool ok = (unsigned)page < (unsigned)a.num_pages;
+    const long long at =
+        ((((long long)page * a.Hkv + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D +
+        lane * E;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(qv[e], ok ? __bfloat162float(a.k[at + e]) : 0.f, s);
+    s = warp_sum(s);
+    const float mn = fmaxf(m, s);
+    const float ms = mn == kNegInf ? 0.f : mn;
+    const float keep = exp2_approx((m - ms) * a.scale_log2);
+    const float w = exp2_approx((s - ms) * a.scale_log2);
+    l = l * keep + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o[e] = fmaf(w, ok ? __bfloat162float(a.v[at + e]) : 0.f, o[e] * keep);
+    m = mn;
+  }
+}
+
+// ---- equal runs of work ------------------------------------------------------
+// The items (request, row tile, kv head) each own a run of key tiles; laid end
+// to end they make `units` tiles, cut into `ctas` runs that differ by at most
+// one tile, so ragged lengths balance by themselves and a single long request
+// spreads over the device.  A CTA's run holds at most two items that it does
+// not own whole: the one it begins inside and the one it ends inside.
+struct Runs {
+  long long units;
+  int ctas;
+  __device__ long long begin(int c) const { return units * c / ctas; }
+  // the CTA whose run holds unit u
+  __device__ int owner(long long u) const { return (int)(((u + 1) * ctas - 1) / units); }
+};
+
+// A split item's partial result: unnormalised sums [rows][D], then maxima and
+// sums [rows] each.  CTA c has two: 2 c + 1 for the item that begins in its run
+// and ends in a later one, 2 c for the one that began in an earlier run.
+__device__ __forceinline__ float *partial_at(const Args &a, int slot, int tile_rows, int D) {
+  return a.partials + (size_t)slot * tile_rows * (D + 2);
+}
+
+// Elements d .. d + 3 of row r, normalised and rounded, and with element 0 the
+// row's log-sum-exp.  A row that attends nothing is zero.
+template <int D>
+__device__ __forceinline__ void store_out4(const Args &a, const Request &rq, int h, int r, int d,
+                                           float4 o, float m, float l) {
+  const int t = r / a.G, g = r - t * a.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2 *>(a.out + (long long)(rq.q0 + t) * a.out_stride +
+                             (long long)(h * a.G + g) * D + d) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (d == 0 && a.lse) a.lse[(long long)(rq.q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
+}
+
+// The same from the partial results of CTAs c0 .. c1, in that order.
+template <int D>
+__device__ __forceinline__ void join_row4(const Args &a, const Request &rq, int h, int r, int rr,
+                                          int d, int c0, int c1, int tile_rows) {
+  float m = kNegInf, l = 0.f;
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const float *part = partial_at(a, 2 * c + (c == c0 ? 1 : 0), tile_rows, D);
+    m = fmaxf(m, __ldcg(part + tile_rows * D + rr));
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float *part = partial_at(a, 2 * c + (c == c0 ? 1 : 0), tile_rows, D);
+    const float mc = __ldcg(part + tile_rows * D + rr), lc = __ldcg(part + tile_rows * (D + 1) + rr);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + rr * D + d));
+    // no keys: nothing (its maximum is -inf, and so may be every other)
+    const float f = mc == kNegInf && lc == 0.f ? 0.f : exp2_approx((mc - m) * a.scale_log2);
+    l = fmaf(lc, f, l);
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  store_out4<D>(a, rq, h, r, d, acc, m, l);
+}
+
+}  // namespace attn
+}  // namespace sv

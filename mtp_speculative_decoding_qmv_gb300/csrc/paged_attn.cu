@@ -1,0 +1,656 @@
+// paged_attn.cu -- attention of a step's new tokens over a paged cache,
+// sm_103a: the entry point, and the kernel for few rows (single tokens and
+// verify blocks); the mathematics and the split of work are in attn_common.cuh.
+//
+// Few rows read each key and value once and do little with it: D products and
+// sums per row against 4 D bytes, so streaming the cache bounds it.  A CTA
+// takes a run of 64-key tiles (attn_common.cuh): one producer warp copies them
+// with TMA, page by page, 128-byte swizzled, into a ring of key and value
+// slots; four consumer warps hold 16 rows each in registers and multiply with
+// mma.sync (16 x 8 x 16): kRowGroups warps side by side in rows, the others
+// splitting a tile's keys, each with its own running maximum and sum (no
+// barrier per tile), joined through shared memory at the end of an item.  The
+// rows of the G query heads of a kv head are packed together, so a key read
+// once serves them all.  Scores, maxima, sums and outputs are fp32; weights
+// are rounded to bf16 for the second product (at most half a step, 2^-8 of
+// each weight, the type of the values they multiply), their sum is not.
+//
+// An item that several CTAs share is joined by the last of them to finish
+// (a counter in the workspace, left at zero for the next call), always in CTA
+// order, so results do not depend on which one that is.
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "qmv_common.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace attn {
+
+__device__ unsigned int g_attn_device_error;
+
+namespace {
+
+constexpr int kBK = 64;  // keys per tile
+constexpr int kWarps = 4;
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kConsumers = kWarps * 32;
+
+template <int D>
+struct RowsShape {
+  static constexpr uint32_t kSlotBytes = kBK * D * 2;    // a tile's keys, or its values
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr int kOutStride = D + 8;               // floats: rows 8 banks apart
+  static constexpr uint32_t kOutBytes = kWarps * 16 * kOutStride * 4;
+  static constexpr uint32_t kSmem = kSlots * kSlotBytes + kOutBytes + 1024;
+  static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
+
+// Key tiles of every item of a request: enough for its longest row tile, so
+// that items can be found by division; an item's own tiles come first and the
+// rest of its run is empty.
+__device__ __forceinline__ int tiles_per_item(const Args &a, const Request &q, int tile_rows) {
+  long long tiles = (q.len + kBK - 1) / kBK;
+  if (a.window > 0)
+    tiles = min(tiles, ((long long)a.window + tile_rows / a.G + 2 + kBK - 1) / kBK + 1);
+  return (int)max(tiles, 1ll);
+}
+__device__ __forceinline__ long long request_units(const Args &a, const Request &q,
+                                                   int tile_rows) {
+  const long long nt = ((long long)q.n * a.G + tile_rows - 1) / tile_rows;
+  return nt * a.Hkv * tiles_per_item(a, q, tile_rows);
+}
+
+struct Segment {
+  Request rq;
+  int b, h, r0, count;       // rows [r0, r0 + count) of kv head h of request b
+  Span span;
+  int tile0, tiles;          // key tiles [tile0, tile0 + tiles) (may be none)
+  long long item;            // first unit of the item
+  int first, n_units, width; // the segment's units of the item, the item's
+};
+
+// Walks a run's segments in order.
+struct Walk {
+  long long u, end, base;  // next unit, end of the run, first unit of request b
+  int b;
+  __device__ bool next(const Args &a, int tile_rows, Segment &s) {
+    if (u >= end) return false;
+    for (;;) {
+      s.rq = load_request(a, b);
+      const long long size = request_units(a, s.rq, tile_rows);
+      if (u - base < size) break;
+      base += size;
+      ++b;
+    }
+    s.b = b;
+    s.width = tiles_per_item(a, s.rq, tile_rows);
+    const long long item = (u - base) / s.width;
+    s.item = base + item * s.width;
+    s.first = (int)(u - s.item);
+    s.n_units = (int)min((long long)(s.width - s.first), end - u);
+    s.h = (int)(item % a.Hkv);
+    s.r0 = (int)(item / a.Hkv) * tile_rows;
+    s.count = min(tile_rows, s.rq.n * a.G - s.r0);
+    s.span = rows_span(a, s.rq, s.r0, s.count);
+    const int t0 = s.span.lo / kBK, t1 = (s.span.hi + kBK - 1) / kBK;
+    s.tile0 = t0 + s.first;
+    s.tiles = max(0, min(t1 - s.tile0, s.n_units));
+    u += s.n_units;
+    return true;
+  }
+};
+
+template <int D, int kRowGroups>
+__global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const Args a) {
+  using S = RowsShape<D>;
+  constexpr int kKeyGroups = kWarps / kRowGroups;
+  constexpr int kWarpKeys = kBK / kKeyGroups;  // 16, 32 or 64
+  constexpr int kTileRows = 16 * kRowGroups;
+  constexpr int kSteps = D / 16;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  __shared__ long long s_scan[kThreads / 32], s_base;
+  __shared__ int s_b, s_nonfinite, s_last;
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t ring = raw + ((1024u - (raw & 1023u)) & 1023u);
+  float *s_out = reinterpret_cast<float *>(smem_raw + (ring - raw) + S::kSlots * S::kSlotBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    s_nonfinite = 0;
+    fence_mbar_init();
+  }
+  // ---- this CTA's run of units, and the request that it begins in ----
+  Runs runs;
+  auto block_sum = [&](long long v, long long &upto) {  // inclusive scan and total
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = v;
+    __syncthreads();
+    long long all = 0;
+    upto = v;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) upto += s_scan[i];
+      all += s_scan[i];
+    }
+    return all;
+  };
+  runs.units = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    long long upto;
+    runs.units += block_sum(
+        b < a.B ? request_units(a, load_request(a, b), kTileRows) : 0, upto);
+  }
+  runs.ctas = (int)min((long long)gridDim.x, runs.units);
+  // rows past the last request's: zero
+  const int used = min(max(__ldg(a.q_start + a.B), 0), a.rows);
+  for (int r = used + blockIdx.x; r < a.rows; r += gridDim.x) {
+    for (int i = tid; i < a.Hq * (D / 8); i += kThreads)
+      reinterpret_cast<uint4 *>(a.out + (long long)r * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(long long)r * a.Hq + i] = kNegInf;
+  }
+  if ((int)blockIdx.x >= runs.ctas) return;  // uniform
+  Walk walk;
+  walk.u = runs.begin(blockIdx.x);
+  walk.end = runs.begin(blockIdx.x + 1);
+  long long sum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    const long long size = b < a.B ? request_units(a, load_request(a, b), kTileRows) : 0;
+    long long upto;
+    const long long all = block_sum(size, upto);
+    upto += sum;
+    if (upto > walk.u && upto - size <= walk.u) {
+      s_b = b;
+      s_base = upto - size;
+    }
+    sum += all;
+    if (sum > walk.u) break;
+  }
+  __syncthreads();
+  walk.b = s_b;
+  walk.base = s_base;
+
+  uint32_t slot = 0, phase = 0;  // of the next ring slot
+  auto advance = [&] {
+    if (++slot == (uint32_t)S::kSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  };
+  bool dead = false;  // a wait gave up: the rest runs without waiting, results are invalid
+  Segment s;
+
+  if (warp == kWarps) {
+    // ------------------------------ producer ------------------------------
+    const int per_page = min(kBK, 1 << a.page_shift);  // rows of one copy
+    const int pages = kBK / per_page;
+    const int boxes = pages * (D / 64);
+    const int blk = lane / pages, pg = lane - blk * pages;
+    long long issued = 0;
+    while (walk.next(a, kTileRows, s)) {
+      for (int t = 0; t < s.tiles; ++t) {
+        const int j = (s.tile0 + t) * kBK + pg * per_page;
+        int y = 0;
+        if (lane < boxes)
+          y = page_row(a, s.b, s.h, j >> a.page_shift, s.span.lo, s.span.hi) +
+              (j & ((1 << a.page_shift) - 1));
+        for (int kv = 0; kv < 2; ++kv) {
+          if (issued >= S::kSlots && !dead && !mbar_wait(&empty[slot], phase ^ 1u)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+          if (dead) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kSlotBytes);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_rows(ring + slot * S::kSlotBytes + (uint32_t)blk * (kBK * 128) +
+                              (uint32_t)pg * per_page * 128,
+                          kv ? &vmap : &kmap, blk * 64, y, smem_addr(&full[slot]));
+          ++issued;
+          advance();
+        }
+        if (dead) break;
+      }
+      if (dead) break;
+    }
+    if (dead && lane == 0) atomicOr(&g_attn_device_error, 1u);
+    // every copy has landed before the CTA may exit
+    for (long long k = max(0ll, issued - S::kSlots); k < issued; ++k)
+      (void)mbar_wait(&full[k % S::kSlots], (uint32_t)((k / S::kSlots) & 1));
+    return;
+  }
+
+  // ------------------------------- consumers ------------------------------
+  const int wr = warp / kKeyGroups, wk = warp % kKeyGroups;
+  const int gq = lane >> 2, gc = lane & 3;  // row and column pair of an accumulator
+  // ldmatrix rows of this lane: keys for the first product, keys for the second
+  const int k_key = wk * kWarpKeys + ((lane >> 4) << 3) + (lane & 7), k_half = (lane >> 3) & 1;
+  const int v_key = wk * kWarpKeys + (lane & 15), v_half = lane >> 4;
+  auto wait_full = [&] {
+    if (!dead && !mbar_wait(&full[slot], phase)) {
+      dead = true;
+      atomicOr(&g_attn_device_error, 2u);
+    }
+  };
+
+  while (walk.next(a, kTileRows, s)) {
+    // queries as A fragments; rows past the tile are zero
+    uint32_t qf[kSteps][4];
+    int last[2], first[2];  // positions that rows gq and gq + 8 attend: first .. last
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int rr = wr * 16 + gq + 8 * i;
+      const int r = s.r0 + rr;
+      const int t = r / a.G, g = r - t * a.G;
+      const bool ok = rr < s.count;
+      last[i] = ok ? s.rq.len - s.rq.n + t : -1;
+      first[i] = a.window > 0 ? last[i] - a.window + 1 : 0;
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(
+          a.q + (long long)(s.rq.q0 + (ok ? t : 0)) * a.q_stride +
+          (long long)(s.h * a.G + (ok ? g : 0)) * D);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qf[k][i] = ok ? __ldg(src + k * 8 + gc) : 0u;
+        qf[k][2 + i] = ok ? __ldg(src + k * 8 + 4 + gc) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+
+    for (int t = 0; t < s.tiles; ++t) {
+      const int j0 = (s.tile0 + t) * kBK;
+      const bool masked = j0 < s.span.all_lo || j0 + kBK > s.span.all_hi;
+      // ---- scores of this warp's keys ----
+      float x[kWarpKeys / 8][4];
+#pragma unroll
+      for (int n = 0; n < kWarpKeys / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+      wait_full();
+      uint32_t base = ring + slot * S::kSlotBytes;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int c = 2 * k + k_half;  // 16-byte column of the key row
+#pragma unroll
+        for (int n = 0; n < kWarpKeys / 16; ++n) {
+          const int key = k_key + 16 * n;
+          uint32_t f[4];
+          qmv::ldmatrix_x4(f, base + (uint32_t)(c >> 3) * (kBK * 128) + (uint32_t)key * 128 +
+                                  (uint32_t)(((c & 7) ^ (key & 7)) << 4));
+          mma_bf16_m16n8k16(x[2 * n], qf[k][0], qf[k][1], qf[k][2], qf[k][3], f[0], f[1]);
+          mma_bf16_m16n8k16(x[2 * n + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], f[2], f[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      advance();
+      if (masked) {
+#pragma unroll
+        for (int n = 0; n < kWarpKeys / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + wk * kWarpKeys + n * 8 + gc * 2 + (e & 1);
+            if (j < first[e >> 1] || j > last[e >> 1]) x[n][e] = kNegInf;
+          }
+      }
+      // ---- running maximum and sum, weights ----
+      float keep[2];
+      uint32_t p[kWarpKeys / 8][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = kNegInf;
+#pragma unroll
+        for (int n = 0; n < kWarpKeys / 8; ++n) mx = fmaxf(mx, fmaxf(x[n][2 * i], x[n][2 * i + 1]));
+        const float mn = fmaxf(m[i], quad_max(mx));
+        const float ms = mn == kNegInf ? 0.f : mn;
+        keep[i] = exp2_approx((m[i] - ms) * a.scale_log2);
+        m[i] = mn;
+        const float off = ms * a.scale_log2;
+        float sum_p = 0.f;
+#pragma unroll
+        for (int n = 0; n < kWarpKeys / 8; ++n) {
+          const float p0 = exp2_approx(fmaf(x[n][2 * i], a.scale_log2, -off));
+          const float p1 = exp2_approx(fmaf(x[n][2 * i + 1], a.scale_log2, -off));
+          sum_p += p0 + p1;
+          p[n][i] = pack_bf16(p0, p1);
+        }
+        l[i] = l[i] * keep[i] + sum_p;
+      }
+      if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          o[d][0] *= keep[0];
+          o[d][1] *= keep[0];
+          o[d][2] *= keep[1];
+          o[d][3] *= keep[1];
+        }
+      }
+      // ---- weights times values ----
+      wait_full();
+      base = ring + slot * S::kSlotBytes;
+      if (masked) {
+        // places no row attends may hold anything: zero, so that a weight of
+        // zero meets no NaN; a non-finite value that some rows attend and
+        // others do not sends the segment to the row-by-row path
+        consumer_sync();
+        const int key = tid >> 1, pos = j0 + key;
+        const bool none = pos < s.span.lo || pos >= s.span.hi;
+        if (none || pos < s.span.all_lo || pos >= s.span.all_hi) {
+          bool odd = false;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint4 *at = reinterpret_cast<uint4 *>(
+                smem_raw + (base - raw) + (size_t)((tid & 1) * (D / 16) + c) / 8 * (kBK * 128) +
+                key * 128 + ((((tid & 1) * (D / 16) + c) & 7) << 4));
+            if (none) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              const uint4 v = *at;
+              odd |= has_nonfinite_bf16x2(v.x) | has_nonfinite_bf16x2(v.y) |
+                     has_nonfinite_bf16x2(v.z) | has_nonfinite_bf16x2(v.w);
+            }
+          }
+          if (odd) s_nonfinite = 1;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        consumer_sync();
+      }
+#pragma unroll
+      for (int n = 0; n < kWarpKeys / 16; ++n) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          const int key = v_key + 16 * n, c = 2 * d + v_half;
+          uint32_t f[4];
+          ldmatrix_x4_trans(f, base + (uint32_t)(c >> 3) * (kBK * 128) + (uint32_t)key * 128 +
+                                   (uint32_t)(((c & 7) ^ (key & 7)) << 4));
+          mma_bf16_m16n8k16(o[2 * d], p[2 * n][0], p[2 * n][1], p[2 * n + 1][0], p[2 * n + 1][1],
+                            f[0], f[1]);
+          mma_bf16_m16n8k16(o[2 * d + 1], p[2 * n][0], p[2 * n][1], p[2 * n + 1][0],
+                            p[2 * n + 1][1], f[2], f[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      advance();
+    }
+
+    // ---- the warps' sums to shared memory ----
+    consumer_sync();  // s_out of the segment before has been read, s_nonfinite is written
+    if (s_nonfinite) {
+      for (int rr = warp; rr < kTileRows; rr += kWarps) {
+        const int w0 = (rr >> 4) * kKeyGroups;
+        float acc[D / 32], mr = kNegInf, lr = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+        if (rr < s.count)
+          attend_row<D>(a, s.b, s.h, s.rq, s.r0 + rr, s.tile0 * kBK, (s.tile0 + s.tiles) * kBK,
+                        acc, mr, lr);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          s_out[(w0 * 16 + (rr & 15)) * S::kOutStride + lane * (D / 32) + e] = acc[e];
+        if (lane < kKeyGroups) {
+          s_m[w0 + lane][rr & 15] = lane == 0 ? mr : kNegInf;
+          s_l[w0 + lane][rr & 15] = lane == 0 ? lr : 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] = quad_sum(l[i]);
+        if (gc == 0) {
+          s_m[warp][gq + 8 * i] = m[i];
+          s_l[warp][gq + 8 * i] = l[i];
+        }
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float2 *>(
+              &s_out[(warp * 16 + gq + 8 * i) * S::kOutStride + d * 8 + gc * 2]) =
+              make_float2(o[d][2 * i], o[d][2 * i + 1]);
+      }
+    }
+    consumer_sync();
+    if (tid == 0) s_nonfinite = 0;  // next written after the next segment's barrier
+
+    const bool whole = s.first == 0 && s.n_units == s.width;
+    const int c0 = whole ? 0 : runs.owner(s.item), c1 = whole ? 0 : runs.owner(s.item + s.width - 1);
+    float *part = partial_at(a, 2 * (int)blockIdx.x + (s.first == 0 ? 1 : 0), kTileRows, D);
+    for (int i = tid; i < s.count * (D / 4); i += kConsumers) {
+      const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
+      const int w0 = (rr >> 4) * kKeyGroups;
+      float mm = kNegInf, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kKeyGroups; ++w) mm = fmaxf(mm, s_m[w0 + w][rr & 15]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kKeyGroups; ++w) {
+        const float mw = s_m[w0 + w][rr & 15];
+        if (mw == kNegInf && s_l[w0 + w][rr & 15] == 0.f) continue;  // no keys
+        const float f = exp2_approx((mw - mm) * a.scale_log2);
+        const float4 v = *reinterpret_cast<const float4 *>(
+            &s_out[((w0 + w) * 16 + (rr & 15)) * S::kOutStride + d]);
+        ll = fmaf(s_l[w0 + w][rr & 15], f, ll);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      if (whole) {
+        store_out4<D>(a, s.rq, s.h, s.r0 + rr, d, acc, mm, ll);
+      } else {
+        __stcg(reinterpret_cast<float4 *>(part + rr * D + d), acc);
+        if (d == 0) {
+          __stcg(part + kTileRows * D + rr, mm);
+          __stcg(part + kTileRows * (D + 1) + rr, ll);
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      consumer_sync();
+      if (tid == 0) {
+        const unsigned n = atomicAdd(a.counters + c0, 1u);
+        s_last = n == (unsigned)(c1 - c0);
+        if (s_last) a.counters[c0] = 0;  // every CTA of the item has arrived
+      }
+      consumer_sync();
+      if (s_last) {
+        __threadfence();
+        for (int i = tid; i < s.count * (D / 4); i += kConsumers) {
+          const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
+          join_row4<D>(a, s.rq, s.h, s.r0 + rr, rr, d, c0, c1, kTileRows);
+        }
+      }
+    }
+  }
+}
+
+template <int D, int kRowGroups>
+sv_status launch_rows(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, int ctas,
+                      cudaStream_t stream) {
+  using S = RowsShape<D>;
+  static PerDeviceOnce once;
+  const cudaError_t ce = once.run([] {
+    return cudaFuncSetAttribute(attn_rows_kernel<D, kRowGroups>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  });
+  if (ce != cudaSuccess)
+    return fail(SV_ERR_CUDA, "paged_attention: cudaFuncSetAttribute failed: %s",
+                cudaGetErrorString(ce));
+  attn_rows_kernel<D, kRowGroups><<<(unsigned)ctas, kThreads, S::kSmem, stream>>>(kmap, vmap, a);
+  return check_launch("paged_attention");
+}
+
+template <int D>
+sv_status launch_rows(int groups, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a,
+                      int ctas, cudaStream_t stream) {
+  if (groups == 1) return launch_rows<D, 1>(kmap, vmap, a, ctas, stream);
+  if (groups == 2) return launch_rows<D, 2>(kmap, vmap, a, ctas, stream);
+  return launch_rows<D, 4>(kmap, vmap, a, ctas, stream);
+}
+
+int rows_ctas(int D) { return std::min(kMaxCtas, device_sm_count() * (D == 256 ? 1 : 2)); }
+
+size_t workspace_bytes(int D) {
+  const size_t rows = (size_t)rows_ctas(D) * 2 * 64 * (D + 2) * 4;
+  return kCounterBytes + rows;
+}
+
+}  // namespace
+}  // namespace attn
+
+unsigned take_device_error_attn() {
+  unsigned v = 0, zero = 0;
+  cudaMemcpyFromSymbol(&v, attn::g_attn_device_error, sizeof v);
+  cudaMemcpyToSymbol(attn::g_attn_device_error, &zero, sizeof zero);
+  return v;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t paged_attention_workspace_bytes(int D) {
+  clear_error();
+  if (D != 64 && D != 128 && D != 256) {
+    fail(SV_ERR_UNSUPPORTED, "paged_attention_workspace_bytes: D=%d is not 64, 128 or 256", D);
+    return 0;
+  }
+  return attn::workspace_bytes(D);
+}
+
+extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
+                                     const uint16_t *k_cache, const uint16_t *v_cache,
+                                     const int32_t *block_table, const int32_t *q_start,
+                                     const int32_t *kv_len, int B, int rows, int max_new, int Hq,
+                                     int Hkv, int D, int page_size, int num_pages, int max_pages,
+                                     float scale, int window, uint16_t *out,
+                                     long long out_row_stride, float *lse, void *workspace,
+                                     size_t workspace_bytes, sv_stream_t stream) {
+  clear_error();
+  const char *who = "paged_attention";
+  if (B < 0 || rows < 0 || max_new < 0 || Hq < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1)
+    return fail(SV_ERR_INVALID_ARG,
+                "%s: need B, rows, max_new >= 0 and Hq, Hkv, num_pages, max_pages >= 1 (B=%d "
+                "rows=%d max_new=%d Hq=%d Hkv=%d num_pages=%d max_pages=%d)",
+                who, B, rows, max_new, Hq, Hkv, num_pages, max_pages);
+  if (Hq % Hkv) return fail(SV_ERR_INVALID_ARG, "%s: Hq=%d is not a multiple of Hkv=%d", who, Hq, Hkv);
+  if (D != 64 && D != 128 && D != 256)
+    return fail(SV_ERR_UNSUPPORTED, "%s: D=%d is not 64, 128 or 256", who, D);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return fail(SV_ERR_UNSUPPORTED, "%s: page_size=%d is not 16, 32, 64, 128 or 256", who,
+                page_size);
+  if (!(scale > 0.f) || scale > 3.0e38f)
+    return fail(SV_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (window < 0) return fail(SV_ERR_INVALID_ARG, "%s: window must be >= 0", who);
+  if (((long long)num_pages + 1) * Hkv * page_size >= (1ll << 31) ||
+      (long long)max_pages * page_size + 256 >= (1ll << 31))
+    return fail(SV_ERR_UNSUPPORTED, "%s: cache rows or positions pass 31 bits", who);
+  if ((long long)rows * (Hq / Hkv) + 256 >= (1ll << 31) || Hq > 65536)
+    return fail(SV_ERR_UNSUPPORTED, "%s: too many rows or heads", who);
+  if (B == 0 || rows == 0) return SV_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !q_start || !kv_len || !out || !workspace)
+    return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (q_row_stride < (long long)Hq * D || out_row_stride < (long long)Hq * D)
+    return fail(SV_ERR_INVALID_ARG, "%s: a row stride is smaller than its row", who);
+  if (q_row_stride % 8 || out_row_stride % 8)
+    return fail(SV_ERR_INVALID_ARG, "%s: row strides must be multiples of 16 bytes", who);
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    return fail(SV_ERR_INVALID_ARG, "%s: q, the caches and out must be 16-byte aligned", who);
+  if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
+      (lse && !aligned(lse, 4)))
+    return fail(SV_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  if (!aligned(workspace, 256))
+    return fail(SV_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  const size_t need = attn::workspace_bytes(D);
+  if (workspace_bytes < need)
+    return fail(SV_ERR_INVALID_ARG, "%s: workspace of %zu bytes, need %zu", who, workspace_bytes,
+                need);
+  const size_t cache = (size_t)num_pages * Hkv * page_size * D * 2;
+  struct Buf {
+    const void *p;
+    size_t n;
+  };
+  const Buf in[] = {{q, ((size_t)(rows - 1) * q_row_stride + (size_t)Hq * D) * 2},
+                    {k_cache, cache}, {v_cache, cache},
+                    {block_table, (size_t)B * max_pages * 4}, {q_start, ((size_t)B + 1) * 4},
+                    {kv_len, (size_t)B * 4}};
+  const Buf outs[] = {{out, ((size_t)(rows - 1) * out_row_stride + (size_t)Hq * D) * 2},
+                      {lse, (size_t)rows * Hq * 4}, {workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Buf &b : in)
+      if (overlaps(outs[i].p, outs[i].n, b.p, b.n))
+        return fail(SV_ERR_INVALID_ARG, "%s: an output or the workspace overlaps an input", who);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(SV_ERR_INVALID_ARG, "%s: two of out, lse and workspace overlap", who);
+  }
+  attn::Args a = {};
+  a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+  a.k = reinterpret_cast<const __nv_bfloat16 *>(k_cache);
+  a.v = reinterpret_cast<const __nv_bfloat16 *>(v_cache);
+  a.q_stride = q_row_stride;
+  a.out_stride = out_row_stride;
+  a.out = reinterpret_cast<__nv_bfloat16 *>(out);
+  a.lse = lse;
+  a.table = block_table;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.rows = rows;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.window = window;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.counters = static_cast<unsigned *>(workspace);
+  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + attn::kCounterBytes);
+
+  const uint32_t box = (uint32_t)std::min(page_size, attn::kBK);
+  const uint64_t cache_rows = (uint64_t)num_pages * Hkv * page_size;
+  CUtensorMap kmap, vmap;
+  sv_status st = qmv::encode_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, (uint64_t)D,
+                                cache_rows, (uint64_t)D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SV_OK) return st;
+  st = qmv::encode_2d(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, v_cache, (uint64_t)D, cache_rows,
+                      (uint64_t)D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SV_OK) return st;
+
+  // Row tiles of 16, 32 or 64 rows, the least that holds a request's rows.
+  const long long most = (long long)std::min(max_new, rows) * a.G;
+  const int groups = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+  const int ctas = attn::rows_ctas(D);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 64) return attn::launch_rows<64>(groups, kmap, vmap, a, ctas, s);
+  if (D == 128) return attn::launch_rows<128>(groups, kmap, vmap, a, ctas, s);
+  return attn::launch_rows<256>(groups, kmap, vmap, a, ctas, s);
+}

@@ -1,0 +1,348 @@
+// rope_append.cu -- a step's queries, keys and values on their way to paged
+// attention, sm_103a: the norm of each query and key head, rotary positions
+// with one or more axes, and the keys and values into their slots of the paged
+// cache, in one pass over the projections' outputs.
+//
+// Per head x of D values (norm where a weight is given, queries and keys only):
+//   y_e = x_e w_e / sqrt(sum_i x_i^2 / D + eps)                        (fp32)
+// and for rotary pair f < R / 2 with elements (a, b) = (f, f + R / 2), or
+// (2f, 2f + 1) when interleaved, and t = position[axis_f] * freq_f:
+//   y_a' = y_a cos t - y_b sin t,   y_b' = y_b cos t + y_a sin t
+// Elements past R pass through; values only change their type.  Everything is
+// computed in fp32 and rounded once, to bf16, at the store.
+//
+// The angle of a far position needs more bits than fp32 has (position 10^6
+// times a frequency near 1 leaves an error of 0.06 rad), so frequencies come
+// as turns per position in 64-bit fixed point (2^-64 turns): the product with
+// the integer position wraps modulo one turn by itself and is exact to
+// position x 2^-65 turns.  Its top 32 bits, a signed fraction of a turn, go to
+// sincospi: an absolute error near 2e-7 rad at any position, with no double
+// precision arithmetic.
+//
+// Memory traffic is the bound: each input read once, each output written once.
+// A warp owns one row and kHeads consecutive heads of its queries, keys and
+// values; lane l holds elements l D / 32 .. (l + 1) D / 32 of each, loaded as
+// one vector, so a head is one contiguous request per warp and all kHeads
+// loads are in flight together.  The lane's angles depend on the row and its
+// elements alone and serve every head.  The partner element of a pair is in
+// the same lane (interleaved) or R / (2 D / 32) lanes away (one shuffle).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "sv_device.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace {
+
+constexpr int kRopeWarps = 4;
+constexpr int kMaxAxes = 4;
+
+struct RopeArgs {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;  // elements from a row to the next
+  const int32_t *positions, *slots;
+  const uint64_t *freqs;
+  const uint8_t *axis;
+  const float *q_weight, *k_weight;
+  float eps;
+  int rows, axes, Hq, Hkv, R, page_shift;
+  int num_slots;
+  __nv_bfloat16 *q_out, *k_cache, *v_cache;
+};
+
+template <typename T, int N>
+struct Vec;
+template <int N>
+struct Vec<float, N> {
+  __device__ static void load(const float *p, float (&x)[N]) {
+    if constexpr (N == 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+      x[0] = v.x, x[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + i);
+        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+      }
+    }
+  }
+};
+template <int N>
+struct Vec<__nv_bfloat16, N> {
+  __device__ static void unpack(uint32_t u, float &a, float &b) {
+    a = __uint_as_float(u << 16);
+    b = __uint_as_float(u & 0xFFFF0000u);
+  }
+  __device__ static void load(const __nv_bfloat16 *p, float (&x)[N]) {
+    if constexpr (N == 2) {
+      unpack(__ldg(reinterpret_cast<const uint32_t *>(p)), x[0], x[1]);
+    } else if constexpr (N == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+      unpack(v.x, x[0], x[1]);
+      unpack(v.y, x[2], x[3]);
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+      unpack(v.x, x[0], x[1]);
+      unpack(v.y, x[2], x[3]);
+      unpack(v.z, x[4], x[5]);
+      unpack(v.w, x[6], x[7]);
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&x)[N]) {
+  if constexpr (N == 2) {
+    *reinterpret_cast<uint32_t *>(p) = pack_bf16(x[0], x[1]);
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  } else {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                               pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+}
+
+template <typename T, int D, bool kPairs, int kHeads>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const RopeArgs a) {
+  constexpr int E = D / 32;  // elements a lane holds
+  const int lane = threadIdx.x & 31;
+  const int total = a.Hq + 2 * a.Hkv;
+  const int groups = (total + kHeads - 1) / kHeads;
+  const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  if (task >= (long long)a.rows * groups) return;
+  const int row = (int)(task / groups);
+  const int h0 = (int)(task - (long long)row * groups) * kHeads;
+  const int e0 = lane * E;
+
+  float x[kHeads][E];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i;
+    const T *src = nullptr;
+    if (h < a.Hq)
+      src = static_cast<const T *>(a.q) + (long long)row * a.q_stride + (long long)h * D;
+    else if (h < a.Hq + a.Hkv)
+      src = static_cast<const T *>(a.k) + (long long)row * a.k_stride + (long long)(h - a.Hq) * D;
+    else if (h < total)
+      src = static_cast<const T *>(a.v) + (long long)row * a.v_stride +
+            (long long)(h - a.Hq - a.Hkv) * D;
+    if (src) {
+      Vec<T, E>::load(src + e0, x[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+    }
+  }
+  const int slot = __ldg(a.slots + row);
+  const bool keep = (unsigned)slot < (unsigned)a.num_slots;
+
+  const int half = a.R / 2;
+  const bool turned = e0 < a.R;  // R is a multiple of 2 E: a lane is wholly in or out
+  float cs[E], sn[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) cs[e] = 1.f, sn[e] = 0.f;
+  if (h0 < a.Hq + a.Hkv && turned) {
+    auto angle = [&](int f, float &c, float &s) {
+      const int ax = a.axis ? min((int)__ldg(a.axis + f), a.axes - 1) : 0;
+      const int pos = __ldg(a.positions + (long long)row * a.axes + ax);
+      const uint64_t turns = (uint64_t)(int64_t)pos * __ldg(a.freqs + f);
+      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+    };
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        angle((e0 + e) / 2, cs[e], sn[e]);
+        cs[e + 1] = cs[e];
+        sn[e + 1] = sn[e];
+        sn[e] = -sn[e];
+      }
+    } else {
+      const bool first = e0 < half;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        angle(e0 + e - (first ? 0 : half), cs[e], sn[e]);
+        if (first) sn[e] = -sn[e];
+      }
+    }
+  }
+  const int partner = !turned ? lane : e0 < half ? lane + half / E : lane - half / E;
+  const long long page = keep ? slot >> a.page_shift : 0;
+  const int off = slot & ((1 << a.page_shift) - 1);
+
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i;  // uniform in the warp
+    if (h >= total) break;
+    if (h < a.Hq + a.Hkv) {
+      const float *w = h < a.Hq ? a.q_weight : a.k_weight;
+      if (w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+        const float r = rsqrtf(warp_sum(ss) * (1.f / D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = x[i][e] * r * __ldg(w + e0 + e);
+      }
+      float y[E];
+      if constexpr (kPairs) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = x[i][e ^ 1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = __shfl_sync(0xffffffffu, x[i][e], partner);
+      }
+      if (turned) {  // else as it is, infinities included
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = fmaf(y[e], sn[e], x[i][e] * cs[e]);
+      }
+    }
+    __nv_bfloat16 *dst;
+    if (h < a.Hq) {
+      dst = a.q_out + ((long long)row * a.Hq + h) * D;
+    } else {
+      if (!keep) continue;
+      const int kh = h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv;
+      dst = (h < a.Hq + a.Hkv ? a.k_cache : a.v_cache) +
+            (((page * a.Hkv + kh) << a.page_shift) + off) * D;
+    }
+    store_bf16<E>(dst + e0, x[i]);
+  }
+}
+
+typedef void (*RopeKernel)(const RopeArgs);
+
+template <typename T, int D>
+RopeKernel pick(bool pairs, bool many) {
+  return pairs ? (many ? rope_append_kernel<T, D, true, 8> : rope_append_kernel<T, D, true, 2>)
+               : (many ? rope_append_kernel<T, D, false, 8> : rope_append_kernel<T, D, false, 2>);
+}
+template <typename T>
+RopeKernel pick(int D, bool pairs, bool many) {
+  return D == 64 ? pick<T, 64>(pairs, many)
+                 : D == 128 ? pick<T, 128>(pairs, many) : pick<T, 256>(pairs, many);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x_dtype,
+                                    long long q_row_stride, long long k_row_stride,
+                                    long long v_row_stride, const int32_t *positions, int axes,
+                                    const int32_t *slots, const uint64_t *freqs,
+                                    const uint8_t *axis, const float *q_weight,
+                                    const float *k_weight, float eps, int rows, int Hq, int Hkv,
+                                    int D, int rotary_dim, int interleaved, int page_size,
+                                    int num_pages, uint16_t *q_out, uint16_t *k_cache,
+                                    uint16_t *v_cache, sv_stream_t stream) {
+  clear_error();
+  const char *who = "rope_kv_append";
+  if (rows < 0 || Hq < 1 || Hkv < 1 || num_pages < 1)
+    return fail(SV_ERR_INVALID_ARG,
+                "%s: need rows >= 0, Hq >= 1, Hkv >= 1, num_pages >= 1 (rows=%d Hq=%d Hkv=%d "
+                "num_pages=%d)",
+                who, rows, Hq, Hkv, num_pages);
+  if (x_dtype != SV_F32 && x_dtype != SV_BF16)
+    return fail(SV_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)x_dtype);
+  if (D != 64 && D != 128 && D != 256)
+    return fail(SV_ERR_UNSUPPORTED, "%s: D=%d is not 64, 128 or 256", who, D);
+  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16)
+    return fail(SV_ERR_INVALID_ARG, "%s: rotary_dim=%d is not a multiple of 16 in [0, D=%d]", who,
+                rotary_dim, D);
+  if (axes < 1 || axes > kMaxAxes)
+    return fail(SV_ERR_UNSUPPORTED, "%s: axes=%d outside [1, %d]", who, axes, kMaxAxes);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return fail(SV_ERR_UNSUPPORTED, "%s: page_size=%d is not 16, 32, 64, 128 or 256", who,
+                page_size);
+  if ((long long)num_pages * page_size >= (1ll << 31))
+    return fail(SV_ERR_UNSUPPORTED, "%s: slots pass 31 bits", who);
+  if (Hq > 4096 || Hkv > 4096) return fail(SV_ERR_UNSUPPORTED, "%s: more than 4096 heads", who);
+  if (!(eps >= 0.f)) return fail(SV_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  if (rows == 0) return SV_OK;
+  if (!q || !k || !v || !positions || !slots || (rotary_dim > 0 && !freqs) || !q_out || !k_cache ||
+      !v_cache || (axes > 1 && rotary_dim > 0 && !axis))
+    return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
+  const int size = x_dtype == SV_F32 ? 4 : 2;
+  if (q_row_stride < (long long)Hq * D || k_row_stride < (long long)Hkv * D ||
+      v_row_stride < (long long)Hkv * D)
+    return fail(SV_ERR_INVALID_ARG, "%s: a row stride is smaller than its row", who);
+  if (q_row_stride * size % 16 || k_row_stride * size % 16 || v_row_stride * size % 16)
+    return fail(SV_ERR_INVALID_ARG, "%s: row strides must be multiples of 16 bytes", who);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(SV_ERR_INVALID_ARG, "%s: q, k, v, q_out and the caches must be 16-byte aligned",
+                who);
+  if (!aligned(positions, 4) || !aligned(slots, 4) || (freqs && !aligned(freqs, 8)) ||
+      (q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4)))
+    return fail(SV_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  const size_t cache = (size_t)num_pages * Hkv * page_size * D * 2;
+  const size_t qo = (size_t)rows * Hq * D * 2;
+  struct Buf {
+    const void *p;
+    size_t n;
+  };
+  const Buf in[] = {
+      {q, ((size_t)(rows - 1) * q_row_stride + (size_t)Hq * D) * size},
+      {k, ((size_t)(rows - 1) * k_row_stride + (size_t)Hkv * D) * size},
+      {v, ((size_t)(rows - 1) * v_row_stride + (size_t)Hkv * D) * size},
+      {positions, (size_t)rows * axes * 4}, {slots, (size_t)rows * 4},
+      {freqs, (size_t)rotary_dim * 4}, {axis, axis ? (size_t)rotary_dim / 2 : 0},
+      {q_weight, (size_t)D * 4}, {k_weight, (size_t)D * 4}};
+  const Buf out[] = {{q_out, qo}, {k_cache, cache}, {v_cache, cache}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Buf &b : in)
+      if (overlaps(out[i].p, out[i].n, b.p, b.n))
+        return fail(SV_ERR_INVALID_ARG, "%s: an output overlaps an input", who);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(SV_ERR_INVALID_ARG, "%s: two outputs overlap", who);
+  }
+  RopeArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.freqs = freqs;
+  a.axis = axes > 1 ? axis : nullptr;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.rows = rows;
+  a.axes = axes;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.R = rotary_dim;
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.num_slots = num_pages * page_size;
+  a.q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
+  a.k_cache = reinterpret_cast<__nv_bfloat16 *>(k_cache);
+  a.v_cache = reinterpret_cast<__nv_bfloat16 *>(v_cache);
+
+  // Two heads a warp while that leaves the SMs fewer than 32 warps each, so a
+  // small step spreads over the device; eight beyond, where a row's angles
+  // serve more heads and more loads are in flight.
+  const int total = Hq + 2 * Hkv;
+  const bool many = (long long)rows * total / 2 > (long long)device_sm_count() * 32;
+  const int per = many ? 8 : 2;
+  const long long tasks = (long long)rows * ((total + per - 1) / per);
+  const long long ctas = (tasks + kRopeWarps - 1) / kRopeWarps;
+  if (ctas >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "%s: too many rows", who);
+  const RopeKernel kernel = x_dtype == SV_F32 ? pick<float>(D, interleaved != 0, many)
+                                              : pick<__nv_bfloat16>(D, interleaved != 0, many);
+  kernel<<<(unsigned)ctas, kRopeWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch(who);
+}

@@ -81,8 +81,10 @@ extern "C" sv_status sv_device_status(void) {
   const unsigned g = sv::take_device_error_gdn();
   const unsigned p = sv::take_device_error_plan();
   const unsigned w = sv::take_device_error_wide();
-  if (q | a | g | p | w)
+  const unsigned t = sv::take_device_error_attn();
+  if (q | a | g | p | w | t)
     return sv::fail(SV_ERR_DEVICE_FLAG,
-                    "device error words: qmv=%u accept=%u gdn=%u plan=%u wide=%u", q, a, g, p, w);
+                    "device error words: qmv=%u accept=%u gdn=%u plan=%u wide=%u attention=%u", q,
+                    a, g, p, w, t);
   return SV_OK;
 }

@@ -53,5 +53,6 @@ unsigned take_device_error_accept();
 unsigned take_device_error_gdn();
 unsigned take_device_error_plan();
 unsigned take_device_error_wide();
+unsigned take_device_error_attn();
 
 }  // namespace sv
