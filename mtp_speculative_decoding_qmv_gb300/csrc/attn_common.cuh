@@ -84,8 +84,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ bool has_nonfinite_bf16x2(uint32_t u) {
-  return (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u;
+// Nonzero when one of the two bf16 values is infinite or NaN: adding a unit to
+// a full exponent carries into the sign's place.
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t u) {
+  return ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -95,6 +97,11 @@ __device__ __forceinline__ float quad_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
+
+// Bounded waits that gave up, per translation unit (paged_attn.cu and
+// paged_attn_tc.cu each have their own word).
+static __device__ unsigned int g_give_up;
+__device__ __forceinline__ void report_give_up(unsigned bit) { atomicOr(&g_give_up, bit); }
 
 // log-sum-exp of a row from its sum l and the maximum m of its raw scores
 __device__ __forceinline__ float row_lse(const Args &a, float m, float l) {
@@ -120,16 +127,17 @@ __device__ __forceinline__ int page_row(const Args &a, int b, int h, int idx, in
 // sum.  Taken where a masked place holds an infinity or NaN value, which a
 // tile's product would multiply by a weight of zero.
 template <int D>
-__device__ __noinline__ void attend_row(const Args &a, int b, int h, const Request &rq, int r,
-                                        int j0, int j1, float (&o)[D / 32], float &m, float &l) {
+__device__ __forceinline__ void attend_row(const Args &a, int b, int h, int q0, int n, int len,
+                                           int r, int j0, int j1, float (&o)[D / 32], float &m,
+                                           float &l) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int t = r / a.G, g = r - t * a.G;
-  const int p = rq.len - rq.n + t;
+  const int p = len - n + t;
   if (a.window > 0) j0 = max(j0, p - a.window + 1);
   j1 = min(j1, p + 1);
   const __nv_bfloat16 *q =
-      a.q + (long long)(rq.q0 + t) * a.q_stride + (long long)(h * a.G + g) * D + lane * E;
+      a.q + (long long)(q0 + t) * a.q_stride + (long long)(h * a.G + g) * D + lane * E;
   float qv[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -194,7 +202,21 @@ __device__ __forceinline__ void store_out4(const Args &a, const Request &rq, int
   if (d == 0 && a.lse) a.lse[(long long)(rq.q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
 }
 
-// The same from the partial results of CTAs c0 .. c1, in that order.
+// The same with lane l of a warp holding elements l D / 32 .. of row r.
+template <int D>
+__device__ __forceinline__ void store_lane(const Args &a, int q0, int h, int r,
+                                           const float (&o)[D / 32], float m, float l) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, t = r / a.G, g = r - t * a.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (long long)(q0 + t) * a.out_stride +
+                                               (long long)(h * a.G + g) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
+}
+
+// As store_out4, from the partial results of CTAs c0 .. c1, in that order.
 template <int D>
 __device__ __forceinline__ void join_row4(const Args &a, const Request &rq, int h, int r, int rr,
                                           int d, int c0, int c1, int tile_rows) {

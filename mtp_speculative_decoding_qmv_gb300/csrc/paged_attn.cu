@@ -21,13 +21,12 @@
 #include <algorithm>
 
 #include "attn_common.cuh"
+#include "attn_host.h"
 #include "qmv_common.cuh"
 #include "sv_internal.h"
 
 namespace sv {
 namespace attn {
-
-__device__ unsigned int g_attn_device_error;
 
 namespace {
 
@@ -110,10 +109,34 @@ struct Walk {
   }
 };
 
+// The consumers' results of a segment, row by row (attend_row), in the place
+// of the first key group's; the other groups' hold nothing.
+template <int D, int kRowGroups>
+__device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
+                                        int r0, int count, int j0, int j1, float *s_out,
+                                        float *s_m, float *s_l) {
+  constexpr int kKeyGroups = kWarps / kRowGroups;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int rr = warp; rr < 16 * kRowGroups; rr += kWarps) {
+    const int w0 = (rr >> 4) * kKeyGroups;
+    float o[D / 32], m = kNegInf, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    if (rr < count) attend_row<D>(a, b, h, q0, n, len, r0 + rr, j0, j1, o, m, l);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      s_out[(w0 * 16 + (rr & 15)) * RowsShape<D>::kOutStride + lane * (D / 32) + e] = o[e];
+    if (lane < kKeyGroups) {
+      s_m[(w0 + lane) * 16 + (rr & 15)] = lane == 0 ? m : kNegInf;
+      s_l[(w0 + lane) * 16 + (rr & 15)] = lane == 0 ? l : 0.f;
+    }
+  }
+}
+
 template <int D, int kRowGroups>
 __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     attn_rows_kernel(const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, const Args a) {
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
   using S = RowsShape<D>;
   constexpr int kKeyGroups = kWarps / kRowGroups;
   constexpr int kWarpKeys = kBK / kKeyGroups;  // 16, 32 or 64
@@ -235,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
       }
       if (dead) break;
     }
-    if (dead && lane == 0) atomicOr(&g_attn_device_error, 1u);
+    if (dead && lane == 0) report_give_up(1u);
     // every copy has landed before the CTA may exit
     for (long long k = max(0ll, issued - S::kSlots); k < issued; ++k)
       (void)mbar_wait(&full[k % S::kSlots], (uint32_t)((k / S::kSlots) & 1));
@@ -251,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
   auto wait_full = [&] {
     if (!dead && !mbar_wait(&full[slot], phase)) {
       dead = true;
-      atomicOr(&g_attn_device_error, 2u);
+      report_give_up(2u);
     }
   };
 
@@ -362,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
         const int key = tid >> 1, pos = j0 + key;
         const bool none = pos < s.span.lo || pos >= s.span.hi;
         if (none || pos < s.span.all_lo || pos >= s.span.all_hi) {
-          bool odd = false;
+          uint32_t odd = 0;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint4 *at = reinterpret_cast<uint4 *>(
@@ -372,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
               *at = make_uint4(0, 0, 0, 0);
             } else {
               const uint4 v = *at;
-              odd |= has_nonfinite_bf16x2(v.x) | has_nonfinite_bf16x2(v.y) |
-                     has_nonfinite_bf16x2(v.z) | has_nonfinite_bf16x2(v.w);
+              odd |= nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) |
+                     nonfinite_bits(v.w);
             }
           }
           if (odd) s_nonfinite = 1;
@@ -403,22 +426,9 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     // ---- the warps' sums to shared memory ----
     consumer_sync();  // s_out of the segment before has been read, s_nonfinite is written
     if (s_nonfinite) {
-      for (int rr = warp; rr < kTileRows; rr += kWarps) {
-        const int w0 = (rr >> 4) * kKeyGroups;
-        float acc[D / 32], mr = kNegInf, lr = 0.f;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-        if (rr < s.count)
-          attend_row<D>(a, s.b, s.h, s.rq, s.r0 + rr, s.tile0 * kBK, (s.tile0 + s.tiles) * kBK,
-                        acc, mr, lr);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          s_out[(w0 * 16 + (rr & 15)) * S::kOutStride + lane * (D / 32) + e] = acc[e];
-        if (lane < kKeyGroups) {
-          s_m[w0 + lane][rr & 15] = lane == 0 ? mr : kNegInf;
-          s_l[w0 + lane][rr & 15] = lane == 0 ? lr : 0.f;
-        }
-      }
+      rows_plain<D, kRowGroups>(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, s.count,
+                                s.tile0 * kBK, (s.tile0 + s.tiles) * kBK, s_out, &s_m[0][0],
+                                &s_l[0][0]);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -517,8 +527,9 @@ sv_status launch_rows(int groups, const CUtensorMap &kmap, const CUtensorMap &vm
 int rows_ctas(int D) { return std::min(kMaxCtas, device_sm_count() * (D == 256 ? 1 : 2)); }
 
 size_t workspace_bytes(int D) {
-  const size_t rows = (size_t)rows_ctas(D) * 2 * 64 * (D + 2) * 4;
-  return kCounterBytes + rows;
+  size_t part = (size_t)rows_ctas(D) * 2 * 64 * (D + 2) * 4;
+  if (D <= 128) part = std::max(part, tc_partial_bytes(D));
+  return kCounterBytes + part;
 }
 
 }  // namespace
@@ -526,9 +537,9 @@ size_t workspace_bytes(int D) {
 
 unsigned take_device_error_attn() {
   unsigned v = 0, zero = 0;
-  cudaMemcpyFromSymbol(&v, attn::g_attn_device_error, sizeof v);
-  cudaMemcpyToSymbol(attn::g_attn_device_error, &zero, sizeof zero);
-  return v;
+  cudaMemcpyFromSymbol(&v, attn::g_give_up, sizeof v);
+  cudaMemcpyToSymbol(attn::g_give_up, &zero, sizeof zero);
+  return v | attn::tc_take_give_up();
 }
 
 }  // namespace sv
@@ -635,21 +646,18 @@ extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
   a.counters = static_cast<unsigned *>(workspace);
   a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + attn::kCounterBytes);
 
-  const uint32_t box = (uint32_t)std::min(page_size, attn::kBK);
-  const uint64_t cache_rows = (uint64_t)num_pages * Hkv * page_size;
-  CUtensorMap kmap, vmap;
-  sv_status st = qmv::encode_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, (uint64_t)D,
-                                cache_rows, (uint64_t)D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != SV_OK) return st;
-  st = qmv::encode_2d(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, v_cache, (uint64_t)D, cache_rows,
-                      (uint64_t)D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != SV_OK) return st;
-
-  // Row tiles of 16, 32 or 64 rows, the least that holds a request's rows.
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // More rows a kv head than a 64-row tile of the streaming kernel holds go to
+  // the tensor-core kernel (its tiles are 128 rows, two at a time).
   const long long most = (long long)std::min(max_new, rows) * a.G;
+  if (most > 64 && D <= 128) return attn::tc_run(D, a, s);
+  CUtensorMap kmap, vmap;
+  sv_status st = attn::encode_cache(&kmap, a.k, D, a, attn::kBK);
+  if (st == SV_OK) st = attn::encode_cache(&vmap, a.v, D, a, attn::kBK);
+  if (st != SV_OK) return st;
+  // Row tiles of 16, 32 or 64 rows, the least that holds a request's rows.
   const int groups = most <= 16 ? 1 : most <= 32 ? 2 : 4;
   const int ctas = attn::rows_ctas(D);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (D == 64) return attn::launch_rows<64>(groups, kmap, vmap, a, ctas, s);
   if (D == 128) return attn::launch_rows<128>(groups, kmap, vmap, a, ctas, s);
   return attn::launch_rows<256>(groups, kmap, vmap, a, ctas, s);

@@ -1,0 +1,890 @@
+// paged_attn_tc.cu -- attention of prompt chunks (many rows a request) over a
+// paged cache on the 5th-generation tensor cores, sm_103a; the mathematics and
+// the split of work are in attn_common.cuh.
+//
+// Per key, R packed rows of a kv head take 4 R D flops against 4 D bytes, so
+// from about 300 rows on (this card's tensor rate over its bandwidth) the
+// tensor cores bound it, not the cache.  A CTA takes 256 rows of one kv head,
+// as two tiles of 128, against a run of 128-key tiles:
+//   warp 9      copies keys and values page by page with TMA, 128-byte
+//               swizzled, through one ring of 128-key slots;
+//   warp 8      issues tcgen05.mma: S = Q K^T (both from shared memory), then
+//               O += P V with the weights P from tensor memory;
+//   warps 0-3   softmax of the first tile, a row a thread: scores from tensor
+//   warps 4-7   memory, running maximum and sum in fp32 registers, weights
+//               back in bf16 over the scores' own columns; same for the second.
+// Tensor memory holds S and O of both tiles (2 x 128 + 2 x D columns).  The
+// tensor cores work for one tile while the other's weights are made: per key
+// tile the issue order is P0 V, Q0 K', P1 V, Q1 K' (K' the next keys), so each
+// softmax has the other tile's two products to hide behind.
+//
+// O is rescaled only when a row's maximum grew by more than 2^8 in weight
+// (the first tile sets it): until then weights up to 2^8 are relative to the
+// older maximum, which loses nothing in bf16 or fp32, and a rescale, a read
+// and write of the row's O, stays rare.  Scores, sums and O are fp32; weights
+// are rounded to bf16 (at most half a step, 2^-8 of each), their sum is not.
+#include <algorithm>
+
+#include "attn_common.cuh"
+#include "attn_host.h"
+#include "qmv_common.cuh"
+#include "sv_internal.h"
+#include "tc05.cuh"
+
+namespace sv {
+namespace attn {
+namespace {
+
+constexpr int kBK = 128;         // keys per tile
+constexpr int kTile = 128;       // rows per tensor-core tile
+constexpr int kRows = 2 * kTile; // rows per item
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kQueryWarp = 10;  // 10 and 11: a tile each
+// The softmax groups take registers from the third warpgroup (launched at 168 a
+// thread: 256 x 216 + 128 x 72 = 384 x 168).
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr uint32_t kTmemCols = 512;
+// An item's cost beside its tiles (queries, the first scores, the last
+// products, the output), in key tiles, when the work is cut into runs.
+constexpr int kItemUnits = 4;
+constexpr float kRescale = 8.f;  // base-2 exponent by which a maximum may lag
+
+template <int D>
+struct TcShape {
+  static constexpr uint32_t kBlock = kBK * 128;              // 64 values of 128 rows
+  static constexpr uint32_t kTileBytes = kBlock * (D / 64);  // queries, keys or values
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr uint32_t kStage = kTile * 128;  // 64 output values of a tile's rows
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 2 * kStage + 1024;
+  static constexpr uint32_t kOCol = 2 * kBK;  // tensor-memory column of O of tile 0
+};
+
+constexpr uint32_t idesc(int n, bool b_mn_major) {
+  return (1u << 4)                              // D: f32
+         | (1u << 7) | (1u << 10)               // A, B: bf16
+         | (b_mn_major ? 1u << 16 : 0u)         // B with its N index contiguous
+         | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void advance(uint32_t slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+struct Segment {
+  Request rq;
+  int b, h, r0, count;
+  Span span;
+  int tile0, tiles;           // key tiles [tile0, tile0 + tiles), maybe none
+  long long item;             // first unit of the item
+  int first, n_units, width;  // the segment's units of the item, the item's
+};
+
+__device__ __forceinline__ int row_tiles(const Args &a, const Request &q) {
+  return (int)(((long long)q.n * a.G + kRows - 1) / kRows);
+}
+__device__ __forceinline__ int item_width(const Args &a, const Request &q, int i) {
+  const Span s = rows_span(a, q, i * kRows, min(kRows, q.n * a.G - i * kRows));
+  return (s.hi + kBK - 1) / kBK - s.lo / kBK + kItemUnits;
+}
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// Units of one kv head of a request, by a whole warp.
+__device__ __forceinline__ long long head_units(const Args &a, const Request &q) {
+  const int nt = row_tiles(a, q), lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int i0 = 0; i0 < nt; i0 += 32)
+    sum += warp_sum_int(i0 + lane < nt ? item_width(a, q, i0 + lane) : 0);
+  return sum;
+}
+
+// Walks a run's segments.  An item is its key tiles and then kItemUnits more; a
+// run that ends among those takes the item to its end, and one that begins
+// there leaves it alone, so only tiles are ever split.  Items are ordered by request, kv head, row tile, so
+// neighbouring CTAs read the same keys at about the same time.  All calls by a
+// whole warp.
+struct Walk {
+  long long u, end, base, per_head, item;
+  int b, h, i, nt, width;
+  Request rq;
+  __device__ void request(const Args &a) {
+    rq = load_request(a, b);
+    nt = row_tiles(a, rq);
+    per_head = head_units(a, rq);
+  }
+  __device__ void start(const Args &a) {  // u, end, base and b are set
+    request(a);
+    const int lane = threadIdx.x & 31;
+    h = (int)((u - base) / per_head);
+    long long rem = u - base - h * per_head;
+    item = base + h * per_head;
+    for (int i0 = 0;; i0 += 32) {
+      const int w = i0 + lane < nt ? item_width(a, rq, i0 + lane) : 0;
+      int upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        i = i0 + src;
+        width = __shfl_sync(0xffffffffu, w, src);
+        item += __shfl_sync(0xffffffffu, upto, src) - width;
+        return;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      rem -= all;
+      item += all;
+    }
+  }
+  __device__ bool next(const Args &a, Segment &s) {
+    if (u >= item + max(width - kItemUnits, 1)) u = max(u, item + width);
+    if (u >= end) return false;
+    if (u == item + width) {  // on to the next item
+      item = u;
+      if (++i == nt) {
+        i = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          base = u;
+          do {
+            ++b;
+            request(a);
+          } while (nt == 0);
+        }
+      }
+      width = item_width(a, rq, i);
+    }
+    s.rq = rq;
+    s.b = b;
+    s.h = h;
+    s.item = item;
+    s.width = width;
+    s.first = (int)(u - item);
+    s.n_units = width - s.first;
+    if (end - u < max(width - kItemUnits, 1) - s.first) s.n_units = (int)(end - u);
+    s.r0 = i * kRows;
+    s.count = min(kRows, rq.n * a.G - s.r0);
+    s.span = rows_span(a, rq, s.r0, s.count);
+    const int t0 = s.span.lo / kBK, t1 = (s.span.hi + kBK - 1) / kBK;
+    s.tile0 = t0 + s.first;
+    s.tiles = max(0, min(t1 - s.tile0, s.n_units));
+    u += s.n_units;
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Uses of registers that a tcgen05.ld fills stay behind its wait.
+__device__ __forceinline__ void pin(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
+                      "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+__device__ __forceinline__ void group_sync(int wg) {  // the softmax warps of one tile
+  asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
+}
+
+// A split item's partial: sums as [D / 4][rows][4] (a thread owns a row, so
+// accesses of a warp are contiguous), then maxima and sums [rows] each.
+template <int D>
+__device__ __forceinline__ float *part_row(const Args &a, int slot, int rr) {
+  return partial_at(a, slot, kRows, D) + rr * 4;
+}
+
+// Rows [rr, rr + count) of the item at r0, one by one by a warp (attend_row):
+// whole results (slot -1), or the partial of this slot.
+template <int D>
+__device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
+                                        int r0, int rr, int count, int j0, int j1, int slot) {
+  const int lane = threadIdx.x & 31;
+  for (int i = 0; i < count; ++i, ++rr) {
+    float o[D / 32], m, l;
+    attend_row<D>(a, b, h, q0, n, len, r0 + rr, j0, j1, o, m, l);
+    if (slot < 0) {
+      store_lane<D>(a, q0, h, r0 + rr, o, m, l);
+    } else {
+      float *part = part_row<D>(a, slot, rr);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const int d = lane * (D / 32) + e;
+        __stcg(part + (size_t)(d >> 2) * kRows * 4 + (d & 3), o[e]);
+      }
+      if (lane == 0) {
+        float *ml = partial_at(a, slot, kRows, D) + kRows * D + rr;
+        __stcg(ml, m);
+        __stcg(ml + kRows, l);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
+  using S = TcShape<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t kv_full[S::kSlots], kv_empty[S::kSlots];
+  __shared__ __align__(8) uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_done[2];
+  __shared__ __align__(8) uint64_t mma_done;
+  __shared__ long long s_scan[kThreads / 32], s_base;
+  __shared__ uint32_t s_row[2][kTile];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_b, s_odd[2], s_last[2];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t q_smem = raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t ring0 = q_smem + 2 * S::kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i][0], 4);
+      mbar_init(&p_full[i][1], 4);
+      mbar_init(&o_done[i], 1);
+      s_odd[i] = 0;
+    }
+    mbar_init(&mma_done, 1);
+    fence_mbar_init();
+  }
+  // ---- this CTA's run of units, and the request that it begins in ----
+  auto block_sum = [&](long long v, long long &upto) {  // inclusive scan and total
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = v;
+    __syncthreads();
+    long long all = 0;
+    upto = v;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) upto += s_scan[i];
+      all += s_scan[i];
+    }
+    return all;
+  };
+  // request tid + b0's units: few row tiles by its thread, more by the warp
+  auto units_of = [&](int b) {
+    const bool real = b < a.B;
+    Request rq = {0, 0, 0};
+    if (real) rq = load_request(a, b);
+    const int nt = real ? row_tiles(a, rq) : 0;
+    long long w = 0;
+    if (nt <= 4)
+      for (int i = 0; i < nt; ++i) w += item_width(a, rq, i);
+    unsigned big = __ballot_sync(0xffffffffu, nt > 4);
+    while (big) {
+      const int src = __ffs(big) - 1;
+      big &= big - 1;
+      Request x;
+      x.q0 = 0;
+      x.n = __shfl_sync(0xffffffffu, rq.n, src);
+      x.len = __shfl_sync(0xffffffffu, rq.len, src);
+      const long long sum = head_units(a, x);
+      if (lane == src) w = sum;
+    }
+    return w * a.Hkv;
+  };
+  Runs runs;
+  runs.units = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    long long upto;
+    runs.units += block_sum(units_of(b0 + tid), upto);
+  }
+  runs.ctas = (int)min((long long)gridDim.x, runs.units);
+  const int used = min(max(__ldg(a.q_start + a.B), 0), a.rows);
+  for (int r = used + blockIdx.x; r < a.rows; r += gridDim.x) {  // past the last request: zero
+    for (int i = tid; i < a.Hq * (D / 8); i += kThreads)
+      reinterpret_cast<uint4 *>(a.out + (long long)r * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(long long)r * a.Hq + i] = kNegInf;
+  }
+  if ((int)blockIdx.x >= runs.ctas) return;  // uniform
+  Walk walk;
+  walk.u = runs.begin(blockIdx.x);
+  walk.end = runs.begin(blockIdx.x + 1);
+  long long sum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const long long size = units_of(b0 + tid);
+    long long upto;
+    const long long all = block_sum(size, upto);
+    upto += sum;
+    if (upto > walk.u && upto - size <= walk.u) {
+      s_b = b0 + tid;
+      s_base = upto - size;
+    }
+    sum += all;
+    if (sum > walk.u) break;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_addr(&s_tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  walk.b = s_b;
+  walk.base = s_base;
+  walk.start(a);
+  const uint32_t tmem = *const_cast<const volatile uint32_t *>(&s_tmem);
+  bool dead = false;  // a wait gave up: the rest runs without waiting, results are invalid
+  Segment s;
+
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kTmaWarp) {
+    // ------------------------------ producer ------------------------------
+    const int per_page = min(kBK, 1 << a.page_shift);
+    const int pages = kBK / per_page;
+    const int boxes = pages * (D / 64);
+    const int blk = lane / pages, pg = lane - blk * pages;
+    Ring ring;
+    long long issued = 0;
+    while (!dead && walk.next(a, s)) {
+      for (int t = 0; !dead && t < s.tiles; ++t) {
+        const int j = (s.tile0 + t) * kBK + pg * per_page;
+        int y = 0;
+        if (lane < boxes)
+          y = page_row(a, s.b, s.h, j >> a.page_shift, s.span.lo, s.span.hi) +
+              (j & ((1 << a.page_shift) - 1));
+        for (int kv = 0; kv < 2; ++kv) {
+          if (issued >= S::kSlots && !mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1u)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+          if (dead) break;
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], S::kTileBytes);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_rows(ring0 + ring.slot * S::kTileBytes + (uint32_t)blk * S::kBlock +
+                              (uint32_t)pg * per_page * 128,
+                          kv ? &vmap : &kmap, blk * 64, y, smem_addr(&kv_full[ring.slot]));
+          ++issued;
+          ring.advance(S::kSlots);
+        }
+      }
+    }
+    if (dead && lane == 0) report_give_up(4u);
+    // every copy has landed before the CTA may exit
+    for (long long k = max(0ll, issued - S::kSlots); k < issued; ++k)
+      (void)mbar_wait(&kv_full[k % S::kSlots], (uint32_t)((k / S::kSlots) & 1));
+  } else if (warp == kMmaWarp) {
+    // -------------------------- matrix products ---------------------------
+    constexpr uint32_t kQk = idesc(kBK, false), kPv = idesc(D, true);
+    Ring ring;
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of q_full and p_full
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      if (!dead && !mbar_wait(bar, phase)) {
+        dead = true;
+        report_give_up(8u);
+      }
+      tc_fence_after();
+    };
+    auto qk = [&](int w, uint32_t slot, bool last) {
+      if (!dead) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32;
+          tc_mma_ss(tmem + (uint32_t)w * kBK,
+                    smem_desc_sw128(q_smem + (uint32_t)w * S::kTileBytes + at),
+                    smem_desc_sw128(ring0 + slot * S::kTileBytes + at), kQk, k > 0);
+        }
+      }
+      tc_commit(smem_addr(&s_full[w]));
+      if (last) tc_commit(smem_addr(&q_free[w]));  // the segment's queries are done with
+    };
+    auto pv = [&](int w, uint32_t slot, bool first) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        wait(&p_full[w][half], pn[w]);
+        if (dead) break;
+#pragma unroll
+        for (int k = half * (kBK / 32); k < (half + 1) * (kBK / 32); ++k)
+          tc_mma_ts(tmem + S::kOCol + (uint32_t)w * D, tmem + (uint32_t)w * kBK + k * 8,
+                    smem_desc_sw128_mn(ring0 + slot * S::kTileBytes + k * 2048, S::kBlock), kPv,
+                    !first || k > 0);
+      }
+      pn[w] ^= 1u;
+      tc_commit(smem_addr(&o_done[w]));
+    };
+    while (walk.next(a, s)) {
+      if (s.tiles == 0) continue;
+      if (lane == 0) {
+        const bool two = s.count > kTile;
+        wait(&q_full[0], qn[0]);
+        qn[0] ^= 1u;
+        wait(&kv_full[ring.slot], ring.phase);
+        qk(0, ring.slot, s.tiles == 1);
+        if (two) {
+          wait(&q_full[1], qn[1]);
+          qn[1] ^= 1u;
+          qk(1, ring.slot, s.tiles == 1);
+        }
+        tc_commit(smem_addr(&kv_empty[ring.slot]));
+        ring.advance(S::kSlots);
+        for (int t = 0; t < s.tiles; ++t) {
+          const uint32_t v_slot = ring.slot;
+          const bool more = t + 1 < s.tiles;
+          wait(&kv_full[v_slot], ring.phase);
+          ring.advance(S::kSlots);
+          pv(0, v_slot, t == 0);
+          // The products run in issue order, so Q K' may overwrite the columns
+          // that hold the weights of the product issued before it.
+          if (more) {
+            wait(&kv_full[ring.slot], ring.phase);
+            qk(0, ring.slot, t + 2 == s.tiles);
+          }
+          if (two) {
+            pv(1, v_slot, t == 0);
+          }
+          tc_commit(smem_addr(&kv_empty[v_slot]));
+          if (more) {
+            if (two) qk(1, ring.slot, t + 2 == s.tiles);
+            tc_commit(smem_addr(&kv_empty[ring.slot]));
+            ring.advance(S::kSlots);
+          }
+        }
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {  // no product is in flight when the tensor memory is freed
+      tc_commit(smem_addr(&mma_done));
+      (void)mbar_wait(&mma_done, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------- queries ------------------------------
+    // the next segment's are fetched while the last products of this one run
+    const int w = warp - kQueryWarp;
+    uint32_t free = 0;
+    bool loaded = false;
+    while (walk.next(a, s)) {
+      const int n = min(kTile, s.count - w * kTile);
+      if (s.tiles == 0 || n <= 0) continue;
+      if (loaded) {
+        if (!dead && !mbar_wait(&q_free[w], free)) {
+          dead = true;
+          report_give_up(32u);
+        }
+        free ^= 1u;
+      }
+      loaded = true;
+      __syncwarp();
+      constexpr int kChunks = D / 8;         // 16-byte pieces of a row
+      constexpr int kStep = 32 / kChunks;    // rows at a time
+      const int ch = lane % kChunks, first = lane / kChunks;
+      int t = (s.r0 + w * kTile + first) / a.G, g = s.r0 + w * kTile + first - t * a.G;
+      const int dt = kStep / a.G, dg = kStep - dt * a.G;
+      const __nv_bfloat16 *src =
+          a.q + (long long)s.rq.q0 * a.q_stride + (long long)s.h * a.G * D + ch * 8;
+      const uint32_t dst = q_smem + (uint32_t)w * S::kTileBytes + (uint32_t)(ch >> 3) * S::kBlock;
+#pragma unroll 4
+      for (int rr = first; rr < kTile; rr += kStep) {
+        const bool real = rr < n;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         dst + (uint32_t)rr * 128 + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4)),
+                     "l"(src + (real ? (long long)t * a.q_stride + (long long)g * D : 0)),
+                     "r"(real ? 16 : 0)
+                     : "memory");
+        t += dt;
+        g += dg;
+        if (g >= a.G) {
+          g -= a.G;
+          ++t;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[w]);
+    }
+  }
+  } else {
+    // ------------------------------- softmax ------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int wg = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 tensor-memory lanes a warp
+    const uint32_t s_at = tmem + lanes + (uint32_t)wg * kBK;
+    const uint32_t o_at = tmem + lanes + S::kOCol + (uint32_t)wg * D;
+    const float c = a.scale_log2;
+    Ring ring;  // of the segment's first key slot
+    uint32_t sn = 0;  // key tiles done by this group
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      if (!dead && !mbar_wait(bar, phase)) {
+        dead = true;
+        report_give_up(16u);
+      }
+      __syncwarp();  // the tensor-memory accesses that follow want the whole warp
+    };
+    while (walk.next(a, s)) {
+      const int count = min(kTile, s.count - wg * kTile);  // rows of this tile, maybe none
+      const bool ok = row < count;
+      const int r = s.r0 + wg * kTile + row;
+      const int t_row = ok ? r / a.G : 0;
+      const int last = ok ? s.rq.len - s.rq.n + t_row : -1;
+      const int first = a.window > 0 ? last - a.window + 1 : 0;
+      const Span own = count > 0 ? rows_span(a, s.rq, s.r0 + wg * kTile, count) : s.span;
+      float m = kNegInf, l = 0.f;
+      bool any_masked = false;
+      if (count > 0) {
+        for (int t = 0; t < s.tiles; ++t, ++sn) {
+          const int j0 = (s.tile0 + t) * kBK;
+          const bool masked = j0 < own.all_lo || j0 + kBK > own.all_hi;
+          ring.advance(S::kSlots);  // to the tile's values
+          wait(&s_full[wg], sn & 1u);
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc_ld_x32(s_at + 32 * q, x[q]);
+          tc_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) pin(x[q]);
+          if (masked) {
+            any_masked = true;
+            const int lo = first - j0, hi = last - j0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * q + i > hi) x[q][i] = __float_as_uint(kNegInf);
+            if (a.window > 0) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (32 * q + i < lo) x[q][i] = __float_as_uint(kNegInf);
+            }
+          }
+          float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1])));
+          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (t == 0) {
+            m = mn;
+          } else {
+            const bool grew = (mn - m) * c > kRescale;
+            if (__any_sync(0xffffffffu, grew)) {
+              float f = 1.f;
+              if (grew) {
+                f = exp2_approx((m - mn) * c);
+                m = mn;
+                l *= f;
+              }
+              wait(&o_done[wg], (sn - 1u) & 1u);
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                uint32_t o[32];
+                tc_ld_x32(o_at + d, o);
+                tc_wait_ld();
+                pin(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tc_st_x32(o_at + d, o);
+              }
+            }
+          }
+          if (masked) {
+            // places no row of the item attends may hold anything: the first
+            // tile's group zeroes their values, so that a weight of zero meets
+            // no NaN; a non-finite value that some rows of the tile attend and
+            // others do not sends the segment to the row-by-row path
+            wait(&kv_full[ring.slot], ring.phase);
+            uint8_t *v = smem_raw + (ring0 - raw) + ring.slot * S::kTileBytes + row * 16;
+            uint32_t odd = 0;
+#pragma unroll 1
+            for (int i = 0; i < kBK / 16; ++i) {  // eight threads a key: a warp reads 512 bytes
+              const int p0 = j0 + i * 16, pos = p0 + (row >> 3);
+              if (p0 >= own.all_lo && p0 + 16 <= own.all_hi) continue;
+              const bool none = pos < s.span.lo || pos >= s.span.hi;
+              const bool part = !none && (pos < own.all_lo || pos >= own.all_hi);
+#pragma unroll
+              for (int blk = 0; blk < D / 64; ++blk) {
+                uint4 *at = reinterpret_cast<uint4 *>(v + blk * S::kBlock + i * 2048);
+                if (part) {
+                  const uint4 y = *at;
+                  odd |= nonfinite_bits(y.x) | nonfinite_bits(y.y) | nonfinite_bits(y.z) |
+                         nonfinite_bits(y.w);
+                }
+                if (none && wg == 0) *at = make_uint4(0, 0, 0, 0);
+              }
+            }
+            if (odd) s_odd[wg] = 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          const float off = m == kNegInf ? 0.f : m * c;
+          const uint64_t c2 = pack2(c, c), off2 = pack2(-off, -off);
+          uint64_t acc[4] = {0, 0, 0, 0};  // pairs of zeros
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float e0, e1;
+              unpack2(fma2(pack2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])),
+                           c2, off2),
+                      e0, e1);
+              e0 = exp2_approx(e0);
+              e1 = exp2_approx(e1);
+              acc[i & 3] = add2(acc[i & 3], pack2(e0, e1));
+              p[i] = pack_bf16(e0, e1);
+            }
+            tc_st_x16(s_at + 16 * q, p);
+            if (q & 1) {  // half of the weights: their product may begin
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[wg][q >> 1]);
+            }
+          }
+          {
+            float e0, e1;
+            unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), e0, e1);
+            l += e0 + e1;
+          }
+          ring.advance(S::kSlots);
+        }
+      } else {
+        for (int t = 0; t < 2 * s.tiles; ++t) ring.advance(S::kSlots);
+      }
+
+      if (count > 0) {
+        const bool whole = s.first == 0 && s.n_units == s.width;
+        const int slot = 2 * (int)blockIdx.x + (s.first == 0 ? 1 : 0);
+        const int rr = wg * kTile + row;
+        bool odd = false;
+        if (any_masked) {  // the same for the group
+          group_sync(wg);
+          odd = s_odd[wg] != 0;
+          group_sync(wg);
+          if (row == 0) s_odd[wg] = 0;
+        }
+        if (s.tiles > 0) {
+          wait(&o_done[wg], (sn - 1u) & 1u);
+          tc_fence_after();
+        }
+        if (odd) {
+          rows_plain<D>(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, wg * kTile + (warp & 3) * 32,
+                        min(count - (warp & 3) * 32, 32), s.tile0 * kBK,
+                        (s.tile0 + s.tiles) * kBK, whole ? -1 : slot);
+        } else {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int g = r - t_row * a.G, t0 = (s.r0 + wg * kTile) / a.G;
+          float *part = part_row<D>(a, slot, rr);
+          // whole rows go through shared memory, so that eight threads write
+          // 128 contiguous bytes of a row
+          s_row[wg][row] = (uint32_t)(t_row - t0) << 16 | (uint32_t)g;
+          uint8_t *stage = smem_raw + (q_smem - raw) + (2 + S::kSlots) * S::kTileBytes +
+                           (uint32_t)wg * S::kStage;
+          __nv_bfloat16 *dst = a.out + (long long)(s.rq.q0 + t0) * a.out_stride +
+                               (long long)s.h * a.G * D;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 64) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 32) {
+              uint32_t o[32];
+              if (s.tiles > 0) {
+                tc_ld_x32(o_at + d + e, o);
+                tc_wait_ld();
+                pin(o);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0;
+              }
+              if (whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  auto two = [&](int k) {
+                    return pack_bf16(__uint_as_float(o[i + k]) * inv,
+                                     __uint_as_float(o[i + k + 1]) * inv);
+                  };
+                  *reinterpret_cast<uint4 *>(stage + row * 128 +
+                                             ((((e + i) >> 3) ^ (row & 7)) << 4)) =
+                      make_uint4(two(0), two(2), two(4), two(6));
+                }
+              } else if (ok) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  __stcg(reinterpret_cast<uint4 *>(part + (size_t)((d + e + i) >> 2) * kRows * 4),
+                         make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+              }
+              __syncwarp();
+            }
+            if (whole) {
+              group_sync(wg);
+#pragma unroll 4
+              for (int i = row >> 3; i < count; i += 16) {
+                const uint32_t at = s_row[wg][i];
+                const uint4 y = *reinterpret_cast<const uint4 *>(
+                    stage + i * 128 + (((row & 7) ^ (i & 7)) << 4));
+                *reinterpret_cast<uint4 *>(dst + (at >> 16) * a.out_stride + (at & 0xFFFFu) * D + d +
+                                           (row & 7) * 8) = y;
+              }
+              group_sync(wg);
+            }
+          }
+          if (ok && whole && a.lse)
+            a.lse[(long long)(s.rq.q0 + t_row) * a.Hq + s.h * a.G + g] = row_lse(a, m, l);
+          if (ok && !whole) {
+            float *ml = partial_at(a, slot, kRows, D) + kRows * D + rr;
+            __stcg(ml, m);
+            __stcg(ml + kRows, l);
+          }
+        }
+        tc_fence_before();  // O has been read before the next segment's products write it
+        if (!whole) {
+          // the last of the item's CTAs joins this tile's partials, in order
+          const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits - 1);
+          __threadfence();
+          group_sync(wg);
+          if (row == 0) {
+            unsigned *counter = a.counters + 2 * c0 + wg;
+            s_last[wg] = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+            if (s_last[wg]) *counter = 0;  // every CTA of the item has arrived
+          }
+          group_sync(wg);
+          if (s_last[wg]) {
+            __threadfence();
+            if (ok) {
+              float mm = kNegInf, ll = 0.f;
+              for (int k = c0; k <= c1; ++k)
+                mm = fmaxf(mm, __ldcg(partial_at(a, 2 * k + (k == c0), kRows, D) + kRows * D + rr));
+              auto weight = [&](int k, float &lk) {
+                const float *ml = partial_at(a, 2 * k + (k == c0), kRows, D) + kRows * D + rr;
+                const float mk = __ldcg(ml);
+                lk = __ldcg(ml + kRows);
+                // no keys: nothing (its maximum is -inf, and so may be every other)
+                return mk == kNegInf && lk == 0.f ? 0.f : exp2_approx((mk - mm) * c);
+              };
+              for (int k = c0; k <= c1; ++k) {
+                float lk;
+                const float f = weight(k, lk);
+                ll = fmaf(lk, f, ll);
+              }
+              const float inv = ll == 0.f ? 0.f : 1.f / ll;
+              const int g = r - t_row * a.G;
+              __nv_bfloat16 *dst = a.out + (long long)(s.rq.q0 + t_row) * a.out_stride +
+                                   (long long)(s.h * a.G + g) * D;
+#pragma unroll 1
+              for (int d = 0; d < D; d += 64) {
+                float o[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                for (int k = c0; k <= c1; ++k) {
+                  float lk;
+                  const float f = weight(k, lk);
+                  const float *part =
+                      part_row<D>(a, 2 * k + (k == c0), rr) + (size_t)(d >> 2) * kRows * 4;
+                  float4 y[16];
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    y[i] = __ldcg(reinterpret_cast<const float4 *>(part + (size_t)i * kRows * 4));
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    o[4 * i] = fmaf(y[i].x, f, o[4 * i]);
+                    o[4 * i + 1] = fmaf(y[i].y, f, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(y[i].z, f, o[4 * i + 2]);
+                    o[4 * i + 3] = fmaf(y[i].w, f, o[4 * i + 3]);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 64; i += 8)
+                  *reinterpret_cast<uint4 *>(dst + d + i) = make_uint4(
+                      pack_bf16(o[i] * inv, o[i + 1] * inv),
+                      pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                      pack_bf16(o[i + 4] * inv, o[i + 5] * inv),
+                      pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+              }
+              if (a.lse)
+                a.lse[(long long)(s.rq.q0 + t_row) * a.Hq + s.h * a.G + g] = row_lse(a, mm, ll);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+sv_status launch(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int ctas,
+                 cudaStream_t stream) {
+  using S = TcShape<D>;
+  static PerDeviceOnce once;
+  const cudaError_t ce = once.run([] {
+    return cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)S::kSmem);
+  });
+  if (ce != cudaSuccess)
+    return fail(SV_ERR_CUDA, "paged_attention: cudaFuncSetAttribute failed: %s",
+                cudaGetErrorString(ce));
+  attn_tc_kernel<D><<<(unsigned)ctas, kThreads, S::kSmem, stream>>>(kmap, vmap, a);
+  return check_launch("paged_attention");
+}
+
+int tc_ctas() { return std::min(kMaxCtas / 2, device_sm_count()); }
+
+}  // namespace
+
+size_t tc_partial_bytes(int D) { return (size_t)tc_ctas() * 2 * kRows * (D + 2) * 4; }
+
+unsigned tc_take_give_up() {
+  unsigned v = 0, zero = 0;
+  cudaMemcpyFromSymbol(&v, g_give_up, sizeof v);
+  cudaMemcpyToSymbol(g_give_up, &zero, sizeof zero);
+  return v;
+}
+
+sv_status tc_run(int D, const Args &a, cudaStream_t stream) {
+  CUtensorMap kmap, vmap;
+  sv_status st = encode_cache(&kmap, a.k, D, a, kBK);
+  if (st == SV_OK) st = encode_cache(&vmap, a.v, D, a, kBK);
+  if (st != SV_OK) return st;
+  return D == 64 ? launch<64>(a, kmap, vmap, tc_ctas(), stream)
+                 : launch<128>(a, kmap, vmap, tc_ctas(), stream);
+}
+
+}  // namespace attn
+}  // namespace sv
