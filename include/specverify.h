@@ -599,10 +599,11 @@ sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x
  * caches 16-byte aligned, row strides multiples of 8 elements; no output
  * overlaps an input.
  * workspace: paged_attention_workspace_bytes(D) bytes on the current device
- * (0 on an unsupported D), 256-byte aligned, zero-filled once by the caller;
- * every call leaves its counters (the first 4096 bytes) at zero for the next,
- * of any shape with this D.  Calls that run concurrently need workspaces of
- * their own.  One launch on `stream`. */
+ * (0 on an unsupported D), 256-byte aligned, its first 4096 bytes zero before
+ * its first call (every call leaves them zero); it serves calls of any shape
+ * with this D.  Calls that run concurrently need workspaces of their own.  One
+ * launch on `stream`, or two (few rows a request: the second joins requests
+ * that were split over the device). */
 size_t paged_attention_workspace_bytes(int D);
 sv_status paged_attention(const uint16_t *q, long long q_row_stride, const uint16_t *k_cache,
                           const uint16_t *v_cache, const int32_t *block_table,

@@ -650,11 +650,38 @@ class KvStep(NamedTuple):
     err_flags: torch.Tensor  # [B]
 
 
-def _out(t, name, dtype, shape, dev):
+def _fits(t, name, dtype, shape, dev, index):
+    """_need, with one test for a tensor that is as it should be: a decode loop
+    makes these calls every few microseconds."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+
+
+def _out(t, name, dtype, shape, dev, index):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, shape, dev)
+    _fits(t, name, dtype, shape, dev, index)
     return t
+
+
+def _on(t: torch.Tensor, name: str) -> int:
+    """The index of the CUDA device that ``t`` (the first argument) is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _call(index: int, where: str, fn, *args) -> None:
+    """fn(*args, current stream of the device), with that device current."""
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != SV_OK:
+        _check(st, where)
 
 
 def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor,
@@ -670,34 +697,32 @@ def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor
     ring) and writes the step's packed rows: slots and positions.  All int32.
     ``length_out=length`` and so on update the state in place."""
     dev, i32 = length.device, torch.int32
+    index = _on(length, "length")
     B, max_pages = block_table.shape
-    _need(length, "length", i32, (B,), dev)
-    _need(held, "held", i32, (B,), dev)
-    _need(cursor, "cursor", i32, (2,), dev)
-    _need(ring, "ring", i32, None, dev)
-    _need(block_table, "block_table", i32, None, dev)
-    _need(n_new, "n_new", i32, (B,), dev)
+    per, rows = (B,), int(rows)
+    _fits(length, "length", i32, per, dev, index)
+    _fits(held, "held", i32, per, dev, index)
+    _fits(cursor, "cursor", i32, (2,), dev, index)
+    _fits(ring, "ring", i32, None, dev, index)
+    _fits(block_table, "block_table", i32, None, dev, index)
+    _fits(n_new, "n_new", i32, per, dev, index)
+    commit, n = None, 0
     if n_commit is not None:
-        _need(n_commit, "n_commit", i32, None, dev)
-    rows = int(rows)
-    step = KvStep(_out(length_out, "length_out", i32, (B,), dev),
-                  _out(held_out, "held_out", i32, (B,), dev),
-                  _out(cursor_out, "cursor_out", i32, (2,), dev),
-                  _out(q_start, "q_start", i32, (B + 1,), dev),
-                  _out(kv_len, "kv_len", i32, (B,), dev),
-                  _out(slots, "slots", i32, (max(rows, 0),), dev),
-                  _out(positions, "positions", i32, (max(rows, 0),), dev),
-                  _out(err_flags, "err_flags", i32, (B,), dev))
-    with torch.cuda.device(dev):
-        st = lib().kv_pages_step(
-            length.data_ptr(), held.data_ptr(), cursor.data_ptr(), n_new.data_ptr(),
-            None if n_commit is None else n_commit.data_ptr(),
-            0 if n_commit is None else n_commit.numel(), int(n_commit_bias), B, int(page_size),
-            max_pages, ring.numel(), rows, block_table.data_ptr(), ring.data_ptr(),
-            step.length.data_ptr(), step.held.data_ptr(), step.cursor.data_ptr(),
-            step.q_start.data_ptr(), step.kv_len.data_ptr(), step.slots.data_ptr(),
-            step.positions.data_ptr(), step.err_flags.data_ptr(), _stream(dev))
-    _check(st, "kv_pages_step")
+        _fits(n_commit, "n_commit", i32, None, dev, index)
+        commit, n = n_commit.data_ptr(), n_commit.numel()
+    each = (max(rows, 0),)
+    step = KvStep(_out(length_out, "length_out", i32, per, dev, index),
+                  _out(held_out, "held_out", i32, per, dev, index),
+                  _out(cursor_out, "cursor_out", i32, (2,), dev, index),
+                  _out(q_start, "q_start", i32, (B + 1,), dev, index),
+                  _out(kv_len, "kv_len", i32, per, dev, index),
+                  _out(slots, "slots", i32, each, dev, index),
+                  _out(positions, "positions", i32, each, dev, index),
+                  _out(err_flags, "err_flags", i32, per, dev, index))
+    _call(index, "kv_pages_step", lib().kv_pages_step, length.data_ptr(), held.data_ptr(),
+          cursor.data_ptr(), n_new.data_ptr(), commit, n, int(n_commit_bias), B, int(page_size),
+          max_pages, ring.numel(), rows, block_table.data_ptr(), ring.data_ptr(),
+          *[t.data_ptr() for t in step])
     return step
 
 
@@ -714,22 +739,20 @@ def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:
     return (high.to(torch.int64) << 32) + low.to(torch.int64)
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype, heads: int, D: int, dev) -> int:
+def _need_rows(t: torch.Tensor, name: str, dtype, heads: int, D: int, dev, index: int) -> int:
     """Packed rows [rows, heads, D] with contiguous heads; returns the row stride."""
-    if t.device != dev:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+    if t.dim() != 3 or t.shape[1:] != (heads, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads}, {D})")
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     return s[0] if t.shape[0] > 1 else heads * D
-
-
-def _need_cache(t: torch.Tensor, name: str, shape, dev) -> None:
-    _need(t, name, torch.bfloat16, shape, dev)
 
 
 def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -746,48 +769,47 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     dev = q.device
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [rows, Hq, D] and the caches [pages, Hkv, page_size, D]")
-    if dev.type != "cuda":
-        raise ValueError("q must be a CUDA tensor")
+    index = _on(q, "q")
     rows, Hq, D = q.shape
-    pages, Hkv, page_size, _ = k_cache.shape
-    if q.dtype not in (torch.float32, torch.bfloat16):
+    cache = k_cache.shape
+    pages, Hkv, page_size, _ = cache
+    dtype = q.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("q, k and v must be float32 or bfloat16")
-    qs = _need_rows(q, "q", q.dtype, Hq, D, dev)
-    ks = _need_rows(k, "k", q.dtype, Hkv, D, dev)
-    vs = _need_rows(v, "v", q.dtype, Hkv, D, dev)
+    qs = _need_rows(q, "q", dtype, Hq, D, dev, index)
+    ks = _need_rows(k, "k", dtype, Hkv, D, dev, index)
+    vs = _need_rows(v, "v", dtype, Hkv, D, dev, index)
     if k.shape[0] != rows or v.shape[0] != rows:
         raise ValueError("q, k and v must have the same rows")
-    _need_cache(k_cache, "k_cache", (pages, Hkv, page_size, D), dev)
-    _need_cache(v_cache, "v_cache", (pages, Hkv, page_size, D), dev)
+    cache = (pages, Hkv, page_size, D)
+    _fits(k_cache, "k_cache", torch.bfloat16, cache, dev, index)
+    _fits(v_cache, "v_cache", torch.bfloat16, cache, dev, index)
     axes = 1 if positions.dim() == 1 else positions.shape[-1]
-    _need(positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes),
-          dev)
-    _need(slots, "slots", torch.int32, (rows,), dev)
-    half = 0
+    _fits(positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes),
+          dev, index)
+    _fits(slots, "slots", torch.int32, (rows,), dev, index)
+    half, words = 0, None
     if freqs is not None:
         if freqs.dim() != 1:
             raise ValueError("freqs must be [rotary_dim / 2]")
-        _need(freqs, "freqs", torch.int64, None, dev)
-        half = freqs.numel()
+        _fits(freqs, "freqs", torch.int64, None, dev, index)
+        half, words = freqs.numel(), freqs.data_ptr()
+    ax = qw = kw = None
     if axis is not None:
-        _need(axis, "axis", torch.uint8, (half,), dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.float32, (D,), dev)
-    if q_out is None:
-        q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
-    _need(q_out, "q_out", torch.bfloat16, (rows, Hq, D), dev)
-    with torch.cuda.device(dev):
-        st = lib().rope_kv_append(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            SV_BF16 if q.dtype == torch.bfloat16 else SV_F32, qs, ks, vs, positions.data_ptr(),
-            axes, slots.data_ptr(), None if freqs is None else freqs.data_ptr(),
-            None if axis is None else axis.data_ptr(),
-            None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), float(eps), rows, Hq, Hkv, D,
-            2 * half, 1 if interleaved else 0, page_size, pages, q_out.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), _stream(dev))
-    _check(st, "rope_kv_append")
+        _fits(axis, "axis", torch.uint8, (half,), dev, index)
+        ax = axis.data_ptr()
+    if q_weight is not None:
+        _fits(q_weight, "q_weight", torch.float32, (D,), dev, index)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _fits(k_weight, "k_weight", torch.float32, (D,), dev, index)
+        kw = k_weight.data_ptr()
+    q_out = _out(q_out, "q_out", torch.bfloat16, (rows, Hq, D), dev, index)
+    _call(index, "rope_kv_append", lib().rope_kv_append, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), SV_BF16 if dtype is torch.bfloat16 else SV_F32, qs, ks, vs,
+          positions.data_ptr(), axes, slots.data_ptr(), words, ax, qw, kw, float(eps), rows, Hq,
+          Hkv, D, 2 * half, 1 if interleaved else 0, page_size, pages, q_out.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr())
     return q_out
 
 
@@ -796,14 +818,14 @@ def paged_attention_workspace_bytes(D: int) -> int:
 
 
 def make_attention_workspace(D: int, device) -> torch.Tensor:
-    """A workspace (uint8) for paged_attention with head dim D, its counters zero."""
+    """A workspace (uint8) for paged_attention with head dim D."""
     device = torch.device(device)
     with torch.cuda.device(device):
         n = paged_attention_workspace_bytes(D)
         if n == 0:
             _check(SV_ERR_UNSUPPORTED, "paged_attention_workspace_bytes")
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        ws[:4096].zero_()
+        ws[:4096].zero_()  # arrival counters; every call leaves them zero
     return ws
 
 
@@ -822,33 +844,32 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [rows, Hq, D], the caches [pages, Hkv, page_size, D] and "
                          "block_table [B, max_pages]")
-    if dev.type != "cuda":
-        raise ValueError("q must be a CUDA tensor")
+    index = _on(q, "q")
     rows, Hq, D = q.shape
     pages, Hkv, page_size, _ = k_cache.shape
     B, max_pages = block_table.shape
-    qs = _need_rows(q, "q", torch.bfloat16, Hq, D, dev)
-    _need_cache(k_cache, "k_cache", (pages, Hkv, page_size, D), dev)
-    _need_cache(v_cache, "v_cache", (pages, Hkv, page_size, D), dev)
-    _need(block_table, "block_table", torch.int32, None, dev)
-    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
-    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    qs = _need_rows(q, "q", torch.bfloat16, Hq, D, dev, index)
+    cache = (pages, Hkv, page_size, D)
+    _fits(k_cache, "k_cache", torch.bfloat16, cache, dev, index)
+    _fits(v_cache, "v_cache", torch.bfloat16, cache, dev, index)
+    _fits(block_table, "block_table", torch.int32, None, dev, index)
+    _fits(q_start, "q_start", torch.int32, (B + 1,), dev, index)
+    _fits(kv_len, "kv_len", torch.int32, (B,), dev, index)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
-    os_ = _need_rows(out, "out", torch.bfloat16, Hq, D, dev)
+    os_ = _need_rows(out, "out", torch.bfloat16, Hq, D, dev, index)
     if out.shape[0] != rows:
         raise ValueError("q and out must have the same rows")
+    lse_ptr = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, (rows, Hq), dev)
+        _fits(lse, "lse", torch.float32, (rows, Hq), dev, index)
+        lse_ptr = lse.data_ptr()
     if workspace is None:
         workspace = make_attention_workspace(D, dev)
-    _need(workspace, "workspace", torch.uint8, None, dev)
-    with torch.cuda.device(dev):
-        st = lib().paged_attention(
-            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            q_start.data_ptr(), kv_len.data_ptr(), B, rows, int(max_new), Hq, Hkv, D, page_size,
-            pages, max_pages, 1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
-            out.data_ptr(), os_, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _stream(dev))
-    _check(st, "paged_attention")
+    _fits(workspace, "workspace", torch.uint8, None, dev, index)
+    _call(index, "paged_attention", lib().paged_attention, q.data_ptr(), qs, k_cache.data_ptr(),
+          v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), B,
+          rows, int(max_new), Hq, Hkv, D, page_size, pages, max_pages,
+          1.0 / math.sqrt(D) if scale is None else float(scale), int(window), out.data_ptr(), os_,
+          lse_ptr, workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -22,8 +22,15 @@ namespace sv {
 namespace attn {
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kMaxCtas = 1024;  // join counters at the start of the workspace
-constexpr size_t kCounterBytes = kMaxCtas * 4;
+constexpr int kMaxCtas = 512;           // of one launch
+constexpr size_t kCounterBytes = 4096;  // the start of the workspace
+
+// The item that begins in a CTA's run and ends in a later one's: its rows
+// [r0, r0 + count) under kv head h of the request whose packed rows begin at
+// q0, shared by n CTAs; n = 0 for none.
+struct SplitItem {
+  int n, q0, h, r0, count, unused[3];
+};
 
 struct Args {
   const __nv_bfloat16 *q, *k, *v;
@@ -34,7 +41,8 @@ struct Args {
   int B, rows, Hq, Hkv, G;
   int num_pages, max_pages, page_shift, window;
   float scale, scale_log2;  // scale, scale * log2(e)
-  unsigned *counters;       // [kMaxCtas], zero between calls
+  unsigned *counters;  // attn_tc_kernel's arrivals, zero between calls
+  SplitItem *splits;   // attn_rows_kernel's split items [CTAs]
   float *partials;
 };
 
@@ -182,9 +190,9 @@ struct Runs {
   __device__ int owner(long long u) const { return (int)(((u + 1) * ctas - 1) / units); }
 };
 
-// A split item's partial result: unnormalised sums [rows][D], then maxima and
-// sums [rows] each.  CTA c has two: 2 c + 1 for the item that begins in its run
-// and ends in a later one, 2 c for the one that began in an earlier run.
+// A split item's partial result: unnormalised sums, then maxima and sums [rows]
+// each.  CTA c has two: 2 c + 1 for the item that begins in its run and ends in
+// a later one, 2 c for the one that began in an earlier run.
 __device__ __forceinline__ float *partial_at(const Args &a, int slot, int tile_rows, int D) {
   return a.partials + (size_t)slot * tile_rows * (D + 2);
 }
@@ -192,14 +200,14 @@ __device__ __forceinline__ float *partial_at(const Args &a, int slot, int tile_r
 // Elements d .. d + 3 of row r, normalised and rounded, and with element 0 the
 // row's log-sum-exp.  A row that attends nothing is zero.
 template <int D>
-__device__ __forceinline__ void store_out4(const Args &a, const Request &rq, int h, int r, int d,
+__device__ __forceinline__ void store_out4(const Args &a, int q0, int h, int r, int d,
                                            float4 o, float m, float l) {
   const int t = r / a.G, g = r - t * a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2 *>(a.out + (long long)(rq.q0 + t) * a.out_stride +
+  *reinterpret_cast<uint2 *>(a.out + (long long)(q0 + t) * a.out_stride +
                              (long long)(h * a.G + g) * D + d) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (d == 0 && a.lse) a.lse[(long long)(rq.q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
+  if (d == 0 && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
 }
 
 // The same with lane l of a warp holding elements l D / 32 .. of row r.
@@ -216,31 +224,10 @@ __device__ __forceinline__ void store_lane(const Args &a, int q0, int h, int r,
   if (lane == 0 && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
 }
 
-// As store_out4, from the partial results of CTAs c0 .. c1, in that order.
-template <int D>
-__device__ __forceinline__ void join_row4(const Args &a, const Request &rq, int h, int r, int rr,
-                                          int d, int c0, int c1, int tile_rows) {
-  float m = kNegInf, l = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const float *part = partial_at(a, 2 * c + (c == c0 ? 1 : 0), tile_rows, D);
-    m = fmaxf(m, __ldcg(part + tile_rows * D + rr));
-  }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float *part = partial_at(a, 2 * c + (c == c0 ? 1 : 0), tile_rows, D);
-    const float mc = __ldcg(part + tile_rows * D + rr), lc = __ldcg(part + tile_rows * (D + 1) + rr);
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + rr * D + d));
-    // no keys: nothing (its maximum is -inf, and so may be every other)
-    const float f = mc == kNegInf && lc == 0.f ? 0.f : exp2_approx((mc - m) * a.scale_log2);
-    l = fmaf(lc, f, l);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
-  }
-  store_out4<D>(a, rq, h, r, d, acc, m, l);
+// Weight of a partial with maximum m and sum l against the joint maximum; one
+// without keys has none (its maximum is -inf, and so may be every other).
+__device__ __forceinline__ float join_weight(const Args &a, float m, float l, float joint) {
+  return m == kNegInf && l == 0.f ? 0.f : exp2_approx((m - joint) * a.scale_log2);
 }
 
 }  // namespace attn

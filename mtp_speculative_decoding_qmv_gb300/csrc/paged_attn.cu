@@ -15,9 +15,8 @@
 // are rounded to bf16 for the second product (at most half a step, 2^-8 of
 // each weight, the type of the values they multiply), their sum is not.
 //
-// An item that several CTAs share is joined by the last of them to finish
-// (a counter in the workspace, left at zero for the next call), always in CTA
-// order, so results do not depend on which one that is.
+// CTAs that share an item leave partial results, which a second launch joins
+// (attn_join_kernel below), in an order that does not depend on the run.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -34,6 +33,9 @@ constexpr int kBK = 64;  // keys per tile
 constexpr int kWarps = 4;
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kConsumers = kWarps * 32;
+// An item's cost beside its tiles (queries, joining the warps, the output), in
+// key tiles, when the work is cut into runs.
+constexpr int kItemUnits = 2;
 
 template <int D>
 struct RowsShape {
@@ -55,8 +57,8 @@ __device__ __forceinline__ void consumer_sync() {
 }
 
 // Key tiles of every item of a request: enough for its longest row tile, so
-// that items can be found by division; an item's own tiles come first and the
-// rest of its run is empty.
+// that items can be found by division; an item's own tiles come first, the
+// rest of them is empty.
 __device__ __forceinline__ int tiles_per_item(const Args &a, const Request &q, int tile_rows) {
   long long tiles = (q.len + kBK - 1) / kBK;
   if (a.window > 0)
@@ -66,51 +68,56 @@ __device__ __forceinline__ int tiles_per_item(const Args &a, const Request &q, i
 __device__ __forceinline__ long long request_units(const Args &a, const Request &q,
                                                    int tile_rows) {
   const long long nt = ((long long)q.n * a.G + tile_rows - 1) / tile_rows;
-  return nt * a.Hkv * tiles_per_item(a, q, tile_rows);
+  return nt * a.Hkv * (tiles_per_item(a, q, tile_rows) + kItemUnits);
 }
 
 struct Segment {
   Request rq;
-  int b, h, r0, count;       // rows [r0, r0 + count) of kv head h of request b
+  int b, h, r0, count;  // rows [r0, r0 + count) of kv head h of request b
   Span span;
-  int tile0, tiles;          // key tiles [tile0, tile0 + tiles) (may be none)
-  long long item;            // first unit of the item
-  int first, n_units, width; // the segment's units of the item, the item's
+  int tile0, tiles;     // key tiles [tile0, tile0 + tiles) (may be none)
+  long long item;       // first unit of the item
+  int first, width;     // the segment's first tile of the item, the item's tiles
+  bool whole;
 };
 
-// Walks a run's segments in order.
+// Walks a run's segments in order.  An item is its tiles and then kItemUnits
+// more; a run that ends among those takes the item to its end, and one that
+// begins there leaves it alone, so only tiles are ever split.
 struct Walk {
   long long u, end, base;  // next unit, end of the run, first unit of request b
   int b;
   __device__ bool next(const Args &a, int tile_rows, Segment &s) {
-    if (u >= end) return false;
     for (;;) {
-      s.rq = load_request(a, b);
-      const long long size = request_units(a, s.rq, tile_rows);
-      if (u - base < size) break;
-      base += size;
-      ++b;
+      if (u >= end) return false;
+      for (;;) {
+        s.rq = load_request(a, b);
+        const long long size = request_units(a, s.rq, tile_rows);
+        if (u - base < size) break;
+        base += size;
+        ++b;
+      }
+      s.width = tiles_per_item(a, s.rq, tile_rows);
+      const long long item = (u - base) / (s.width + kItemUnits);
+      s.item = base + item * (s.width + kItemUnits);
+      s.h = (int)(item % a.Hkv);
+      s.r0 = (int)(item / a.Hkv) * tile_rows;
+      s.first = (int)(u - s.item);
+      if (s.first < s.width) break;
+      u = s.item + s.width + kItemUnits;
     }
+    const int n = (int)min((long long)(s.width - s.first), end - u);
     s.b = b;
-    s.width = tiles_per_item(a, s.rq, tile_rows);
-    const long long item = (u - base) / s.width;
-    s.item = base + item * s.width;
-    s.first = (int)(u - s.item);
-    s.n_units = (int)min((long long)(s.width - s.first), end - u);
-    s.h = (int)(item % a.Hkv);
-    s.r0 = (int)(item / a.Hkv) * tile_rows;
     s.count = min(tile_rows, s.rq.n * a.G - s.r0);
     s.span = rows_span(a, s.rq, s.r0, s.count);
-    const int t0 = s.span.lo / kBK, t1 = (s.span.hi + kBK - 1) / kBK;
-    s.tile0 = t0 + s.first;
-    s.tiles = max(0, min(t1 - s.tile0, s.n_units));
-    u += s.n_units;
+    s.whole = n == s.width;
+    s.tile0 = s.span.lo / kBK + s.first;
+    s.tiles = max(0, min((s.span.hi + kBK - 1) / kBK - s.tile0, n));
+    u = s.first + n == s.width ? s.item + s.width + kItemUnits : u + n;
     return true;
   }
 };
 
-// The consumers' results of a segment, row by row (attend_row), in the place
-// of the first key group's; the other groups' hold nothing.
 template <int D, int kRowGroups>
 __device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
                                         int r0, int count, int j0, int j1, float *s_out,
@@ -146,7 +153,10 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
   __shared__ __align__(8) uint64_t full[S::kSlots], empty[S::kSlots];
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   __shared__ long long s_scan[kThreads / 32], s_base;
-  __shared__ int s_b, s_nonfinite, s_last;
+  __shared__ int s_b, s_nonfinite, s_more;
+  __shared__ Runs s_runs;
+  __shared__ Walk s_walk;  // the consumers': their registers hold the tiles
+  __shared__ Segment s;
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t ring = raw + ((1024u - (raw & 1023u)) & 1023u);
   float *s_out = reinterpret_cast<float *>(smem_raw + (ring - raw) + S::kSlots * S::kSlotBytes);
@@ -179,12 +189,15 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     }
     return all;
   };
-  runs.units = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    long long upto;
-    runs.units += block_sum(
-        b < a.B ? request_units(a, load_request(a, b), kTileRows) : 0, upto);
+  auto units_of = [&](int b) {
+    return b < a.B ? request_units(a, load_request(a, b), kTileRows) : 0;
+  };
+  long long size = units_of(tid), upto;  // the first block of requests, kept for the search
+  long long all = block_sum(size, upto);
+  runs.units = all;
+  for (int b0 = kThreads; b0 < a.B; b0 += kThreads) {
+    long long past;
+    runs.units += block_sum(units_of(b0 + tid), past);
   }
   runs.ctas = (int)min((long long)gridDim.x, runs.units);
   // rows past the last request's: zero
@@ -195,23 +208,23 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     if (a.lse)
       for (int i = tid; i < a.Hq; i += kThreads) a.lse[(long long)r * a.Hq + i] = kNegInf;
   }
+  pdl_launch_dependents();
+  if (tid == 0) a.splits[blockIdx.x].n = 0;
   if ((int)blockIdx.x >= runs.ctas) return;  // uniform
   Walk walk;
   walk.u = runs.begin(blockIdx.x);
   walk.end = runs.begin(blockIdx.x + 1);
-  long long sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    const long long size = b < a.B ? request_units(a, load_request(a, b), kTileRows) : 0;
-    long long upto;
-    const long long all = block_sum(size, upto);
-    upto += sum;
-    if (upto > walk.u && upto - size <= walk.u) {
-      s_b = b;
-      s_base = upto - size;
+  long long before = 0;  // units of the blocks of requests already searched
+  for (int b0 = 0;;) {
+    if (before + upto > walk.u && before + upto - size <= walk.u) {
+      s_b = b0 + tid;
+      s_base = before + upto - size;
     }
-    sum += all;
-    if (sum > walk.u) break;
+    b0 += kThreads;
+    if (b0 >= a.B) break;
+    before += all;
+    size = units_of(b0 + tid);
+    all = block_sum(size, upto);
   }
   __syncthreads();
   walk.b = s_b;
@@ -225,7 +238,6 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     }
   };
   bool dead = false;  // a wait gave up: the rest runs without waiting, results are invalid
-  Segment s;
 
   if (warp == kWarps) {
     // ------------------------------ producer ------------------------------
@@ -234,12 +246,13 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     const int boxes = pages * (D / 64);
     const int blk = lane / pages, pg = lane - blk * pages;
     long long issued = 0;
-    while (walk.next(a, kTileRows, s)) {
-      for (int t = 0; t < s.tiles; ++t) {
-        const int j = (s.tile0 + t) * kBK + pg * per_page;
+    Segment x;
+    while (walk.next(a, kTileRows, x)) {
+      for (int t = 0; t < x.tiles; ++t) {
+        const int j = (x.tile0 + t) * kBK + pg * per_page;
         int y = 0;
         if (lane < boxes)
-          y = page_row(a, s.b, s.h, j >> a.page_shift, s.span.lo, s.span.hi) +
+          y = page_row(a, x.b, x.h, j >> a.page_shift, x.span.lo, x.span.hi) +
               (j & ((1 << a.page_shift) - 1));
         for (int kv = 0; kv < 2; ++kv) {
           if (issued >= S::kSlots && !dead && !mbar_wait(&empty[slot], phase ^ 1u)) dead = true;
@@ -278,7 +291,14 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     }
   };
 
-  while (walk.next(a, kTileRows, s)) {
+  if (tid == 0) {
+    s_walk = walk;
+    s_runs = runs;
+  }
+  for (;;) {
+    if (tid == 0) s_more = s_walk.next(a, kTileRows, s);
+    consumer_sync();
+    if (!s_more) break;
     // queries as A fragments; rows past the tile are zero
     uint32_t qf[kSteps][4];
     int last[2], first[2];  // positions that rows gq and gq + 8 attend: first .. last
@@ -447,8 +467,6 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
     consumer_sync();
     if (tid == 0) s_nonfinite = 0;  // next written after the next segment's barrier
 
-    const bool whole = s.first == 0 && s.n_units == s.width;
-    const int c0 = whole ? 0 : runs.owner(s.item), c1 = whole ? 0 : runs.owner(s.item + s.width - 1);
     float *part = partial_at(a, 2 * (int)blockIdx.x + (s.first == 0 ? 1 : 0), kTileRows, D);
     for (int i = tid; i < s.count * (D / 4); i += kConsumers) {
       const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
@@ -470,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
         acc.z = fmaf(v.z, f, acc.z);
         acc.w = fmaf(v.w, f, acc.w);
       }
-      if (whole) {
-        store_out4<D>(a, s.rq, s.h, s.r0 + rr, d, acc, mm, ll);
+      if (s.whole) {
+        store_out4<D>(a, s.rq.q0, s.h, s.r0 + rr, d, acc, mm, ll);
       } else {
         __stcg(reinterpret_cast<float4 *>(part + rr * D + d), acc);
         if (d == 0) {
@@ -480,24 +498,165 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
         }
       }
     }
-    if (!whole) {
-      __threadfence();
-      consumer_sync();
-      if (tid == 0) {
-        const unsigned n = atomicAdd(a.counters + c0, 1u);
-        s_last = n == (unsigned)(c1 - c0);
-        if (s_last) a.counters[c0] = 0;  // every CTA of the item has arrived
+    if (tid == 0 && s.first == 0 && !s.whole)
+      a.splits[blockIdx.x] = SplitItem{s_runs.owner(s.item + s.width - 1) - (int)blockIdx.x + 1,
+                                       s.rq.q0, s.h, s.r0, s.count, {0, 0, 0}};
+    consumer_sync();  // the segment has been read
+  }
+}
+
+// ---- joining split items ------------------------------------------------------
+// With M the largest of an item's partials' maxima, each row's
+//   out = sum_k 2^(c (m_k - M)) O_k / sum_k 2^(c (m_k - M)) l_k.
+// The partials are a few megabytes in L2 and each is read once: latency is the
+// cost.  A piece of work is a few rows of an item, the fewer the more partials
+// it has; a block's threads split the partials of a row among them, keep eight
+// loads in flight each and have the first on their way before the weights are
+// known; every block finds its pieces by itself from the items' list.
+// (Joining in the CTA that finishes last instead took 5 us for 16 partials of
+// five rows and 60 us for 304: a fence, an atomic and one SM's latency.)
+constexpr int kJoinThreads = 512;
+constexpr int kJoinDepth = 8;                // loads in flight a thread
+constexpr int kJoinWeights = 4 * kMaxCtas;   // rows of a piece x partials, at most
+
+// Rows of a piece of an item with n partials: a power of two of thread groups
+// that take kJoinDepth partials each, but four rows at least.
+__device__ __forceinline__ int piece_rows(int n, int D) {
+  int rows = kJoinThreads / (D / 4);
+  while (rows > 4 && rows * (D / 4) * n > kJoinThreads * kJoinDepth) rows >>= 1;
+  return rows;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    attn_join_kernel(const __grid_constant__ Args a, int ctas, int tile_rows) {
+  __shared__ float s_f[kJoinWeights], s_l[kJoinWeights];
+  __shared__ float4 s_sum[kJoinThreads];
+  __shared__ int s_end[kMaxCtas], s_warp[kJoinThreads / 32];
+  static_assert(kMaxCtas <= kJoinThreads, "an item a thread");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  // pieces up to and with each CTA's item
+  int pieces = 0;
+  if (tid < ctas && a.splits[tid].n > 0) {
+    const int rows = piece_rows(a.splits[tid].n, D);
+    pieces = (a.splits[tid].count + rows - 1) / rows;
+  }
+  if (!__syncthreads_or(pieces)) return;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(0xffffffffu, pieces, o);
+    if (lane >= o) pieces += w;
+  }
+  if (lane == 31) s_warp[warp] = pieces;
+  __syncthreads();
+  int total = 0;
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) pieces += s_warp[i];
+    total += s_warp[i];
+  }
+  if (tid < ctas) s_end[tid] = pieces;
+  __syncthreads();
+
+  for (int piece = blockIdx.x; piece < total; piece += gridDim.x) {
+    int c0 = 0, hi = ctas - 1;  // the first item whose pieces end after this one
+    while (c0 < hi) {
+      const int mid = (c0 + hi) >> 1;
+      if (s_end[mid] > piece)
+        hi = mid;
+      else
+        c0 = mid + 1;
+    }
+    const SplitItem it = a.splits[c0];
+    const int most = piece_rows(it.n, D);
+    const int row0 = (piece - (c0 > 0 ? s_end[c0 - 1] : 0)) * most;
+    const int rows = min(most, it.count - row0);
+    const int items = rows * (D / 4);         // at most kJoinThreads
+    const int groups = kJoinThreads / items;  // of partials
+    const int i = tid % items, group = tid / items;
+    const int rr = i / (D / 4), d = 4 * (i % (D / 4));
+    // partial k: the first CTA's second place, the others' first
+    auto part = [&](int k) { return partial_at(a, 2 * (c0 + k) + (k == 0 ? 1 : 0), tile_rows, D); };
+    float4 v[kJoinDepth];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int u = 0; u < kJoinDepth; ++u)
+        if (group < groups && k0 + u * groups < it.n)
+          v[u] = __ldcg(reinterpret_cast<const float4 *>(part(k0 + u * groups) +
+                                                         (row0 + rr) * D + d));
+    };
+    load(group);
+    for (int j = tid; j < it.n * rows; j += kJoinThreads) {
+      const int k = j / rows;
+      const float *ml = part(k) + tile_rows * D + row0 + (j - k * rows);
+      s_f[j] = __ldcg(ml);
+      s_l[j] = __ldcg(ml + tile_rows);
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += kJoinThreads / 32) {
+      float m = kNegInf, l = 0.f;
+      for (int k = lane; k < it.n; k += 32) m = fmaxf(m, s_f[k * rows + r]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int k = lane; k < it.n; k += 32) {
+        const float lk = s_l[k * rows + r], f = join_weight(a, s_f[k * rows + r], lk, m);
+        l = fmaf(lk, f, l);
+        s_f[k * rows + r] = f;
       }
-      consumer_sync();
-      if (s_last) {
-        __threadfence();
-        for (int i = tid; i < s.count * (D / 4); i += kConsumers) {
-          const int rr = i / (D / 4), d = 4 * (i - rr * (D / 4));
-          join_row4<D>(a, s.rq, s.h, s.r0 + rr, rr, d, c0, c1, kTileRows);
-        }
+      l = warp_sum(l);
+      __syncwarp();
+      if (lane == 0) {  // at least two partials
+        s_l[r] = m;
+        s_l[rows + r] = l;
       }
     }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = group; group < groups;) {
+#pragma unroll
+      for (int u = 0; u < kJoinDepth; ++u)
+        if (k0 + u * groups < it.n) {
+          const float f = s_f[(k0 + u * groups) * rows + rr];
+          acc.x = fmaf(v[u].x, f, acc.x);
+          acc.y = fmaf(v[u].y, f, acc.y);
+          acc.z = fmaf(v[u].z, f, acc.z);
+          acc.w = fmaf(v[u].w, f, acc.w);
+        }
+      k0 += kJoinDepth * groups;
+      if (k0 >= it.n) break;
+      load(k0);
+    }
+    s_sum[tid] = acc;
+    __syncthreads();
+    if (group == 0) {
+      for (int g = 1; g < groups; ++g) {
+        const float4 x = s_sum[g * items + i];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      store_out4<D>(a, it.q0, it.h, it.r0 + row0 + rr, d, acc, s_l[rr], s_l[rows + rr]);
+    }
+    __syncthreads();
   }
+}
+
+template <int D>
+sv_status join(const Args &a, int ctas, int tile_rows, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * device_sm_count()));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, a, ctas, tile_rows) != cudaSuccess)
+    return fail(SV_ERR_CUDA, "paged_attention: join launch failed: %s",
+                cudaGetErrorString(cudaGetLastError()));
+  return check_launch("paged_attention (join)");
 }
 
 template <int D, int kRowGroups>
@@ -513,7 +672,8 @@ sv_status launch_rows(const CUtensorMap &kmap, const CUtensorMap &vmap, const Ar
     return fail(SV_ERR_CUDA, "paged_attention: cudaFuncSetAttribute failed: %s",
                 cudaGetErrorString(ce));
   attn_rows_kernel<D, kRowGroups><<<(unsigned)ctas, kThreads, S::kSmem, stream>>>(kmap, vmap, a);
-  return check_launch("paged_attention");
+  const sv_status st = check_launch("paged_attention");
+  return st == SV_OK ? join<D>(a, ctas, 16 * kRowGroups, stream) : st;
 }
 
 template <int D>
@@ -524,12 +684,13 @@ sv_status launch_rows(int groups, const CUtensorMap &kmap, const CUtensorMap &vm
   return launch_rows<D, 4>(kmap, vmap, a, ctas, stream);
 }
 
+size_t split_bytes() { return (size_t)kMaxCtas * sizeof(SplitItem); }
 int rows_ctas(int D) { return std::min(kMaxCtas, device_sm_count() * (D == 256 ? 1 : 2)); }
 
 size_t workspace_bytes(int D) {
   size_t part = (size_t)rows_ctas(D) * 2 * 64 * (D + 2) * 4;
   if (D <= 128) part = std::max(part, tc_partial_bytes(D));
-  return kCounterBytes + part;
+  return kCounterBytes + split_bytes() + part;
 }
 
 }  // namespace
@@ -643,8 +804,10 @@ extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
   a.window = window;
   a.scale = scale;
   a.scale_log2 = scale * 1.44269504088896340736f;
-  a.counters = static_cast<unsigned *>(workspace);
-  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + attn::kCounterBytes);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.counters = reinterpret_cast<unsigned *>(ws);
+  a.splits = reinterpret_cast<attn::SplitItem *>(ws + attn::kCounterBytes);
+  a.partials = reinterpret_cast<float *>(ws + attn::kCounterBytes + attn::split_bytes());
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // More rows a kv head than a 64-row tile of the streaming kernel holds go to

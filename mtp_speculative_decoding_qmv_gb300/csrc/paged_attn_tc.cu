@@ -244,6 +244,53 @@ __device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int
   }
 }
 
+// ---- joining split items ------------------------------------------------------
+// The CTAs c0 .. c1 that share an item each leave a partial.  Most often there
+// are two or three, of every row, and the last CTA to arrive joins them while
+// others still work (a launch of its own for it made a 5000-token prompt 290
+// instead of 210 us).  More than kJoin are joined in two rounds, groups of
+// kJoin (the result takes the first member's place) and then the groups, so
+// that no CTA reads more than about kJoin of them.  Partials are always added
+// in CTA order, whichever CTA does it.
+constexpr int kMaxTcCtas = 170;
+constexpr int kJoin = 16;
+static_assert(2 * 3 * kMaxTcCtas * 4 <= kCounterBytes, "counters");
+static_assert(kMaxTcCtas <= kJoin * kJoin && kJoin * kTile * 4 <= 128 * kTile, "weights in the stage");
+struct Group {
+  int first, stride, n;  // CTAs first, first + stride, ..
+  int counter;           // its arrivals, of 3 ctas
+  bool final;            // its result is the item's
+};
+// The group in which CTA c of the item arrives first, or with `again` the
+// groups' own.  `ctas` bounds the CTA numbers.
+__device__ __forceinline__ Group join_group(int c0, int c1, int c, bool again, int ctas) {
+  const int n = c1 - c0 + 1;
+  Group g;
+  if (again) {
+    g.first = c0;
+    g.stride = kJoin;
+    g.n = (n + kJoin - 1) / kJoin;
+    g.counter = 2 * ctas + c0;
+    g.final = true;
+  } else {
+    const int k = (c - c0) / kJoin * kJoin;
+    g.first = c0 + k;
+    g.stride = 1;
+    g.n = min(kJoin, n - k);
+    // a CTA can be first of a group in the item that it ends and in the one
+    // that it begins
+    g.counter = 2 * g.first + (k == 0 ? 1 : 0);
+    g.final = n <= kJoin;
+  }
+  return g;
+}
+// Partial k of the group (see partial_at): an item's first CTA has it in its
+// second place.
+__device__ __forceinline__ int join_slot(const Group &g, int c0, int k) {
+  const int c = g.first + k * g.stride;
+  return 2 * c + (c == c0 ? 1 : 0);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -781,48 +828,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();  // O has been read before the next segment's products write it
         if (!whole) {
-          // the last of the item's CTAs joins this tile's partials, in order
+          // ---- the last CTA to arrive joins this tile's partials ----
           const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits - 1);
-          __threadfence();
-          group_sync(wg);
-          if (row == 0) {
-            unsigned *counter = a.counters + 2 * c0 + wg;
-            s_last[wg] = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-            if (s_last[wg]) *counter = 0;  // every CTA of the item has arrived
-          }
-          group_sync(wg);
-          if (s_last[wg]) {
+          float *weights = reinterpret_cast<float *>(  // [partial][row]
+              smem_raw + (q_smem - raw) + (2 + S::kSlots) * S::kTileBytes +
+              (uint32_t)wg * S::kStage);
+          for (int again = 0; again < 2; ++again) {
+            const Group gr = join_group(c0, c1, (int)blockIdx.x, again != 0, (int)gridDim.x);
+            __threadfence();
+            group_sync(wg);
+            if (row == 0) {
+              unsigned *counter = a.counters + wg * 3 * gridDim.x + gr.counter;
+              s_last[wg] = atomicAdd(counter, 1u) == (unsigned)(gr.n - 1);
+              if (s_last[wg]) *counter = 0;  // all have arrived: ready for the next call
+            }
+            group_sync(wg);
+            if (!s_last[wg]) break;
             __threadfence();
             if (ok) {
               float mm = kNegInf, ll = 0.f;
-              for (int k = c0; k <= c1; ++k)
-                mm = fmaxf(mm, __ldcg(partial_at(a, 2 * k + (k == c0), kRows, D) + kRows * D + rr));
-              auto weight = [&](int k, float &lk) {
-                const float *ml = partial_at(a, 2 * k + (k == c0), kRows, D) + kRows * D + rr;
-                const float mk = __ldcg(ml);
-                lk = __ldcg(ml + kRows);
-                // no keys: nothing (its maximum is -inf, and so may be every other)
-                return mk == kNegInf && lk == 0.f ? 0.f : exp2_approx((mk - mm) * c);
-              };
-              for (int k = c0; k <= c1; ++k) {
-                float lk;
-                const float f = weight(k, lk);
+#pragma unroll 4
+              for (int k = 0; k < gr.n; ++k)
+                mm = fmaxf(mm, __ldcg(partial_at(a, join_slot(gr, c0, k), kRows, D) + kRows * D + rr));
+#pragma unroll 4
+              for (int k = 0; k < gr.n; ++k) {
+                const float *ml = partial_at(a, join_slot(gr, c0, k), kRows, D) + kRows * D + rr;
+                const float lk = __ldcg(ml + kRows), f = join_weight(a, __ldcg(ml), lk, mm);
                 ll = fmaf(lk, f, ll);
+                weights[k * kTile + row] = f;  // read by this thread alone
               }
               const float inv = ll == 0.f ? 0.f : 1.f / ll;
               const int g = r - t_row * a.G;
               __nv_bfloat16 *dst = a.out + (long long)(s.rq.q0 + t_row) * a.out_stride +
                                    (long long)(s.h * a.G + g) * D;
+              const int to = join_slot(gr, c0, 0);
 #pragma unroll 1
               for (int d = 0; d < D; d += 64) {
                 float o[64];
 #pragma unroll
                 for (int i = 0; i < 64; ++i) o[i] = 0.f;
-                for (int k = c0; k <= c1; ++k) {
-                  float lk;
-                  const float f = weight(k, lk);
-                  const float *part =
-                      part_row<D>(a, 2 * k + (k == c0), rr) + (size_t)(d >> 2) * kRows * 4;
+#pragma unroll 2
+                for (int k = 0; k < gr.n; ++k) {
+                  const float f = weights[k * kTile + row];
+                  const float *part = part_row<D>(a, join_slot(gr, c0, k), rr) +
+                                      (size_t)(d >> 2) * kRows * 4;
                   float4 y[16];
 #pragma unroll
                   for (int i = 0; i < 16; ++i)
@@ -835,17 +884,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o[4 * i + 3] = fmaf(y[i].w, f, o[4 * i + 3]);
                   }
                 }
+                if (gr.final) {
 #pragma unroll
-                for (int i = 0; i < 64; i += 8)
-                  *reinterpret_cast<uint4 *>(dst + d + i) = make_uint4(
-                      pack_bf16(o[i] * inv, o[i + 1] * inv),
-                      pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                      pack_bf16(o[i + 4] * inv, o[i + 5] * inv),
-                      pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+                  for (int i = 0; i < 64; i += 8)
+                    *reinterpret_cast<uint4 *>(dst + d + i) = make_uint4(
+                        pack_bf16(o[i] * inv, o[i + 1] * inv),
+                        pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                        pack_bf16(o[i + 4] * inv, o[i + 5] * inv),
+                        pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+                } else {
+                  float *part = part_row<D>(a, to, rr) + (size_t)(d >> 2) * kRows * 4;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    __stcg(reinterpret_cast<float4 *>(part + (size_t)i * kRows * 4),
+                           make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+                }
               }
-              if (a.lse)
+              if (!gr.final) {
+                float *ml = partial_at(a, to, kRows, D) + kRows * D + rr;
+                __stcg(ml, mm);
+                __stcg(ml + kRows, ll);
+              } else if (a.lse) {
                 a.lse[(long long)(s.rq.q0 + t_row) * a.Hq + s.h * a.G + g] = row_lse(a, mm, ll);
+              }
             }
+            if (gr.final) break;
           }
         }
       }
@@ -876,7 +939,7 @@ sv_status launch(const Args &a, const CUtensorMap &kmap, const CUtensorMap &vmap
   return check_launch("paged_attention");
 }
 
-int tc_ctas() { return std::min(kMaxCtas / 2, device_sm_count()); }
+int tc_ctas() { return std::min(kMaxTcCtas, device_sm_count()); }
 
 }  // namespace
 
