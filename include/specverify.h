@@ -563,8 +563,8 @@ sv_status kv_pages_step(const int32_t *length, const int32_t *held, const int32_
  * [rotary_dim / 2] (turns per position in units of 2^-64); axis uint8
  * [rotary_dim / 2] (NULL with one axis; values past axes - 1 count as that).
  * Requires D 64, 128 or 256; rotary_dim a multiple of 16 in [0, D]; axes 1..4;
- * q, k, v, q_out and the caches 16-byte aligned, row strides multiples of 16
- * bytes; no output overlaps an input or another output. */
+ * q, k, v, the weights, q_out and the caches 16-byte aligned, row strides
+ * multiples of 16 bytes; no output overlaps an input or another output. */
 sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x_dtype,
                          long long q_row_stride, long long k_row_stride, long long v_row_stride,
                          const int32_t *positions, int axes, const int32_t *slots,

@@ -20,12 +20,13 @@
 // precision arithmetic.
 //
 // Memory traffic is the bound: each input read once, each output written once.
-// A warp owns one row and kHeads consecutive heads of its queries, keys and
-// values; lane l holds elements l D / 32 .. (l + 1) D / 32 of each, loaded as
-// one vector, so a head is one contiguous request per warp and all kHeads
-// loads are in flight together.  The lane's angles depend on the row and its
-// elements alone and serve every head.  The partner element of a pair is in
-// the same lane (interleaved) or R / (2 D / 32) lanes away (one shuffle).
+// A lane holds eight consecutive elements of a head (one or two 16-byte loads),
+// so D / 8 lanes hold a head and a warp 1, 2 or 4 heads of D 256, 128 or 64 at
+// a time; it takes kIter such sets of one row's queries, keys and values, all
+// loads in flight together.  The row's angles are computed once by the warp,
+// spread over its lanes, and shared by shuffles; they serve all its heads.  The
+// partner element of a pair is in the same lane (interleaved) or R / 16 lanes
+// away (one shuffle).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,45 +55,28 @@ struct RopeArgs {
   __nv_bfloat16 *q_out, *k_cache, *v_cache;
 };
 
-template <typename T, int N>
-struct Vec;
-template <int N>
-struct Vec<float, N> {
-  __device__ static void load(const float *p, float (&x)[N]) {
-    if constexpr (N == 2) {
-      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-      x[0] = v.x, x[1] = v.y;
-    } else {
+// N values as they lie in memory, 32 bits at a time, and widened.
+template <int W>
+__device__ __forceinline__ void load_words(const void *p, uint32_t (&x)[W]) {
 #pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + i);
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-      }
+  for (int i = 0; i < W / 4; ++i) {
+    const uint4 v = __ldg(static_cast<const uint4 *>(p) + i);
+    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+  }
+}
+template <typename T, int W, int N>
+__device__ __forceinline__ void widen(const uint32_t (&x)[W], float (&y)[N]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = __uint_as_float(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      y[2 * i] = __uint_as_float(x[i] << 16);
+      y[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
     }
   }
-};
-template <int N>
-struct Vec<__nv_bfloat16, N> {
-  __device__ static void unpack(uint32_t u, float &a, float &b) {
-    a = __uint_as_float(u << 16);
-    b = __uint_as_float(u & 0xFFFF0000u);
-  }
-  __device__ static void load(const __nv_bfloat16 *p, float (&x)[N]) {
-    if constexpr (N == 2) {
-      unpack(__ldg(reinterpret_cast<const uint32_t *>(p)), x[0], x[1]);
-    } else if constexpr (N == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-      unpack(v.x, x[0], x[1]);
-      unpack(v.y, x[2], x[3]);
-    } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-      unpack(v.x, x[0], x[1]);
-      unpack(v.y, x[2], x[3]);
-      unpack(v.z, x[4], x[5]);
-      unpack(v.w, x[6], x[7]);
-    }
-  }
-};
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   uint32_t d;
@@ -101,45 +85,38 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 template <int N>
 __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&x)[N]) {
-  if constexpr (N == 2) {
-    *reinterpret_cast<uint32_t *>(p) = pack_bf16(x[0], x[1]);
-  } else if constexpr (N == 4) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-  } else {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                               pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-  }
+  static_assert(N == 8, "16 bytes");
+  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                             pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-template <typename T, int D, bool kPairs, int kHeads>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const RopeArgs a) {
-  constexpr int E = D / 32;  // elements a lane holds
+template <typename T, int D, bool kPairs, int kIter>
+__global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_append_kernel(const RopeArgs a) {
+  constexpr int E = 8;                        // elements a lane holds
+  constexpr int W = E * (int)sizeof(T) / 4;
+  constexpr int kLanes = D / E, kSet = 32 / kLanes;  // lanes a head, heads a set
   const int lane = threadIdx.x & 31;
-  const int total = a.Hq + 2 * a.Hkv;
-  const int groups = (total + kHeads - 1) / kHeads;
-  const long long task = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  if (task >= (long long)a.rows * groups) return;
+  const int rotated = a.Hq + a.Hkv, total = rotated + a.Hkv;
+  const unsigned groups = (unsigned)(total + kIter * kSet - 1) / (kIter * kSet);
+  const unsigned task = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  if (task >= (unsigned)a.rows * groups) return;
   const int row = (int)(task / groups);
-  const int h0 = (int)(task - (long long)row * groups) * kHeads;
-  const int e0 = lane * E;
+  const int h_warp = (int)(task - (unsigned)row * groups) * (kIter * kSet);
+  const int h0 = h_warp + lane / kLanes, e0 = lane % kLanes * E;
 
-  float x[kHeads][E];
+  // every head's load is issued before anything waits for one
+  uint32_t raw[kIter][W];
+  {
+    const T *q = static_cast<const T *>(a.q) + (long long)row * a.q_stride + e0;
+    const T *k = static_cast<const T *>(a.k) + (long long)row * a.k_stride + e0;
+    const T *v = static_cast<const T *>(a.v) + (long long)row * a.v_stride + e0;
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i;
-    const T *src = nullptr;
-    if (h < a.Hq)
-      src = static_cast<const T *>(a.q) + (long long)row * a.q_stride + (long long)h * D;
-    else if (h < a.Hq + a.Hkv)
-      src = static_cast<const T *>(a.k) + (long long)row * a.k_stride + (long long)(h - a.Hq) * D;
-    else if (h < total)
-      src = static_cast<const T *>(a.v) + (long long)row * a.v_stride +
-            (long long)(h - a.Hq - a.Hkv) * D;
-    if (src) {
-      Vec<T, E>::load(src + e0, x[i]);
-    } else {
+    for (int i = 0; i < kIter; ++i) {
+      const int h = h0 + i * kSet;
+      const T *src = h < a.Hq ? q + h * D : h < rotated ? k + (h - a.Hq) * D : v + (h - rotated) * D;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      for (int j = 0; j < W; ++j) raw[i][j] = 0;
+      if (h < total) load_words<W>(src, raw[i]);
     }
   }
   const int slot = __ldg(a.slots + row);
@@ -147,74 +124,109 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_append_kernel(const Rope
 
   const int half = a.R / 2;
   const bool turned = e0 < a.R;  // R is a multiple of 2 E: a lane is wholly in or out
+  const bool first = e0 < half;
   float cs[E], sn[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) cs[e] = 1.f, sn[e] = 0.f;
-  if (h0 < a.Hq + a.Hkv && turned) {
+  if (h_warp < rotated && half > 0) {
     auto angle = [&](int f, float &c, float &s) {
       const int ax = a.axis ? min((int)__ldg(a.axis + f), a.axes - 1) : 0;
       const int pos = __ldg(a.positions + (long long)row * a.axes + ax);
       const uint64_t turns = (uint64_t)(int64_t)pos * __ldg(a.freqs + f);
       sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
     };
-    if constexpr (kPairs) {
+    // the lane's elements turn by angles f0 .. (every second element a new one
+    // when interleaved); the warp computes each angle once, kOwn a lane, or one
+    // where 32 lanes are enough
+    constexpr int kOwn = D / 64;
+    constexpr int kStep = kPairs ? 2 : 1;
+    const int f0 = kPairs ? e0 / 2 : first ? e0 : e0 - half;
+    if (half <= 32) {
+      float c, s;
+      angle(min(lane, half - 1), c, s);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        angle((e0 + e) / 2, cs[e], sn[e]);
+      for (int e = 0; e < E; e += kStep) {
+        cs[e] = __shfl_sync(0xffffffffu, c, f0 + e / kStep);
+        sn[e] = __shfl_sync(0xffffffffu, s, f0 + e / kStep);
+      }
+    } else {
+      float c[kOwn], s[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) angle(min(lane * kOwn + i, half - 1), c[i], s[i]);
+#pragma unroll
+      for (int e = 0; e < E; e += kStep) {
+        const int f = e / kStep;  // f0 is a multiple of 4, so of kOwn
+        cs[e] = __shfl_sync(0xffffffffu, c[f % kOwn], (f0 + f) / kOwn);
+        sn[e] = __shfl_sync(0xffffffffu, s[f % kOwn], (f0 + f) / kOwn);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += kStep) {
+      if (!turned) cs[e] = 1.f, sn[e] = 0.f;
+      if constexpr (kPairs) {
         cs[e + 1] = cs[e];
         sn[e + 1] = sn[e];
         sn[e] = -sn[e];
-      }
-    } else {
-      const bool first = e0 < half;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        angle(e0 + e - (first ? 0 : half), cs[e], sn[e]);
-        if (first) sn[e] = -sn[e];
+      } else if (first) {
+        sn[e] = -sn[e];
       }
     }
   }
-  const int partner = !turned ? lane : e0 < half ? lane + half / E : lane - half / E;
+  const int partner = !turned ? lane : first ? lane + half / E : lane - half / E;
+  float w[E];  // the weights of the lane's elements, the queries' or the keys'
+  const float *held = nullptr;
   const long long page = keep ? slot >> a.page_shift : 0;
   const int off = slot & ((1 << a.page_shift) - 1);
+  __nv_bfloat16 *q_out = a.q_out + (long long)row * a.Hq * D + e0;
+  const long long cache = (((page * a.Hkv) << a.page_shift) + off) * D + e0;
+  const int per_head = D << a.page_shift;
 
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i;  // uniform in the warp
-    if (h >= total) break;
-    if (h < a.Hq + a.Hkv) {
-      const float *w = h < a.Hq ? a.q_weight : a.k_weight;
-      if (w) {
+  for (int i = 0; i < kIter; ++i) {
+    if (h_warp + i * kSet >= total) break;  // the same for the warp
+    const int h = h0 + i * kSet;
+    float x[E];
+    widen<T>(raw[i], x);
+    if (h_warp + i * kSet < rotated) {  // some head of the set is a query or a key
+      const bool value = h >= rotated;
+      const float *weights = value ? nullptr : h < a.Hq ? a.q_weight : a.k_weight;
+      if (weights != held && weights) {
+        uint32_t y[E];
+        load_words<E>(weights + e0, y);
+        widen<float>(y, w);
+      }
+      held = weights;
+      if (a.q_weight || a.k_weight) {  // the same for the warp
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-        const float r = rsqrtf(warp_sum(ss) * (1.f / D) + a.eps);
+        for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = x[i][e] * r * __ldg(w + e0 + e);
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        if (weights) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = x[e] * r * w[e];
+        }
       }
       float y[E];
       if constexpr (kPairs) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = x[i][e ^ 1];
+        for (int e = 0; e < E; ++e) y[e] = x[e ^ 1];
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = __shfl_sync(0xffffffffu, x[i][e], partner);
+        for (int e = 0; e < E; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner);
       }
-      if (turned) {  // else as it is, infinities included
+      if (turned && !value) {  // else as it is, infinities included
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = fmaf(y[e], sn[e], x[i][e] * cs[e]);
+        for (int e = 0; e < E; ++e) x[e] = fmaf(y[e], sn[e], x[e] * cs[e]);
       }
     }
-    __nv_bfloat16 *dst;
-    if (h < a.Hq) {
-      dst = a.q_out + ((long long)row * a.Hq + h) * D;
-    } else {
-      if (!keep) continue;
-      const int kh = h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv;
-      dst = (h < a.Hq + a.Hkv ? a.k_cache : a.v_cache) +
-            (((page * a.Hkv + kh) << a.page_shift) + off) * D;
-    }
-    store_bf16<E>(dst + e0, x[i]);
+    if (h < a.Hq)
+      store_bf16<E>(q_out + h * D, x);
+    else if (keep && h < total)
+      store_bf16<E>(h < rotated ? a.k_cache + cache + (long long)(h - a.Hq) * per_head
+                                : a.v_cache + cache + (long long)(h - rotated) * per_head,
+                    x);
   }
 }
 
@@ -222,8 +234,8 @@ typedef void (*RopeKernel)(const RopeArgs);
 
 template <typename T, int D>
 RopeKernel pick(bool pairs, bool many) {
-  return pairs ? (many ? rope_append_kernel<T, D, true, 8> : rope_append_kernel<T, D, true, 2>)
-               : (many ? rope_append_kernel<T, D, false, 8> : rope_append_kernel<T, D, false, 2>);
+  return pairs ? (many ? rope_append_kernel<T, D, true, 4> : rope_append_kernel<T, D, true, 1>)
+               : (many ? rope_append_kernel<T, D, false, 4> : rope_append_kernel<T, D, false, 1>);
 }
 template <typename T>
 RopeKernel pick(int D, bool pairs, bool many) {
@@ -283,7 +295,7 @@ extern "C" sv_status rope_kv_append(const void *q, const void *k, const void *v,
     return fail(SV_ERR_INVALID_ARG, "%s: q, k, v, q_out and the caches must be 16-byte aligned",
                 who);
   if (!aligned(positions, 4) || !aligned(slots, 4) || (freqs && !aligned(freqs, 8)) ||
-      (q_weight && !aligned(q_weight, 4)) || (k_weight && !aligned(k_weight, 4)))
+      (q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
     return fail(SV_ERR_INVALID_ARG, "%s: misaligned pointer", who);
   const size_t cache = (size_t)num_pages * Hkv * page_size * D * 2;
   const size_t qo = (size_t)rows * Hq * D * 2;
@@ -332,15 +344,15 @@ extern "C" sv_status rope_kv_append(const void *q, const void *k, const void *v,
   a.k_cache = reinterpret_cast<__nv_bfloat16 *>(k_cache);
   a.v_cache = reinterpret_cast<__nv_bfloat16 *>(v_cache);
 
-  // Two heads a warp while that leaves the SMs fewer than 32 warps each, so a
-  // small step spreads over the device; eight beyond, where a row's angles
+  // One set of heads a warp while that leaves the SMs fewer than 32 warps each,
+  // so a small step spreads over the device; four beyond, where a row's angles
   // serve more heads and more loads are in flight.
-  const int total = Hq + 2 * Hkv;
-  const bool many = (long long)rows * total / 2 > (long long)device_sm_count() * 32;
-  const int per = many ? 8 : 2;
+  const int total = Hq + 2 * Hkv, set = 256 / D;
+  const bool many = (long long)rows * total / set > (long long)device_sm_count() * 32;
+  const int per = set * (many ? 4 : 1);
   const long long tasks = (long long)rows * ((total + per - 1) / per);
   const long long ctas = (tasks + kRopeWarps - 1) / kRopeWarps;
-  if (ctas >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "%s: too many rows", who);
+  if (ctas * kRopeWarps >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "%s: too many rows", who);
   const RopeKernel kernel = x_dtype == SV_F32 ? pick<float>(D, interleaved != 0, many)
                                               : pick<__nv_bfloat16>(D, interleaved != 0, many);
   kernel<<<(unsigned)ctas, kRopeWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
