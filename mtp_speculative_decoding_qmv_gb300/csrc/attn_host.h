@@ -23,6 +23,10 @@ inline sv_status encode_cache(CUtensorMap *map, const void *cache, int D, const 
 size_t tc_partial_bytes(int D);
 unsigned tc_take_give_up();
 sv_status tc_run(int D, const Args &a, cudaStream_t stream);
+// paged_attn_tc256.cu: the same for D 256
+size_t tc256_partial_bytes();
+unsigned tc256_take_give_up();
+sv_status tc256_run(const Args &a, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace sv

@@ -689,7 +689,7 @@ int rows_ctas(int D) { return std::min(kMaxCtas, device_sm_count() * (D == 256 ?
 
 size_t workspace_bytes(int D) {
   size_t part = (size_t)rows_ctas(D) * 2 * 64 * (D + 2) * 4;
-  if (D <= 128) part = std::max(part, tc_partial_bytes(D));
+  part = std::max(part, D == 256 ? tc256_partial_bytes() : tc_partial_bytes(D));
   return kCounterBytes + split_bytes() + part;
 }
 
@@ -700,7 +700,7 @@ unsigned take_device_error_attn() {
   unsigned v = 0, zero = 0;
   cudaMemcpyFromSymbol(&v, attn::g_give_up, sizeof v);
   cudaMemcpyToSymbol(attn::g_give_up, &zero, sizeof zero);
-  return v | attn::tc_take_give_up();
+  return v | attn::tc_take_give_up() | attn::tc256_take_give_up();
 }
 
 }  // namespace sv
@@ -811,9 +811,9 @@ extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // More rows a kv head than a 64-row tile of the streaming kernel holds go to
-  // the tensor-core kernel (its tiles are 128 rows, two at a time).
+  // the tensor-core kernels (their tiles are 128 rows).
   const long long most = (long long)std::min(max_new, rows) * a.G;
-  if (most > 64 && D <= 128) return attn::tc_run(D, a, s);
+  if (most > 64) return D == 256 ? attn::tc256_run(a, s) : attn::tc_run(D, a, s);
   CUtensorMap kmap, vmap;
   sv_status st = attn::encode_cache(&kmap, a.k, D, a, attn::kBK);
   if (st == SV_OK) st = attn::encode_cache(&vmap, a.v, D, a, attn::kBK);

@@ -27,27 +27,15 @@
 
 #include "attn_common.cuh"
 #include "attn_host.h"
+#include "attn_tc.cuh"
 #include "qmv_common.cuh"
 #include "sv_internal.h"
-#include "tc05.cuh"
 
 namespace sv {
 namespace attn {
 namespace {
 
-constexpr int kBK = 128;         // keys per tile
-constexpr int kTile = 128;       // rows per tensor-core tile
-constexpr int kRows = 2 * kTile; // rows per item
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kQueryWarp = 10;  // 10 and 11: a tile each
-// The softmax groups take registers from the third warpgroup (launched at 168 a
-// thread: 256 x 216 + 128 x 72 = 384 x 168).
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
-constexpr uint32_t kTmemCols = 512;
-// An item's cost beside its tiles (queries, the first scores, the last
-// products, the output), in key tiles, when the work is cut into runs.
-constexpr int kItemUnits = 4;
-constexpr float kRescale = 8.f;  // base-2 exponent by which a maximum may lag
+constexpr int kRows = 2 * kTile;  // rows per item
 
 template <int D>
 struct TcShape {
@@ -57,158 +45,8 @@ struct TcShape {
   static constexpr uint32_t kStage = kTile * 128;  // 64 output values of a tile's rows
   static constexpr uint32_t kSmem = (2 + kSlots) * kTileBytes + 2 * kStage + 1024;
   static constexpr uint32_t kOCol = 2 * kBK;  // tensor-memory column of O of tile 0
+  static_assert(kJoin * kTile * 4 <= kStage, "a join's weights");
 };
-
-constexpr uint32_t idesc(int n, bool b_mn_major) {
-  return (1u << 4)                              // D: f32
-         | (1u << 7) | (1u << 10)               // A, B: bf16
-         | (b_mn_major ? 1u << 16 : 0u)         // B with its N index contiguous
-         | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-}
-
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void advance(uint32_t slots) {
-    if (++slot == slots) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
-struct Segment {
-  Request rq;
-  int b, h, r0, count;
-  Span span;
-  int tile0, tiles;           // key tiles [tile0, tile0 + tiles), maybe none
-  long long item;             // first unit of the item
-  int first, n_units, width;  // the segment's units of the item, the item's
-};
-
-__device__ __forceinline__ int row_tiles(const Args &a, const Request &q) {
-  return (int)(((long long)q.n * a.G + kRows - 1) / kRows);
-}
-__device__ __forceinline__ int item_width(const Args &a, const Request &q, int i) {
-  const Span s = rows_span(a, q, i * kRows, min(kRows, q.n * a.G - i * kRows));
-  return (s.hi + kBK - 1) / kBK - s.lo / kBK + kItemUnits;
-}
-__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
-
-// Units of one kv head of a request, by a whole warp.
-__device__ __forceinline__ long long head_units(const Args &a, const Request &q) {
-  const int nt = row_tiles(a, q), lane = threadIdx.x & 31;
-  long long sum = 0;
-  for (int i0 = 0; i0 < nt; i0 += 32)
-    sum += warp_sum_int(i0 + lane < nt ? item_width(a, q, i0 + lane) : 0);
-  return sum;
-}
-
-// Walks a run's segments.  An item is its key tiles and then kItemUnits more; a
-// run that ends among those takes the item to its end, and one that begins
-// there leaves it alone, so only tiles are ever split.  Items are ordered by request, kv head, row tile, so
-// neighbouring CTAs read the same keys at about the same time.  All calls by a
-// whole warp.
-struct Walk {
-  long long u, end, base, per_head, item;
-  int b, h, i, nt, width;
-  Request rq;
-  __device__ void request(const Args &a) {
-    rq = load_request(a, b);
-    nt = row_tiles(a, rq);
-    per_head = head_units(a, rq);
-  }
-  __device__ void start(const Args &a) {  // u, end, base and b are set
-    request(a);
-    const int lane = threadIdx.x & 31;
-    h = (int)((u - base) / per_head);
-    long long rem = u - base - h * per_head;
-    item = base + h * per_head;
-    for (int i0 = 0;; i0 += 32) {
-      const int w = i0 + lane < nt ? item_width(a, rq, i0 + lane) : 0;
-      int upto = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, upto > rem);
-      if (past) {
-        const int src = __ffs(past) - 1;
-        i = i0 + src;
-        width = __shfl_sync(0xffffffffu, w, src);
-        item += __shfl_sync(0xffffffffu, upto, src) - width;
-        return;
-      }
-      const int all = __shfl_sync(0xffffffffu, upto, 31);
-      rem -= all;
-      item += all;
-    }
-  }
-  __device__ bool next(const Args &a, Segment &s) {
-    if (u >= item + max(width - kItemUnits, 1)) u = max(u, item + width);
-    if (u >= end) return false;
-    if (u == item + width) {  // on to the next item
-      item = u;
-      if (++i == nt) {
-        i = 0;
-        if (++h == a.Hkv) {
-          h = 0;
-          base = u;
-          do {
-            ++b;
-            request(a);
-          } while (nt == 0);
-        }
-      }
-      width = item_width(a, rq, i);
-    }
-    s.rq = rq;
-    s.b = b;
-    s.h = h;
-    s.item = item;
-    s.width = width;
-    s.first = (int)(u - item);
-    s.n_units = width - s.first;
-    if (end - u < max(width - kItemUnits, 1) - s.first) s.n_units = (int)(end - u);
-    s.r0 = i * kRows;
-    s.count = min(kRows, rq.n * a.G - s.r0);
-    s.span = rows_span(a, rq, s.r0, s.count);
-    const int t0 = s.span.lo / kBK, t1 = (s.span.hi + kBK - 1) / kBK;
-    s.tile0 = t0 + s.first;
-    s.tiles = max(0, min(t1 - s.tile0, s.n_units));
-    u += s.n_units;
-    return true;
-  }
-};
-
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t d, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-// Uses of registers that a tcgen05.ld fills stay behind its wait.
-__device__ __forceinline__ void pin(uint32_t (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
-                      "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
-}
-__device__ __forceinline__ void group_sync(int wg) {  // the softmax warps of one tile
-  asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
-}
 
 // A split item's partial: sums as [D / 4][rows][4] (a thread owns a row, so
 // accesses of a warp are contiguous), then maxima and sums [rows] each.
@@ -242,53 +80,6 @@ __device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int
       }
     }
   }
-}
-
-// ---- joining split items ------------------------------------------------------
-// The CTAs c0 .. c1 that share an item each leave a partial.  Most often there
-// are two or three, of every row, and the last CTA to arrive joins them while
-// others still work (a launch of its own for it made a 5000-token prompt 290
-// instead of 210 us).  More than kJoin are joined in two rounds, groups of
-// kJoin (the result takes the first member's place) and then the groups, so
-// that no CTA reads more than about kJoin of them.  Partials are always added
-// in CTA order, whichever CTA does it.
-constexpr int kMaxTcCtas = 170;
-constexpr int kJoin = 16;
-static_assert(2 * 3 * kMaxTcCtas * 4 <= kCounterBytes, "counters");
-static_assert(kMaxTcCtas <= kJoin * kJoin && kJoin * kTile * 4 <= 128 * kTile, "weights in the stage");
-struct Group {
-  int first, stride, n;  // CTAs first, first + stride, ..
-  int counter;           // its arrivals, of 3 ctas
-  bool final;            // its result is the item's
-};
-// The group in which CTA c of the item arrives first, or with `again` the
-// groups' own.  `ctas` bounds the CTA numbers.
-__device__ __forceinline__ Group join_group(int c0, int c1, int c, bool again, int ctas) {
-  const int n = c1 - c0 + 1;
-  Group g;
-  if (again) {
-    g.first = c0;
-    g.stride = kJoin;
-    g.n = (n + kJoin - 1) / kJoin;
-    g.counter = 2 * ctas + c0;
-    g.final = true;
-  } else {
-    const int k = (c - c0) / kJoin * kJoin;
-    g.first = c0 + k;
-    g.stride = 1;
-    g.n = min(kJoin, n - k);
-    // a CTA can be first of a group in the item that it ends and in the one
-    // that it begins
-    g.counter = 2 * g.first + (k == 0 ? 1 : 0);
-    g.final = n <= kJoin;
-  }
-  return g;
-}
-// Partial k of the group (see partial_at): an item's first CTA has it in its
-// second place.
-__device__ __forceinline__ int join_slot(const Group &g, int c0, int k) {
-  const int c = g.first + k * g.stride;
-  return 2 * c + (c == c0 ? 1 : 0);
 }
 
 template <int D>
@@ -326,77 +117,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mma_done, 1);
     fence_mbar_init();
   }
-  // ---- this CTA's run of units, and the request that it begins in ----
-  auto block_sum = [&](long long v, long long &upto) {  // inclusive scan and total
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = v;
-    __syncthreads();
-    long long all = 0;
-    upto = v;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) upto += s_scan[i];
-      all += s_scan[i];
-    }
-    return all;
-  };
-  // request tid + b0's units: few row tiles by its thread, more by the warp
-  auto units_of = [&](int b) {
-    const bool real = b < a.B;
-    Request rq = {0, 0, 0};
-    if (real) rq = load_request(a, b);
-    const int nt = real ? row_tiles(a, rq) : 0;
-    long long w = 0;
-    if (nt <= 4)
-      for (int i = 0; i < nt; ++i) w += item_width(a, rq, i);
-    unsigned big = __ballot_sync(0xffffffffu, nt > 4);
-    while (big) {
-      const int src = __ffs(big) - 1;
-      big &= big - 1;
-      Request x;
-      x.q0 = 0;
-      x.n = __shfl_sync(0xffffffffu, rq.n, src);
-      x.len = __shfl_sync(0xffffffffu, rq.len, src);
-      const long long sum = head_units(a, x);
-      if (lane == src) w = sum;
-    }
-    return w * a.Hkv;
-  };
   Runs runs;
-  runs.units = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    long long upto;
-    runs.units += block_sum(units_of(b0 + tid), upto);
-  }
-  runs.ctas = (int)min((long long)gridDim.x, runs.units);
-  const int used = min(max(__ldg(a.q_start + a.B), 0), a.rows);
-  for (int r = used + blockIdx.x; r < a.rows; r += gridDim.x) {  // past the last request: zero
-    for (int i = tid; i < a.Hq * (D / 8); i += kThreads)
-      reinterpret_cast<uint4 *>(a.out + (long long)r * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(long long)r * a.Hq + i] = kNegInf;
-  }
-  if ((int)blockIdx.x >= runs.ctas) return;  // uniform
-  Walk walk;
-  walk.u = runs.begin(blockIdx.x);
-  walk.end = runs.begin(blockIdx.x + 1);
-  long long sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const long long size = units_of(b0 + tid);
-    long long upto;
-    const long long all = block_sum(size, upto);
-    upto += sum;
-    if (upto > walk.u && upto - size <= walk.u) {
-      s_b = b0 + tid;
-      s_base = upto - size;
-    }
-    sum += all;
-    if (sum > walk.u) break;
-  }
+  Walk<kRows> walk;
+  if (!begin_run<kRows, D>(a, s_scan, &s_b, &s_base, runs, walk)) return;  // uniform
   if (warp == kMmaWarp) {
     tmem_alloc(smem_addr(&s_tmem), kTmemCols);
     tmem_relinquish();
@@ -664,6 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = mn;
                 l *= f;
               }
+              // (these scores were issued after the product before the last, so
+              // the barrier is at most one phase behind)
               wait(&o_done[wg], (sn - 1u) & 1u);
               tc_fence_after();
 #pragma unroll 1

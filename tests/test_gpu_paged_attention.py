@@ -237,3 +237,49 @@ def test_large_scores(sv):
     """Scores of some thousands: every weight but the largest underflows."""
     c = Case(64, 2, 1, 16, [80], [2], seed=10, spread=300.0)
     c.check(sv)
+
+
+def _dense(q, k, v, table, page, ctx, n, scale):
+    """One request in float64 on the device: out, lse."""
+    Hq, D = q.shape[1:]
+    Hkv = k.shape[1]
+    held = table[0, :-(-(ctx + n) // page)].long()
+    kk, vv = (t[held].transpose(0, 1).reshape(Hkv, -1, D)[:, :ctx + n].double() for t in (k, v))
+    x = torch.einsum("tgd,gjd->gtj", q.double(), kk.repeat_interleave(Hq // Hkv, 0)) * scale
+    at = torch.arange(ctx + n, device=q.device)
+    x = x.masked_fill(at[None, None, :] > ctx + torch.arange(n, device=q.device)[None, :, None],
+                      -math.inf)
+    out = torch.einsum("gtj,gjd->tgd", x.softmax(-1), vv.repeat_interleave(Hq // Hkv, 0))
+    return out, x.logsumexp(-1).T
+
+
+@pytest.mark.parametrize("D,n,ctx,Hq,Hkv,page", [
+    (64, 600, 9000, 4, 1, 16), (128, 600, 9000, 4, 1, 64), (256, 600, 9000, 4, 1, 16),
+    (256, 300, 20000, 2, 2, 128), (128, 2000, 0, 10, 2, 16), (256, 2000, 0, 10, 2, 32),
+    (256, 70, 40000, 1, 1, 64), (128, 70, 40000, 1, 1, 64)])
+def test_long_chunks(sv, D, n, ctx, Hq, Hkv, page):
+    """Segments of many tiles, where a wait on a wrong phase shows: no wait may
+    give up, and every run gives the same bits."""
+    d = dev()
+    g = torch.Generator(device=d)
+    g.manual_seed(n + ctx + D)
+    held = -(-(ctx + n) // page)
+    k, v = (torch.randn(held, Hkv, page, D, generator=g, device=d, dtype=torch.bfloat16)
+            for _ in range(2))
+    q = torch.randn(n, Hq, D, generator=g, device=d, dtype=torch.bfloat16) * 1.5
+    table = torch.randperm(held, generator=g, device=d).to(torch.int32)[None].contiguous()
+    qs = torch.tensor([0, n], dtype=torch.int32, device=d)
+    kl = torch.tensor([ctx + n], dtype=torch.int32, device=d)
+    lse = torch.empty(n, Hq, device=d)
+    ws = sv.make_attention_workspace(D, d)
+    scale = 1.0 / math.sqrt(D)
+    out = sv.paged_attention(q, k, v, table, qs, kl, n, lse=lse, workspace=ws)[0].clone()
+    sv.device_status()
+    for _ in range(10):
+        assert torch.equal(sv.paged_attention(q, k, v, table, qs, kl, n, workspace=ws)[0], out)
+    sv.device_status()
+    want, want_lse = _dense(q, k, v, table, page, ctx, n, scale)
+    # weights and outputs are rounded to bf16 (2^-8 at most each, in norm as well)
+    assert float((out.double() - want).norm() / want.norm()) < 2 * ref.HALF_BF16
+    # scores of magnitude 10: D fp32 sums, the exponential's 2^-21, 20000 sums
+    assert float((lse.double() - want_lse).abs().max()) < 10 * (D + 4) * 2.0 ** -24 + 2.0 ** -9
