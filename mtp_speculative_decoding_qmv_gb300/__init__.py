@@ -650,19 +650,19 @@ class KvStep(NamedTuple):
     err_flags: torch.Tensor  # [B]
 
 
-def _fits(t, name, dtype, shape, dev, index):
-    """_need, with one test for a tensor that is as it should be: a decode loop
-    makes these calls every few microseconds."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        _need(t, name, dtype, shape, dev)
-
-
-def _out(t, name, dtype, shape, dev, index):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _fits(t, name, dtype, shape, dev, index)
-    return t
+def _fit(dev, index, *wanted):
+    """_need for each (tensor, name, dtype, shape), in one pass over tensors that
+    are as they should be: a decode loop makes these calls every few
+    microseconds."""
+    try:
+        for t, name, dtype, shape in wanted:
+            if (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()
+                    or (shape is not None and t.shape != shape)):
+                _need(t, name, dtype, shape, dev)
+    except AttributeError:  # not a tensor
+        for t, name, dtype, shape in wanted:
+            _need(t, name, dtype, shape, dev)
+        raise
 
 
 def _on(t: torch.Tensor, name: str) -> int:
@@ -684,6 +684,11 @@ def _call(index: int, where: str, fn, *args) -> None:
         _check(st, where)
 
 
+_STEP_NAMES = ("length_out", "held_out", "cursor_out", "q_start", "kv_len", "slots", "positions",
+               "err_flags")
+_STEP_TYPES = (torch.int32,) * 8
+
+
 def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor,
                   ring: torch.Tensor, block_table: torch.Tensor, n_new: torch.Tensor,
                   page_size: int, rows: int, *, n_commit: torch.Tensor | None = None,
@@ -699,26 +704,23 @@ def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor
     dev, i32 = length.device, torch.int32
     index = _on(length, "length")
     B, max_pages = block_table.shape
-    per, rows = (B,), int(rows)
-    _fits(length, "length", i32, per, dev, index)
-    _fits(held, "held", i32, per, dev, index)
-    _fits(cursor, "cursor", i32, (2,), dev, index)
-    _fits(ring, "ring", i32, None, dev, index)
-    _fits(block_table, "block_table", i32, None, dev, index)
-    _fits(n_new, "n_new", i32, per, dev, index)
+    per, two, rows = (B,), (2,), int(rows)
+    each = (max(rows, 0),)
+    _fit(dev, index, (length, "length", i32, per), (held, "held", i32, per),
+         (cursor, "cursor", i32, two), (ring, "ring", i32, None),
+         (block_table, "block_table", i32, None), (n_new, "n_new", i32, per))
     commit, n = None, 0
     if n_commit is not None:
-        _fits(n_commit, "n_commit", i32, None, dev, index)
+        _fit(dev, index, (n_commit, "n_commit", i32, None))
         commit, n = n_commit.data_ptr(), n_commit.numel()
-    each = (max(rows, 0),)
-    step = KvStep(_out(length_out, "length_out", i32, per, dev, index),
-                  _out(held_out, "held_out", i32, per, dev, index),
-                  _out(cursor_out, "cursor_out", i32, (2,), dev, index),
-                  _out(q_start, "q_start", i32, (B + 1,), dev, index),
-                  _out(kv_len, "kv_len", i32, per, dev, index),
-                  _out(slots, "slots", i32, each, dev, index),
-                  _out(positions, "positions", i32, each, dev, index),
-                  _out(err_flags, "err_flags", i32, per, dev, index))
+    step = (length_out, held_out, cursor_out, q_start, kv_len, slots, positions, err_flags)
+    shapes = (per, per, two, (B + 1,), per, each, each, per)
+    if (length_out is None or held_out is None or cursor_out is None or q_start is None
+            or kv_len is None or slots is None or positions is None or err_flags is None):
+        step = tuple(torch.empty(shape, dtype=i32, device=dev) if t is None else t
+                     for t, shape in zip(step, shapes))
+    _fit(dev, index, *zip(step, _STEP_NAMES, _STEP_TYPES, shapes))
+    step = KvStep(*step)
     _call(index, "kv_pages_step", lib().kv_pages_step, length.data_ptr(), held.data_ptr(),
           cursor.data_ptr(), n_new.data_ptr(), commit, n, int(n_commit_bias), B, int(page_size),
           max_pages, ring.numel(), rows, block_table.data_ptr(), ring.data_ptr(),
@@ -747,12 +749,13 @@ def _need_rows(t: torch.Tensor, name: str, dtype, heads: int, D: int, dev, index
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads}, {D})")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != D):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (rows, {heads}, {D})")
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if t.shape[0] > 1 else heads * D
+    return row if shape[0] > 1 else heads * D
 
 
 def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -771,8 +774,8 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
         raise ValueError("q must be [rows, Hq, D] and the caches [pages, Hkv, page_size, D]")
     index = _on(q, "q")
     rows, Hq, D = q.shape
-    cache = k_cache.shape
-    pages, Hkv, page_size, _ = cache
+    pages, Hkv, page_size, _ = k_cache.shape
+    cache = (pages, Hkv, page_size, D)
     dtype = q.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("q, k and v must be float32 or bfloat16")
@@ -781,30 +784,30 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     vs = _need_rows(v, "v", dtype, Hkv, D, dev, index)
     if k.shape[0] != rows or v.shape[0] != rows:
         raise ValueError("q, k and v must have the same rows")
-    cache = (pages, Hkv, page_size, D)
-    _fits(k_cache, "k_cache", torch.bfloat16, cache, dev, index)
-    _fits(v_cache, "v_cache", torch.bfloat16, cache, dev, index)
     axes = 1 if positions.dim() == 1 else positions.shape[-1]
-    _fits(positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes),
-          dev, index)
-    _fits(slots, "slots", torch.int32, (rows,), dev, index)
+    if q_out is None:
+        q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
+    _fit(dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
+         (v_cache, "v_cache", torch.bfloat16, cache),
+         (positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes)),
+         (slots, "slots", torch.int32, (rows,)),
+         (q_out, "q_out", torch.bfloat16, (rows, Hq, D)))
     half, words = 0, None
     if freqs is not None:
+        _fit(dev, index, (freqs, "freqs", torch.int64, None))
         if freqs.dim() != 1:
             raise ValueError("freqs must be [rotary_dim / 2]")
-        _fits(freqs, "freqs", torch.int64, None, dev, index)
         half, words = freqs.numel(), freqs.data_ptr()
     ax = qw = kw = None
     if axis is not None:
-        _fits(axis, "axis", torch.uint8, (half,), dev, index)
+        _fit(dev, index, (axis, "axis", torch.uint8, (half,)))
         ax = axis.data_ptr()
     if q_weight is not None:
-        _fits(q_weight, "q_weight", torch.float32, (D,), dev, index)
+        _fit(dev, index, (q_weight, "q_weight", torch.float32, (D,)))
         qw = q_weight.data_ptr()
     if k_weight is not None:
-        _fits(k_weight, "k_weight", torch.float32, (D,), dev, index)
+        _fit(dev, index, (k_weight, "k_weight", torch.float32, (D,)))
         kw = k_weight.data_ptr()
-    q_out = _out(q_out, "q_out", torch.bfloat16, (rows, Hq, D), dev, index)
     _call(index, "rope_kv_append", lib().rope_kv_append, q.data_ptr(), k.data_ptr(),
           v.data_ptr(), SV_BF16 if dtype is torch.bfloat16 else SV_F32, qs, ks, vs,
           positions.data_ptr(), axes, slots.data_ptr(), words, ax, qw, kw, float(eps), rows, Hq,
@@ -847,26 +850,25 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     index = _on(q, "q")
     rows, Hq, D = q.shape
     pages, Hkv, page_size, _ = k_cache.shape
+    cache = (pages, Hkv, page_size, D)
     B, max_pages = block_table.shape
     qs = _need_rows(q, "q", torch.bfloat16, Hq, D, dev, index)
-    cache = (pages, Hkv, page_size, D)
-    _fits(k_cache, "k_cache", torch.bfloat16, cache, dev, index)
-    _fits(v_cache, "v_cache", torch.bfloat16, cache, dev, index)
-    _fits(block_table, "block_table", torch.int32, None, dev, index)
-    _fits(q_start, "q_start", torch.int32, (B + 1,), dev, index)
-    _fits(kv_len, "kv_len", torch.int32, (B,), dev, index)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
     os_ = _need_rows(out, "out", torch.bfloat16, Hq, D, dev, index)
     if out.shape[0] != rows:
         raise ValueError("q and out must have the same rows")
-    lse_ptr = None
-    if lse is not None:
-        _fits(lse, "lse", torch.float32, (rows, Hq), dev, index)
-        lse_ptr = lse.data_ptr()
     if workspace is None:
         workspace = make_attention_workspace(D, dev)
-    _fits(workspace, "workspace", torch.uint8, None, dev, index)
+    _fit(dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
+         (v_cache, "v_cache", torch.bfloat16, cache),
+         (block_table, "block_table", torch.int32, None),
+         (q_start, "q_start", torch.int32, (B + 1,)), (kv_len, "kv_len", torch.int32, (B,)),
+         (workspace, "workspace", torch.uint8, None))
+    lse_ptr = None
+    if lse is not None:
+        _fit(dev, index, (lse, "lse", torch.float32, (rows, Hq)))
+        lse_ptr = lse.data_ptr()
     _call(index, "paged_attention", lib().paged_attention, q.data_ptr(), qs, k_cache.data_ptr(),
           v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), B,
           rows, int(max_new), Hq, Hkv, D, page_size, pages, max_pages,
