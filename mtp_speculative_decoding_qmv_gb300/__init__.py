@@ -17,6 +17,7 @@ the library is missing, every call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 from pathlib import Path
 from typing import NamedTuple
@@ -650,19 +651,32 @@ class KvStep(NamedTuple):
     err_flags: torch.Tensor  # [B]
 
 
+_checks = None
+
+
+def _load_checks():
+    """The compiled tensor checks; raises if they have not been built."""
+    global _checks
+    if _checks is None:
+        try:
+            built = importlib.import_module("._tensors", __name__)
+        except ImportError as e:
+            raise RuntimeError("_tensors.so is not built; run `python -m "
+                               "mtp_speculative_decoding_qmv_gb300.build` (or "
+                               "__graft_entry__.build())") from e
+        _checks = built
+    return _checks
+
+
 def _fit(dev, index, *wanted):
-    """_need for each (tensor, name, dtype, shape), in one pass over tensors that
-    are as they should be: a decode loop makes these calls every few
-    microseconds."""
-    try:
-        for t, name, dtype, shape in wanted:
-            if (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()
-                    or (shape is not None and t.shape != shape)):
-                _need(t, name, dtype, shape, dev)
-    except AttributeError:  # not a tensor
+    """Addresses of the tensors of (tensor, name, dtype, shape or None), each as
+    _need wants it."""
+    at = (_checks or _load_checks()).fit(index, *wanted)
+    if at is None:
         for t, name, dtype, shape in wanted:
             _need(t, name, dtype, shape, dev)
-        raise
+        raise RuntimeError("a tensor was refused")  # not reached: one of them raised
+    return at
 
 
 def _on(t: torch.Tensor, name: str) -> int:
@@ -675,7 +689,7 @@ def _on(t: torch.Tensor, name: str) -> int:
 
 def _call(index: int, where: str, fn, *args) -> None:
     """fn(*args, current stream of the device), with that device current."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -706,26 +720,24 @@ def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor
     B, max_pages = block_table.shape
     per, two, rows = (B,), (2,), int(rows)
     each = (max(rows, 0),)
-    _fit(dev, index, (length, "length", i32, per), (held, "held", i32, per),
-         (cursor, "cursor", i32, two), (ring, "ring", i32, None),
-         (block_table, "block_table", i32, None), (n_new, "n_new", i32, per))
+    state = _fit(dev, index, (length, "length", i32, per), (held, "held", i32, per),
+                 (cursor, "cursor", i32, two), (n_new, "n_new", i32, per),
+                 (ring, "ring", i32, None), (block_table, "block_table", i32, None))
     commit, n = None, 0
     if n_commit is not None:
-        _fit(dev, index, (n_commit, "n_commit", i32, None))
-        commit, n = n_commit.data_ptr(), n_commit.numel()
+        commit, = _fit(dev, index, (n_commit, "n_commit", i32, None))
+        n = n_commit.numel()
     step = (length_out, held_out, cursor_out, q_start, kv_len, slots, positions, err_flags)
     shapes = (per, per, two, (B + 1,), per, each, each, per)
     if (length_out is None or held_out is None or cursor_out is None or q_start is None
             or kv_len is None or slots is None or positions is None or err_flags is None):
         step = tuple(torch.empty(shape, dtype=i32, device=dev) if t is None else t
                      for t, shape in zip(step, shapes))
-    _fit(dev, index, *zip(step, _STEP_NAMES, _STEP_TYPES, shapes))
-    step = KvStep(*step)
-    _call(index, "kv_pages_step", lib().kv_pages_step, length.data_ptr(), held.data_ptr(),
-          cursor.data_ptr(), n_new.data_ptr(), commit, n, int(n_commit_bias), B, int(page_size),
-          max_pages, ring.numel(), rows, block_table.data_ptr(), ring.data_ptr(),
-          *[t.data_ptr() for t in step])
-    return step
+    at = _fit(dev, index, *zip(step, _STEP_NAMES, _STEP_TYPES, shapes))
+    _call(index, "kv_pages_step", lib().kv_pages_step, *state[:4], commit, n,
+          int(n_commit_bias), B, int(page_size), max_pages, ring.numel(), rows, state[5],
+          state[4], *at)
+    return KvStep(*step)
 
 
 def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:
@@ -741,21 +753,20 @@ def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:
     return (high.to(torch.int64) << 32) + low.to(torch.int64)
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype, heads: int, D: int, dev, index: int) -> int:
-    """Packed rows [rows, heads, D] with contiguous heads; returns the row stride."""
+def _need_rows(t: torch.Tensor, name: str, dtype, rows: int, heads: int, D: int, dev, index: int):
+    """Packed rows [rows, heads, D] with contiguous heads: address, row stride."""
+    at = (_checks or _load_checks()).fit_rows(index, t, dtype, rows, heads, D)
+    if at is not None:
+        return at
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected (rows, {heads}, {D})")
-    row, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != D):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return row if shape[0] > 1 else heads * D
+    if tuple(t.shape) != (rows, heads, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {heads}, {D})")
+    raise ValueError(f"{name}: the heads of a row must be contiguous")
 
 
 def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -779,40 +790,35 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     dtype = q.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("q, k and v must be float32 or bfloat16")
-    qs = _need_rows(q, "q", dtype, Hq, D, dev, index)
-    ks = _need_rows(k, "k", dtype, Hkv, D, dev, index)
-    vs = _need_rows(v, "v", dtype, Hkv, D, dev, index)
-    if k.shape[0] != rows or v.shape[0] != rows:
-        raise ValueError("q, k and v must have the same rows")
-    axes = 1 if positions.dim() == 1 else positions.shape[-1]
+    q_at, qs = _need_rows(q, "q", dtype, rows, Hq, D, dev, index)
+    k_at, ks = _need_rows(k, "k", dtype, rows, Hkv, D, dev, index)
+    v_at, vs = _need_rows(v, "v", dtype, rows, Hkv, D, dev, index)
+    cache = (pages, Hkv, page_size, D)
+    one_axis = positions.dim() == 1
+    axes = 1 if one_axis else positions.shape[-1]
     if q_out is None:
         q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
-    _fit(dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
-         (v_cache, "v_cache", torch.bfloat16, cache),
-         (positions, "positions", torch.int32, (rows,) if positions.dim() == 1 else (rows, axes)),
-         (slots, "slots", torch.int32, (rows,)),
-         (q_out, "q_out", torch.bfloat16, (rows, Hq, D)))
-    half, words = 0, None
+    pos_at, slots_at, q_out_at, kc_at, vc_at = _fit(
+        dev, index, (positions, "positions", torch.int32, (rows,) if one_axis else (rows, axes)),
+        (slots, "slots", torch.int32, (rows,)),
+        (q_out, "q_out", torch.bfloat16, (rows, Hq, D)),
+        (k_cache, "k_cache", torch.bfloat16, cache), (v_cache, "v_cache", torch.bfloat16, cache))
+    half, words, ax, qw, kw = 0, None, None, None, None
     if freqs is not None:
-        _fit(dev, index, (freqs, "freqs", torch.int64, None))
+        words, = _fit(dev, index, (freqs, "freqs", torch.int64, None))
         if freqs.dim() != 1:
             raise ValueError("freqs must be [rotary_dim / 2]")
-        half, words = freqs.numel(), freqs.data_ptr()
-    ax = qw = kw = None
+        half = freqs.numel()
     if axis is not None:
-        _fit(dev, index, (axis, "axis", torch.uint8, (half,)))
-        ax = axis.data_ptr()
+        ax, = _fit(dev, index, (axis, "axis", torch.uint8, (half,)))
     if q_weight is not None:
-        _fit(dev, index, (q_weight, "q_weight", torch.float32, (D,)))
-        qw = q_weight.data_ptr()
+        qw, = _fit(dev, index, (q_weight, "q_weight", torch.float32, (D,)))
     if k_weight is not None:
-        _fit(dev, index, (k_weight, "k_weight", torch.float32, (D,)))
-        kw = k_weight.data_ptr()
-    _call(index, "rope_kv_append", lib().rope_kv_append, q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), SV_BF16 if dtype is torch.bfloat16 else SV_F32, qs, ks, vs,
-          positions.data_ptr(), axes, slots.data_ptr(), words, ax, qw, kw, float(eps), rows, Hq,
-          Hkv, D, 2 * half, 1 if interleaved else 0, page_size, pages, q_out.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr())
+        kw, = _fit(dev, index, (k_weight, "k_weight", torch.float32, (D,)))
+    _call(index, "rope_kv_append", lib().rope_kv_append, q_at, k_at, v_at,
+          SV_BF16 if dtype is torch.bfloat16 else SV_F32, qs, ks, vs, pos_at, axes, slots_at,
+          words, ax, qw, kw, float(eps), rows, Hq, Hkv, D, 2 * half, 1 if interleaved else 0,
+          page_size, pages, q_out_at, kc_at, vc_at)
     return q_out
 
 
@@ -852,26 +858,24 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     pages, Hkv, page_size, _ = k_cache.shape
     cache = (pages, Hkv, page_size, D)
     B, max_pages = block_table.shape
-    qs = _need_rows(q, "q", torch.bfloat16, Hq, D, dev, index)
+    cache = (pages, Hkv, page_size, D)
     if out is None:
         out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
-    os_ = _need_rows(out, "out", torch.bfloat16, Hq, D, dev, index)
-    if out.shape[0] != rows:
-        raise ValueError("q and out must have the same rows")
     if workspace is None:
         workspace = make_attention_workspace(D, dev)
-    _fit(dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
-         (v_cache, "v_cache", torch.bfloat16, cache),
-         (block_table, "block_table", torch.int32, None),
-         (q_start, "q_start", torch.int32, (B + 1,)), (kv_len, "kv_len", torch.int32, (B,)),
-         (workspace, "workspace", torch.uint8, None))
-    lse_ptr = None
+    q_at, qs = _need_rows(q, "q", torch.bfloat16, rows, Hq, D, dev, index)
+    out_at, outs = _need_rows(out, "out", torch.bfloat16, rows, Hq, D, dev, index)
+    kc_at, vc_at, table_at, start_at, len_at, ws_at = _fit(
+        dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
+        (v_cache, "v_cache", torch.bfloat16, cache),
+        (block_table, "block_table", torch.int32, None),
+        (q_start, "q_start", torch.int32, (B + 1,)), (kv_len, "kv_len", torch.int32, (B,)),
+        (workspace, "workspace", torch.uint8, None))
+    lse_at = None
     if lse is not None:
-        _fit(dev, index, (lse, "lse", torch.float32, (rows, Hq)))
-        lse_ptr = lse.data_ptr()
-    _call(index, "paged_attention", lib().paged_attention, q.data_ptr(), qs, k_cache.data_ptr(),
-          v_cache.data_ptr(), block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), B,
-          rows, int(max_new), Hq, Hkv, D, page_size, pages, max_pages,
-          1.0 / math.sqrt(D) if scale is None else float(scale), int(window), out.data_ptr(), os_,
-          lse_ptr, workspace.data_ptr(), workspace.numel())
+        lse_at, = _fit(dev, index, (lse, "lse", torch.float32, (rows, Hq)))
+    _call(index, "paged_attention", lib().paged_attention, q_at, qs, kc_at, vc_at, table_at,
+          start_at, len_at, B, rows, int(max_new), Hq, Hkv, D, page_size, pages, max_pages,
+          1.0 / math.sqrt(D) if scale is None else float(scale), int(window), out_at, outs,
+          lse_at, ws_at, workspace.numel())
     return out, lse

@@ -1,7 +1,8 @@
 """Builds libspecverify.so (sm_103a) in-tree with nvcc.
 
 Each CUDA translation unit is compiled in parallel, then linked into one
-shared library next to this file.  Usage: ``python -m
+shared library next to this file; beside them g++ compiles the bindings' tensor
+checks (``csrc/tensors.cpp``, against the installed torch's headers).  Usage: ``python -m
 mtp_speculative_decoding_qmv_gb300.build [--force] [--debug]``.
 """
 from __future__ import annotations
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -20,6 +22,8 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libspecverify.so"
+CHECKS = PKG / "_tensors.so"
+CUDA = "/usr/local/cuda"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -41,10 +45,32 @@ def _stale(target: Path, deps: list[Path]) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def build_checks() -> None:
+    """The CPython extension of csrc/tensors.cpp."""
+    import torch
+
+    src = CSRC / "tensors.cpp"
+    root = Path(torch.__file__).parent
+    tmp = CHECKS.with_suffix(".so.tmp")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
+           "-I" + sysconfig.get_paths()["include"], f"-I{CUDA}/include", str(src), "-o", str(tmp),
+           f"-L{root / 'lib'}", f"-Wl,-rpath,{root / 'lib'}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src.name}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CHECKS)
+
+
 def build(force: bool = False, debug: bool = False, verbose: bool = False) -> Path:
     headers = list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
     srcs = sources()
+    checks = force or _stale(CHECKS, [CSRC / "tensors.cpp", Path(__file__)])
     if not force and not _stale(LIB, srcs + headers + [Path(__file__)]):
+        if checks:
+            build_checks()
         return LIB
     BUILD.mkdir(exist_ok=True)
     flags = ARCH + ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -66,7 +92,10 @@ def build(force: bool = False, debug: bool = False, verbose: bool = False) -> Pa
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        extension = ex.submit(build_checks) if checks else None
         objs = list(ex.map(compile_one, srcs))
+        if extension:
+            extension.result()
     tmp = LIB.with_suffix(".so.tmp")
     cmd = [cc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
