@@ -21,7 +21,10 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
 // An item's cost beside its tiles (queries, the first scores, the last
 // products, the output), in key tiles, when the work is cut into runs.
-constexpr int kItemUnits = 4;
+constexpr int kItemUnits = 3;
+// Items of at most so many key tiles are not split: writing and joining partials
+// costs about eight tiles' time, half an item is the most it could even out.
+constexpr int kWholeTiles = 8;
 constexpr float kRescale = 8.f;  // base-2 exponent by which a maximum may lag
 
 constexpr uint32_t idesc(int n, bool b_mn_major) {
@@ -73,7 +76,8 @@ __device__ __forceinline__ long long head_units(const Args &a, const Request &q)
 
 // Walks a run's segments.  An item is its key tiles and then kItemUnits more; a
 // run that ends among those takes the item to its end, and one that begins
-// there leaves it alone, so only tiles are ever split.  Items are ordered by
+// there leaves it alone, so only tiles are ever split; an item of few tiles goes
+// as a whole to the run on the side of its larger part.  Items are ordered by
 // request, kv head, row tile, so neighbouring CTAs read the same keys at about
 // the same time.  All calls by a whole warp.
 template <int kRows>
@@ -106,15 +110,20 @@ struct Walk {
         i = i0 + src;
         width = __shfl_sync(0xffffffffu, w, src);
         item += __shfl_sync(0xffffffffu, upto, src) - width;
-        return;
+        break;
       }
       const int all = __shfl_sync(0xffffffffu, upto, 31);
       rem -= all;
       item += all;
     }
+    const int tiles = max(width - kItemUnits, 1);
+    const long long at = u - item;
+    if (at >= tiles || (tiles <= kWholeTiles && 2 * at > tiles))
+      u = item + width;
+    else if (tiles <= kWholeTiles)
+      u = item;
   }
   __device__ bool next(const Args &a, Segment &s) {
-    if (u >= item + max(width - kItemUnits, 1)) u = max(u, item + width);
     if (u >= end) return false;
     if (u == item + width) {  // on to the next item
       item = u;
@@ -138,7 +147,15 @@ struct Walk {
     s.width = width;
     s.first = (int)(u - item);
     s.n_units = width - s.first;
-    if (end - u < max(width - kItemUnits, 1) - s.first) s.n_units = (int)(end - u);
+    const int tiles = max(width - kItemUnits, 1);
+    if (end - u < tiles - s.first) {  // the run ends among its tiles
+      if (tiles > kWholeTiles) {
+        s.n_units = (int)(end - u);
+      } else if (2 * (end - item) <= tiles) {
+        u = end;
+        return false;
+      }
+    }
     s.r0 = i * kRows;
     s.count = min(kRows, rq.n * a.G - s.r0);
     s.span = rows_span(a, rq, s.r0, s.count);
@@ -225,10 +242,12 @@ __device__ __forceinline__ bool begin_run(const Args &a, long long *s_scan, int 
     }
     return w * a.Hkv;
   };
-  runs.units = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    long long upto;
-    runs.units += block_sum(units_of(b0 + tid), upto);
+  long long size = units_of(tid), upto;  // the first block of requests, kept for the search
+  long long all = block_sum(size, upto);
+  runs.units = all;
+  for (int b0 = kThreads; b0 < a.B; b0 += kThreads) {
+    long long past;
+    runs.units += block_sum(units_of(b0 + tid), past);
   }
   runs.ctas = (int)min((long long)gridDim.x, runs.units);
   const int used = min(max(__ldg(a.q_start + a.B), 0), a.rows);
@@ -241,18 +260,17 @@ __device__ __forceinline__ bool begin_run(const Args &a, long long *s_scan, int 
   if ((int)blockIdx.x >= runs.ctas) return false;  // uniform
   walk.u = runs.begin(blockIdx.x);
   walk.end = runs.begin(blockIdx.x + 1);
-  long long sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const long long size = units_of(b0 + tid);
-    long long upto;
-    const long long all = block_sum(size, upto);
-    upto += sum;
-    if (upto > walk.u && upto - size <= walk.u) {
+  long long before = 0;  // units of the blocks of requests already searched
+  for (int b0 = 0;;) {
+    if (before + upto > walk.u && before + upto - size <= walk.u) {
       *s_b = b0 + tid;
-      *s_base = upto - size;
+      *s_base = before + upto - size;
     }
-    sum += all;
-    if (sum > walk.u) break;
+    b0 += kThreads;
+    if (b0 >= a.B) break;
+    before += all;
+    size = units_of(b0 + tid);
+    all = block_sum(size, upto);
   }
   return true;
 }
