@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring ring;
     uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of q_full and p_full
     auto wait = [&](uint64_t *bar, uint32_t phase) {
-      if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
+      if (!__all_sync(0xffffffffu, mbar_test(bar, phase)) && !dead)
+        dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
       tc_fence_after();
     };
     const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(ring0),
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring ring;  // of the segment's first key slot
     uint32_t sn = 0;  // key tiles done by this group
     auto wait = [&](uint64_t *bar, uint32_t phase) {
-      if (!dead && !mbar_wait(bar, phase)) {
+      if (!mbar_test(bar, phase) && !dead && !mbar_wait(bar, phase)) {
         dead = true;
         report_give_up(16u);
       }

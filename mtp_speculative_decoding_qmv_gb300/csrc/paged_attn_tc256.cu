@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool leader = elect_one();
       uint32_t g = 0, sn = 0, qn = 0;  // block groups and key tiles so far, phase of q_full
       auto wait = [&](uint64_t *bar, uint32_t phase) {
-        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
+        if (!__all_sync(0xffffffffu, mbar_test(bar, phase)) && !dead)
+          dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
         tc_fence_after();
       };
       const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(ring0),
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     uint32_t g0 = 0, sn = 0;  // block groups of the segments before, key tiles so far
     auto wait = [&](uint64_t *bar, uint32_t phase) {
-      if (!dead && !mbar_wait(bar, phase)) {
+      if (!mbar_test(bar, phase) && !dead && !mbar_wait(bar, phase)) {
         dead = true;
         report_give_up(16u);
       }
