@@ -78,6 +78,23 @@ __device__ __forceinline__ void widen(const uint32_t (&x)[W], float (&y)[N]) {
   }
 }
 
+// Two fp32 operations in one instruction, each rounded as the scalar one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
@@ -91,7 +108,8 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16 *p, const float (&x)[N]
 }
 
 template <typename T, int D, bool kPairs, int kIter>
-__global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 4 ? 5 : 6)
+    rope_append_kernel(const RopeArgs a) {
   constexpr int E = 8;                        // elements a lane holds
   constexpr int W = E * (int)sizeof(T) / 4;
   constexpr int kLanes = D / E, kSet = 32 / kLanes;  // lanes a head, heads a set
@@ -197,15 +215,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_append_kernel(const R
       }
       held = weights;
       if (a.q_weight || a.k_weight) {  // the same for the warp
-        float ss = 0.f;
+        float2 two = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = make_float2(x[e], x[e + 1]);
+          two = fma2(v, v, two);
+        }
+        float ss = two.x + two.y;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = rsqrtf(ss * (1.f / D) + a.eps);
         if (weights) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = x[e] * r * w[e];
+          for (int e = 0; e < E; e += 2) {
+            const float2 v = mul2(mul2(make_float2(x[e], x[e + 1]), make_float2(r, r)),
+                                  make_float2(w[e], w[e + 1]));
+            x[e] = v.x;
+            x[e + 1] = v.y;
+          }
         }
       }
       float y[E];
@@ -218,7 +245,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 6) rope_append_kernel(const R
       }
       if (turned && !value) {  // else as it is, infinities included
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(y[e], sn[e], x[e] * cs[e]);
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = fma2(make_float2(y[e], y[e + 1]), make_float2(sn[e], sn[e + 1]),
+                                mul2(make_float2(x[e], x[e + 1]), make_float2(cs[e], cs[e + 1])));
+          x[e] = v.x;
+          x[e + 1] = v.y;
+        }
       }
     }
     if (h < a.Hq)
