@@ -594,10 +594,10 @@ sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x
  * more rows is still computed.  Scores, sums and outputs are fp32, weights
  * are rounded to bf16 before they multiply the values, out once at the end.
  * Results do not depend on the run (no floating-point atomics).
- * Requires Hq a multiple of Hkv; D 64, 128 or 256; scale positive and finite;
- * window >= 0; (num_pages + 1) * Hkv * page_size below 2^31; q, out and the
- * caches 16-byte aligned, row strides multiples of 8 elements; no output
- * overlaps an input.
+ * Requires Hq a multiple of Hkv; D 64, 128 or 256; 0 < scale <= 2e38;
+ * window >= 0; (num_pages + 1) * Hkv * page_size and max_pages * page_size +
+ * rows + 256 below 2^31; q, out and the caches 16-byte aligned, row strides
+ * multiples of 8 elements; no output overlaps an input.
  * workspace: paged_attention_workspace_bytes(D) bytes on the current device
  * (0 on an unsupported D), 256-byte aligned, its first 4096 bytes zero before
  * its first call (every call leaves them zero); it serves calls of any shape

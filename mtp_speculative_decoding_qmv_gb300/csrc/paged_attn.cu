@@ -737,11 +737,11 @@ extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
     return fail(SV_ERR_UNSUPPORTED, "%s: page_size=%d is not 16, 32, 64, 128 or 256", who,
                 page_size);
-  if (!(scale > 0.f) || scale > 3.0e38f)
+  if (!(scale > 0.f) || scale > 2.0e38f)  // times log2(e) finite as well
     return fail(SV_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
   if (window < 0) return fail(SV_ERR_INVALID_ARG, "%s: window must be >= 0", who);
   if (((long long)num_pages + 1) * Hkv * page_size >= (1ll << 31) ||
-      (long long)max_pages * page_size + 256 >= (1ll << 31))
+      (long long)max_pages * page_size + rows + 256 >= (1ll << 31))
     return fail(SV_ERR_UNSUPPORTED, "%s: cache rows or positions pass 31 bits", who);
   if ((long long)rows * (Hq / Hkv) + 256 >= (1ll << 31) || Hq > 65536)
     return fail(SV_ERR_UNSUPPORTED, "%s: too many rows or heads", who);
@@ -801,7 +801,8 @@ extern "C" sv_status paged_attention(const uint16_t *q, long long q_row_stride,
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   while ((1 << a.page_shift) < page_size) ++a.page_shift;
-  a.window = window;
+  // a window of every position is none (and positions minus it stay in 32 bits)
+  a.window = window >= max_pages * page_size ? 0 : window;
   a.scale = scale;
   a.scale_log2 = scale * 1.44269504088896340736f;
   uint8_t *ws = static_cast<uint8_t *>(workspace);

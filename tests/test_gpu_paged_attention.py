@@ -283,3 +283,21 @@ def test_long_chunks(sv, D, n, ctx, Hq, Hkv, page):
     assert float((out.double() - want).norm() / want.norm()) < 2 * ref.HALF_BF16
     # scores of magnitude 10: D fp32 sums, the exponential's 2^-21, 20000 sums
     assert float((lse.double() - want_lse).abs().max()) < 10 * (D + 4) * 2.0 ** -24 + 2.0 ** -9
+
+
+@pytest.mark.parametrize("D,most", [(64, 2), (128, 2), (256, 1), (64, 40), (128, 40), (256, 40)])
+def test_more_requests_than_threads(sv, D, most):
+    """The search for a CTA's first request goes on in the next block of them."""
+    rng = np.random.default_rng(D + most)
+    B = 900
+    lens = rng.integers(0, 60, B).tolist()
+    news = [int(min(n, rng.integers(0, most + 1))) for n in lens]
+    lens[500], news[500] = 700, most
+    Case(D, 2, 1, 16, lens, news, seed=most).check(sv, max_new=100 if most > 2 else None)
+
+
+@pytest.mark.parametrize("D,news", [(64, [7, 3]), (128, [90, 3]), (256, [90, 7])])
+def test_the_widest_window_is_none(sv, D, news):
+    c = Case(D, 4, 2, 16, [40, 5], news, seed=11)
+    c.check(sv, 2 ** 31 - 1)
+    c.check(sv, 45)

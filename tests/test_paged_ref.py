@@ -162,7 +162,8 @@ def _attend(L, q=A, qs=1024, kc=A + M, vc=A + 2 * M, table=A + 3 * M, q_start=A 
     ({"pages": 0}, 1), ({"max_pages": 0}, 1), ({"D": 80}, 2), ({"page": 20}, 2),
     ({"scale": 0.0}, 1), ({"scale": -1.0}, 1), ({"scale": float("inf")}, 1),
     ({"scale": float("nan")}, 1), ({"window": -1}, 1), ({"pages": 1 << 26}, 2),
-    ({"max_pages": 1 << 27}, 2), ({"rows": 1 << 30}, 2), ({"q": 0}, 1), ({"ws": 0}, 1),
+    ({"max_pages": 1 << 27}, 2), ({"rows": 1 << 30}, 2), ({"max_pages": (1 << 27) - 17, "rows": 16}, 2),
+    ({"scale": 2.5e38}, 1), ({"q": 0}, 1), ({"ws": 0}, 1),
     ({"qs": 1016}, 1), ({"os": 1028}, 1), ({"kc": A + M + 8}, 1), ({"out": A + 6 * M + 4}, 1),
     ({"lse": A + 7 * M + 2}, 1), ({"ws": A + 8 * M + 128}, 1), ({"nbytes": 4096}, 1),
     ({"out": A}, 1), ({"lse": A + 4 * M}, 1), ({"ws": A + M}, 1), ({"lse": A + 6 * M}, 1),
