@@ -3,7 +3,8 @@
 A thin binding over libspecverify's C ABI (``include/specverify.h``): each
 function here has the C entry point's name, checks and marshals torch
 tensors (device, dtype, shape, contiguity) and calls the C function on the
-current CUDA stream.  All arithmetic runs in the library's CUDA kernels; if
+current CUDA stream, through ctypes or, for the calls of every layer of a decode
+step, through a compiled extension (``csrc/tensors.cpp``).  All arithmetic runs in the library's CUDA kernels; if
 the library is missing, every call raises -- there is no fallback.
 
   qmv_smallm        4-bit affine group-64 mat-vec over M = 1..16 verify rows
@@ -651,32 +652,24 @@ class KvStep(NamedTuple):
     err_flags: torch.Tensor  # [B]
 
 
-_checks = None
+_direct = None
 
 
-def _load_checks():
-    """The compiled tensor checks; raises if they have not been built."""
-    global _checks
-    if _checks is None:
+def _load_direct():
+    """The compiled calls (``csrc/tensors.cpp``); raises if they have not been
+    built."""
+    global _direct
+    if _direct is None:
         try:
             built = importlib.import_module("._tensors", __name__)
         except ImportError as e:
             raise RuntimeError("_tensors.so is not built; run `python -m "
                                "mtp_speculative_decoding_qmv_gb300.build` (or "
                                "__graft_entry__.build())") from e
-        _checks = built
-    return _checks
-
-
-def _fit(dev, index, *wanted):
-    """Addresses of the tensors of (tensor, name, dtype, shape or None), each as
-    _need wants it."""
-    at = (_checks or _load_checks()).fit(index, *wanted)
-    if at is None:
-        for t, name, dtype, shape in wanted:
-            _need(t, name, dtype, shape, dev)
-        raise RuntimeError("a tensor was refused")  # not reached: one of them raised
-    return at
+        built.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                     (lib().kv_pages_step, lib().rope_kv_append, lib().paged_attention)))
+        _direct = built
+    return _direct
 
 
 def _on(t: torch.Tensor, name: str) -> int:
@@ -687,20 +680,33 @@ def _on(t: torch.Tensor, name: str) -> int:
     return index
 
 
-def _call(index: int, where: str, fn, *args) -> None:
-    """fn(*args, current stream of the device), with that device current."""
+def _call(index: int, fn, *args):
+    """fn(index, current stream of the device, *args), with that device current:
+    the library's status, None where a tensor does not fit the call."""
     if torch._C._cuda_getDevice() == index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st != SV_OK:
-        _check(st, where)
+        return fn(index, torch._C._cuda_getCurrentRawStream(index), *args)
+    with torch.cuda.device(index):
+        return fn(index, torch._C._cuda_getCurrentRawStream(index), *args)
+
+
+def _refuse(where: str, status, wanted) -> None:
+    """Raises for a call that did not go through: by the first of ``wanted``,
+    (check, tensor, name, dtype, shape or None, device), that does not fit, or
+    by the library's own words."""
+    if status is None:
+        for check, *tensor in wanted:
+            check(*tensor)
+        raise RuntimeError(f"{where}: a tensor was refused")  # not reached: one raised
+    _check(status, where)
 
 
 _STEP_NAMES = ("length_out", "held_out", "cursor_out", "q_start", "kv_len", "slots", "positions",
                "err_flags")
-_STEP_TYPES = (torch.int32,) * 8
+
+
+def _step_shapes(B: int, rows: int):
+    per, two, each = (B,), (2,), (max(int(rows), 0),)
+    return per, per, two, (B + 1,), per, each, each, per
 
 
 def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor,
@@ -715,28 +721,24 @@ def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor
     pages for its ``n_new`` tokens (-1: it ended, its pages return to the
     ring) and writes the step's packed rows: slots and positions.  All int32.
     ``length_out=length`` and so on update the state in place."""
-    dev, i32 = length.device, torch.int32
     index = _on(length, "length")
     B, max_pages = block_table.shape
-    per, two, rows = (B,), (2,), int(rows)
-    each = (max(rows, 0),)
-    state = _fit(dev, index, (length, "length", i32, per), (held, "held", i32, per),
-                 (cursor, "cursor", i32, two), (n_new, "n_new", i32, per),
-                 (ring, "ring", i32, None), (block_table, "block_table", i32, None))
-    commit, n = None, 0
-    if n_commit is not None:
-        commit, = _fit(dev, index, (n_commit, "n_commit", i32, None))
-        n = n_commit.numel()
     step = (length_out, held_out, cursor_out, q_start, kv_len, slots, positions, err_flags)
-    shapes = (per, per, two, (B + 1,), per, each, each, per)
     if (length_out is None or held_out is None or cursor_out is None or q_start is None
             or kv_len is None or slots is None or positions is None or err_flags is None):
-        step = tuple(torch.empty(shape, dtype=i32, device=dev) if t is None else t
-                     for t, shape in zip(step, shapes))
-    at = _fit(dev, index, *zip(step, _STEP_NAMES, _STEP_TYPES, shapes))
-    _call(index, "kv_pages_step", lib().kv_pages_step, *state[:4], commit, n,
-          int(n_commit_bias), B, int(page_size), max_pages, ring.numel(), rows, state[5],
-          state[4], *at)
+        step = tuple(torch.empty(shape, dtype=torch.int32, device=length.device) if t is None
+                     else t for t, shape in zip(step, _step_shapes(B, rows)))
+    st = _call(index, (_direct or _load_direct()).kv_pages_step, length, held, cursor, ring,
+               block_table, n_new, n_commit, int(n_commit_bias), int(page_size), int(rows), *step)
+    if st != SV_OK:
+        per, two = (B,), (2,)
+        wanted = [(length, "length", per), (held, "held", per), (cursor, "cursor", two),
+                  (n_new, "n_new", per), (ring, "ring", None), (block_table, "block_table", None)]
+        if n_commit is not None:
+            wanted.append((n_commit, "n_commit", None))
+        wanted += zip(step, _STEP_NAMES, _step_shapes(B, rows))
+        _refuse("kv_pages_step", st, [(_need, t, name, torch.int32, shape, length.device)
+                                      for t, name, shape in wanted])
     return KvStep(*step)
 
 
@@ -753,20 +755,18 @@ def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:
     return (high.to(torch.int64) << 32) + low.to(torch.int64)
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype, rows: int, heads: int, D: int, dev, index: int):
-    """Packed rows [rows, heads, D] with contiguous heads: address, row stride."""
-    at = (_checks or _load_checks()).fit_rows(index, t, dtype, rows, heads, D)
-    if at is not None:
-        return at
+def _need_rows(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """Packed rows [rows, heads, D] with contiguous heads."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, heads, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {heads}, {D})")
-    raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
 
 
 def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -780,45 +780,40 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     after the norm of each head where a weight fp32 [D] is given; writes q to
     ``q_out`` bf16 and k, v to ``slots`` of the caches bf16
     [pages, Hkv, page_size, D] in place.  Returns q_out."""
-    dev = q.device
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [rows, Hq, D] and the caches [pages, Hkv, page_size, D]")
     index = _on(q, "q")
-    rows, Hq, D = q.shape
-    pages, Hkv, page_size, _ = k_cache.shape
-    cache = (pages, Hkv, page_size, D)
-    dtype = q.dtype
-    if dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("q, k and v must be float32 or bfloat16")
-    q_at, qs = _need_rows(q, "q", dtype, rows, Hq, D, dev, index)
-    k_at, ks = _need_rows(k, "k", dtype, rows, Hkv, D, dev, index)
-    v_at, vs = _need_rows(v, "v", dtype, rows, Hkv, D, dev, index)
-    cache = (pages, Hkv, page_size, D)
-    one_axis = positions.dim() == 1
-    axes = 1 if one_axis else positions.shape[-1]
     if q_out is None:
-        q_out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
-    pos_at, slots_at, q_out_at, kc_at, vc_at = _fit(
-        dev, index, (positions, "positions", torch.int32, (rows,) if one_axis else (rows, axes)),
-        (slots, "slots", torch.int32, (rows,)),
-        (q_out, "q_out", torch.bfloat16, (rows, Hq, D)),
-        (k_cache, "k_cache", torch.bfloat16, cache), (v_cache, "v_cache", torch.bfloat16, cache))
-    half, words, ax, qw, kw = 0, None, None, None, None
-    if freqs is not None:
-        words, = _fit(dev, index, (freqs, "freqs", torch.int64, None))
-        if freqs.dim() != 1:
-            raise ValueError("freqs must be [rotary_dim / 2]")
-        half = freqs.numel()
-    if axis is not None:
-        ax, = _fit(dev, index, (axis, "axis", torch.uint8, (half,)))
-    if q_weight is not None:
-        qw, = _fit(dev, index, (q_weight, "q_weight", torch.float32, (D,)))
-    if k_weight is not None:
-        kw, = _fit(dev, index, (k_weight, "k_weight", torch.float32, (D,)))
-    _call(index, "rope_kv_append", lib().rope_kv_append, q_at, k_at, v_at,
-          SV_BF16 if dtype is torch.bfloat16 else SV_F32, qs, ks, vs, pos_at, axes, slots_at,
-          words, ax, qw, kw, float(eps), rows, Hq, Hkv, D, 2 * half, 1 if interleaved else 0,
-          page_size, pages, q_out_at, kc_at, vc_at)
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    st = _call(index, (_direct or _load_direct()).rope_kv_append, q, k, v, positions, slots, freqs,
+               k_cache, v_cache, axis, q_weight, k_weight, float(eps), interleaved, q_out)
+    if st != SV_OK:
+        rows, Hq, D = q.shape
+        cache, dtype, dev = tuple(k_cache.shape[:3]) + (D,), q.dtype, q.device
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q, k and v must be float32 or bfloat16")
+        kv = (rows, cache[1], D)
+        wanted = [(_need_rows, q, "q", dtype, (rows, Hq, D)), (_need_rows, k, "k", dtype, kv),
+                  (_need_rows, v, "v", dtype, kv),
+                  (_need, positions, "positions", torch.int32,
+                   (rows,) if positions.dim() != 2 else (rows, positions.shape[1])),
+                  (_need, slots, "slots", torch.int32, (rows,)),
+                  (_need, q_out, "q_out", torch.bfloat16, (rows, Hq, D)),
+                  (_need, k_cache, "k_cache", torch.bfloat16, cache),
+                  (_need, v_cache, "v_cache", torch.bfloat16, cache)]
+        half = 0
+        if freqs is not None:
+            wanted.append((_need, freqs, "freqs", torch.int64, None))
+            if freqs.dim() != 1:
+                raise ValueError("freqs must be [rotary_dim / 2]")
+            half = freqs.numel()
+        if axis is not None:
+            wanted.append((_need, axis, "axis", torch.uint8, (half,)))
+        if q_weight is not None:
+            wanted.append((_need, q_weight, "q_weight", torch.float32, (D,)))
+        if k_weight is not None:
+            wanted.append((_need, k_weight, "k_weight", torch.float32, (D,)))
+        _refuse("rope_kv_append", st, [w + (dev,) for w in wanted])
     return q_out
 
 
@@ -849,33 +844,28 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ``scale``: 1 / sqrt(D) when omitted.  Returns (out bf16 [rows, Hq, D],
     lse); lse fp32 [rows, Hq] is written when given.  ``workspace`` (from
     make_attention_workspace) is made per call when omitted."""
-    dev = q.device
     if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [rows, Hq, D], the caches [pages, Hkv, page_size, D] and "
                          "block_table [B, max_pages]")
     index = _on(q, "q")
-    rows, Hq, D = q.shape
-    pages, Hkv, page_size, _ = k_cache.shape
-    cache = (pages, Hkv, page_size, D)
-    B, max_pages = block_table.shape
-    cache = (pages, Hkv, page_size, D)
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if workspace is None:
-        workspace = make_attention_workspace(D, dev)
-    q_at, qs = _need_rows(q, "q", torch.bfloat16, rows, Hq, D, dev, index)
-    out_at, outs = _need_rows(out, "out", torch.bfloat16, rows, Hq, D, dev, index)
-    kc_at, vc_at, table_at, start_at, len_at, ws_at = _fit(
-        dev, index, (k_cache, "k_cache", torch.bfloat16, cache),
-        (v_cache, "v_cache", torch.bfloat16, cache),
-        (block_table, "block_table", torch.int32, None),
-        (q_start, "q_start", torch.int32, (B + 1,)), (kv_len, "kv_len", torch.int32, (B,)),
-        (workspace, "workspace", torch.uint8, None))
-    lse_at = None
-    if lse is not None:
-        lse_at, = _fit(dev, index, (lse, "lse", torch.float32, (rows, Hq)))
-    _call(index, "paged_attention", lib().paged_attention, q_at, qs, kc_at, vc_at, table_at,
-          start_at, len_at, B, rows, int(max_new), Hq, Hkv, D, page_size, pages, max_pages,
-          1.0 / math.sqrt(D) if scale is None else float(scale), int(window), out_at, outs,
-          lse_at, ws_at, workspace.numel())
+        workspace = make_attention_workspace(q.shape[2], q.device)
+    st = _call(index, (_direct or _load_direct()).paged_attention, q, k_cache, v_cache, block_table,
+               q_start, kv_len, int(max_new), scale, int(window), out, lse, workspace)
+    if st != SV_OK:
+        rows, Hq, D = q.shape
+        cache, B, bf16 = tuple(k_cache.shape[:3]) + (D,), block_table.shape[0], torch.bfloat16
+        wanted = [(_need_rows, q, "q", bf16, (rows, Hq, D)),
+                  (_need_rows, out, "out", bf16, (rows, Hq, D)),
+                  (_need, k_cache, "k_cache", bf16, cache),
+                  (_need, v_cache, "v_cache", bf16, cache),
+                  (_need, block_table, "block_table", torch.int32, None),
+                  (_need, q_start, "q_start", torch.int32, (B + 1,)),
+                  (_need, kv_len, "kv_len", torch.int32, (B,)),
+                  (_need, workspace, "workspace", torch.uint8, None)]
+        if lse is not None:
+            wanted.append((_need, lse, "lse", torch.float32, (rows, Hq)))
+        _refuse("paged_attention", st, [w + (q.device,) for w in wanted])
     return out, lse

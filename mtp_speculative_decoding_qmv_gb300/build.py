@@ -55,7 +55,7 @@ def build_checks() -> None:
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
-           "-I" + sysconfig.get_paths()["include"], f"-I{CUDA}/include", str(src), "-o", str(tmp),
+           "-I" + sysconfig.get_paths()["include"], f"-I{CUDA}/include", f"-I{INCLUDE}", str(src), "-o", str(tmp),
            f"-L{root / 'lib'}", f"-Wl,-rpath,{root / 'lib'}", "-ltorch_python", "-ltorch_cpu",
            "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -67,7 +67,8 @@ def build_checks() -> None:
 def build(force: bool = False, debug: bool = False, verbose: bool = False) -> Path:
     headers = list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
     srcs = sources()
-    checks = force or _stale(CHECKS, [CSRC / "tensors.cpp", Path(__file__)])
+    checks = force or _stale(CHECKS, [CSRC / "tensors.cpp", INCLUDE / "specverify.h",
+                                       Path(__file__)])
     if not force and not _stale(LIB, srcs + headers + [Path(__file__)]):
         if checks:
             build_checks()
