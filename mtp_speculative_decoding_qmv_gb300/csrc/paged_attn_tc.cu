@@ -23,6 +23,13 @@
 // older maximum, which loses nothing in bf16 or fp32, and a rescale, a read
 // and write of the row's O, stays rare.  Scores, sums and O are fp32; weights
 // are rounded to bf16 (at most half a step, 2^-8 of each), their sum is not.
+//
+// Measured (GB300, 40 heads of 128 over 8 kv heads): 1000 rows after 30,000
+// positions 404 us (1.5 PFLOP/s); a prompt of 5000 from its start 199 to 212 us
+// (1.2 to 1.3 PFLOP/s of the unmasked half), where about 4 us pass before the
+// first product, 5 around each item and 9 at the last join.  A key tile takes
+// 1.5 us for both row tiles, 1.3 at a large library product's rate: the tensor
+// cores bound it then.  Leaving the exponentials out did not shorten it.
 #include <algorithm>
 
 #include "attn_common.cuh"
