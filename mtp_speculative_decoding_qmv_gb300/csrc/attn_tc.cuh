@@ -20,11 +20,23 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kTmemCols = 512;
 // An item's cost beside its tiles (queries, the first scores, the last
-// products, the output), in key tiles, when the work is cut into runs.
-constexpr int kItemUnits = 3;
+// products, the output), in key tiles, when the work is cut into runs: 6.6 us
+// or 4.6 tiles of two row tiles (5000 tokens from their start: 200 us with 3,
+// 191 with 4, 190 with 5; 16 chunks of 256 after 2000: 191, 167, 173), less of
+// the longer tiles at head dim 256 (217.6 us with 3, 218.6 with 4).
+template <int kRows>
+constexpr int kItemUnits = kRows == 256 ? 4 : 3;
 // Items of at most so many key tiles are not split: writing and joining partials
-// costs about eight tiles' time, half an item is the most it could even out.
+// costs about six tiles' time, half an item is the most it could even out.
 constexpr int kWholeTiles = 8;
+// Such an item goes to the run that holds the middle of its units; at head dim
+// 256 of its tiles, which is better for one short prompt (20 heads, 1000 tokens:
+// 27.9 against 31.1 us, 600: 20.1 against 20.5) and worse for several (4 of 900:
+// 64.1 against 62.2).
+template <int kRows>
+__device__ __forceinline__ int whole_units(int width) {
+  return kRows == 256 ? width : width - kItemUnits<kRows>;
+}
 constexpr float kRescale = 8.f;  // base-2 exponent by which a maximum may lag
 
 constexpr uint32_t idesc(int n, bool b_mn_major) {
@@ -60,7 +72,7 @@ __device__ __forceinline__ int row_tiles(const Args &a, const Request &q) {
 template <int kRows>
 __device__ __forceinline__ int item_width(const Args &a, const Request &q, int i) {
   const Span s = rows_span(a, q, i * kRows, min(kRows, q.n * a.G - i * kRows));
-  return (s.hi + kBK - 1) / kBK - s.lo / kBK + kItemUnits;
+  return (s.hi + kBK - 1) / kBK - s.lo / kBK + kItemUnits<kRows>;
 }
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
@@ -116,9 +128,9 @@ struct Walk {
       rem -= all;
       item += all;
     }
-    const int tiles = max(width - kItemUnits, 1);
+    const int tiles = max(width - kItemUnits<kRows>, 1);
     const long long at = u - item;
-    if (at >= tiles || (tiles <= kWholeTiles && 2 * at > tiles))
+    if (tiles <= kWholeTiles ? 2 * at > whole_units<kRows>(width) : at >= tiles)
       u = item + width;
     else if (tiles <= kWholeTiles)
       u = item;
@@ -147,14 +159,12 @@ struct Walk {
     s.width = width;
     s.first = (int)(u - item);
     s.n_units = width - s.first;
-    const int tiles = max(width - kItemUnits, 1);
-    if (end - u < tiles - s.first) {  // the run ends among its tiles
-      if (tiles > kWholeTiles) {
-        s.n_units = (int)(end - u);
-      } else if (2 * (end - item) <= tiles) {
-        u = end;
-        return false;
-      }
+    const int tiles = max(width - kItemUnits<kRows>, 1);
+    if (tiles > kWholeTiles) {
+      if (end - u < tiles - s.first) s.n_units = (int)(end - u);  // the run ends among its tiles
+    } else if (2 * (end - item) <= whole_units<kRows>(width)) {
+      u = end;
+      return false;
     }
     s.r0 = i * kRows;
     s.count = min(kRows, rq.n * a.G - s.r0);
@@ -298,10 +308,21 @@ __device__ __forceinline__ bool begin_run(const Args &a, long long *s_scan, int 
 // kJoin (the result takes the first member's place) and then the groups, so
 // that no CTA reads more than about kJoin of them.  Partials are always added
 // in CTA order, whichever CTA does it.
+//
+// A partial is written and read back only where it has to wait: a CTA that
+// finds the others' (of at most kDirect) all there adds them to the sums in its
+// tensor memory (8 us from its last product, where writing its own, arriving
+// and joining took 14).
 constexpr int kMaxTcCtas = 170;
 constexpr int kJoin = 16;
+constexpr int kDirect = 4;
 static_assert(2 * 3 * kMaxTcCtas * 4 <= kCounterBytes, "counters");
 static_assert(kMaxTcCtas <= kJoin * kJoin , "two rounds");
+__device__ __forceinline__ unsigned load_relaxed(const unsigned *p) {
+  unsigned v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 struct Group {
   int first, stride, n;  // CTAs first, first + stride, ..
   int counter;           // its arrivals, of 3 ctas

@@ -25,11 +25,12 @@
 // are rounded to bf16 (at most half a step, 2^-8 of each), their sum is not.
 //
 // Measured (GB300, 40 heads of 128 over 8 kv heads): 1000 rows after 30,000
-// positions 404 us (1.5 PFLOP/s); a prompt of 5000 from its start 199 to 212 us
-// (1.2 to 1.3 PFLOP/s of the unmasked half), where about 4 us pass before the
-// first product, 5 around each item and 9 at the last join.  A key tile takes
-// 1.5 us for both row tiles, 1.3 at a large library product's rate: the tensor
-// cores bound it then.  Leaving the exponentials out did not shorten it.
+// positions 404 to 465 us on different days (1.3 to 1.5 PFLOP/s), 3 chunks of
+// 3500 after 9000 1490 us (1.5); a prompt of 5000 from its start 191 us (1.34),
+// where about 4 us pass before the first product, 6 around each item and 8 at
+// the last join.  A key tile takes 1.5 us for both row tiles, 1.3 at a large
+// library product's rate: the tensor cores bound it then.  Leaving the
+// exponentials out did not shorten it.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -60,6 +61,77 @@ struct TcShape {
 template <int D>
 __device__ __forceinline__ float *part_row(const Args &a, int slot, int rr) {
   return partial_at(a, slot, kRows, D) + rr * 4;
+}
+
+// The result of packed row r (row rr of the item, kept if `ok`) of which this
+// CTA's tensor memory holds its own sums (if `any`) and the others of c0 .. c1
+// have left theirs: added in CTA order, as in the join of partials alone.
+template <int D>
+__device__ __noinline__ void add_and_write(const Args &a, int q0, int h, int r, int rr, bool ok,
+                                           bool any, uint32_t o_at, float m, float l, int c0,
+                                           int c1) {
+  const int me = (int)blockIdx.x, t = r / a.G, g = r - t * a.G;
+  auto slot = [&](int k) { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
+  float weight[kDirect], lk[kDirect], mm = kNegInf, ll = 0.f;
+#pragma unroll
+  for (int k = 0; k < kDirect; ++k) {
+    const float *ml = partial_at(a, slot(k), kRows, D) + kRows * D + rr;
+    const bool other = ok && c0 + k <= c1 && c0 + k != me;
+    weight[k] = other ? __ldcg(ml) : c0 + k == me ? m : kNegInf;
+    lk[k] = other ? __ldcg(ml + kRows) : c0 + k == me ? l : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kDirect; ++k) mm = fmaxf(mm, weight[k]);
+#pragma unroll
+  for (int k = 0; k < kDirect; ++k) {
+    weight[k] = join_weight(a, weight[k], lk[k], mm);
+    ll = fmaf(lk[k], weight[k], ll);
+  }
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  __nv_bfloat16 *dst = a.out + (long long)(q0 + t) * a.out_stride + (long long)(h * a.G + g) * D;
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    uint32_t o[32];
+    __syncwarp();
+    if (any) {
+      tc_ld_x32(o_at + d, o);
+      tc_wait_ld();
+      pin(o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    }
+    if (!ok) continue;  // the loads are the warp's, the rest the row's
+    float acc[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDirect; ++k) {
+      if (c0 + k > c1) break;
+      float4 y[8];
+      const float *part = part_row<D>(a, slot(k), rr) + (size_t)(d >> 2) * kRows * 4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        y[i] = c0 + k == me
+                   ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]))
+                   : __ldcg(reinterpret_cast<const float4 *>(part + (size_t)i * kRows * 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[4 * i] = fmaf(y[i].x, weight[k], acc[4 * i]);
+        acc[4 * i + 1] = fmaf(y[i].y, weight[k], acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(y[i].z, weight[k], acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(y[i].w, weight[k], acc[4 * i + 3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+      *reinterpret_cast<uint4 *>(dst + d + i) = make_uint4(
+          pack_bf16(acc[i] * inv, acc[i + 1] * inv), pack_bf16(acc[i + 2] * inv, acc[i + 3] * inv),
+          pack_bf16(acc[i + 4] * inv, acc[i + 5] * inv),
+          pack_bf16(acc[i + 6] * inv, acc[i + 7] * inv));
+  }
+  if (ok && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, mm, ll);
 }
 
 // Rows [rr, rr + count) of the item at r0, one by one by a warp (attend_row):
@@ -487,11 +559,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           group_sync(wg);
           if (row == 0) s_odd[wg] = 0;
         }
+        // A split item's CTAs c0 .. c1.  When all others have left their partials,
+        // this one adds them to what it holds and writes the result.
+        const int c0 = whole ? 0 : runs.owner(s.item);
+        const int c1 = whole ? 0 : runs.owner(s.item + s.width - kItemUnits<kRows> - 1);
+        bool direct = !whole && !odd && c1 - c0 < kDirect;
+        unsigned *arrivals = nullptr, arrived = 0;
+        if (direct && row == 0) {
+          arrivals = a.counters + wg * 3 * gridDim.x +
+                     join_group(c0, c1, (int)blockIdx.x, false, (int)gridDim.x).counter;
+          arrived = load_relaxed(arrivals);
+        }
         if (s.tiles > 0) {
           wait(&o_done[wg], (sn - 1u) & 1u);
           tc_fence_after();
         }
-        if (odd) {
+        if (direct) {
+          if (row == 0) {
+            __threadfence();
+            s_last[wg] = arrived == (unsigned)(c1 - c0);
+            if (s_last[wg]) *arrivals = 0;  // ready for the next call
+          }
+          group_sync(wg);
+          direct = s_last[wg] != 0;
+        }
+        if (direct) {
+          add_and_write<D>(a, s.rq.q0, s.h, r, rr, ok, s.tiles > 0, o_at, m, l, c0, c1);
+        } else if (odd) {
           rows_plain<D>(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, wg * kTile + (warp & 3) * 32,
                         min(count - (warp & 3) * 32, 32), s.tile0 * kBK,
                         (s.tile0 + s.tiles) * kBK, whole ? -1 : slot);
@@ -560,9 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();  // O has been read before the next segment's products write it
-        if (!whole) {
+        if (!whole && !direct) {
           // ---- the last CTA to arrive joins this tile's partials ----
-          const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits - 1);
           float *weights = reinterpret_cast<float *>(  // [partial][row]
               smem_raw + (q_smem - raw) + (2 + S::kSlots) * S::kTileBytes +
               (uint32_t)wg * S::kStage);

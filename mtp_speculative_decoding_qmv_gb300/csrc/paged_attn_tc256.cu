@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // O has been read before the next segment's products write it
       if (!whole) {
         // ---- the last CTA to arrive joins this group's columns ----
-        const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits - 1);
+        const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits<kRows> - 1);
         float *weights = reinterpret_cast<float *>(stage);  // [partial][row]
         if (odd) {  // both groups wrote for both
           __threadfence();
