@@ -31,8 +31,8 @@
 // Measured (GB300): 8191 rows of 20 + 4 + 4 bf16 heads of 256, normed, a quarter
 // turned: 52.4 us (235 MB, 4.5 TB/s), with 65 % of the issue slots used, most by
 // the norm's and the turn's fp32 work.  From fp32, without the norm, it streams
-// at 6.0 TB/s.  4 rows: 1.9 us, 128 rows: 2.9 us, the
-// launch and one round trip to memory.
+// at 6.0 TB/s.  4 rows: 2.1 us, 128 rows: 3.1 us, the launch and one round trip
+// to memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
