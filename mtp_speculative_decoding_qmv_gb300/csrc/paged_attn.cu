@@ -19,9 +19,9 @@
 // (attn_join_kernel below), in an order that does not depend on the run.
 //
 // Measured (GB300, head dim 128 unless said): 4 rows over 100,005 positions of
-// 40 kv heads 300 us (6.8 TB/s, a plain copy's rate), 32 requests' 4 rows over
-// ragged contexts 165 us (5.7 TB/s), 16 single tokens at head dim 256 76 us
-// (5.3 TB/s); one token over 999 positions 10.4 us: two launches and the
+// 40 kv heads 297 us (6.9 TB/s, a plain copy's rate), 32 requests' 4 rows over
+// ragged contexts 153 us (6.2 TB/s), 16 single tokens at head dim 256 76 us
+// (5.3 TB/s); one token over 999 positions 10.4 to 11.5 us: two launches and the
 // dependent trips to memory of each, not the 4 MB of keys and values.
 #include <algorithm>
 
@@ -39,9 +39,13 @@ constexpr int kBK = 64;  // keys per tile
 constexpr int kWarps = 4;
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kConsumers = kWarps * 32;
-// An item's cost beside its tiles (queries, joining the warps, the output), in
-// key tiles, when the work is cut into runs.
-constexpr int kItemUnits = 2;
+// An item's cost beside its tiles (queries, joining the warps, the output: about
+// 6 us, of which the ring's two tiles hide some), in key tiles, when the work is
+// cut into runs.  With 2, 4 and 5: 32 verify blocks over 200 to 30,000 positions
+// 163, 153 and 150 us, 300 tokens over 20 to 3000 at head dim 256 156, 138 and
+// 134, 48 blocks of 40 kv heads 257, 242 and 245, one request of one kv head over
+// 100,000 28.7, 28.9 and 30.9, one token over 999 10.7, 11.5 and 11.5.
+constexpr int kItemUnits = 4;
 
 template <int D>
 struct RowsShape {
