@@ -736,6 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (gr.final) break;
           }
+          // the weights have been read: the next item's rows may be staged over
+          // them (one without key tiles waits for nothing before it does)
+          group_sync(wg);
         }
       }
     }
