@@ -558,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           odd = s_odd[wg] != 0;
           group_sync(wg);
           if (row == 0) s_odd[wg] = 0;
+          group_sync(wg);  // before the next item's tiles may set it
         }
         // A split item's CTAs c0 .. c1.  When all others have left their partials,
         // this one adds them to what it holds and writes the result.

@@ -77,3 +77,30 @@ def test_a_refused_request_after_a_split_one(sv, D, Hq, new, ctx):
     for _ in range(100):
         assert torch.equal(sv.paged_attention(*c.args(), 300, workspace=ws)[0], out)
     sv.device_status()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_items_with_infinities_one_after_another(sv, D):
+    """Many short requests whose newest value is infinite, several a CTA: each
+    item finds its own."""
+    d = dev()
+    B, new, Hq = 700, 5, 15  # 75 rows of one kv head
+    c = Long(D, Hq, 1, 16, [(11, new)] * B, D)
+    clean = c.v.clone()
+    page, offset = c.table[:, 0].long(), 15
+    odd = torch.arange(B, device=d) % 3 != 1
+    c.v[page[odd], 0, offset, ::7] = math.inf
+    ws = sv.make_attention_workspace(D, d)
+    scale = c.scale
+    k, v = (t[page, 0].double() for t in (c.k, clean))  # [B, 16, D]
+    q = c.q.view(B, new, Hq, D).double()
+    x = torch.einsum("btgd,bjd->btgj", q, k) * scale
+    at = torch.arange(16, device=d)
+    x = x.masked_fill(at > 11 + torch.arange(new, device=d)[:, None, None], -math.inf)
+    want = torch.einsum("btgj,bjd->btgd", x.softmax(-1), v)
+    infinite = torch.zeros_like(want, dtype=torch.bool)
+    infinite[odd, new - 1, :, ::7] = True  # seen by the last row alone
+    for _ in range(20):
+        out = sv.paged_attention(*c.args(), 100, workspace=ws)[0].view(B, new, Hq, D).double()
+        assert torch.equal(torch.isposinf(out), infinite)
+        assert _close(out[~infinite], want[~infinite])
