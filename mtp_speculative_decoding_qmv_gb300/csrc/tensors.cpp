@@ -3,10 +3,13 @@
 // at and the library is called within a microsecond or two, where Python and
 // ctypes take six.  Each function returns the library's status, or None when a
 // tensor is not as the call wants it; the caller then finds out which and
-// raises.  On one GB300's host a call of rope_kv_append for one verify block
-// takes the calling thread 3.6 us, most of it the launch (8.8 us when the checks
-// returned addresses to Python and ctypes made the call).
+// raises.  What torch throws here (for a tensor without storage, as a transform
+// hands out, or of a layout without strides) becomes a Python exception.  On one
+// GB300's host a call of rope_kv_append for one verify block takes the calling
+// thread 3.6 us, most of it the launch (8.8 us when the checks returned
+// addresses to Python and ctypes made the call).
 #include <Python.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -98,10 +101,20 @@ bool begin(PyObject *const *args, Py_ssize_t n, Py_ssize_t want, Reader *r, sv_s
   *r = Reader{args, PyLong_AsLong(args[0])};
   return !PyErr_Occurred();
 }
-#define CALL(expression)                    \
-  sv_status st;                             \
-  Py_BEGIN_ALLOW_THREADS st = (expression); \
-  Py_END_ALLOW_THREADS return PyLong_FromLong(st)
+// The library is called without the interpreter's lock, held again on any way out.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F>
+PyObject *call(F library) {
+  sv_status st;
+  {
+    const Unlocked unlocked;
+    st = library();
+  }
+  return PyLong_FromLong(st);
+}
 
 // bind(kv_pages_step, rope_kv_append, paged_attention): the library's addresses
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -118,6 +131,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // None, n_commit_bias, page_size, rows, length_out, held_out, cursor_out, q_start, kv_len,
 // slots, positions, err_flags)
 PyObject *pages(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Reader r;
   sv_stream_t stream;
   if (!begin(args, n, 20, &r, &stream)) return nullptr;
@@ -142,14 +156,18 @@ PyObject *pages(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (!to_int(b, &B) || !to_int(table->size(1), &max_pages) || !to_int(in_ring, &ring_n) ||
       !to_int(commits, &commits_n))
     return nullptr;
-  CALL(pages_fn(length, held, cursor, n_new, n_commit, commits_n, bias, B, page_size, max_pages,
-                ring_n, rows, pages, ring, length_out, held_out, cursor_out, q_start, kv_len,
-                slots, positions, flags, stream));
+  return call([&] {
+    return pages_fn(length, held, cursor, n_new, n_commit, commits_n, bias, B, page_size,
+                    max_pages, ring_n, rows, pages, ring, length_out, held_out, cursor_out,
+                    q_start, kv_len, slots, positions, flags, stream);
+  });
+  END_HANDLE_TH_ERRORS
 }
 
 // rope_kv_append(device, stream, q, k, v, positions, slots, freqs or None, k_cache, v_cache,
 // axis, q_weight, k_weight (each or None), eps, interleaved, q_out)
 PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Reader r;
   sv_stream_t stream;
   if (!begin(args, n, 16, &r, &stream)) return nullptr;
@@ -190,14 +208,18 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const int64_t sizes[8] = {axes, rows, hq, hkv, d, 2 * half, page, pages};
   for (int i = 0; i < 8; ++i)
     if (!to_int(sizes[i], &v[i])) return nullptr;
-  CALL(append_fn(q_at, k_at, v_at, type == at::kBFloat16 ? SV_BF16 : SV_F32, qs, ks, vs, pos_at,
-                 v[0], slots, freqs, axis, qw, kw, (float)eps, v[1], v[2], v[3], v[4], v[5],
-                 interleaved, v[6], v[7], q_out, kc, vc, stream));
+  return call([&] {
+    return append_fn(q_at, k_at, v_at, type == at::kBFloat16 ? SV_BF16 : SV_F32, qs, ks, vs,
+                     pos_at, v[0], slots, freqs, axis, qw, kw, (float)eps, v[1], v[2], v[3],
+                     v[4], v[5], interleaved, v[6], v[7], q_out, kc, vc, stream);
+  });
+  END_HANDLE_TH_ERRORS
 }
 
 // paged_attention(device, stream, q, k_cache, v_cache, block_table, q_start, kv_len, max_new,
 // scale or None for 1 / sqrt(D), window, out, lse or None, workspace)
 PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
   Reader r;
   sv_stream_t stream;
   if (!begin(args, n, 14, &r, &stream)) return nullptr;
@@ -227,9 +249,12 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const int64_t sizes[8] = {b, rows, hq, hkv, d, page, pages, table->size(1)};
   for (int i = 0; i < 8; ++i)
     if (!to_int(sizes[i], &v[i])) return nullptr;
-  CALL(attend_fn(q_at, qs, kc, vc, table_at, q_start, kv_len, v[0], v[1], max_new, v[2], v[3],
-                 v[4], v[5], v[6], v[7], (float)scale, window, out, outs, lse, workspace,
-                 (size_t)bytes, stream));
+  return call([&] {
+    return attend_fn(q_at, qs, kc, vc, table_at, q_start, kv_len, v[0], v[1], max_new, v[2],
+                     v[3], v[4], v[5], v[6], v[7], (float)scale, window, out, outs, lse,
+                     workspace, (size_t)bytes, stream);
+  });
+  END_HANDLE_TH_ERRORS
 }
 
 #define METHOD(name, function) \
