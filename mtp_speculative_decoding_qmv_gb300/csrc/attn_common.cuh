@@ -1,7 +1,7 @@
-// attn_common.cuh -- shared by the two paged-attention kernels: the call's
-// arguments, which keys each packed query row may attend, how the work is cut
-// into equal runs of key tiles, the joining of split results, and the plain
-// row-by-row path for non-finite values in masked places.
+// attn_common.cuh -- shared by the paged-attention kernels: the call's arguments,
+// which keys each packed query row may attend, how the work is cut into equal
+// runs of key tiles, the joining of split results, and non-finite values in
+// places that some rows attend and others do not.
 //
 // Row r = t G + g of request b and kv head h is token t (of n_b) under query
 // head h G + g (G = Hq / Hkv query heads share a kv head), so all rows of
@@ -129,51 +129,35 @@ __device__ __forceinline__ int page_row(const Args &a, int b, int h, int idx, in
   return (page * a.Hkv + (page < a.num_pages ? h : 0)) << a.page_shift;
 }
 
-// One row by a whole warp, straight from memory, over its keys in [j0, j1):
-// only keys that the row attends are read.  Lane l returns elements
-// l D / 32 .. of the unnormalised sum, with the row's maximum raw score and
-// sum.  Taken where a masked place holds an infinity or NaN value, which a
-// tile's product would multiply by a weight of zero.
-template <int D>
-__device__ __forceinline__ void attend_row(const Args &a, int b, int h, int q0, int n, int len,
-                                           int r, int j0, int j1, float (&o)[D / 32], float &m,
-                                           float &l) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int t = r / a.G, g = r - t * a.G;
-  const int p = len - n + t;
-  if (a.window > 0) j0 = max(j0, p - a.window + 1);
-  j1 = min(j1, p + 1);
-  const __nv_bfloat16 *q =
-      a.q + (long long)(q0 + t) * a.q_stride + (long long)(h * a.G + g) * D + lane * E;
-  float qv[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __bfloat162float(q[e]);
-    o[e] = 0.f;
-  }
-  m = kNegInf;
-  l = 0.f;
-  for (int j = max(j0, 0); j < j1; ++j) {
-    const int page = __ldg(a.table + (size_t)b * a.max_pages + (j >> a.page_shift));
-    const bool ok = (unsigned)page < (unsigned)a.num_pages;
-    const long long at =
-        ((((long long)page * a.Hkv + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D +
-        lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], ok ? __bfloat162float(a.k[at + e]) : 0.f, s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float ms = mn == kNegInf ? 0.f : mn;
-    const float keep = exp2_approx((m - ms) * a.scale_log2);
-    const float w = exp2_approx((s - ms) * a.scale_log2);
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(w, ok ? __bfloat162float(a.v[at + e]) : 0.f, o[e] * keep);
-    m = mn;
-  }
+// A value that some rows of a tile attend and others do not would meet weights of
+// zero; where it is not finite the kernels put zero in its place, in shared
+// memory (clear_nonfinite), and afterwards add it to the rows that attend it.  A
+// weight of a finite score is positive, so the sum gets the value itself; a
+// score of -inf has weight zero, and the product is NaN.  Such positions lie
+// outside [all_lo, all_hi): at most a tile's tokens on either side (and what a
+// shorter window leaves between), however long the context is.
+__device__ __forceinline__ uint32_t nonfinite_bits(const uint4 &v) {
+  return nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) | nonfinite_bits(v.w);
+}
+__device__ __forceinline__ void clear_nonfinite(uint4 &v) {
+  v.x &= ~((nonfinite_bits(v.x) >> 15) * 0xFFFFu);
+  v.y &= ~((nonfinite_bits(v.y) >> 15) * 0xFFFFu);
+  v.z &= ~((nonfinite_bits(v.z) >> 15) * 0xFFFFu);
+  v.w &= ~((nonfinite_bits(v.w) >> 15) * 0xFFFFu);
+}
+__device__ __forceinline__ float2 two_floats(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ float add_if_nonfinite(float sum, float v, bool weightless) {
+  if (fabsf(v) < -kNegInf) return sum;
+  return weightless ? __int_as_float(0x7fffffff) : sum + v;
+}
+// The first element of position j's key and value under head h, or -1 where the
+// page's id is out of range.
+__device__ __forceinline__ long long position_at(const Args &a, int b, int h, int j, int D) {
+  const int page = __ldg(a.table + (size_t)b * a.max_pages + (j >> a.page_shift));
+  if ((unsigned)page >= (unsigned)a.num_pages) return -1;
+  return ((((long long)page * a.Hkv + h) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
 }
 
 // ---- equal runs of work ------------------------------------------------------
@@ -208,20 +192,6 @@ __device__ __forceinline__ void store_out4(const Args &a, int q0, int h, int r, 
                              (long long)(h * a.G + g) * D + d) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   if (d == 0 && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
-}
-
-// The same with lane l of a warp holding elements l D / 32 .. of row r.
-template <int D>
-__device__ __forceinline__ void store_lane(const Args &a, int q0, int h, int r,
-                                           const float (&o)[D / 32], float m, float l) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, t = r / a.G, g = r - t * a.G;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (long long)(q0 + t) * a.out_stride +
-                                               (long long)(h * a.G + g) * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, m, l);
 }
 
 // Weight of a partial with maximum m and sum l against the joint maximum; one

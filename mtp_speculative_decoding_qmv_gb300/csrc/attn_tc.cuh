@@ -217,6 +217,56 @@ __device__ __forceinline__ void pin(uint32_t (&v)[32]) {
     asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
                       "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
 }
+// Adds to the kCols output columns from col0 on that a thread's row has in tensor
+// memory (at o_at) the non-finite values of positions [lo, hi) that the row
+// attends (first .. last) and that not all rows do.  q is the row's query, null
+// for none.  By whole warps.
+template <int D, int kCols>
+__device__ __noinline__ void add_nonfinite(const Args &a, int b, int h, int lo, int hi, int all_lo,
+                                           int all_hi, const __nv_bfloat16 *q, int first, int last,
+                                           uint32_t o_at, int col0) {
+  const int lane = threadIdx.x & 31;
+  for (int j = lo; j < hi; ++j) {
+    if (j >= all_lo && j < all_hi) {
+      j = all_hi - 1;
+      continue;
+    }
+    const long long at = position_at(a, b, h, j, D);
+    if (at < 0) continue;  // zeros
+    const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v + at + col0);
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < kCols / 64; ++i) odd |= nonfinite_bits(v[i * 32 + lane]);
+    const bool mine = q && j >= first && j <= last;
+    if (!__any_sync(0xffffffffu, odd) || !__any_sync(0xffffffffu, mine)) continue;
+    float s = 0.f;
+    if (mine)
+      for (int d = 0; d < D; d += 2) {
+        const float2 x = two_floats(*reinterpret_cast<const uint32_t *>(q + d));
+        const float2 k = two_floats(*reinterpret_cast<const uint32_t *>(a.k + at + d));
+        s = fmaf(x.y, k.y, fmaf(x.x, k.x, s));
+      }
+#pragma unroll 1
+    for (int d = 0; d < kCols; d += 32) {
+      uint32_t o[32];
+      __syncwarp();
+      tc_ld_x32(o_at + d, o);
+      tc_wait_ld();
+      pin(o);
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 y = two_floats(v[(d + i) / 2]);
+          o[i] = __float_as_uint(add_if_nonfinite(__uint_as_float(o[i]), y.x, s == kNegInf));
+          o[i + 1] = __float_as_uint(add_if_nonfinite(__uint_as_float(o[i + 1]), y.y, s == kNegInf));
+        }
+      }
+      __syncwarp();
+      tc_st_x32(o_at + d, o);
+    }
+    tc_wait_st();
+  }
+}
 __device__ __forceinline__ void group_sync(int wg) {  // the warps of a softmax group
   asm volatile("bar.sync %0, 128;" ::"r"(wg + 1) : "memory");
 }

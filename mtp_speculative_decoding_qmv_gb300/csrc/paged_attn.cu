@@ -128,24 +128,48 @@ struct Walk {
   }
 };
 
+// Adds to the rows' sums in shared memory the non-finite values that the tiles
+// left out (see clear_nonfinite), a row a warp at a time, into the sums of the
+// warps whose maximum is the row's.
 template <int D, int kRowGroups>
-__device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
-                                        int r0, int count, int j0, int j1, float *s_out,
-                                        float *s_m, float *s_l) {
-  constexpr int kKeyGroups = kWarps / kRowGroups;
+__device__ __noinline__ void add_nonfinite(const Args &a, const Segment &s, float *s_out,
+                                           const float (*s_m)[16]) {
+  constexpr int kKeyGroups = kWarps / kRowGroups, E = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int rr = warp; rr < 16 * kRowGroups; rr += kWarps) {
-    const int w0 = (rr >> 4) * kKeyGroups;
-    float o[D / 32], m = kNegInf, l = 0.f;
+  for (int rr = warp; rr < s.count; rr += kWarps) {
+    const int t = (s.r0 + rr) / a.G, g = s.r0 + rr - t * a.G;
+    const int last = s.rq.len - s.rq.n + t;
+    const int lo = max(max(s.span.lo, s.tile0 * kBK), a.window > 0 ? last - a.window + 1 : 0);
+    const int hi = min(min(s.span.hi, (s.tile0 + s.tiles) * kBK), last + 1);
+    const __nv_bfloat16 *q = a.q + (long long)(s.rq.q0 + t) * a.q_stride +
+                             (long long)(s.h * a.G + g) * D + lane * E;
+    int w = (rr >> 4) * kKeyGroups;
+    for (int i = w + 1; i < (rr >> 4) * kKeyGroups + kKeyGroups; ++i)
+      if (s_m[i][rr & 15] > s_m[w][rr & 15]) w = i;
+    float *sums = s_out + (w * 16 + (rr & 15)) * RowsShape<D>::kOutStride + lane * E;
+    for (int j = lo; j < hi; ++j) {
+      if (j >= s.span.all_lo && j < s.span.all_hi) {
+        j = s.span.all_hi - 1;
+        continue;
+      }
+      const long long at = position_at(a, s.b, s.h, j, D);
+      if (at < 0) continue;  // zeros
+      const uint32_t *v = reinterpret_cast<const uint32_t *>(a.v + at + lane * E);
+      uint32_t odd = 0;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    if (rr < count) attend_row<D>(a, b, h, q0, n, len, r0 + rr, j0, j1, o, m, l);
+      for (int e = 0; e < E; e += 2) odd |= nonfinite_bits(v[e / 2]);
+      if (!__any_sync(0xffffffffu, odd)) continue;
+      float score = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-      s_out[(w0 * 16 + (rr & 15)) * RowsShape<D>::kOutStride + lane * (D / 32) + e] = o[e];
-    if (lane < kKeyGroups) {
-      s_m[(w0 + lane) * 16 + (rr & 15)] = lane == 0 ? m : kNegInf;
-      s_l[(w0 + lane) * 16 + (rr & 15)] = lane == 0 ? l : 0.f;
+      for (int e = 0; e < E; ++e)
+        score = fmaf(__bfloat162float(q[e]), __bfloat162float(a.k[at + lane * E + e]), score);
+      score = warp_sum(score);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = two_floats(v[e / 2]);
+        sums[e] = add_if_nonfinite(sums[e], y.x, score == kNegInf);
+        sums[e + 1] = add_if_nonfinite(sums[e + 1], y.y, score == kNegInf);
+      }
     }
   }
 }
@@ -409,13 +433,13 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
       base = ring + slot * S::kSlotBytes;
       if (masked) {
         // places no row attends may hold anything: zero, so that a weight of
-        // zero meets no NaN; a non-finite value that some rows attend and
-        // others do not sends the segment to the row-by-row path
+        // zero meets no NaN, and so is what is not finite where some rows attend
+        // and others do not (added to their sums at the end)
         consumer_sync();
         const int key = tid >> 1, pos = j0 + key;
         const bool none = pos < s.span.lo || pos >= s.span.hi;
         if (none || pos < s.span.all_lo || pos >= s.span.all_hi) {
-          uint32_t odd = 0;
+          bool odd = false;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint4 *at = reinterpret_cast<uint4 *>(
@@ -424,9 +448,12 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
             if (none) {
               *at = make_uint4(0, 0, 0, 0);
             } else {
-              const uint4 v = *at;
-              odd |= nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) |
-                     nonfinite_bits(v.w);
+              uint4 v = *at;
+              if (nonfinite_bits(v)) {
+                clear_nonfinite(v);
+                *at = v;
+                odd = true;
+              }
             }
           }
           if (odd) s_nonfinite = 1;
@@ -455,27 +482,26 @@ __global__ void __launch_bounds__(kThreads, RowsShape<D>::kCtasPerSm)
 
     // ---- the warps' sums to shared memory ----
     consumer_sync();  // s_out of the segment before has been read, s_nonfinite is written
-    if (s_nonfinite) {
-      rows_plain<D, kRowGroups>(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, s.count,
-                                s.tile0 * kBK, (s.tile0 + s.tiles) * kBK, s_out, &s_m[0][0],
-                                &s_l[0][0]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] = quad_sum(l[i]);
-        if (gc == 0) {
-          s_m[warp][gq + 8 * i] = m[i];
-          s_l[warp][gq + 8 * i] = l[i];
-        }
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d)
-          *reinterpret_cast<float2 *>(
-              &s_out[(warp * 16 + gq + 8 * i) * S::kOutStride + d * 8 + gc * 2]) =
-              make_float2(o[d][2 * i], o[d][2 * i + 1]);
+    for (int i = 0; i < 2; ++i) {
+      l[i] = quad_sum(l[i]);
+      if (gc == 0) {
+        s_m[warp][gq + 8 * i] = m[i];
+        s_l[warp][gq + 8 * i] = l[i];
       }
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        *reinterpret_cast<float2 *>(
+            &s_out[(warp * 16 + gq + 8 * i) * S::kOutStride + d * 8 + gc * 2]) =
+            make_float2(o[d][2 * i], o[d][2 * i + 1]);
     }
+    const bool odd = s_nonfinite != 0;
     consumer_sync();
-    if (tid == 0) s_nonfinite = 0;  // next written after the next segment's barrier
+    if (odd) {
+      add_nonfinite<D, kRowGroups>(a, s, s_out, s_m);
+      if (tid == 0) s_nonfinite = 0;  // next written after the next segment's barrier
+      consumer_sync();
+    }
 
     float *part = partial_at(a, 2 * (int)blockIdx.x + (s.first == 0 ? 1 : 0), kTileRows, D);
     for (int i = tid; i < s.count * (D / 4); i += kConsumers) {

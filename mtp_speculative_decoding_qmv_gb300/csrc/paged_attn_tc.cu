@@ -134,33 +134,6 @@ __device__ __noinline__ void add_and_write(const Args &a, int q0, int h, int r, 
   if (ok && a.lse) a.lse[(long long)(q0 + t) * a.Hq + h * a.G + g] = row_lse(a, mm, ll);
 }
 
-// Rows [rr, rr + count) of the item at r0, one by one by a warp (attend_row):
-// whole results (slot -1), or the partial of this slot.
-template <int D>
-__device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
-                                        int r0, int rr, int count, int j0, int j1, int slot) {
-  const int lane = threadIdx.x & 31;
-  for (int i = 0; i < count; ++i, ++rr) {
-    float o[D / 32], m, l;
-    attend_row<D>(a, b, h, q0, n, len, r0 + rr, j0, j1, o, m, l);
-    if (slot < 0) {
-      store_lane<D>(a, q0, h, r0 + rr, o, m, l);
-    } else {
-      float *part = part_row<D>(a, slot, rr);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        const int d = lane * (D / 32) + e;
-        __stcg(part + (size_t)(d >> 2) * kRows * 4 + (d & 3), o[e]);
-      }
-      if (lane == 0) {
-        float *ml = partial_at(a, slot, kRows, D) + kRows * D + rr;
-        __stcg(ml, m);
-        __stcg(ml + kRows, l);
-      }
-    }
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -173,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ long long s_scan[kThreads / 32], s_base;
   __shared__ uint32_t s_row[2][kTile];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_b, s_odd[2], s_last[2];
+  __shared__ int s_b, s_last[2];
+  __shared__ uint32_t s_odd[2][2];  // items with non-finite values left out (see the softmax)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t q_smem = raw + ((1024u - (raw & 1023u)) & 1023u);
   const uint32_t ring0 = q_smem + 2 * S::kTileBytes;
@@ -191,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i][0], 4);
       mbar_init(&p_full[i][1], 4);
       mbar_init(&o_done[i], 1);
-      s_odd[i] = 0;
+      s_odd[i][0] = s_odd[i][1] = 0;
     }
     mbar_init(&mma_done, 1);
     fence_mbar_init();
@@ -403,6 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     Ring ring;  // of the segment's first key slot
     uint32_t sn = 0;  // key tiles done by this group
+    // The first group clears the values of masked places for both, and where one
+    // that some rows attend was not finite it leaves the item's number among those
+    // of two row tiles (or of one) in s_odd, for the rows to add it at the end.
+    // Numbers alternate between two words: an item's products wait for the
+    // weights of all warps concerned, so a word is written again only when all
+    // have read it.
+    uint32_t items[2] = {0, 0};
     auto wait = [&](uint64_t *bar, uint32_t phase) {
       if (!mbar_test(bar, phase) && !dead && !mbar_wait(bar, phase)) {
         dead = true;
@@ -419,7 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = a.window > 0 ? last - a.window + 1 : 0;
       const Span own = count > 0 ? rows_span(a, s.rq, s.r0 + wg * kTile, count) : s.span;
       float m = kNegInf, l = 0.f;
-      bool any_masked = false;
+      const bool two = s.count > kTile;
+      uint32_t item_no = 0;
+      if (s.tiles > 0) item_no = two ? ++items[1] : ++items[0];
+      volatile uint32_t *odd_word = &s_odd[two ? 1 : 0][item_no & 1u];
       if (count > 0) {
         for (int t = 0; t < s.tiles; ++t, ++sn) {
           const int j0 = (s.tile0 + t) * kBK;
@@ -434,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) pin(x[q]);
           if (masked) {
-            any_masked = true;
             const int lo = first - j0, hi = last - j0;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -483,32 +466,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (masked) {
-            // places no row of the item attends may hold anything: the first
-            // tile's group zeroes their values, so that a weight of zero meets
-            // no NaN; a non-finite value that some rows of the tile attend and
-            // others do not sends the segment to the row-by-row path
+          if (wg == 0 && (j0 < s.span.all_lo || j0 + kBK > s.span.all_hi)) {
+            // places no row of the item attends may hold anything: their values
+            // are zeroed, so that a weight of zero meets no NaN, and so is what is
+            // not finite where some rows attend and others do not
             wait(&kv_full[ring.slot], ring.phase);
             uint8_t *v = smem_raw + (ring0 - raw) + ring.slot * S::kTileBytes + row * 16;
-            uint32_t odd = 0;
+            bool odd = false;
 #pragma unroll 1
             for (int i = 0; i < kBK / 16; ++i) {  // eight threads a key: a warp reads 512 bytes
               const int p0 = j0 + i * 16, pos = p0 + (row >> 3);
-              if (p0 >= own.all_lo && p0 + 16 <= own.all_hi) continue;
+              if (p0 >= s.span.all_lo && p0 + 16 <= s.span.all_hi) continue;
               const bool none = pos < s.span.lo || pos >= s.span.hi;
-              const bool part = !none && (pos < own.all_lo || pos >= own.all_hi);
+              const bool part = !none && (pos < s.span.all_lo || pos >= s.span.all_hi);
+              uint4 *at = reinterpret_cast<uint4 *>(v + i * 2048), y[D / 64];
+              if (part) {
+                uint32_t bits = 0;
 #pragma unroll
-              for (int blk = 0; blk < D / 64; ++blk) {
-                uint4 *at = reinterpret_cast<uint4 *>(v + blk * S::kBlock + i * 2048);
-                if (part) {
-                  const uint4 y = *at;
-                  odd |= nonfinite_bits(y.x) | nonfinite_bits(y.y) | nonfinite_bits(y.z) |
-                         nonfinite_bits(y.w);
+                for (int blk = 0; blk < D / 64; ++blk) {
+                  y[blk] = at[blk * (S::kBlock / 16)];
+                  bits |= nonfinite_bits(y[blk]);
                 }
-                if (none && wg == 0) *at = make_uint4(0, 0, 0, 0);
+                if (bits) {
+                  odd = true;
+#pragma unroll
+                  for (int blk = 0; blk < D / 64; ++blk) {
+                    clear_nonfinite(y[blk]);
+                    at[blk * (S::kBlock / 16)] = y[blk];
+                  }
+                }
               }
+              if (none)
+#pragma unroll
+                for (int blk = 0; blk < D / 64; ++blk)
+                  at[blk * (S::kBlock / 16)] = make_uint4(0, 0, 0, 0);
             }
-            if (odd) s_odd[wg] = 1;
+            if (odd) *odd_word = item_no;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
@@ -552,19 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = s.first == 0 && s.n_units == s.width;
         const int slot = 2 * (int)blockIdx.x + (s.first == 0 ? 1 : 0);
         const int rr = wg * kTile + row;
-        bool odd = false;
-        if (any_masked) {  // the same for the group
-          group_sync(wg);
-          odd = s_odd[wg] != 0;
-          group_sync(wg);
-          if (row == 0) s_odd[wg] = 0;
-          group_sync(wg);  // before the next item's tiles may set it
-        }
         // A split item's CTAs c0 .. c1.  When all others have left their partials,
         // this one adds them to what it holds and writes the result.
         const int c0 = whole ? 0 : runs.owner(s.item);
         const int c1 = whole ? 0 : runs.owner(s.item + s.width - kItemUnits<kRows> - 1);
-        bool direct = !whole && !odd && c1 - c0 < kDirect;
+        bool direct = !whole && c1 - c0 < kDirect;
         unsigned *arrivals = nullptr, arrived = 0;
         if (direct && row == 0) {
           arrivals = a.counters + wg * 3 * gridDim.x +
@@ -574,6 +559,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s.tiles > 0) {
           wait(&o_done[wg], (sn - 1u) & 1u);
           tc_fence_after();
+          if (*odd_word == item_no)
+            add_nonfinite<D, D>(a, s.b, s.h, max(s.span.lo, s.tile0 * kBK),
+                                min(s.span.hi, (s.tile0 + s.tiles) * kBK), s.span.all_lo,
+                                s.span.all_hi,
+                                ok ? a.q + (long long)(s.rq.q0 + t_row) * a.q_stride +
+                                         (long long)(s.h * a.G + (r - t_row * a.G)) * D
+                                   : nullptr,
+                                first, last, o_at, 0);
         }
         if (direct) {
           if (row == 0) {
@@ -586,10 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (direct) {
           add_and_write<D>(a, s.rq.q0, s.h, r, rr, ok, s.tiles > 0, o_at, m, l, c0, c1);
-        } else if (odd) {
-          rows_plain<D>(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, wg * kTile + (warp & 3) * 32,
-                        min(count - (warp & 3) * 32, 32), s.tile0 * kBK,
-                        (s.tile0 + s.tiles) * kBK, whole ? -1 : slot);
         } else {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int g = r - t_row * a.G, t0 = (s.r0 + wg * kTile) / a.G;

@@ -56,31 +56,6 @@ __device__ __forceinline__ void pair_sync() {  // both softmax groups
   asm volatile("bar.sync 3, 256;" ::: "memory");
 }
 
-// Rows [rr, rr + count) of the item at r0, one by one by a warp (attend_row):
-// whole results (slot -1), or the partial of this slot.
-__device__ __noinline__ void rows_plain(const Args &a, int b, int h, int q0, int n, int len,
-                                        int r0, int rr, int count, int j0, int j1, int slot) {
-  const int lane = threadIdx.x & 31;
-  for (int i = 0; i < count; ++i, ++rr) {
-    float o[D / 32], m, l;
-    attend_row<D>(a, b, h, q0, n, len, r0 + rr, j0, j1, o, m, l);
-    if (slot < 0) {
-      store_lane<D>(a, q0, h, r0 + rr, o, m, l);
-    } else {
-      float *part = part_base(a, slot) + rr * 4;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        const int d = lane * (D / 32) + e;
-        __stcg(part + (size_t)(d >> 2) * kRows * 4 + (d & 3), o[e]);
-      }
-      if (lane < 2) {
-        __stcg(part_ml(a, slot, lane) + rr, m);
-        __stcg(part_ml(a, slot, lane) + kRows + rr, l);
-      }
-    }
-  }
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc256_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
@@ -382,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (masked) {
           // as in paged_attn_tc.cu, two blocks of the tile's values a group
           const uint32_t vg = g0 + (t + 1 < s.tiles ? 2 + 2 * t : 2 * s.tiles - 1);
-          uint32_t odd = 0;
+          bool odd = false;
           // the values before these in the slot have landed when their product
           // is done (at a first tile it held what is long multiplied)
           if (t > 0) wait_product(sn - 1u);
@@ -400,9 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (none) {
                 *at = make_uint4(0, 0, 0, 0);
               } else if (pos < s.span.all_lo || pos >= s.span.all_hi) {
-                const uint4 y = *at;
-                odd |= nonfinite_bits(y.x) | nonfinite_bits(y.y) | nonfinite_bits(y.z) |
-                       nonfinite_bits(y.w);
+                uint4 y = *at;
+                if (nonfinite_bits(y)) {
+                  clear_nonfinite(y);
+                  *at = y;
+                  odd = true;
+                }
               }
             }
           }
@@ -453,78 +431,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s.tiles > 0) {
         wait_product(sn - 1u);
         tc_fence_after();
+        if (odd)
+          add_nonfinite<D, D / 2>(a, s.b, s.h, max(s.span.lo, s.tile0 * kBK),
+                                  min(s.span.hi, (s.tile0 + s.tiles) * kBK), s.span.all_lo,
+                                  s.span.all_hi,
+                                  ok ? a.q + (long long)(s.rq.q0 + t_row) * a.q_stride +
+                                           (long long)(s.h * a.G + (r - t_row * a.G)) * D
+                                     : nullptr,
+                                  first, last, o_at, wg * (D / 2));
       }
       uint8_t *stage = smem_raw + (stage0 - raw) + (uint32_t)wg * kStage;
       const int g = r - t_row * a.G, t0 = s.r0 / a.G;
       if (wg == 0) s_row[row] = (uint32_t)(t_row - t0) << 16 | (uint32_t)g;
       pair_sync();  // s_x has been read, s_row is written
-      if (odd) {
-        const int at = (warp & 3) * 32 + wg * 16;
-        rows_plain(a, s.b, s.h, s.rq.q0, s.rq.n, s.rq.len, s.r0, at, min(s.count - at, 16),
-                   s.tile0 * kBK, (s.tile0 + s.tiles) * kBK, whole ? -1 : slot);
-      } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        float *part = part_base(a, slot) + row * 4;
-        __nv_bfloat16 *dst = a.out + (long long)(s.rq.q0 + t0) * a.out_stride +
-                             (long long)s.h * a.G * D + wg * (D / 2);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float *part = part_base(a, slot) + row * 4;
+      __nv_bfloat16 *dst = a.out + (long long)(s.rq.q0 + t0) * a.out_stride +
+                           (long long)s.h * a.G * D + wg * (D / 2);
 #pragma unroll 1
-        for (int d = 0; d < D / 2; d += 32) {
-          uint32_t o[32];
-          if (s.tiles > 0) {
-            tc_ld_x32(o_at + d, o);
-            tc_wait_ld();
-            pin(o);
-          } else {
+      for (int d = 0; d < D / 2; d += 32) {
+        uint32_t o[32];
+        if (s.tiles > 0) {
+          tc_ld_x32(o_at + d, o);
+          tc_wait_ld();
+          pin(o);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (whole) {
+          // through shared memory: four threads write 64 bytes of a row
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            auto two = [&](int k) {
+              return pack_bf16(__uint_as_float(o[i + k]) * inv,
+                               __uint_as_float(o[i + k + 1]) * inv);
+            };
+            *reinterpret_cast<uint4 *>(stage + row * 64 +
+                                       (((i >> 3) ^ ((row >> 1) & 3)) << 4)) =
+                make_uint4(two(0), two(2), two(4), two(6));
           }
-          if (whole) {
-            // through shared memory: four threads write 64 bytes of a row
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              auto two = [&](int k) {
-                return pack_bf16(__uint_as_float(o[i + k]) * inv,
-                                 __uint_as_float(o[i + k + 1]) * inv);
-              };
-              *reinterpret_cast<uint4 *>(stage + row * 64 +
-                                         (((i >> 3) ^ ((row >> 1) & 3)) << 4)) =
-                  make_uint4(two(0), two(2), two(4), two(6));
-            }
-            group_sync(wg);
+          group_sync(wg);
 #pragma unroll 4
-            for (int i = row >> 2; i < s.count; i += 32) {
-              const uint32_t at = s_row[i];
-              const uint4 y = *reinterpret_cast<const uint4 *>(
-                  stage + i * 64 + (((row & 3) ^ ((i >> 1) & 3)) << 4));
-              *reinterpret_cast<uint4 *>(dst + (at >> 16) * a.out_stride + (at & 0xFFFFu) * D + d +
-                                         (row & 3) * 8) = y;
-            }
-            group_sync(wg);
-          } else if (ok) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              __stcg(reinterpret_cast<uint4 *>(
-                         part + (size_t)((wg * (D / 2) + d + i) >> 2) * kRows * 4),
-                     make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+          for (int i = row >> 2; i < s.count; i += 32) {
+            const uint32_t at = s_row[i];
+            const uint4 y = *reinterpret_cast<const uint4 *>(
+                stage + i * 64 + (((row & 3) ^ ((i >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4 *>(dst + (at >> 16) * a.out_stride + (at & 0xFFFFu) * D + d +
+                                       (row & 3) * 8) = y;
           }
-          __syncwarp();
+          group_sync(wg);
+        } else if (ok) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            __stcg(reinterpret_cast<uint4 *>(
+                       part + (size_t)((wg * (D / 2) + d + i) >> 2) * kRows * 4),
+                   make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
-        if (ok && whole && a.lse && wg == 0)
-          a.lse[(long long)(s.rq.q0 + t_row) * a.Hq + s.h * a.G + g] = row_lse(a, m, l);
-        if (ok && !whole) {
-          __stcg(part_ml(a, slot, wg) + row, m);
-          __stcg(part_ml(a, slot, wg) + kRows + row, l);
-        }
+        __syncwarp();
+      }
+      if (ok && whole && a.lse && wg == 0)
+        a.lse[(long long)(s.rq.q0 + t_row) * a.Hq + s.h * a.G + g] = row_lse(a, m, l);
+      if (ok && !whole) {
+        __stcg(part_ml(a, slot, wg) + row, m);
+        __stcg(part_ml(a, slot, wg) + kRows + row, l);
       }
       tc_fence_before();  // O has been read before the next segment's products write it
       if (!whole) {
         // ---- the last CTA to arrive joins this group's columns ----
         const int c0 = runs.owner(s.item), c1 = runs.owner(s.item + s.width - kItemUnits<kRows> - 1);
         float *weights = reinterpret_cast<float *>(stage);  // [partial][row]
-        if (odd) {  // both groups wrote for both
-          __threadfence();
-          pair_sync();
-        }
         for (int again = 0; again < 2; ++again) {
           const Group gr = join_group(c0, c1, (int)blockIdx.x, again != 0, (int)gridDim.x);
           __threadfence();

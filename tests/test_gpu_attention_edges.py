@@ -1,13 +1,14 @@
 """paged_attention where a CTA goes from one item to the next: split requests
-beside refused ones."""
+beside refused ones, non-finite values that some rows attend and others do not."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import attention_ref as ref
 from gpu_util import dev, sv_module
-from test_gpu_paged_attention import _dense
+from test_gpu_paged_attention import Case, _dense
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,60 @@ def test_items_with_infinities_one_after_another(sv, D):
         out = sv.paged_attention(*c.args(), 100, workspace=ws)[0].view(B, new, Hq, D).double()
         assert torch.equal(torch.isposinf(out), infinite)
         assert _close(out[~infinite], want[~infinite])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [4, 30, 100, 150])  # with G = 2: row tiles of 16 to 256, two items
+@pytest.mark.parametrize("window", [0, 20, 130])
+def test_non_finite_values_reach_the_rows_that_attend_them(sv, D, new, window):
+    """Infinities of both signs and NaN in the first and last places of the rows:
+    the same places are infinite and NaN as in float64, the others as exact as
+    ever."""
+    c = Case(D, 4, 2, 32, [340, 5], [new, 2], seed=D + new + window)
+    first = 340 - new
+    places = [339, 338, first + 1, first + new // 2]
+    if window:
+        places += [max(0, first - window + 3), max(0, first + new // 2 - window + 1)]
+    for i, j in enumerate(places):
+        p, o = c.table[0, j // 32], j % 32
+        c.v[p, :, o, i::7] = [math.inf, -math.inf, math.nan][i % 3]
+        c.v[p, 1, o, 5] = math.inf  # of several positions
+        c.v[p, 1, o, 6] = math.inf if i % 2 else -math.inf
+    c.k[c.table[0, 338 // 32], 0, 338 % 32] = -math.inf  # weight zero, or NaN
+    t = c.device()
+    lse = torch.empty(c.rows, 4, device=dev())
+    out, _ = sv.paged_attention(*t, new, scale=c.scale, window=window, lse=lse)
+    sv.device_status()
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want, want_lse, mag, smag = c.want(window)
+    assert np.array_equal(np.isnan(out), np.isnan(want))
+    infinite = np.isinf(want)
+    assert infinite.any() and np.array_equal(infinite, np.isinf(out))
+    assert np.array_equal(out[infinite], want[infinite])
+    keep = np.isfinite(smag).all(1)  # rows whose scores are finite
+    assert keep.sum() > 2
+    zero = lambda a: np.where(infinite, 0.0, a)[keep]  # noqa: E731
+    ref.check_attention(zero(out), lse[keep],
+                        (zero(want), want_lse[keep], zero(mag), smag[keep]), D, 340)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [60, 100])
+def test_an_infinity_in_a_long_context(sv, D, new):
+    """The newest token's value is infinite in every head of a context of 250,000:
+    the rows that do not attend it and the items after it are as without it."""
+    H, ctx = 40, 250000
+    c = Long(D, H, H, 128, [(ctx, new)], D)
+    clean = c.v.clone()
+    page, offset = int(c.table[0, (ctx + new - 1) // 128]), (ctx + new - 1) % 128
+    c.v[page, :, offset, ::3] = math.inf
+    out = sv.paged_attention(*c.args(), new)[0]
+    sv.device_status()
+    infinite = torch.zeros(new, 1, D, dtype=torch.bool, device=dev())
+    infinite[-1, :, ::3] = True
+    assert torch.equal(torch.isposinf(out), infinite.expand(new, H, D))
+    for h in (0, 1, 17, 38, 39):
+        want, _ = _dense(c.q[:, h:h + 1], c.k[:, h:h + 1], clean[:, h:h + 1], c.table, 128, ctx,
+                         new, c.scale)
+        assert _close(out[:, h:h + 1][~infinite], want[~infinite]), h
