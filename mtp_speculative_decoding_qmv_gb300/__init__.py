@@ -739,7 +739,14 @@ def kv_pages_step(length: torch.Tensor, held: torch.Tensor, cursor: torch.Tensor
         wanted += zip(step, _STEP_NAMES, _step_shapes(B, rows))
         _refuse("kv_pages_step", st, [(_need, t, name, torch.int32, shape, length.device)
                                       for t, name, shape in wanted])
-    return KvStep(*step)
+    step = KvStep(*step)
+    if not B:  # the library does nothing: no rows, and the ring as it is
+        if step.cursor is not cursor:
+            step.cursor.copy_(cursor)
+        step.q_start.zero_()
+        step.slots.fill_(-1)
+        step.positions.zero_()
+    return step
 
 
 def rope_freqs(inv_freq: torch.Tensor) -> torch.Tensor:

@@ -162,3 +162,21 @@ def test_an_infinity_in_a_long_context(sv, D, new):
         want, _ = _dense(c.q[:, h:h + 1], c.k[:, h:h + 1], clean[:, h:h + 1], c.table, 128, ctx,
                          new, c.scale)
         assert _close(out[:, h:h + 1][~infinite], want[~infinite]), h
+
+
+def _none(*shape):
+    return torch.zeros(shape, dtype=torch.int32, device=dev())
+
+
+def test_a_step_without_requests(sv):
+    """Its rows have no slots, and the cursor is carried on."""
+    cursor = torch.tensor([3, 5], dtype=torch.int32, device=dev())
+    given = {k: _none(n) + 9 for k, n in
+             (("cursor_out", 2), ("q_start", 1), ("slots", 6), ("positions", 6))}
+    step = sv.kv_pages_step(_none(0), _none(0), cursor, _none(8), _none(0, 4), _none(0), 16, 6,
+                            **given)
+    assert step.cursor.tolist() == [3, 5] and step.q_start.tolist() == [0]
+    assert step.slots.tolist() == [-1] * 6 and step.positions.tolist() == [0] * 6
+    step = sv.kv_pages_step(_none(0), _none(0), cursor, _none(8), _none(0, 4), _none(0), 16, 6,
+                            cursor_out=cursor)
+    assert step.cursor is cursor and cursor.tolist() == [3, 5]
