@@ -581,7 +581,7 @@ sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x
  * (G = Hq / Hkv) read kv head h:
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)
  * A row that attends nothing (p < 0) is zero with lse -inf, and so are rows
- * from q_start[B] on.  Positions j come from page block_table[b][j / page_size];
+ * from q_start[B] on (B = 0 is a no-op).  Positions j come from page block_table[b][j / page_size];
  * a page id outside [0, num_pages) reads as zeros.  What no row attends is not
  * read, or has no effect whatever it holds: slots past kv_len, pages before
  * the window, later tokens of a chunk, NaN and infinities included.

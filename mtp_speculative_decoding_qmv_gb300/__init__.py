@@ -875,4 +875,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         if lse is not None:
             wanted.append((_need, lse, "lse", torch.float32, (rows, Hq)))
         _refuse("paged_attention", st, [w + (q.device,) for w in wanted])
+    if not block_table.shape[0]:  # the library does nothing: rows past the last request's
+        out.zero_()
+        if lse is not None:
+            lse.fill_(-math.inf)
     return out, lse

@@ -180,3 +180,14 @@ def test_a_step_without_requests(sv):
     step = sv.kv_pages_step(_none(0), _none(0), cursor, _none(8), _none(0, 4), _none(0), 16, 6,
                             cursor_out=cursor)
     assert step.cursor is cursor and cursor.tolist() == [3, 5]
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_without_requests_attend_nothing(sv, D):
+    q = torch.ones(6, 4, D, dtype=torch.bfloat16, device=dev())
+    cache = torch.ones(8, 2, 16, D, dtype=torch.bfloat16, device=dev())
+    out, lse = torch.full_like(q, 7.0), torch.full((6, 4), 7.0, device=dev())
+    for rows in (6, 0):
+        got, got_lse = sv.paged_attention(q[:rows], cache, cache, _none(0, 4), _none(1), _none(0),
+                                          4, out=out[:rows], lse=lse[:rows])
+        assert (got == 0).all() and torch.isneginf(got_lse).all() and len(got) == rows
