@@ -23,7 +23,7 @@ INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libspecverify.so"
 CHECKS = PKG / "_tensors.so"
-CUDA = "/usr/local/cuda"
+CHECKS_FOR = BUILD / "_tensors.for"  # what _tensors.so was compiled for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,30 +45,46 @@ def _stale(target: Path, deps: list[Path]) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def interpreter() -> str:
+    """What the extension's ABI depends on: torch and Python."""
+    import torch
+
+    return f"torch {torch.__version__} at {torch.__file__}, Python {sys.version}"
+
+
+def checks_stale() -> bool:
+    """_tensors.so is older than its sources, or was compiled for another torch."""
+    return (_stale(CHECKS, [CSRC / "tensors.cpp", INCLUDE / "specverify.h", Path(__file__)])
+            or not CHECKS_FOR.exists() or CHECKS_FOR.read_text() != interpreter())
+
+
 def build_checks() -> None:
     """The CPython extension of csrc/tensors.cpp."""
     import torch
 
+    cuda = Path(nvcc()).resolve().parents[1]
     src = CSRC / "tensors.cpp"
     root = Path(torch.__file__).parent
     tmp = CHECKS.with_suffix(".so.tmp")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
-           "-I" + sysconfig.get_paths()["include"], f"-I{CUDA}/include", f"-I{INCLUDE}", str(src), "-o", str(tmp),
+           "-I" + sysconfig.get_paths()["include"], f"-I{cuda / 'include'}", f"-I{INCLUDE}",
+           str(src), "-o", str(tmp),
            f"-L{root / 'lib'}", f"-Wl,-rpath,{root / 'lib'}", "-ltorch_python", "-ltorch_cpu",
            "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src.name}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CHECKS)
+    BUILD.mkdir(exist_ok=True)
+    CHECKS_FOR.write_text(interpreter())
 
 
 def build(force: bool = False, debug: bool = False, verbose: bool = False) -> Path:
     headers = list(CSRC.glob("*.h")) + list(CSRC.glob("*.cuh")) + list(INCLUDE.glob("*.h"))
     srcs = sources()
-    checks = force or _stale(CHECKS, [CSRC / "tensors.cpp", INCLUDE / "specverify.h",
-                                       Path(__file__)])
+    checks = force or checks_stale()
     if not force and not _stale(LIB, srcs + headers + [Path(__file__)]):
         if checks:
             build_checks()
