@@ -191,3 +191,63 @@ def test_rows_without_requests_attend_nothing(sv, D):
         got, got_lse = sv.paged_attention(q[:rows], cache, cache, _none(0, 4), _none(1), _none(0),
                                           4, out=out[:rows], lse=lse[:rows])
         assert (got == 0).all() and torch.isneginf(got_lse).all() and len(got) == rows
+
+
+def test_two_streams_at_once(sv):
+    """Calls of both families side by side, each stream with its workspace: the
+    bits of calls one after another."""
+    d = dev()
+    cases = [(Long(128, 8, 2, 16, [(9000, 300), (None, 5), (200, 40)], 1), 300),
+             (Long(128, 8, 2, 64, [(20000, 4), (300, 1), (7, 4)], 2), 4)]
+    work = []
+    for c, most in cases:
+        ws = sv.make_attention_workspace(128, d)
+        out = torch.empty_like(c.q)
+        sv.paged_attention(*c.args(), most, out=out, workspace=ws)
+        work.append((c, most, ws, out.clone(), [torch.empty_like(out) for _ in range(30)],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(30):
+        for c, most, ws, _, outs, stream in work:
+            with torch.cuda.stream(stream):
+                sv.paged_attention(*c.args(), most, out=outs[i], workspace=ws)
+    torch.cuda.synchronize()
+    sv.device_status()
+    for _, _, _, want, outs, _ in work:
+        assert all(torch.equal(o, want) for o in outs)
+
+
+def test_the_calls_allocate_nothing(sv):
+    d = dev()
+    B, rows, page, D = 3, 7, 16, 64
+    i32 = dict(dtype=torch.int32, device=d)
+    length, held, cursor = _none(B), _none(B), torch.tensor([0, 64], **i32)
+    ring, table, n_new = torch.arange(64, **i32), _none(B, 8), torch.tensor([4, 1, 2], **i32)
+    commit = torch.tensor([1, 1, 1], **i32)
+    kw = dict(length_out=length, held_out=held, cursor_out=cursor, q_start=_none(B + 1),
+              kv_len=_none(B), slots=_none(rows), positions=_none(rows), err_flags=_none(B))
+    x = torch.randn(rows, 8, D, device=d)
+    cache = torch.zeros(2, 64, 2, page, D, dtype=torch.bfloat16, device=d)
+    freqs = sv.rope_freqs(torch.ones(8, dtype=torch.float64, device=d))
+    q, out = (torch.empty(rows, 4, D, dtype=torch.bfloat16, device=d) for _ in range(2))
+    lse, ws = torch.empty(rows, 4, device=d), sv.make_attention_workspace(D, d)
+
+    def step():
+        s = sv.kv_pages_step(length, held, cursor, ring, table, n_new, page, rows, n_commit=commit,
+                             **kw)
+        sv.rope_kv_append(x[:, :4], x[:, 4:6], x[:, 6:], s.positions, s.slots, freqs, cache[0],
+                          cache[1], q_out=q)
+        for most in (4, 100):  # both families
+            sv.paged_attention(q, cache[0], cache[1], table, s.q_start, s.kv_len, most, out=out,
+                               lse=lse, workspace=ws)
+
+    def held_memory():
+        torch.cuda.synchronize()
+        return (torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0])
+
+    step()
+    before = held_memory()
+    for _ in range(5):
+        step()
+    assert held_memory() == before
+    assert torch.isfinite(out.float()).all()
