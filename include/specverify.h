@@ -553,8 +553,9 @@ sv_status kv_pages_step(const int32_t *length, const int32_t *held, const int32_
  *     x_e w_e / sqrt(mean(x^2) + eps);
  *   their first rotary_dim elements are turned: pair f of rotary_dim / 2, the
  *     elements (f, f + rotary_dim / 2), or (2f, 2f + 1) when interleaved, by
- *     the angle  2 pi 2^-64 freqs[f] * positions[row][axis[f]]  (modulo a
- *     turn, exact to 2^-34 turns at any 31-bit position);
+ *     the angle  2 pi 2^-64 freqs[f] * positions[row][axis[f]]: the product
+ *     wraps modulo a turn exactly at any 31-bit position, and is then taken to
+ *     2^-26 of a turn (1e-7 rad);
  *   q goes to q_out bf16 [rows][Hq][D], k and v to slot slots[row] of the
  *     caches bf16 [num_pages][Hkv][page_size][D]; a slot outside
  *     [0, num_pages * page_size) writes nothing to the caches.
@@ -580,7 +581,8 @@ sv_status rope_kv_append(const void *q, const void *k, const void *v, sv_dtype x
  * the request (from 0 when window is 0); its query heads h G .. h G + G - 1
  * (G = Hq / Hkv) read kv head h:
  *   out = sum_j softmax_j(scale q . k_j) v_j,   lse = ln sum_j exp(scale q . k_j)
- * A row that attends nothing (p < 0) is zero with lse -inf, and so are rows
+ * A row that attends nothing (p < 0), or whose every score is -inf, is zero
+ * with lse -inf, and so are rows
  * from q_start[B] on (B = 0 is a no-op).  Positions j come from page block_table[b][j / page_size];
  * a page id outside [0, num_pages) reads as zeros.  What no row attends is not
  * read, or has no effect whatever it holds: slots past kv_len, pages before

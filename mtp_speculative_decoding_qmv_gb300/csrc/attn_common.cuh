@@ -106,8 +106,7 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// Bounded waits that gave up, per translation unit (paged_attn.cu and
-// paged_attn_tc.cu each have their own word).
+// Bounded waits that gave up, a word for each translation unit.
 static __device__ unsigned int g_give_up;
 __device__ __forceinline__ void report_give_up(unsigned bit) { atomicOr(&g_give_up, bit); }
 

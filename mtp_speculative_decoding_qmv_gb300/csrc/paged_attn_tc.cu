@@ -190,183 +190,184 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTmaWarp) {
-    // ------------------------------ producer ------------------------------
-    const int per_page = min(kBK, 1 << a.page_shift);
-    const int pages = kBK / per_page;
-    const int boxes = pages * (D / 64);
-    const int blk = lane / pages, pg = lane - blk * pages;
-    Ring ring;
-    long long issued = 0;
-    while (!dead && walk.next(a, s)) {
-      for (int t = 0; !dead && t < s.tiles; ++t) {
-        const int j = (s.tile0 + t) * kBK + pg * per_page;
-        int y = 0;
-        if (lane < boxes)
-          y = page_row(a, s.b, s.h, j >> a.page_shift, s.span.lo, s.span.hi) +
-              (j & ((1 << a.page_shift) - 1));
-        for (int kv = 0; kv < 2; ++kv) {
-          if (issued >= S::kSlots && !mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1u)) dead = true;
-          dead = __any_sync(0xffffffffu, dead);
-          if (dead) break;
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], S::kTileBytes);
-          __syncwarp();
+      // ------------------------------ producer ------------------------------
+      const int per_page = min(kBK, 1 << a.page_shift);
+      const int pages = kBK / per_page;
+      const int boxes = pages * (D / 64);
+      const int blk = lane / pages, pg = lane - blk * pages;
+      Ring ring;
+      long long issued = 0;
+      while (!dead && walk.next(a, s)) {
+        for (int t = 0; !dead && t < s.tiles; ++t) {
+          const int j = (s.tile0 + t) * kBK + pg * per_page;
+          int y = 0;
           if (lane < boxes)
-            tma_load_rows(ring0 + ring.slot * S::kTileBytes + (uint32_t)blk * S::kBlock +
-                              (uint32_t)pg * per_page * 128,
-                          kv ? &vmap : &kmap, blk * 64, y, smem_addr(&kv_full[ring.slot]));
-          ++issued;
-          ring.advance(S::kSlots);
-        }
-      }
-    }
-    if (dead && lane == 0) report_give_up(4u);
-    // every copy has landed before the CTA may exit
-    for (long long k = max(0ll, issued - S::kSlots); k < issued; ++k)
-      (void)mbar_wait(&kv_full[k % S::kSlots], (uint32_t)((k / S::kSlots) & 1));
-  } else if (warp == kMmaWarp) {
-    // -------------------------- matrix products ---------------------------
-    // The whole warp walks and waits, so that descriptors stay in uniform
-    // registers; one lane issues.
-    constexpr uint32_t kQk = idesc(kBK, false), kPv = idesc(D, true);
-    const bool leader = elect_one();
-    Ring ring;
-    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of q_full and p_full
-    auto wait = [&](uint64_t *bar, uint32_t phase) {
-      if (!__all_sync(0xffffffffu, mbar_test(bar, phase)) && !dead)
-        dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
-      tc_fence_after();
-    };
-    const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(ring0),
-                   v_desc = smem_desc_sw128_mn(ring0, S::kBlock);
-    // a descriptor's address field counts 16-byte units: offsets add to it
-    auto qk = [&](int w, uint32_t slot, bool last) {
-      const uint64_t qd = q_desc + (uint32_t)w * (S::kTileBytes >> 4);
-      const uint64_t kd = k_desc + slot * (S::kTileBytes >> 4);
-      if (leader) {
-        if (!dead) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32) >> 4;
-            tc_mma_ss(tmem + (uint32_t)w * kBK, qd + at, kd + at, kQk, k > 0);
+            y = page_row(a, s.b, s.h, j >> a.page_shift, s.span.lo, s.span.hi) +
+                (j & ((1 << a.page_shift) - 1));
+          for (int kv = 0; kv < 2; ++kv) {
+            if (issued >= S::kSlots && !mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1u))
+          dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], S::kTileBytes);
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_rows(ring0 + ring.slot * S::kTileBytes + (uint32_t)blk * S::kBlock +
+                                (uint32_t)pg * per_page * 128,
+                            kv ? &vmap : &kmap, blk * 64, y, smem_addr(&kv_full[ring.slot]));
+            ++issued;
+            ring.advance(S::kSlots);
           }
         }
-        tc_commit(smem_addr(&s_full[w]));
-        if (last) tc_commit(smem_addr(&q_free[w]));  // the segment's queries are done with
       }
-      __syncwarp();
-    };
-    auto pv = [&](int w, uint32_t slot, bool first) {
-      const uint64_t vd = v_desc + slot * (S::kTileBytes >> 4);
+      if (dead && lane == 0) report_give_up(4u);
+      // every copy has landed before the CTA may exit
+      for (long long k = max(0ll, issued - S::kSlots); k < issued; ++k)
+        (void)mbar_wait(&kv_full[k % S::kSlots], (uint32_t)((k / S::kSlots) & 1));
+    } else if (warp == kMmaWarp) {
+      // -------------------------- matrix products ---------------------------
+      // The whole warp walks and waits, so that descriptors stay in uniform
+      // registers; one lane issues.
+      constexpr uint32_t kQk = idesc(kBK, false), kPv = idesc(D, true);
+      const bool leader = elect_one();
+      Ring ring;
+      uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // phases of q_full and p_full
+      auto wait = [&](uint64_t *bar, uint32_t phase) {
+        if (!__all_sync(0xffffffffu, mbar_test(bar, phase)) && !dead)
+          dead = !__all_sync(0xffffffffu, mbar_wait(bar, phase));
+        tc_fence_after();
+      };
+      const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(ring0),
+                     v_desc = smem_desc_sw128_mn(ring0, S::kBlock);
+      // a descriptor's address field counts 16-byte units: offsets add to it
+      auto qk = [&](int w, uint32_t slot, bool last) {
+        const uint64_t qd = q_desc + (uint32_t)w * (S::kTileBytes >> 4);
+        const uint64_t kd = k_desc + slot * (S::kTileBytes >> 4);
+        if (leader) {
+          if (!dead) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        wait(&p_full[w][half], pn[w]);
-        if (leader && !dead) {
-#pragma unroll
-          for (int k = half * (kBK / 32); k < (half + 1) * (kBK / 32); ++k)
-            tc_mma_ts(tmem + S::kOCol + (uint32_t)w * D, tmem + (uint32_t)w * kBK + k * 8,
-                      vd + k * (2048 >> 4), kPv, !first || k > 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = ((uint32_t)(k >> 2) * S::kBlock + (uint32_t)(k & 3) * 32) >> 4;
+              tc_mma_ss(tmem + (uint32_t)w * kBK, qd + at, kd + at, kQk, k > 0);
+            }
+          }
+          tc_commit(smem_addr(&s_full[w]));
+          if (last) tc_commit(smem_addr(&q_free[w]));  // the segment's queries are done with
         }
         __syncwarp();
-      }
-      pn[w] ^= 1u;
-      if (leader) tc_commit(smem_addr(&o_done[w]));
-      __syncwarp();
-    };
-    auto release = [&](uint32_t slot) {
-      if (leader) tc_commit(smem_addr(&kv_empty[slot]));
-      __syncwarp();
-    };
-    while (walk.next(a, s)) {
-      if (s.tiles == 0) continue;
-      const bool two = s.count > kTile;
-      wait(&q_full[0], qn[0]);
-      qn[0] ^= 1u;
-      wait(&kv_full[ring.slot], ring.phase);
-      qk(0, ring.slot, s.tiles == 1);
-      if (two) {
-        wait(&q_full[1], qn[1]);
-        qn[1] ^= 1u;
-        qk(1, ring.slot, s.tiles == 1);
-      }
-      release(ring.slot);
-      ring.advance(S::kSlots);
-      for (int t = 0; t < s.tiles; ++t) {
-        const uint32_t v_slot = ring.slot;
-        const bool more = t + 1 < s.tiles;
-        wait(&kv_full[v_slot], ring.phase);
+      };
+      auto pv = [&](int w, uint32_t slot, bool first) {
+        const uint64_t vd = v_desc + slot * (S::kTileBytes >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          wait(&p_full[w][half], pn[w]);
+          if (leader && !dead) {
+#pragma unroll
+            for (int k = half * (kBK / 32); k < (half + 1) * (kBK / 32); ++k)
+              tc_mma_ts(tmem + S::kOCol + (uint32_t)w * D, tmem + (uint32_t)w * kBK + k * 8,
+                        vd + k * (2048 >> 4), kPv, !first || k > 0);
+          }
+          __syncwarp();
+        }
+        pn[w] ^= 1u;
+        if (leader) tc_commit(smem_addr(&o_done[w]));
+        __syncwarp();
+      };
+      auto release = [&](uint32_t slot) {
+        if (leader) tc_commit(smem_addr(&kv_empty[slot]));
+        __syncwarp();
+      };
+      while (walk.next(a, s)) {
+        if (s.tiles == 0) continue;
+        const bool two = s.count > kTile;
+        wait(&q_full[0], qn[0]);
+        qn[0] ^= 1u;
+        wait(&kv_full[ring.slot], ring.phase);
+        qk(0, ring.slot, s.tiles == 1);
+        if (two) {
+          wait(&q_full[1], qn[1]);
+          qn[1] ^= 1u;
+          qk(1, ring.slot, s.tiles == 1);
+        }
+        release(ring.slot);
         ring.advance(S::kSlots);
-        pv(0, v_slot, t == 0);
-        // The products run in issue order, so Q K' may overwrite the columns
-        // that hold the weights of the product issued before it.
-        if (more) {
-          wait(&kv_full[ring.slot], ring.phase);
-          qk(0, ring.slot, t + 2 == s.tiles);
-        }
-        if (two) pv(1, v_slot, t == 0);
-        release(v_slot);
-        if (more) {
-          if (two) qk(1, ring.slot, t + 2 == s.tiles);
-          release(ring.slot);
+        for (int t = 0; t < s.tiles; ++t) {
+          const uint32_t v_slot = ring.slot;
+          const bool more = t + 1 < s.tiles;
+          wait(&kv_full[v_slot], ring.phase);
           ring.advance(S::kSlots);
+          pv(0, v_slot, t == 0);
+          // The products run in issue order, so Q K' may overwrite the columns
+          // that hold the weights of the product issued before it.
+          if (more) {
+            wait(&kv_full[ring.slot], ring.phase);
+            qk(0, ring.slot, t + 2 == s.tiles);
+          }
+          if (two) pv(1, v_slot, t == 0);
+          release(v_slot);
+          if (more) {
+            if (two) qk(1, ring.slot, t + 2 == s.tiles);
+            release(ring.slot);
+            ring.advance(S::kSlots);
+          }
         }
       }
-    }
-    if (dead && lane == 0) report_give_up(8u);
-    if (leader) {  // no product is in flight when the tensor memory is freed
-      tc_commit(smem_addr(&mma_done));
-      (void)mbar_wait(&mma_done, 0);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------- queries ------------------------------
-    // the next segment's are fetched while the last products of this one run
-    const int w = warp - kQueryWarp;
-    uint32_t free = 0;
-    bool loaded = false;
-    while (walk.next(a, s)) {
-      const int n = min(kTile, s.count - w * kTile);
-      if (s.tiles == 0 || n <= 0) continue;
-      if (loaded) {
-        if (!dead && !mbar_wait(&q_free[w], free)) {
-          dead = true;
-          report_give_up(32u);
-        }
-        free ^= 1u;
+      if (dead && lane == 0) report_give_up(8u);
+      if (leader) {  // no product is in flight when the tensor memory is freed
+        tc_commit(smem_addr(&mma_done));
+        (void)mbar_wait(&mma_done, 0);
       }
-      loaded = true;
       __syncwarp();
-      constexpr int kChunks = D / 8;         // 16-byte pieces of a row
-      constexpr int kStep = 32 / kChunks;    // rows at a time
-      const int ch = lane % kChunks, first = lane / kChunks;
-      // a row's address moves with its token and head, without a division a row
-      const int t = (s.r0 + w * kTile + first) / a.G;
-      int g = s.r0 + w * kTile + first - t * a.G;
-      const int dt = kStep / a.G, dg = kStep - dt * a.G;
-      const long long step = dt * a.q_stride + dg * D, carry = a.q_stride - (long long)a.G * D;
-      const __nv_bfloat16 *base =
-          a.q + (long long)s.rq.q0 * a.q_stride + (long long)s.h * a.G * D + ch * 8;
-      const __nv_bfloat16 *src = base + (long long)t * a.q_stride + (long long)g * D;
-      const uint32_t dst = q_smem + (uint32_t)w * S::kTileBytes + (uint32_t)(ch >> 3) * S::kBlock;
+    } else {
+      // ------------------------------- queries ------------------------------
+      // the next segment's are fetched while the last products of this one run
+      const int w = warp - kQueryWarp;
+      uint32_t free = 0;
+      bool loaded = false;
+      while (walk.next(a, s)) {
+        const int n = min(kTile, s.count - w * kTile);
+        if (s.tiles == 0 || n <= 0) continue;
+        if (loaded) {
+          if (!dead && !mbar_wait(&q_free[w], free)) {
+            dead = true;
+            report_give_up(32u);
+          }
+          free ^= 1u;
+        }
+        loaded = true;
+        __syncwarp();
+        constexpr int kChunks = D / 8;         // 16-byte pieces of a row
+        constexpr int kStep = 32 / kChunks;    // rows at a time
+        const int ch = lane % kChunks, first = lane / kChunks;
+        // a row's address moves with its token and head, without a division a row
+        const int t = (s.r0 + w * kTile + first) / a.G;
+        int g = s.r0 + w * kTile + first - t * a.G;
+        const int dt = kStep / a.G, dg = kStep - dt * a.G;
+        const long long step = dt * a.q_stride + dg * D, carry = a.q_stride - (long long)a.G * D;
+        const __nv_bfloat16 *base =
+            a.q + (long long)s.rq.q0 * a.q_stride + (long long)s.h * a.G * D + ch * 8;
+        const __nv_bfloat16 *src = base + (long long)t * a.q_stride + (long long)g * D;
+        const uint32_t dst = q_smem + (uint32_t)w * S::kTileBytes + (uint32_t)(ch >> 3) * S::kBlock;
 #pragma unroll 4
-      for (int rr = first; rr < kTile; rr += kStep) {
-        const bool real = rr < n;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         dst + (uint32_t)rr * 128 + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4)),
-                     "l"(real ? src : base), "r"(real ? 16 : 0)
-                     : "memory");
-        src += step;
-        g += dg;
-        if (g >= a.G) {
-          g -= a.G;
-          src += carry;
+        for (int rr = first; rr < kTile; rr += kStep) {
+          const bool real = rr < n;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           dst + (uint32_t)rr * 128 + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4)),
+                       "l"(real ? src : base), "r"(real ? 16 : 0)
+                       : "memory");
+          src += step;
+          g += dg;
+          if (g >= a.G) {
+            g -= a.G;
+            src += carry;
+          }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[w]);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[w]);
     }
-  }
   } else {
     // ------------------------------- softmax ------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));

@@ -16,8 +16,8 @@
 // as turns per position in 64-bit fixed point (2^-64 turns): the product with
 // the integer position wraps modulo one turn by itself and is exact to
 // position x 2^-65 turns.  Its top 32 bits, a signed fraction of a turn, go to
-// sincospi: an absolute error near 2e-7 rad at any position, with no double
-// precision arithmetic.
+// sincospi as a float (2^-26 turns at most off): an absolute error near 2e-7 rad
+// at any position, with no double precision arithmetic.
 //
 // Memory traffic is the bound: each input read once, each output written once.
 // A lane holds eight consecutive elements of a head (one or two 16-byte loads),
@@ -29,7 +29,7 @@
 // away (one shuffle).
 //
 // Measured (GB300): 8191 rows of 20 + 4 + 4 bf16 heads of 256, normed, a quarter
-// turned: 52.4 us (235 MB, 4.5 TB/s), with 65 % of the issue slots used, most by
+// turned: 52.4 us (235 MB, 4.5 TB/s), with 60 % of the issue slots used, most by
 // the norm's and the turn's fp32 work.  From fp32, without the norm, it streams
 // at 6.0 TB/s.  4 rows: 2.1 us, 128 rows: 3.1 us, the launch and one round trip
 // to memory.
