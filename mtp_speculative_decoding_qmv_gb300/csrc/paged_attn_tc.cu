@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 (j & ((1 << a.page_shift) - 1));
           for (int kv = 0; kv < 2; ++kv) {
             if (issued >= S::kSlots && !mbar_wait(&kv_empty[ring.slot], ring.phase ^ 1u))
-          dead = true;
+              dead = true;
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             if (lane == 0) mbar_arrive_expect_tx(&kv_full[ring.slot], S::kTileBytes);
