@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t_row = ok ? r / a.G : 0;
       const int last = ok ? s.rq.len - s.rq.n + t_row : -1;
       const int first = a.window > 0 ? last - a.window + 1 : 0;
-      const Span own = count > 0 ? rows_span(a, s.rq, s.r0 + wg * kTile, count) : s.span;
       float m = kNegInf, l = 0.f;
       const bool two = s.count > kTile;
       uint32_t item_no = 0;
@@ -408,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (count > 0) {
         for (int t = 0; t < s.tiles; ++t, ++sn) {
           const int j0 = (s.tile0 + t) * kBK;
-          const bool masked = j0 < own.all_lo || j0 + kBK > own.all_hi;
+          const bool masked = j0 < s.span.all_lo || j0 + kBK > s.span.all_hi;
           ring.advance(S::kSlots);  // to the tile's values
           wait(&s_full[wg], sn & 1u);
           tc_fence_after();
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (wg == 0 && (j0 < s.span.all_lo || j0 + kBK > s.span.all_hi)) {
+          if (wg == 0 && masked) {
             // places no row of the item attends may hold anything: their values
             // are zeroed, so that a weight of zero meets no NaN, and so is what is
             // not finite where some rows attend and others do not
