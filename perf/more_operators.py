@@ -33,44 +33,44 @@ def listed():
     return [
         # one request's verify block of K + 1 = 4 rows, fp32 to fp32 for the tape;
         # its window is committed later
-        {"name": "inputs, one verify block", "op": "inputs", "seqs": 1, "new_lo": 4, "new_hi": 4,
+        {"name": "inputs: one verify block", "op": "inputs", "seqs": 1, "new_lo": 4, "new_hi": 4,
          "kheads": 48, "heads": 48, "dk": 128, "dv": 128, "width": 4, "src": "f32", "dst": "f32",
          "update": False, "mix": 1},
         # a server's single tokens, shared key heads
-        {"name": "inputs, 256 tokens", "op": "inputs", "seqs": 256, "new_lo": 1, "new_hi": 1,
+        {"name": "inputs: 256 tokens", "op": "inputs", "seqs": 256, "new_lo": 1, "new_hi": 1,
          "kheads": 16, "heads": 48, "dk": 128, "dv": 128, "width": 4, "src": "bf16", "dst": "bf16",
          "update": True, "mix": 2},
         # chunks of three prompts
-        {"name": "inputs, prompts", "op": "inputs", "seqs": 3, "new_lo": 1000, "new_hi": 4001,
+        {"name": "inputs: prompts", "op": "inputs", "seqs": 3, "new_lo": 1000, "new_hi": 4001,
          "kheads": 16, "heads": 48, "dk": 128, "dv": 128, "width": 4, "src": "bf16", "dst": "bf16",
          "update": True, "mix": 3},
         # a single token of one request: latency
-        {"name": "advance, one token", "op": "advance", "seqs": 1, "new_lo": 1, "new_hi": 1,
+        {"name": "advance: one token", "op": "advance", "seqs": 1, "new_lo": 1, "new_hi": 1,
          "kheads": 16, "heads": 48, "dk": 128, "dv": 128, "dtype": "bf16", "empty": False, "mix": 4},
         # single tokens of a batch: the states' traffic
-        {"name": "advance, 64 tokens", "op": "advance", "seqs": 64, "new_lo": 1, "new_hi": 1,
+        {"name": "advance: 64 tokens", "op": "advance", "seqs": 64, "new_lo": 1, "new_hi": 1,
          "kheads": 48, "heads": 48, "dk": 128, "dv": 128, "dtype": "bf16", "empty": False, "mix": 5},
         # a few fp32 rows each, narrow keys, a sequence without rows
-        {"name": "advance, short ragged", "op": "advance", "seqs": 9, "new_lo": 1, "new_hi": 13,
+        {"name": "advance: short ragged", "op": "advance", "seqs": 9, "new_lo": 1, "new_hi": 13,
          "kheads": 20, "heads": 20, "dk": 64, "dv": 128, "dtype": "f32", "empty": True, "mix": 6},
         # one whole prompt
-        {"name": "advance, one prompt", "op": "advance", "seqs": 1, "new_lo": 5000, "new_hi": 5000,
+        {"name": "advance: one prompt", "op": "advance", "seqs": 1, "new_lo": 5000, "new_hi": 5000,
          "kheads": 48, "heads": 48, "dk": 128, "dv": 128, "dtype": "bf16", "empty": False, "mix": 7},
         # prompts of different lengths, packed, shared key heads
-        {"name": "advance, packed prompts", "op": "advance", "seqs": 5, "new_lo": 77,
+        {"name": "advance: packed prompts", "op": "advance", "seqs": 5, "new_lo": 77,
          "new_hi": 2001, "kheads": 16, "heads": 48, "dk": 128, "dv": 128, "dtype": "bf16",
          "empty": False, "mix": 8},
         # one token, many small experts: latency
-        {"name": "experts, one token", "op": "experts", "rows": 1, "hidden": 2048, "inter": 512,
+        {"name": "experts: one token", "op": "experts", "rows": 1, "hidden": 2048, "inter": 512,
          "experts": 256, "top": 8},
         # a verify block of a wide model
-        {"name": "experts, verify block", "op": "experts", "rows": 4, "hidden": 5120,
+        {"name": "experts: verify block", "op": "experts", "rows": 4, "hidden": 5120,
          "inter": 1024, "experts": 64, "top": 6},
         # a few requests' tokens, sizes that no tile divides
-        {"name": "experts, 19 tokens", "op": "experts", "rows": 19, "hidden": 2560, "inter": 896,
+        {"name": "experts: 19 tokens", "op": "experts", "rows": 19, "hidden": 2560, "inter": 896,
          "experts": 60, "top": 4},
         # 32 verify blocks
-        {"name": "experts, 32 verify blocks", "op": "experts", "rows": 128, "hidden": 2048,
+        {"name": "experts: 32 verify blocks", "op": "experts", "rows": 128, "hidden": 2048,
          "inter": 1024, "experts": 96, "top": 6},
     ]
 
