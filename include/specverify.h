@@ -19,6 +19,10 @@
  *                     (gate, innovation, key) tape per token and head
  *   gdn_tape_replay   rebuild the recurrent state over an accepted prefix
  *   conv_window_*     short convolution windows: outputs, commit of a prefix
+ *   gdn_inputs        a GatedDeltaNet layer's convolution, head norms and gates
+ *                     over packed rows
+ *   gdn_advance       the gated delta rule over packed rows: single tokens and
+ *                     prompts, the states in place
  *   qmv_identity_probe  start-up check: block verify rows == single-row calls
  *   qmv_requantize    a bf16 weight matrix -> the 4-bit layout above (the
  *                     drafter's own 4-bit LM head)
@@ -34,8 +38,8 @@
  *
  * Conventions (all entry points):
  *  - Every tensor argument is a DEVICE pointer owned by the caller, to
- *    contiguous row-major memory (rope_kv_append and paged_attention take a
- *    row stride for their packed rows).  The library allocates no device memory and
+ *    contiguous row-major memory (rope_kv_append, paged_attention, gdn_inputs
+ *    and gdn_advance take a row stride for their packed rows).  The library allocates no device memory and
  *    keeps no pointer after a call returns, except a qmv plan (below), which
  *    holds the pointers it was created with.
  *  - Calls are asynchronous on `stream` (NULL = the legacy default stream) and
@@ -498,6 +502,65 @@ sv_status conv_window_capture(const float *window, const float *x, const float *
 sv_status conv_window_replay(float *window, const float *x, const int32_t *n_replay,
                              int n_replay_count, int n_replay_bias, int B, int T, int C, int W,
                              int32_t *err_flags, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* GatedDeltaNet layers over packed rows: prompts and single tokens.         */
+/* ------------------------------------------------------------------------ */
+/* The tape above serves a verify block, whose tokens may be rejected.  These
+ * two take tokens that stand -- prompts, chunks of prompts, single tokens --
+ * through such a layer: packed rows as in the attention layers below, sequence
+ * b's at q_start[b] .. q_start[b+1] (int32 [B+1], ascending from 0, clamped to
+ * [0, rows]), lengths mixed as they come, zero included.  The state and the
+ * window of sequence b are those of slot state_index[b] / window_index[b] (b
+ * itself where the index is NULL); distinct sequences have distinct slots.  A
+ * sequence whose slot is outside [0, slots) has zeros for its rows and touches
+ * nothing else, and so have the rows from q_start[B] on.  max_new: the
+ * caller's bound on a sequence's rows, which picks the kernel; a longer
+ * sequence is still computed.  Hv is a multiple of Hk: v head h goes with q and
+ * k head h / (Hv / Hk).  dk and dv are multiples of 8 in [8, 128].
+ *
+ * gdn_inputs: from a row x of C = 2 Hk dk + Hv dv channels (q heads, k heads,
+ * v heads) and its gate projections a, b [rows][Hv]:
+ *   y     = silu(causal depthwise convolution of width W)  (weight [W][C] and
+ *           window [slots][W-1][C] as in conv_window_capture; silu(z) =
+ *           z / (1 + exp(-z)))
+ *   q     = q_scale y_q / sqrt(sum(y_q^2) + eps)  per head,
+ *   k     = y_k / sqrt(sum(y_k^2) + eps)  per head,   v = y_v
+ *   alpha = exp(-exp(a_log[h]) log(1 + exp(a + dt_bias[h]))),
+ *   beta  = 1 / (1 + exp(-b))
+ * x, a and b are fp32 or bf16 with rows x_row_stride etc. elements apart; q, k
+ * [rows][Hk][dk] and v [rows][Hv][dv] are fp32 or bf16 (fp32: what
+ * gdn_tape_capture takes), alpha and beta fp32 [rows][Hv].  Arithmetic is fp32,
+ * rounded once.  With update_window the window of every sequence with rows
+ * becomes its last W-1 inputs (an exact copy); without, it is read only, for a
+ * verify block whose inputs conv_window_replay commits later.
+ * Requires 2 <= W <= 8; x, weight, window, q, k, v 16-byte aligned, x's row
+ * stride a multiple of 4 elements; no output overlaps an input or another
+ * output. */
+sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_dtype x_dtype,
+                     long long x_row_stride, long long a_row_stride, long long b_row_stride,
+                     const float *weight, float *window, const float *a_log,
+                     const float *dt_bias, const int32_t *q_start, const int32_t *window_index,
+                     int B, int rows, int max_new, int slots, int W, int Hk, int Hv, int dk,
+                     int dv, int update_window, float q_scale, float eps, sv_dtype out_dtype,
+                     void *q, void *k, void *v, float *alpha, float *beta, sv_stream_t stream);
+
+/* gdn_advance: the gated delta rule in the order of the tape's definition,
+ *     S' = alpha_t S;  e_t = beta_t (v_t - S' k_t);  S = S' + e_t k_t^T;  o_t = S q_t
+ * for every row of every sequence, in place on its state fp32
+ * [slots][Hv][dv][dk]; a sequence without rows keeps its state.  q, k
+ * [rows][Hk][dk], v and out [rows][Hv][dv], all fp32 or all bf16, their rows
+ * q_row_stride etc. elements apart; alpha, beta fp32 [rows][Hv].  States and
+ * sums are fp32, out is rounded once.
+ * Requires q, k, v, state and out 16-byte aligned, row strides multiples of 8
+ * elements; neither out nor state overlaps an input or the other.  Results do
+ * not depend on the run. */
+sv_status gdn_advance(const void *q, const void *k, const void *v, sv_dtype dtype,
+                      long long q_row_stride, long long k_row_stride, long long v_row_stride,
+                      const float *alpha, const float *beta, float *state,
+                      const int32_t *q_start, const int32_t *state_index, int B, int rows,
+                      int max_new, int slots, int Hk, int Hv, int dk, int dv, void *out,
+                      long long out_row_stride, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Attention layers: a paged cache, and attention of the new tokens over it. */

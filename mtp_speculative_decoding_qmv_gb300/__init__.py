@@ -11,6 +11,8 @@ the library is missing, every call raises -- there is no fallback.
   spec_accept       fp32 probability-ratio acceptance, residual, bonus token
   gdn_tape_capture  GatedDeltaNet recurrence + innovation tape
   gdn_tape_replay   rebuild the recurrent state over an accepted prefix
+  gdn_inputs        a GatedDeltaNet layer's convolution, head norms and gates
+  gdn_advance       the gated delta rule over packed rows, states in place
   kv_pages_step     a paged cache's bookkeeping of one step
   rope_kv_append    rotary positions; keys and values into the paged cache
   paged_attention   a step's new tokens over the paged cache
@@ -32,6 +34,7 @@ __all__ = [
     "spec_accept_noalloc_scratch_bytes", "conv_window_capture", "conv_window_replay",
     "KvStep", "kv_pages_step", "rope_freqs", "rope_kv_append", "paged_attention",
     "make_attention_workspace", "paged_attention_workspace_bytes",
+    "GdnInputs", "gdn_inputs", "gdn_advance",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
@@ -143,6 +146,12 @@ def lib() -> ctypes.CDLL:
         L.paged_attention.argtypes = [P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P,
                                       LL, P, P, Z, P]
         L.paged_attention.restype = I
+        L.gdn_inputs.argtypes = [P, P, P, I, LL, LL, LL, P, P, P, P, P, P, I, I, I, I, I, I, I, I,
+                                 I, I, F, F, I, P, P, P, P, P, P]
+        L.gdn_inputs.restype = I
+        L.gdn_advance.argtypes = [P, P, P, I, LL, LL, LL, P, P, P, P, P, I, I, I, I, I, I, I, I,
+                                  P, LL, P]
+        L.gdn_advance.restype = I
         _lib = L
     return _lib
 
@@ -667,7 +676,8 @@ def _load_direct():
                                "mtp_speculative_decoding_qmv_gb300.build` (or "
                                "__graft_entry__.build())") from e
         built.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                     (lib().kv_pages_step, lib().rope_kv_append, lib().paged_attention)))
+                     (lib().kv_pages_step, lib().rope_kv_append, lib().paged_attention,
+                      lib().gdn_inputs, lib().gdn_advance)))
         _direct = built
     return _direct
 
@@ -880,3 +890,126 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         if lse is not None:
             lse.fill_(-math.inf)
     return out, lse
+
+
+# ----------------------------------------------------------------------------
+class GdnInputs(NamedTuple):
+    """What :func:`gdn_inputs` writes."""
+    q: torch.Tensor      # [rows, k_heads, dk]
+    k: torch.Tensor      # [rows, k_heads, dk]
+    v: torch.Tensor      # [rows, v_heads, dv]
+    alpha: torch.Tensor  # fp32 [rows, v_heads]
+    beta: torch.Tensor   # fp32 [rows, v_heads]
+
+
+def _need_2d(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """Rows [rows, width] of contiguous numbers."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the numbers of a row must be contiguous")
+
+
+def gdn_inputs(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, weight: torch.Tensor,
+               window: torch.Tensor, a_log: torch.Tensor, dt_bias: torch.Tensor,
+               q_start: torch.Tensor, max_new: int, *, k_heads: int | None = None,
+               dk: int | None = None, window_index: torch.Tensor | None = None,
+               update_window: bool = True, q_scale: float = 1.0, eps: float = 1e-6,
+               dtype: torch.dtype = torch.bfloat16, out=None) -> GdnInputs:
+    """Short convolution, SiLU, head norms and gates of a GatedDeltaNet layer
+    over packed rows: x [rows, C] (C = 2 k_heads dk + v_heads dv: q, k and v
+    heads) and the gate projections a, b [rows, v_heads], fp32 or bf16 (slices of
+    wider rows will do); weight fp32 [W, C]; window fp32 [slots, W-1, C], in
+    place unless ``update_window`` is false; a_log, dt_bias fp32 [v_heads].
+    Sequence s's rows are q_start[s]:q_start[s+1], its slot window_index[s] (s
+    when omitted); rows past the last sequence are zero.  ``max_new``: a bound
+    on a sequence's rows.  q, k and v are made in ``dtype`` for ``k_heads`` of
+    ``dk``, or are the first three of ``out``."""
+    if x.dim() != 2 or a.dim() != 2 or weight.dim() != 2 or window.dim() != 3:
+        raise ValueError("x and a must be [rows, width], weight [W, C], window [slots, W-1, C]")
+    index = _on(x, "x")
+    rows, C = x.shape
+    Hv = a.shape[1]
+    if out is None:
+        if k_heads is None or dk is None:
+            raise ValueError("k_heads and dk are needed where out is not given")
+        Hk, left = int(k_heads), C - 2 * int(k_heads) * int(dk)
+        if Hk < 1 or dk < 1 or Hv < 1 or left <= 0 or left % Hv:
+            raise ValueError(f"{C} channels are not 2 * {k_heads} heads of {dk} and {Hv} of dv")
+        qk, dev = (rows, Hk, int(dk)), x.device
+        out = (torch.empty(qk, dtype=dtype, device=dev), torch.empty(qk, dtype=dtype, device=dev),
+               torch.empty((rows, Hv, left // Hv), dtype=dtype, device=dev),
+               torch.empty((rows, Hv), dtype=torch.float32, device=dev),
+               torch.empty((rows, Hv), dtype=torch.float32, device=dev))
+    out = GdnInputs(*out)
+    st = _call(index, (_direct or _load_direct()).gdn_inputs, x, a, b, weight, window, a_log,
+               dt_bias, q_start, window_index, int(max_new), update_window, float(q_scale),
+               float(eps), *out)
+    if st != SV_OK:
+        f32, dev = torch.float32, x.device
+        if x.dtype not in (f32, torch.bfloat16) or out.q.dtype not in (f32, torch.bfloat16):
+            raise TypeError("x and the outputs must be float32 or bfloat16")
+        if out.q.dim() != 3 or out.v.dim() != 3 or q_start.dim() != 1 or not q_start.numel():
+            raise ValueError("q and v must be [rows, heads, dim], q_start [sequences + 1]")
+        (Hk, dim), dv = out.q.shape[1:], out.v.shape[2]
+        if C != 2 * Hk * dim + Hv * dv:
+            raise ValueError(f"{C} channels are not 2 * {Hk} heads of {dim} and {Hv} of {dv}")
+        W, B, to = weight.shape[0], q_start.numel() - 1, out.q.dtype
+        wanted = [(_need_2d, x, "x", x.dtype, (rows, C)), (_need_2d, a, "a", x.dtype, (rows, Hv)),
+                  (_need_2d, b, "b", x.dtype, (rows, Hv)), (_need, weight, "weight", f32, (W, C)),
+                  (_need, window, "window", f32, (window.shape[0], W - 1, C)),
+                  (_need, a_log, "a_log", f32, (Hv,)), (_need, dt_bias, "dt_bias", f32, (Hv,)),
+                  (_need, q_start, "q_start", torch.int32, (B + 1,)),
+                  (_need, out.q, "q", to, (rows, Hk, dim)), (_need, out.k, "k", to, (rows, Hk, dim)),
+                  (_need, out.v, "v", to, (rows, Hv, dv)),
+                  (_need, out.alpha, "alpha", f32, (rows, Hv)),
+                  (_need, out.beta, "beta", f32, (rows, Hv))]
+        if window_index is not None:
+            wanted.append((_need, window_index, "window_index", torch.int32, (B,)))
+        _refuse("gdn_inputs", st, [w + (dev,) for w in wanted])
+    return out
+
+
+def gdn_advance(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
+                beta: torch.Tensor, state: torch.Tensor, q_start: torch.Tensor, max_new: int, *,
+                state_index: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated delta rule over packed rows, ``state`` fp32 [slots, v_heads, dv,
+    dk] in place: q, k [rows, k_heads, dk] and v [rows, v_heads, dv] fp32 or
+    bf16, alpha, beta fp32 [rows, v_heads]; sequence s's rows are
+    q_start[s]:q_start[s+1], its slot state_index[s] (s when omitted).
+    ``max_new``: a bound on a sequence's rows, which picks the kernel.  Returns
+    out [rows, v_heads, dv] of q's dtype; rows past the last sequence are zero."""
+    if q.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [rows, k_heads, dk] and state [slots, v_heads, dv, dk]")
+    index = _on(q, "q")
+    if out is None:
+        out = torch.empty((q.shape[0], state.shape[1], state.shape[2]), dtype=q.dtype,
+                          device=q.device)
+    st = _call(index, (_direct or _load_direct()).gdn_advance, q, k, v, alpha, beta, state, q_start,
+               state_index, int(max_new), out)
+    if st != SV_OK:
+        if q.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("q, k and v must be float32 or bfloat16")
+        if q_start.dim() != 1 or not q_start.numel():
+            raise ValueError("q_start must be [sequences + 1]")
+        rows, Hk, dk = q.shape
+        slots, Hv, dv, _ = state.shape
+        B, f32 = q_start.numel() - 1, torch.float32
+        wanted = [(_need_rows, q, "q", q.dtype, (rows, Hk, dk)),
+                  (_need_rows, k, "k", q.dtype, (rows, Hk, dk)),
+                  (_need_rows, v, "v", q.dtype, (rows, Hv, dv)),
+                  (_need_rows, out, "out", q.dtype, (rows, Hv, dv)),
+                  (_need, alpha, "alpha", f32, (rows, Hv)), (_need, beta, "beta", f32, (rows, Hv)),
+                  (_need, state, "state", f32, (slots, Hv, dv, dk)),
+                  (_need, q_start, "q_start", torch.int32, (B + 1,))]
+        if state_index is not None:
+            wanted.append((_need, state_index, "state_index", torch.int32, (B,)))
+        _refuse("gdn_advance", st, [w + (q.device,) for w in wanted])
+    return out

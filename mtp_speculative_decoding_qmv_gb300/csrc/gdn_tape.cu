@@ -420,8 +420,6 @@ sv_status validate(const char *who, int B, int T, int H, int dk, int dv) {
 
 }  // namespace
 
-unsigned take_device_error_gdn() { return 0u; }  // no bounded waits in this unit
-
 }  // namespace sv
 
 using namespace sv;

@@ -24,6 +24,8 @@ namespace {
 decltype(&kv_pages_step) pages_fn = nullptr;
 decltype(&rope_kv_append) append_fn = nullptr;
 decltype(&paged_attention) attend_fn = nullptr;
+decltype(&gdn_inputs) inputs_fn = nullptr;
+decltype(&gdn_advance) advance_fn = nullptr;
 
 // What a call's arguments are read with.  `fits` turns false at the first
 // tensor that is not as wanted; later reads of that call then give null.
@@ -74,6 +76,17 @@ struct Reader {
     *stride = n > 1 ? x->stride(0) : heads * dim;
     return static_cast<T *>(const_cast<void *>(x->const_data_ptr()));
   }
+  // Rows of numbers [rows, width]: address, row stride.
+  const void *rows(int i, at::ScalarType type, int64_t n, int64_t width, long long *stride) {
+    const at::Tensor *x = tensor(i);
+    if (!x || x->scalar_type() != type || x->dim() != 2 || x->size(0) != n ||
+        x->size(1) != width || (width > 1 && x->stride(1) != 1)) {
+      fits = false;
+      return nullptr;
+    }
+    *stride = n > 1 ? x->stride(0) : width;
+    return x->const_data_ptr();
+  }
   bool given(int i) const { return args[i] != Py_None; }
 };
 
@@ -116,14 +129,18 @@ PyObject *call(F library) {
   return PyLong_FromLong(st);
 }
 
-// bind(kv_pages_step, rope_kv_append, paged_attention): the library's addresses
+// bind(kv_pages_step, rope_kv_append, paged_attention, gdn_inputs, gdn_advance): the
+// library's addresses
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  void *at[3] = {};
-  for (int i = 0; i < 3 && n == 3; ++i) at[i] = PyLong_AsVoidPtr(args[i]);
+  constexpr int kCalls = 5;
+  void *at[kCalls] = {};
+  for (int i = 0; i < kCalls && n == kCalls; ++i) at[i] = PyLong_AsVoidPtr(args[i]);
   if (PyErr_Occurred()) return nullptr;
   pages_fn = reinterpret_cast<decltype(pages_fn)>(at[0]);
   append_fn = reinterpret_cast<decltype(append_fn)>(at[1]);
   attend_fn = reinterpret_cast<decltype(attend_fn)>(at[2]);
+  inputs_fn = reinterpret_cast<decltype(inputs_fn)>(at[3]);
+  advance_fn = reinterpret_cast<decltype(advance_fn)>(at[4]);
   Py_RETURN_NONE;
 }
 
@@ -257,10 +274,97 @@ PyObject *attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// gdn_inputs(device, stream, x, a, b, weight, window, a_log, dt_bias, q_start, window_index or
+// None, max_new, update_window, q_scale, eps, q, k, v, alpha, beta)
+PyObject *inputs(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Reader r;
+  sv_stream_t stream;
+  if (!begin(args, n, 20, &r, &stream)) return nullptr;
+  int max_new;
+  if (!to_int(args[11], &max_new)) return nullptr;
+  const int update = PyObject_IsTrue(args[12]);
+  const double scale = PyFloat_AsDouble(args[13]), eps = PyFloat_AsDouble(args[14]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor *x = r.tensor(2), *a = r.tensor(3), *weight = r.tensor(5), *window = r.tensor(6),
+                   *start = r.tensor(9), *q = r.tensor(15), *v = r.tensor(17);
+  if (!r.fits || x->dim() != 2 || a->dim() != 2 || weight->dim() != 2 || window->dim() != 3 ||
+      start->dim() != 1 || q->dim() != 3 || v->dim() != 3)
+    Py_RETURN_NONE;
+  const auto type = x->scalar_type(), to = q->scalar_type(), f32 = at::kFloat;
+  if ((type != f32 && type != at::kBFloat16) || (to != f32 && to != at::kBFloat16)) Py_RETURN_NONE;
+  const int64_t rows = x->size(0), c = x->size(1), hv = a->size(1), w = weight->size(0),
+                slots = window->size(0), b = start->size(0) - 1, hk = q->size(1), dk = q->size(2),
+                dv = v->size(2);
+  if (b < 0 || c != 2 * hk * dk + hv * dv) Py_RETURN_NONE;
+  long long xs = 0, as = 0, bs = 0;
+  const void *x_at = r.rows(2, type, rows, c, &xs), *a_at = r.rows(3, type, rows, hv, &as),
+             *b_at = r.rows(4, type, rows, hv, &bs);
+  const auto *w_at = r.at<float>(5, f32, {w, c});
+  auto *win = r.at<float>(6, f32, {slots, w - 1, c});
+  const auto *a_log = r.at<float>(7, f32, {hv}), *dt = r.at<float>(8, f32, {hv});
+  const auto *q_start = r.at<int32_t>(9, at::kInt, {b + 1});
+  const auto *index = r.given(10) ? r.at<int32_t>(10, at::kInt, {b}) : nullptr;
+  void *q_at = r.at<void>(15, to, {rows, hk, dk}), *k_at = r.at<void>(16, to, {rows, hk, dk}),
+       *v_at = r.at<void>(17, to, {rows, hv, dv});
+  auto *al = r.at<float>(18, f32, {rows, hv}), *be = r.at<float>(19, f32, {rows, hv});
+  if (!r.fits) Py_RETURN_NONE;
+  int s[8];
+  const int64_t sizes[8] = {b, rows, slots, w, hk, hv, dk, dv};
+  for (int i = 0; i < 8; ++i)
+    if (!to_int(sizes[i], &s[i])) return nullptr;
+  return call([&] {
+    return inputs_fn(x_at, a_at, b_at, type == f32 ? SV_F32 : SV_BF16, xs, as, bs, w_at, win,
+                     a_log, dt, q_start, index, s[0], s[1], max_new, s[2], s[3], s[4], s[5], s[6],
+                     s[7], update, (float)scale, (float)eps, to == f32 ? SV_F32 : SV_BF16, q_at,
+                     k_at, v_at, al, be, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
+// gdn_advance(device, stream, q, k, v, alpha, beta, state, q_start, state_index or None, max_new,
+// out)
+PyObject *advance(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Reader r;
+  sv_stream_t stream;
+  if (!begin(args, n, 12, &r, &stream)) return nullptr;
+  int max_new;
+  if (!to_int(args[10], &max_new)) return nullptr;
+  const at::Tensor *q = r.tensor(2), *state = r.tensor(7), *start = r.tensor(8);
+  if (!r.fits || q->dim() != 3 || state->dim() != 4 || start->dim() != 1) Py_RETURN_NONE;
+  const auto type = q->scalar_type(), f32 = at::kFloat;
+  if (type != f32 && type != at::kBFloat16) Py_RETURN_NONE;
+  const int64_t rows = q->size(0), hk = q->size(1), dk = q->size(2), b = start->size(0) - 1,
+                slots = state->size(0), hv = state->size(1), dv = state->size(2);
+  if (b < 0) Py_RETURN_NONE;
+  long long qs = 0, ks = 0, vs = 0, os = 0;
+  const void *q_at = r.rows<void>(2, type, rows, hk, dk, &qs);
+  const void *k_at = r.rows<void>(3, type, rows, hk, dk, &ks);
+  const void *v_at = r.rows<void>(4, type, rows, hv, dv, &vs);
+  const auto *al = r.at<float>(5, f32, {rows, hv}), *be = r.at<float>(6, f32, {rows, hv});
+  auto *state_at = r.at<float>(7, f32, {slots, hv, dv, dk});
+  const auto *q_start = r.at<int32_t>(8, at::kInt, {b + 1});
+  const auto *index = r.given(9) ? r.at<int32_t>(9, at::kInt, {b}) : nullptr;
+  void *out = r.rows<void>(11, type, rows, hv, dv, &os);
+  if (!r.fits) Py_RETURN_NONE;
+  int s[7];
+  const int64_t sizes[7] = {b, rows, slots, hk, hv, dk, dv};
+  for (int i = 0; i < 7; ++i)
+    if (!to_int(sizes[i], &s[i])) return nullptr;
+  return call([&] {
+    return advance_fn(q_at, k_at, v_at, type == f32 ? SV_F32 : SV_BF16, qs, ks, vs, al, be,
+                      state_at, q_start, index, s[0], s[1], max_new, s[2], s[3], s[4], s[5], s[6],
+                      out, os, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name, function) \
   {name, (PyCFunction)(void *)function, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD("bind", bind), METHOD("kv_pages_step", pages),
                          METHOD("rope_kv_append", append), METHOD("paged_attention", attend),
+                         METHOD("gdn_inputs", inputs), METHOD("gdn_advance", advance),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
