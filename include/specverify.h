@@ -554,13 +554,19 @@ sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_dtype x_dty
  * sums are fp32, out is rounded once.
  * Requires q, k, v, state and out 16-byte aligned, row strides multiples of 8
  * elements; neither out nor state overlaps an input or the other.  Results do
- * not depend on the run. */
+ * not depend on the run.
+ * workspace: gdn_advance_workspace_bytes(..) bytes (0 where none is needed, as for
+ * single tokens and fp32 rows; else 41984 a head and 64 rows begun), 256-byte
+ * aligned, with no required contents; it overlaps no other argument.  Calls that
+ * run concurrently need workspaces of their own.  One launch on `stream`, or two. */
+size_t gdn_advance_workspace_bytes(sv_dtype dtype, int B, int rows, int max_new, int Hv);
 sv_status gdn_advance(const void *q, const void *k, const void *v, sv_dtype dtype,
                       long long q_row_stride, long long k_row_stride, long long v_row_stride,
                       const float *alpha, const float *beta, float *state,
                       const int32_t *q_start, const int32_t *state_index, int B, int rows,
                       int max_new, int slots, int Hk, int Hv, int dk, int dv, void *out,
-                      long long out_row_stride, sv_stream_t stream);
+                      long long out_row_stride, void *workspace, size_t workspace_bytes,
+                      sv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Attention layers: a paged cache, and attention of the new tokens over it. */

@@ -34,7 +34,7 @@ __all__ = [
     "spec_accept_noalloc_scratch_bytes", "conv_window_capture", "conv_window_replay",
     "KvStep", "kv_pages_step", "rope_freqs", "rope_kv_append", "paged_attention",
     "make_attention_workspace", "paged_attention_workspace_bytes",
-    "GdnInputs", "gdn_inputs", "gdn_advance",
+    "GdnInputs", "gdn_inputs", "gdn_advance", "gdn_advance_workspace_bytes",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
@@ -150,8 +150,10 @@ def lib() -> ctypes.CDLL:
                                  I, I, F, F, I, P, P, P, P, P, P]
         L.gdn_inputs.restype = I
         L.gdn_advance.argtypes = [P, P, P, I, LL, LL, LL, P, P, P, P, P, I, I, I, I, I, I, I, I,
-                                  P, LL, P]
+                                  P, LL, P, Z, P]
         L.gdn_advance.restype = I
+        L.gdn_advance_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.gdn_advance_workspace_bytes.restype = Z
         _lib = L
     return _lib
 
@@ -976,24 +978,39 @@ def gdn_inputs(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, weight: torch.
     return out
 
 
+def gdn_advance_workspace_bytes(dtype: torch.dtype, sequences: int, rows: int, max_new: int,
+                                v_heads: int) -> int:
+    """Bytes of a workspace for gdn_advance; 0 where none is needed."""
+    return int(lib().gdn_advance_workspace_bytes(SV_BF16 if dtype == torch.bfloat16 else SV_F32,
+                                                 sequences, rows, max_new, v_heads))
+
+
 def gdn_advance(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
                 beta: torch.Tensor, state: torch.Tensor, q_start: torch.Tensor, max_new: int, *,
-                state_index: torch.Tensor | None = None,
-                out: torch.Tensor | None = None) -> torch.Tensor:
+                state_index: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The gated delta rule over packed rows, ``state`` fp32 [slots, v_heads, dv,
     dk] in place: q, k [rows, k_heads, dk] and v [rows, v_heads, dv] fp32 or
     bf16, alpha, beta fp32 [rows, v_heads]; sequence s's rows are
     q_start[s]:q_start[s+1], its slot state_index[s] (s when omitted).
-    ``max_new``: a bound on a sequence's rows, which picks the kernel.  Returns
-    out [rows, v_heads, dv] of q's dtype; rows past the last sequence are zero."""
+    ``max_new``: a bound on a sequence's rows, which picks the kernel.
+    ``workspace``: uint8, gdn_advance_workspace_bytes of them, made per call when
+    omitted and needed.  Returns out [rows, v_heads, dv] of q's dtype; rows past
+    the last sequence are zero."""
     if q.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [rows, k_heads, dk] and state [slots, v_heads, dv, dk]")
     index = _on(q, "q")
     if out is None:
         out = torch.empty((q.shape[0], state.shape[1], state.shape[2]), dtype=q.dtype,
                           device=q.device)
+    max_new = int(max_new)
+    if workspace is None and max_new > 1:
+        n = gdn_advance_workspace_bytes(q.dtype, q_start.numel() - 1, q.shape[0], max_new,
+                                        state.shape[1])
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     st = _call(index, (_direct or _load_direct()).gdn_advance, q, k, v, alpha, beta, state, q_start,
-               state_index, int(max_new), out)
+               state_index, max_new, out, workspace)
     if st != SV_OK:
         if q.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("q, k and v must be float32 or bfloat16")
@@ -1011,5 +1028,7 @@ def gdn_advance(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.
                   (_need, q_start, "q_start", torch.int32, (B + 1,))]
         if state_index is not None:
             wanted.append((_need, state_index, "state_index", torch.int32, (B,)))
+        if workspace is not None:
+            wanted.append((_need, workspace, "workspace", torch.uint8, None))
         _refuse("gdn_advance", st, [w + (q.device,) for w in wanted])
     return out

@@ -169,13 +169,18 @@ sv_status recur_run(const AdvanceArgs &a, cudaStream_t stream) {
 using namespace sv;
 using namespace sv::gdn;
 
+extern "C" size_t gdn_advance_workspace_bytes(sv_dtype dtype, int B, int rows, int max_new, int Hv) {
+  if (B < 0 || rows < 0 || Hv < 1 || dtype != SV_BF16 || max_new < kChunkFrom) return 0;
+  return chunk_workspace_bytes(rows, B, Hv);
+}
+
 extern "C" sv_status gdn_advance(const void *q, const void *k, const void *v, sv_dtype dtype,
                                  long long q_row_stride, long long k_row_stride,
                                  long long v_row_stride, const float *alpha, const float *beta,
                                  float *state, const int32_t *q_start, const int32_t *state_index,
                                  int B, int rows, int max_new, int slots, int Hk, int Hv, int dk,
-                                 int dv, void *out, long long out_row_stride,
-                                 sv_stream_t stream) {
+                                 int dv, void *out, long long out_row_stride, void *workspace,
+                                 size_t workspace_bytes, sv_stream_t stream) {
   clear_error();
   const char *who = "gdn_advance";
   if (B < 0 || rows < 0 || max_new < 0 || slots < 0)
@@ -229,6 +234,20 @@ extern "C" sv_status gdn_advance(const void *q, const void *k, const void *v, sv
         return fail(SV_ERR_INVALID_ARG, "%s: an output overlaps an input", who);
   if (overlaps(to[0].p, to[0].n, to[1].p, to[1].n))
     return fail(SV_ERR_INVALID_ARG, "%s: out overlaps the state", who);
+  const size_t need = gdn_advance_workspace_bytes(dtype, B, rows, max_new, Hv);
+  if (need) {
+    if (!workspace || !aligned(workspace, 256))
+      return fail(SV_ERR_INVALID_ARG, "%s: the workspace must be 256-byte aligned", who);
+    if (workspace_bytes < need)
+      return fail(SV_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %zu are needed", who,
+                  workspace_bytes, need);
+    for (const Buf &i : in)
+      if (overlaps(workspace, need, i.p, i.n))
+        return fail(SV_ERR_INVALID_ARG, "%s: the workspace overlaps an input", who);
+    for (const Buf &o : to)
+      if (overlaps(workspace, need, o.p, o.n))
+        return fail(SV_ERR_INVALID_ARG, "%s: the workspace overlaps an output", who);
+  }
   AdvanceArgs a = {};
   a.q = q;
   a.k = k;
@@ -251,6 +270,6 @@ extern "C" sv_status gdn_advance(const void *q, const void *k, const void *v, sv
   a.dk = dk;
   a.dv = dv;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == SV_BF16 && max_new >= kChunkFrom) return chunk_run(a, s);
+  if (dtype == SV_BF16 && max_new >= kChunkFrom) return chunk_run(a, workspace, s);
   return dtype == SV_F32 ? recur_run<float>(a, s) : recur_run<__nv_bfloat16>(a, s);
 }

@@ -9,10 +9,13 @@
 // With L = tril(beta D K K^T, -1), T = (1 + L)^-1 and P = tril(D Q K^T), as columns
 // over the chunk's rows:
 //   R = beta (V - G S0 K^T);  E = R T^T;  O = G S0 Q^T + E P^T;  S = G[63] S0 + E' K
-// so the state enters five products a chunk, each with 128 rows (dv) in tensor
-// memory's lanes: S0, R and E are A operands in tensor memory, K, Q, T and P (bf16,
-// shared memory) are B.  K serves both as rows of dk (S0 K^T) and with dk
-// contiguous (E' K), from one copy.
+// Two launches.  The first makes T and P of every chunk of every head, all chunks
+// side by side (mma.sync for K K^T and Q K^T, whose results are wanted in
+// registers; T by substitution in fp32).  The second follows the state from chunk
+// to chunk, a CTA a (sequence, head): five products a chunk, each with 128 rows
+// (dv) in tensor memory's lanes; S0, R and E are A operands in tensor memory, K, Q,
+// T and P (bf16, shared memory) are B.  K serves both as rows of dk (S0 K^T) and
+// with dk contiguous (E' K), from one copy.
 //
 // Precision: the state stays in fp32 registers.  An fp32 operand is cut into three
 // bf16 parts that add up to it exactly (8 bits of it each), so what reaches the
@@ -20,15 +23,16 @@
 // parts, R T^T with the six products of parts above 2^-24.  The output, bf16 in
 // the end, takes two parts of S0, E and P: 2^-16, far below its own rounding.
 //
-// What bounds it is the chain from chunk to chunk, one CTA a (sequence, head): per
-// chunk about 2000 cycles of tensor-core time on the chain (S0 K^T 768, R T^T 480,
-// E' K 768), and between them the hand-overs to the warps that cut the parts.
-// Everything off the chain runs beside it: S0 Q^T and E P^T in the gaps, T and P of
-// the next chunk on four warps of their own (mma.sync for K K^T and Q K^T: small,
-// and their results are wanted in registers), loads two chunks ahead.
+// What bounds the second is the chain from chunk to chunk: tensor-core time of S0
+// K^T, R T^T and E' K (about 2000 cycles a chunk), and between them the warps that
+// read a product, cut it and write the next operand.  The chunk's rows, and the
+// state's columns, go through in two halves, so that one half's products run while
+// the other half is cut.  S0 Q^T and E P^T run in the gaps.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "gdn_rows.cuh"
+#include "qmv_common.cuh"
 #include "tc05.cuh"
 
 namespace sv {
@@ -37,56 +41,22 @@ namespace {
 
 constexpr int kC = 64;    // rows a chunk
 constexpr int kD = 128;   // dk and dv, narrower ones padded with zeros
-constexpr int kChainWarps = 8, kPrepWarps = 4, kMmaWarp = 12, kLoadWarp = 13, kLoadWarps = 3;
-constexpr int kThreads = 512;
-// 256 x 160 + 256 x 96 = 512 x 128 registers
-constexpr int kChainRegs = 160, kOtherRegs = 96;
 
-// ---- shared memory ----------------------------------------------------------
+// What the first launch leaves of a chunk of a head, as the second wants it in
+// shared memory: T in three parts and P in two ([64 rows][64 columns] bf16 each, in
+// the 128-byte swizzle), G, D[63] and beta.
 constexpr uint32_t kTile = kC * kD * 2;             // K, Q or V of a chunk
 constexpr uint32_t kPanel = kC * 128;               // 64 columns of it, 128-byte swizzle
-constexpr uint32_t kStage = 3 * kTile;
-constexpr uint32_t kPart = kC * kC * 2;             // a bf16 part of T or P
-constexpr uint32_t kTParts = 3, kPParts = 2;
-constexpr uint32_t kMats = (kTParts + kPParts) * kPart;
-constexpr int kPitch = kC + 4;                      // floats a row of the scratch matrix
-constexpr uint32_t kOffMats = 2 * kStage;
-constexpr uint32_t kOffScratch = kOffMats + 2 * kMats;
-constexpr uint32_t kOffGates = kOffScratch + kC * kPitch * 4;  // [2][alpha 64 | beta 64]
-constexpr uint32_t kOffDecay = kOffGates + 2 * 2 * kC * 4;     // [2][G 64 | D[63] 64]
-constexpr uint32_t kOffBars = kOffDecay + 2 * 2 * kC * 4;
-enum Bar { kKvFull = 0, kKvEmpty = 2, kMatFull = 4, kMatEmpty = 6, kState = 8, kKs, kR, kTr, kQs, kE, kSu, kOut, kBars };
-constexpr uint32_t kOffTmem = kOffBars + 8 * kBars;
-constexpr uint32_t kSmem = kOffTmem + 16 + 1024;
-
-// ---- tensor memory (columns) ------------------------------------------------
-// The state's parts: of each half of dk (64 columns of it), three parts of 32
-// columns; E' K of that half first lands in the same place.
-constexpr uint32_t kColState = 0, kColHalf = 96;
-constexpr uint32_t kColK = 192;   // S0 K^T, then E's two parts
-constexpr uint32_t kColQ = 256;   // S0 Q^T
-constexpr uint32_t kColE = 320;   // R T^T, then E P^T
-constexpr uint32_t kColR = 384;   // R's parts, then E''s
-constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kPart = kC * kC * 2;
+constexpr int kTParts = 3, kPParts = 2;
+constexpr uint32_t kOffP = kTParts * kPart, kOffG = kOffP + kPParts * kPart;
+constexpr uint32_t kOffLast = kOffG + kC * 4, kOffBeta = kOffLast + kC * 4;
+constexpr uint32_t kBlob = kOffG + 1024;
 
 __device__ unsigned int g_give_up;
 
-constexpr uint32_t idesc(int n, bool mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10)  // D fp32; A, B bf16
-         | (mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
-}
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
-  return mbar_wait_u32(bar, parity);
-}
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-// Uses of registers that a tcgen05.ld fills stay behind its wait.
-__device__ __forceinline__ void pin(uint32_t (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
-                      "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
 }
 // Cuts 2 kN values into kParts bf16 parts, packed in pairs: each part is the upper
 // half of what the parts before it leave, an exact difference.
@@ -109,95 +79,118 @@ __device__ __forceinline__ void cut(const float *x, uint32_t (&part)[kParts][kN]
     }
   }
 }
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// 16 bytes to shared memory, zeros where there is no source.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
 // Address of the 16-byte piece `piece` (of 8) of a row of a 128-byte swizzled panel.
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
   return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-struct Item {
-  int start, n, slot, h, hk, chunks;
-};
+// ---- T and P of a chunk: four warps ----------------------------------------------
+constexpr int kPrepThreads = 128;
+constexpr int kPitch = kC + 4;  // floats a row of the scratch matrix
+// K lies where T's parts go, Q where P's go
+constexpr uint32_t kPrepQ = kOffP;
+constexpr uint32_t kPrepScratch = kBlob, kPrepAlpha = kPrepScratch + kC * kPitch * 4;
+constexpr uint32_t kPrepSmem = kPrepAlpha + kC * 4 + 1024;
+static_assert(kTile <= kOffP && kPParts * kPart == kTile, "K and Q under T and P");
 
-// ---- the loads: K, Q, V and the gates of chunk c into stage c % 2 --------------
-__device__ void load_chunk(const AdvanceArgs &a, const Item &it, uint8_t *smem, uint32_t base, int c,
-                           int tid) {
-  const int s = c & 1, t0 = c * kC, left = min(kC, it.n - t0);
-  using B = __nv_bfloat16;
-  const long long row0 = it.start + t0;
-  const B *k = static_cast<const B *>(a.k) + row0 * a.k_stride + (long long)it.hk * a.dk;
-  const B *q = static_cast<const B *>(a.q) + row0 * a.q_stride + (long long)it.hk * a.dk;
-  const B *v = static_cast<const B *>(a.v) + row0 * a.v_stride + (long long)it.h * a.dv;
-  const uint32_t at = base + s * kStage;
-  for (int i = tid; i < kC * 16; i += kLoadWarps * 32) {
-    const int row = i >> 4, piece = i & 15;
-    const bool in = row < left;
-    const bool col = in && 8 * piece < a.dk;
-    const uint32_t to = (piece >> 3) * kPanel + swizzled(row, piece & 7);
-    copy16(at + to, col ? k + row * a.k_stride + 8 * piece : k, col);
-    copy16(at + kTile + to, col ? q + row * a.q_stride + 8 * piece : q, col);
-    const bool value = in && 8 * piece < a.dv;
-    copy16(at + 2 * kTile + row * (kD * 2) + piece * 16, value ? v + row * a.v_stride + 8 * piece : v,
-           value);
-  }
-  float *gates = reinterpret_cast<float *>(smem + kOffGates) + s * 2 * kC;
-  for (int i = tid; i < kC; i += kLoadWarps * 32) {
-    const long long g = (row0 + i) * a.H + it.h;
-    gates[i] = i < left ? __ldg(a.alpha + g) : 1.f;
-    gates[kC + i] = i < left ? __ldg(a.beta + g) : 0.f;
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+  // 16 bytes to shared memory, zeros where there is no source
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
 }
-
-// ---- T and P of chunk c, by four warps ------------------------------------------
-__device__ __forceinline__ void store_parts(uint8_t *mats, int i, int j, float x) {
-  float a = x;
+__device__ __forceinline__ void store_parts(uint8_t *t, int i, int j, float x) {
 #pragma unroll
-  for (int p = 0; p < (int)kTParts; ++p) {
-    const uint32_t u = __float_as_uint(a);
-    *reinterpret_cast<uint16_t *>(mats + p * kPart + swizzled(i, j >> 3) + (j & 7) * 2) =
+  for (int p = 0; p < kTParts; ++p) {
+    const uint32_t u = __float_as_uint(x);
+    *reinterpret_cast<uint16_t *>(t + p * kPart + swizzled(i, j >> 3) + (j & 7) * 2) =
         (uint16_t)(u >> 16);
-    a -= __uint_as_float(u & 0xFFFF0000u);
+    x -= __uint_as_float(u & 0xFFFF0000u);
   }
 }
 
-__device__ void prepare(uint8_t *smem, uint32_t base, int c) {
-  const int s = c & 1, tid = threadIdx.x - kChainWarps * 32, warp = tid >> 5, lane = tid & 31;
-  float *scratch = reinterpret_cast<float *>(smem + kOffScratch);
-  const float *alpha = reinterpret_cast<const float *>(smem + kOffGates) + s * 2 * kC;
-  const float *beta = alpha + kC;
-  float *decay = reinterpret_cast<float *>(smem + kOffDecay) + s * 2 * kC;
-  uint8_t *mats = smem + kOffMats + s * kMats;
-  // D below the diagonal, a column a thread, by products (a gate of 0 or gates
-  // whose product underflows need no care); the column before the first is G
-  if (tid <= kC) {
-    float d = 1.f;
-    const int j = tid - 1;
-#pragma unroll 8
-    for (int i = 0; i < kC; ++i) {
-      if (i > j) d *= alpha[i];
-      if (j < 0)
-        decay[i] = d;
-      else
-        scratch[i * kPitch + j] = i >= j ? d : 0.f;
+__global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const AdvanceArgs a,
+                                                                   uint8_t *blobs) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % a.H, place = blockIdx.x / a.H, hk = h / (a.H / a.Hk);
+  int c;
+  const int b = tile_owner(a.q_start, a.B, a.rows, kC, place, c);
+  if (b >= a.B) return;
+  const Rows s = rows_of(a.q_start, b, a.rows);
+  if (c < 0 || c * kC >= s.n || slot_of(a.state_index, b, a.slots) < 0) return;
+  const int left = min(kC, s.n - c * kC);
+  const long long row0 = s.start + c * kC;
+  float *scratch = reinterpret_cast<float *>(smem + kPrepScratch);
+  float *alpha = reinterpret_cast<float *>(smem + kPrepAlpha);
+  float *beta = reinterpret_cast<float *>(smem + kOffBeta);
+  float *G = reinterpret_cast<float *>(smem + kOffG), *last = G + kC;
+  {
+    using B16 = __nv_bfloat16;
+    const B16 *k = static_cast<const B16 *>(a.k) + row0 * a.k_stride + (long long)hk * a.dk;
+    const B16 *q = static_cast<const B16 *>(a.q) + row0 * a.q_stride + (long long)hk * a.dk;
+    const int piece = tid & 15;
+    const uint32_t to = (piece >> 3) * kPanel;
+#pragma unroll
+    for (int row = tid >> 4; row < kC; row += kPrepThreads / 16) {
+      const bool in = row < left && 8 * piece < a.dk;
+      const uint32_t at = base + to + swizzled(row, piece & 7);
+      copy16(at, in ? k + row * a.k_stride + 8 * piece : k, in);
+      copy16(at + kPrepQ, in ? q + row * a.q_stride + 8 * piece : q, in);
     }
-    if (j >= 0) decay[kC + j] = d;
+    if (tid < kC) {
+      const long long g = (row0 + tid) * a.H + h;
+      alpha[tid] = tid < left ? __ldg(a.alpha + g) : 1.f;
+      beta[tid] = tid < left ? __ldg(a.beta + g) : 0.f;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncthreads();
+  // D from the diagonal down, by products (a gate of 0 or gates whose product
+  // underflows need no care): warp 0 rows 0..31 of columns 0..31, warps 2 and 3
+  // rows 32..63, a column a thread; warp 1 G, by a scan
+  if (warp == 1) {
+    const float2 x = *reinterpret_cast<const float2 *>(alpha + 2 * lane);
+    float upto = x.x * x.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto *= y;
+    }
+    float before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) before = 1.f;
+    *reinterpret_cast<float2 *>(G + 2 * lane) = make_float2(before * x.x, before * x.x * x.y);
+  } else {
+    const int j = warp == 3 ? 32 + lane : lane, low = warp ? 32 : 0;
+    float al[32], d = 1.f;
+    if (warp == 2) {
+#pragma unroll
+      for (int i = 1; i < 32; ++i) {
+        const float x = alpha[i];
+        if (i > j) d *= x;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(alpha + low + i);
+      al[i] = x.x;
+      al[i + 1] = x.y;
+      al[i + 2] = x.z;
+      al[i + 3] = x.w;
+    }
+    float *to = scratch + low * kPitch + j;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (low + i > j) d *= al[i];
+      to[i * kPitch] = d;  // 1 above the diagonal, where it is not used
+    }
+    if (warp) last[j] = d;
   }
   // K K^T and Q K^T of the warp's 16 rows and the columns up to them
-  const uint32_t k_at = base + s * kStage, q_at = k_at + kTile;
+  const uint32_t k_at = base, q_at = base + kPrepQ;
   float kk[8][4], qk[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -209,23 +202,24 @@ __device__ void prepare(uint8_t *smem, uint32_t base, int c) {
     const int piece = (ks & 3) * 2;
     uint32_t ak[4], aq[4];
     const uint32_t a_off = panel + swizzled(16 * warp + (lane & 15), piece + (lane >> 4));
-    ldmatrix_x4(ak, k_at + a_off);
-    ldmatrix_x4(aq, q_at + a_off);
+    qmv::ldmatrix_x4(ak, k_at + a_off);
+    qmv::ldmatrix_x4(aq, q_at + a_off);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       if (np <= warp) {
-        uint32_t b[4];
+        uint32_t x[4];
         const int row = 16 * np + ((lane >> 4) << 3) + (lane & 7);
-        ldmatrix_x4(b, k_at + panel + swizzled(row, piece + ((lane >> 3) & 1)));
-        mma_bf16_m16n8k16(kk[2 * np], ak[0], ak[1], ak[2], ak[3], b[0], b[1]);
-        mma_bf16_m16n8k16(kk[2 * np + 1], ak[0], ak[1], ak[2], ak[3], b[2], b[3]);
-        mma_bf16_m16n8k16(qk[2 * np], aq[0], aq[1], aq[2], aq[3], b[0], b[1]);
-        mma_bf16_m16n8k16(qk[2 * np + 1], aq[0], aq[1], aq[2], aq[3], b[2], b[3]);
+        qmv::ldmatrix_x4(x, k_at + panel + swizzled(row, piece + ((lane >> 3) & 1)));
+        mma_bf16_m16n8k16(kk[2 * np], ak[0], ak[1], ak[2], ak[3], x[0], x[1]);
+        mma_bf16_m16n8k16(kk[2 * np + 1], ak[0], ak[1], ak[2], ak[3], x[2], x[3]);
+        mma_bf16_m16n8k16(qk[2 * np], aq[0], aq[1], aq[2], aq[3], x[0], x[1]);
+        mma_bf16_m16n8k16(qk[2 * np + 1], aq[0], aq[1], aq[2], aq[3], x[2], x[3]);
       }
     }
   }
-  prep_sync();  // D is there
+  __syncthreads();  // D is there, K and Q have been read
   const int g8 = lane >> 2, t4 = lane & 3;
+  const float be2[2] = {beta[16 * warp + g8], beta[16 * warp + g8 + 8]};
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
     if (nt >= 2 * (warp + 1)) continue;
@@ -234,59 +228,102 @@ __device__ void prepare(uint8_t *smem, uint32_t base, int c) {
       const int i = 16 * warp + g8 + 8 * half, j = 8 * nt + 2 * t4;
       float2 *d = reinterpret_cast<float2 *>(scratch + i * kPitch + j);
       const float2 w = *d;
-      const float be = beta[i];
-      // above the diagonal D is 0; the diagonal is P's alone
-      float p[2] = {j <= i ? qk[nt][2 * half] * w.x : 0.f, j < i ? qk[nt][2 * half + 1] * w.y : 0.f};
-      *d = make_float2(j < i ? be * (kk[nt][2 * half] * w.x) : 0.f,
-                       j + 1 < i ? be * (kk[nt][2 * half + 1] * w.y) : 0.f);
+      // the diagonal is P's alone
+      const float p[2] = {j <= i ? qk[nt][2 * half] * w.x : 0.f,
+                          j < i ? qk[nt][2 * half + 1] * w.y : 0.f};
+      *d = make_float2(j < i ? be2[half] * (kk[nt][2 * half] * w.x) : 0.f,
+                       j + 1 < i ? be2[half] * (kk[nt][2 * half + 1] * w.y) : 0.f);
       uint32_t part[kPParts][1];
       cut<1, kPParts>(p, part);
 #pragma unroll
-      for (int x = 0; x < (int)kPParts; ++x)
-        *reinterpret_cast<uint32_t *>(mats + (kTParts + x) * kPart + swizzled(i, nt) + t4 * 4) =
+      for (int x = 0; x < kPParts; ++x)
+        *reinterpret_cast<uint32_t *>(smem + kOffP + x * kPart + swizzled(i, nt) + t4 * 4) =
             part[x][0];
     }
   }
-  prep_sync();  // L is there
-  // T: the two diagonal blocks of 32, a column a lane, by substitution
-  if (warp < 2) {
-    const float *block = scratch + (32 * kPitch + 32) * warp;
-    float t[32];
-    t[0] = lane == 0 ? 1.f : 0.f;
+  __syncthreads();  // L is there
+  // T: the four diagonal blocks of 16, one a warp, a column a lane, by substitution
+  {
+    const int col = lane & 15;
+    float *block = scratch + 16 * warp * (kPitch + 1);
+    float t[16];
+    t[0] = col == 0 ? 1.f : 0.f;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) {
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 1; i < 16; ++i) {
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int m = 0; m < i; m += 4) {
         const float4 l = *reinterpret_cast<const float4 *>(block + i * kPitch + m);
         const float lm[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (m + x < i) sum[x] = fmaf(lm[x], t[m + x], sum[x]);
+          if (m + x < i) sum[x & 1] = fmaf(lm[x], t[m + x], sum[x & 1]);
       }
-      t[i] = (lane == i ? 1.f : 0.f) - ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      t[i] = (col == i ? 1.f : 0.f) - (sum[0] + sum[1]);
     }
     __syncwarp();
-    float *to = scratch + (32 * kPitch + 32) * warp + lane;
+    if (lane < 16) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      to[i * kPitch] = t[i];
-      store_parts(mats, 32 * warp + i, 32 * warp + lane, t[i]);
+      for (int i = 0; i < 16; ++i) block[i * kPitch + col] = t[i];
+    } else if (!(warp & 1)) {  // zeros beside the upper block of a pair
+#pragma unroll
+      for (int i = 0; i < 16; ++i) block[i * kPitch + lane] = 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      store_parts(smem, 16 * warp + (lane < 16 ? i : 8 + i), 16 * warp + col,
+                  lane < 16 ? t[i] : t[8 + i]);
   }
-  prep_sync();
-  // the block below: -T11 (L10 T00), two rows by four columns a thread
+  __syncthreads();
+  // the 16 x 16 blocks below them, -T11 (L10 T00) of each pair, four columns a thread
+  {
+    float *pair = scratch + 32 * (warp >> 1) * (kPitch + 1);
+    const int r = (tid & 63) >> 2, c4 = 4 * (tid & 3);
+    auto times = [&](const float *left_of, const float *right) {
+      float2 x0 = make_float2(0.f, 0.f), x1 = x0;
+#pragma unroll
+      for (int m = 0; m < 16; m += 4) {
+        const float4 l = *reinterpret_cast<const float4 *>(left_of + m);
+        const float w[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float4 t = *reinterpret_cast<const float4 *>(right + (m + y) * kPitch);
+          x0 = __ffma2_rn(make_float2(w[y], w[y]), make_float2(t.x, t.y), x0);
+          x1 = __ffma2_rn(make_float2(w[y], w[y]), make_float2(t.z, t.w), x1);
+        }
+      }
+      return make_float4(x0.x, x0.y, x1.x, x1.y);
+    };
+    float *below = pair + (16 + r) * kPitch;
+    const float4 x = times(below, pair + c4);
+    __syncwarp();  // the rows of L10 that this warp reads are its own
+    *reinterpret_cast<float4 *>(below + c4) = x;
+    __syncthreads();
+    const float4 y = times(below + 16, pair + 16 * kPitch + c4);
+    const float v[4] = {-y.x, -y.y, -y.z, -y.w};
+    __syncthreads();
+    *reinterpret_cast<float4 *>(below + c4) = make_float4(v[0], v[1], v[2], v[3]);
+    uint32_t part[kTParts][2];
+    cut<2, kTParts>(v, part);
+    const int row = 32 * (warp >> 1) + 16 + r, at = 32 * (warp >> 1) + c4;
+#pragma unroll
+    for (int p = 0; p < kTParts; ++p)
+      *reinterpret_cast<uint2 *>(smem + p * kPart + swizzled(row, at >> 3) + (at & 7) * 2) =
+          make_uint2(part[p][0], part[p][1]);
+  }
+  __syncthreads();
+  // the 32 x 32 block below, the same way, two rows by four columns a thread
   const int r = 2 * (tid >> 3), c4 = 4 * (tid & 7);
-#pragma unroll 1
+#pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     // pass 0: X = L10 T00 in L10's place; pass 1: T11 X
-    const float *left = scratch + (32 + r) * kPitch + (pass ? 32 : 0);
+    const float *left_of = scratch + (32 + r) * kPitch + (pass ? 32 : 0);
     const float *right = scratch + (pass ? 32 * kPitch : 0) + c4;
     float2 x[2][2] = {};
 #pragma unroll
     for (int m = 0; m < 32; m += 4) {
-      const float4 l0 = *reinterpret_cast<const float4 *>(left + m);
-      const float4 l1 = *reinterpret_cast<const float4 *>(left + kPitch + m);
+      const float4 l0 = *reinterpret_cast<const float4 *>(left_of + m);
+      const float4 l1 = *reinterpret_cast<const float4 *>(left_of + kPitch + m);
       const float w0[4] = {l0.x, l0.y, l0.z, l0.w}, w1[4] = {l1.x, l1.y, l1.z, l1.w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
@@ -299,12 +336,12 @@ __device__ void prepare(uint8_t *smem, uint32_t base, int c) {
       }
     }
     if (pass == 0) {
-      __syncwarp();  // the rows of L10 that this warp reads are this warp's alone
+      __syncwarp();
 #pragma unroll
       for (int y = 0; y < 2; ++y)
         *reinterpret_cast<float4 *>(scratch + (32 + r + y) * kPitch + c4) =
             make_float4(x[y][0].x, x[y][0].y, x[y][1].x, x[y][1].y);
-      prep_sync();
+      __syncthreads();
     } else {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -312,42 +349,135 @@ __device__ void prepare(uint8_t *smem, uint32_t base, int c) {
         uint32_t part[kTParts][2];
         cut<2, kTParts>(v, part);
 #pragma unroll
-        for (int p = 0; p < (int)kTParts; ++p)
-          *reinterpret_cast<uint2 *>(mats + p * kPart + swizzled(32 + r + y, c4 >> 3) + (c4 & 7) * 2) =
+        for (int p = 0; p < kTParts; ++p)
+          *reinterpret_cast<uint2 *>(smem + p * kPart + swizzled(32 + r + y, c4 >> 3) + (c4 & 7) * 2) =
               make_uint2(part[p][0], part[p][1]);
       }
     }
   }
+  fence_async();
+  __syncthreads();
+  if (tid == 0) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     blobs + (long long)blockIdx.x * kBlob),
+                 "r"(base), "r"(kBlob)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  }
 }
 
-// E or the outputs: D[dv][64 rows] (+)= A parts x B parts, lower triangular: the
-// 16 columns of k step j reach the rows from 16 j on.
-template <int kNa, int kNb>
-__device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b, int least) {
-  uint32_t acc = 0;
+// ---- the state from chunk to chunk ---------------------------------------------------
+constexpr int kChainWarps = 16, kMmaWarp = 16;  // and a loading warp
+constexpr int kThreads = 576;
+constexpr uint32_t kStage = 3 * kTile + kBlob;  // K, Q, V, blob
+constexpr uint32_t kOffBars = 2 * kStage;
+enum Bar {
+  kFull = 0,     // [2 stages] loaded
+  kEmpty = 2,    // [2] read
+  kTail = 4,     // the last chunk's loads, whose rows past the end are then zeroed
+  kState = 5,    // [2 halves of dk] the state's parts are written
+  kR = 7,        // [2 halves of the rows] R's are
+  kE = 9,        // [2] E's are
+  kOutRead = 11, // S0 Q^T and E P^T have been read
+  kKs = 12,      // [2 halves of the rows] S0 K^T is there
+  kTr = 14,      // [2] R T^T is
+  kQs = 16,      // S0 Q^T is
+  kSu = 17,      // [2 halves of dk] E' K is
+  kOut = 19,     // E P^T is
+  kPair = 20,    // [8] the two warps that share a place of tensor memory have read it
+  kBars = 28
+};
+constexpr uint32_t kOffTmem = kOffBars + 8 * kBars;
+constexpr uint32_t kSmem = kOffTmem + 16 + 1024;
+
+// Tensor memory (columns).  The state's parts: of each half of dk three parts of 32
+// columns; E' K of that half first lands in the same place.
+constexpr uint32_t kColState = 0, kColHalf = 96;
+constexpr uint32_t kColK = 192;   // S0 K^T, then E's two parts
+constexpr uint32_t kColQ = 256;   // S0 Q^T
+constexpr uint32_t kColE = 320;   // R T^T, then E P^T
+constexpr uint32_t kColR = 384;   // R's parts, then those of E'
+constexpr uint32_t kTmemCols = 512;
+
+constexpr uint32_t idesc(int n, bool mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10)  // D fp32; A, B bf16
+         | (mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld_x16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+        "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+// Uses of registers that a tcgen05.ld fills stay behind its wait.
+template <int kN>
+__device__ __forceinline__ void pin(uint32_t (&v)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
+                      "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+
+struct Item {
+  int start, n, slot, h, hk, chunks;
+  long long blob;  // of its first chunk; the next H further
+};
+
+// R T^T or E P^T, D[dv][64 rows] (+)= A parts x B parts, both lower triangular: the
+// 16 columns of step j reach the rows from 16 j on.  Steps [kJ0, kJ1); the product
+// begins with step 0.  Parts whose weights add up past `kLeast` are left out.
+template <int kNa, int kNb, int kLeast, int kJ0, int kJ1>
+__device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int pa = 0; pa < kNa; ++pa)
 #pragma unroll
     for (int pb = 0; pb < kNb; ++pb) {
-      if (pa + pb > least) continue;  // below the last part's weight
+      if (pa + pb > kLeast) continue;
 #pragma unroll
-      for (int j = 0; j < kC / 16; ++j) {
+      for (int j = kJ0; j < kJ1; ++j)
         tc_mma_ts(d + 16 * j, a + 32 * pa + 8 * j,
-                  smem_desc_sw128(b + pb * kPart + j * 2048 + j * 32), idesc(kC - 16 * j, false), acc);
-        acc = 1;
-      }
+                  smem_desc_sw128(b + pb * kPart + j * 2048 + j * 32), idesc(kC - 16 * j, false),
+                  pa + pb + j > 0);
     }
 }
-// S0 times K^T or Q^T.
-template <int kNp>
-__device__ __forceinline__ void mma_state(uint32_t d, uint32_t tmem, uint32_t b) {
+// S0 times kRows rows of K or Q, from half `half` of dk.
+template <int kParts, int kRowsOf>
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t tmem, uint32_t b, int half) {
 #pragma unroll
-  for (int p = 0; p < kNp; ++p)
+  for (int p = 0; p < kParts; ++p)
 #pragma unroll
-    for (int ks = 0; ks < kD / 16; ++ks)
-      tc_mma_ts(d, tmem + kColState + (ks >> 2) * kColHalf + 32 * p + 8 * (ks & 3),
-                smem_desc_sw128(b + (ks >> 2) * kPanel + (ks & 3) * 32), idesc(kC, false),
-                p + ks > 0);
+    for (int ks = 0; ks < 4; ++ks)
+      tc_mma_ts(d, tmem + kColState + half * kColHalf + 32 * p + 8 * ks,
+                smem_desc_sw128(b + half * kPanel + ks * 32), idesc(kRowsOf, false),
+                half + p + ks > 0);
+}
+// E' K: steps [j0, j0 + 2) of the chunk's rows, half `half` of dk.
+__device__ __forceinline__ void mma_update(uint32_t tmem, uint32_t k_at, int half, int j0) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      tc_mma_ts(tmem + kColState + half * kColHalf, tmem + kColR + 32 * p + 8 * (j0 + j),
+                smem_desc_sw128_mn(k_at + half * kPanel + (j0 + j) * 2048, kPanel), idesc(64, true),
+                j0 + p + j > 0);
 }
 
 __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
@@ -355,75 +485,91 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
   const bool one = elect_one();
   bool ok = true;
   auto wait = [&](int i, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(i), parity));
+    ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(i), parity));
     tc_fence_after();
     return ok;
   };
-  for (int c = 0; c < it.chunks && ok; ++c) {
+  for (int c = 0; c < it.chunks; ++c) {
     const uint32_t s = c & 1, odd = c & 1, pair = (c >> 1) & 1;
     const uint32_t k_at = base + s * kStage, q_at = k_at + kTile;
-    const uint32_t t_at = base + kOffMats + s * kMats, p_at = t_at + kTParts * kPart;
-    if (c > 0 && !wait(kOut, odd ^ 1)) break;  // E P^T read what S0 K^T overwrites
-    if (!wait(kKvFull + s, pair) || !wait(kState, odd)) break;
+    const uint32_t t_at = k_at + 3 * kTile, p_at = t_at + kOffP;
+    if (c > 0 && !wait(kOut, odd ^ 1)) break;  // E P^T has read what S0 K^T overwrites
+    if (!wait(kFull + s, pair) || !wait(kState, odd)) break;
+    if (one) mma_state<3, 64>(tmem + kColK, tmem, k_at, 0);
+    __syncwarp();
+    if (!wait(kState + 1, odd)) break;
     if (one) {
-      mma_state<3>(tmem + kColK, tmem, k_at);
+      mma_state<3, 32>(tmem + kColK, tmem, k_at, 1);
       tc_commit(bar(kKs));
+      mma_state<3, 32>(tmem + kColK + 32, tmem, k_at + 32 * 128, 1);
+      tc_commit(bar(kKs + 1));
     }
     __syncwarp();
-    if (!wait(kMatFull + s, pair) || !wait(kR, odd)) break;
+    if (c > 0 && !wait(kOutRead, odd ^ 1)) break;
     if (one) {
-      mma_lower<3, 3>(tmem + kColE, tmem + kColR, t_at, 2);
-      tc_commit(bar(kTr));
-      mma_state<2>(tmem + kColQ, tmem, q_at);
+      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 0);
+      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 1);
       tc_commit(bar(kQs));
     }
     __syncwarp();
-    if (!wait(kQs, odd) || !wait(kE, odd)) break;
+    if (!wait(kR, odd)) break;
     if (one) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int j = 0; j < kC / 16; ++j)
-            tc_mma_ts(tmem + kColState + half * kColHalf, tmem + kColR + 32 * p + 8 * j,
-                      smem_desc_sw128_mn(k_at + half * kPanel + j * 2048, kPanel), idesc(64, true),
-                      p + j > 0);
+      mma_lower<3, 3, 2, 0, 2>(tmem + kColE, tmem + kColR, t_at);
+      tc_commit(bar(kTr));
+    }
+    __syncwarp();
+    if (!wait(kR + 1, odd)) break;
+    if (one) {
+      mma_lower<3, 3, 2, 2, 4>(tmem + kColE, tmem + kColR, t_at);
+      tc_commit(bar(kTr + 1));
+    }
+    __syncwarp();
+    if (!wait(kQs, odd) || !wait(kE, odd)) break;  // S0 Q^T has read what E' K overwrites
+    if (one) {
+      mma_update(tmem, k_at, 0, 0);
+      mma_update(tmem, k_at, 1, 0);
+    }
+    __syncwarp();
+    if (!wait(kE + 1, odd)) break;
+    if (one) {
+      mma_update(tmem, k_at, 0, 2);
       tc_commit(bar(kSu));
-      mma_lower<2, 2>(tmem + kColE, tmem + kColK, p_at, 1);
+      mma_update(tmem, k_at, 1, 2);
+      tc_commit(bar(kSu + 1));
+      mma_lower<2, 2, 1, 0, 4>(tmem + kColE, tmem + kColK, p_at);
       tc_commit(bar(kOut));
-      tc_commit(bar(kKvEmpty + s));
-      tc_commit(bar(kMatEmpty + s));
+      tc_commit(bar(kEmpty + s));
     }
     __syncwarp();
   }
   if (!ok && one) atomicOr(&g_give_up, 1u);
 }
 
-// ---- the chain: lane = row of the state (dv), warps 0..3 the first half of the
-// chunk's rows and of dk, 4..7 the second ------------------------------------------
+// The chain's warps: lane = row of the state (dv); warps 4 g .. 4 g + 3 take rows
+// 16 g .. of the chunk and columns 32 g .. of the state.
 __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, uint32_t base,
                           uint32_t tmem_base) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = 32 * (warp & 3) + lane, half = warp >> 2;
+  const int i = 32 * (warp & 3) + lane, g = warp >> 2, half = g >> 1;
   const uint32_t tmem = tmem_base + ((uint32_t)(warp & 3) << 21);
   auto bar = [&](int b) { return base + kOffBars + 8u * b; };
   auto arrive = [&](int b) {
+    tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive_u32(bar(b));
   };
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity));
+    ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(b), parity));
     tc_fence_after();
     return ok;
   };
-  float S[64];
-  float *state = a.state + (((long long)it.slot * a.H + it.h) * a.dv + (i < a.dv ? i : 0)) * a.dk + 64 * half;
+  float S[32];
+  float *state = a.state + (((long long)it.slot * a.H + it.h) * a.dv + (i < a.dv ? i : 0)) * a.dk + 32 * g;
 #pragma unroll
-  for (int m = 0; m < 64; m += 4) {
+  for (int m = 0; m < 32; m += 4) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < a.dv && 64 * half + m < a.dk) x = __ldcg(reinterpret_cast<const float4 *>(state + m));
+    if (i < a.dv && 32 * g + m < a.dk) x = __ldcg(reinterpret_cast<const float4 *>(state + m));
     S[m] = x.x;
     S[m + 1] = x.y;
     S[m + 2] = x.z;
@@ -432,70 +578,67 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
   const uint32_t s_at = tmem + kColState + half * kColHalf;
   auto put_state = [&] {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      uint32_t part[3][16];
-      cut<16, 3>(S + 32 * g, part);
+    for (int x = 0; x < 2; ++x) {
+      uint32_t part[3][8];
+      cut<8, 3>(S + 16 * x, part);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) tc_st_x16(s_at + 32 * p + 16 * g, part[p]);
+      for (int p = 0; p < 3; ++p) tc_st_x8(s_at + 32 * p + 16 * (g & 1) + 8 * x, part[p]);
     }
     tc_wait_st();
-    tc_fence_before();
-    arrive(kState);
+    arrive(kState + half);
   };
   put_state();
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (long long)it.start * a.out_stride +
-                       (long long)it.h * a.dv + i;
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                       (long long)(it.start + 16 * g) * a.out_stride + (long long)it.h * a.dv + i;
   for (int c = 0; c < it.chunks; ++c) {
     const uint32_t s = c & 1, odd = c & 1, pair = (c >> 1) & 1;
-    const float *beta = reinterpret_cast<const float *>(smem + kOffGates) + s * 2 * kC + kC + 32 * half;
-    const float *G = reinterpret_cast<const float *>(smem + kOffDecay) + s * 2 * kC + 32 * half;
-    const float *last = G + kC;
-    const uint16_t *v = reinterpret_cast<const uint16_t *>(smem + s * kStage + 2 * kTile) +
-                        32 * half * kD + i;
-    const int left = it.n - c * kC - 32 * half;  // rows of this half
+    const uint8_t *stage = smem + s * kStage, *blob = stage + 3 * kTile;
+    const float *G = reinterpret_cast<const float *>(blob + kOffG) + 16 * g;
+    const float *last = G + kC, *beta = last + kC;
+    const uint16_t *v = reinterpret_cast<const uint16_t *>(stage + 2 * kTile) + 16 * g * kD + i;
+    const int left = it.n - c * kC - 16 * g;  // rows of this warp's 16
     // R = beta (v - G S0 k)
-    if (!wait(kKvFull + s, pair) || !wait(kMatFull + s, pair) || !wait(kKs, odd)) break;
-    {
-      uint32_t x[32];
-      tc_ld_x32(tmem + kColK + 32 * half, x);
-      float val[32];
+    if (!wait(kFull + s, pair)) break;
+    float val[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) val[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
+    for (int j = 0; j < 16; ++j) val[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
+    if (!wait(kKs + half, odd)) break;
+    {
+      uint32_t x[16];
+      tc_ld_x16(tmem + kColK + 16 * g, x);
       tc_wait_ld();
       pin(x);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
+      for (int j = 0; j < 16; j += 4) {
         const float4 be = *reinterpret_cast<const float4 *>(beta + j);
-        const float4 g = *reinterpret_cast<const float4 *>(G + j);
-        val[j] = be.x * fmaf(-g.x, __uint_as_float(x[j]), val[j]);
-        val[j + 1] = be.y * fmaf(-g.y, __uint_as_float(x[j + 1]), val[j + 1]);
-        val[j + 2] = be.z * fmaf(-g.z, __uint_as_float(x[j + 2]), val[j + 2]);
-        val[j + 3] = be.w * fmaf(-g.w, __uint_as_float(x[j + 3]), val[j + 3]);
+        const float4 f = *reinterpret_cast<const float4 *>(G + j);
+        val[j] = be.x * fmaf(-f.x, __uint_as_float(x[j]), val[j]);
+        val[j + 1] = be.y * fmaf(-f.y, __uint_as_float(x[j + 1]), val[j + 1]);
+        val[j + 2] = be.z * fmaf(-f.z, __uint_as_float(x[j + 2]), val[j + 2]);
+        val[j + 3] = be.w * fmaf(-f.w, __uint_as_float(x[j + 3]), val[j + 3]);
       }
-      if (left < 32) {  // no row: a state that is not finite must not reach it
+      if (left < 16) {  // no row: what lies there, or a state that is not finite, must not count
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
           if (j >= left) val[j] = 0.f;
       }
-      uint32_t part[3][16];
-      cut<16, 3>(val, part);
+      uint32_t part[3][8];
+      cut<8, 3>(val, part);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) tc_st_x16(tmem + kColR + 32 * p + 16 * half, part[p]);
+      for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
       tc_wait_st();
-      tc_fence_before();
-      arrive(kR);
-      arrive(kKvEmpty + s);
+      arrive(kR + half);
     }
     // E and E' = D[63] E
-    if (!wait(kTr, odd)) break;
+    if (!wait(kTr + half, odd)) break;
     {
-      uint32_t x[32];
-      tc_ld_x32(tmem + kColE + 32 * half, x);
+      uint32_t x[16];
+      tc_ld_x16(tmem + kColE + 16 * g, x);
       tc_wait_ld();
       pin(x);
-      float e[32];
+      float e[16];
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
+      for (int j = 0; j < 16; j += 4) {
         const float4 d = *reinterpret_cast<const float4 *>(last + j);
         e[j] = d.x * __uint_as_float(x[j]);
         e[j + 1] = d.y * __uint_as_float(x[j + 1]);
@@ -503,63 +646,76 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
         e[j + 3] = d.w * __uint_as_float(x[j + 3]);
       }
       {
-        uint32_t part[3][16];
-        cut<16, 3>(e, part);
+        uint32_t part[3][8];
+        cut<8, 3>(e, part);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) tc_st_x16(tmem + kColR + 32 * p + 16 * half, part[p]);
+        for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
       }
 #pragma unroll
-      for (int j = 0; j < 32; ++j) e[j] = __uint_as_float(x[j]);
+      for (int j = 0; j < 16; ++j) e[j] = __uint_as_float(x[j]);
       {
-        uint32_t part[2][16];
-        cut<16, 2>(e, part);
+        uint32_t part[2][8];
+        cut<8, 2>(e, part);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) tc_st_x16(tmem + kColK + 32 * p + 16 * half, part[p]);
+        for (int p = 0; p < 2; ++p) tc_st_x8(tmem + kColK + 32 * p + 8 * g, part[p]);
       }
       tc_wait_st();
-      tc_fence_before();
-      arrive(kE);
+      arrive(kE + half);
     }
     // S = G[63] S0 + E' K
-    if (!wait(kSu, odd)) break;
+    if (!wait(kSu + half, odd)) break;
     {
-      const float g = reinterpret_cast<const float *>(smem + kOffDecay)[s * 2 * kC + kC - 1];
-      const float2 g2 = make_float2(g, g);
+      const float all = reinterpret_cast<const float *>(blob + kOffG)[kC - 1];
+      const float2 all2 = make_float2(all, all);
+      uint32_t x[2][16];
+      tc_ld_x16(s_at + 32 * (g & 1), x[0]);
+      tc_ld_x16(s_at + 32 * (g & 1) + 16, x[1]);
+      tc_wait_ld();
+      pin(x[0]);
+      pin(x[1]);
 #pragma unroll
-      for (int m = 0; m < 64; m += 32) {
-        uint32_t x[32];
-        tc_ld_x32(s_at + m, x);
-        tc_wait_ld();
-        pin(x);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 n = __ffma2_rn(g2, make_float2(S[m + j], S[m + j + 1]),
-                                      make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
-          S[m + j] = n.x;
-          S[m + j + 1] = n.y;
-        }
+      for (int j = 0; j < 32; j += 2) {
+        const float2 n = __ffma2_rn(all2, make_float2(S[j], S[j + 1]),
+                                    make_float2(__uint_as_float(x[j >> 4][j & 15]),
+                                                __uint_as_float(x[j >> 4][(j & 15) + 1])));
+        S[j] = n.x;
+        S[j + 1] = n.y;
       }
-      if (c + 1 < it.chunks) put_state();
+      if (c + 1 < it.chunks) {
+        const int shared = kPair + 4 * half + (warp & 3);
+        arrive(shared);
+        if (!wait(shared, odd)) break;
+        put_state();
+      }
     }
     // o = G S0 q + E P
     if (!wait(kOut, odd)) break;
     {
-      uint32_t x[32], y[32];
-      tc_ld_x32(tmem + kColQ + 32 * half, x);
-      tc_ld_x32(tmem + kColE + 32 * half, y);
+      uint32_t x[16], y[16];
+      tc_ld_x16(tmem + kColQ + 16 * g, x);
+      tc_ld_x16(tmem + kColE + 16 * g, y);
       tc_wait_ld();
       pin(x);
       pin(y);
-      __nv_bfloat16 *to = out + (long long)(c * kC + 32 * half) * a.out_stride;
-      if (i < a.dv) {
+      float o[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < left)
-            to[j * a.out_stride] =
-                __float2bfloat16_rn(fmaf(G[j], __uint_as_float(x[j]), __uint_as_float(y[j])));
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(G + j);
+        o[j] = fmaf(f.x, __uint_as_float(x[j]), __uint_as_float(y[j]));
+        o[j + 1] = fmaf(f.y, __uint_as_float(x[j + 1]), __uint_as_float(y[j + 1]));
+        o[j + 2] = fmaf(f.z, __uint_as_float(x[j + 2]), __uint_as_float(y[j + 2]));
+        o[j + 3] = fmaf(f.w, __uint_as_float(x[j + 3]), __uint_as_float(y[j + 3]));
       }
-      tc_fence_before();
-      arrive(kMatEmpty + s);
+      arrive(kOutRead);
+      if (lane == 0) mbar_arrive_u32(bar(kEmpty + s));
+      const int stored = i < a.dv ? left : 0;
+      __nv_bfloat16 *to = out;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (j < stored) *to = __float2bfloat16_rn(o[j]);
+        to += a.out_stride;
+      }
+      out += kC * a.out_stride;
     }
   }
   if (!ok) {
@@ -568,18 +724,67 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
   }
   if (i < a.dv) {
 #pragma unroll
-    for (int m = 0; m < 64; m += 4)
-      if (64 * half + m < a.dk)
+    for (int m = 0; m < 32; m += 4)
+      if (32 * g + m < a.dk)
         *reinterpret_cast<float4 *>(state + m) = make_float4(S[m], S[m + 1], S[m + 2], S[m + 3]);
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const AdvanceArgs a) {
+__device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
+                            const uint8_t *blobs, int H, const Item &it, uint8_t *smem, uint32_t base) {
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return base + kOffBars + 8u * i; };
+  bool ok = true;
+  int c = 0;
+  for (; c < it.chunks; ++c) {
+    const uint32_t s = c & 1, at = base + s * kStage;
+    if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(kEmpty + s), ((c >> 1) & 1) ^ 1));
+    if (!ok) break;
+    const int left = it.n - c * kC;
+    const uint32_t full = bar(left < kC ? (int)kTail : (int)(kFull + s));
+    if (lane == 0) {
+      const int row = it.start + c * kC;
+      mbar_arrive_expect_tx_u32(full, kStage);
+      for (int x = 0; x < 2; ++x) {
+        tma_load_3d(at + x * kPanel, kmap, 64 * x, it.hk, row, full);
+        tma_load_3d(at + kTile + x * kPanel, qmap, 64 * x, it.hk, row, full);
+      }
+      tma_load_3d(at + 2 * kTile, vmap, 0, it.h, row, full);
+      asm volatile(
+          "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              at + 3 * kTile),
+          "l"(blobs + (it.blob + (long long)c * H) * kBlob), "r"(kBlob), "r"(full)
+          : "memory");
+    }
+    __syncwarp();
+    if (left < kC) {
+      // the rows behind the sequence are another's: as K's they must not meet E'
+      ok = __all_sync(0xffffffffu, mbar_wait_u32(full, 0));
+      uint8_t *k = smem + s * kStage;
+      for (int x = lane; x < (kC - left) * 16; x += 32)
+        *reinterpret_cast<uint4 *>(k + (x & 1) * kPanel + (left + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_u32(bar(kFull + s));
+    }
+  }
+  if (!ok) {
+    if (lane == 0) atomicOr(&g_give_up, 4u);
+    for (int x = max(0, c - 2); x < c; ++x)  // the copies in flight
+      if (it.n - x * kC >= kC) (void)mbar_wait_u32(bar(kFull + (x & 1)), (x >> 1) & 1);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gdn_chunk_states(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap vmap, const AdvanceArgs a,
+                     const uint8_t *blobs) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   Item it;
   it.h = blockIdx.x;
   it.hk = it.h / (a.H / a.Hk);
@@ -603,79 +808,33 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const AdvanceArg
     return;
   }
   it.chunks = (it.n + kC - 1) / kC;
+  it.blob = (long long)(it.start / kC + b) * a.H + it.h;
   auto bar = [&](int i) { return base + kOffBars + 8u * i; };
   if (warp == kMmaWarp) tmem_alloc(base + kOffTmem, kTmemCols);
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init_u32(bar(kKvFull + s), kLoadWarps * 32);
-      mbar_init_u32(bar(kKvEmpty + s), 1 + kChainWarps + kPrepWarps);
-      mbar_init_u32(bar(kMatFull + s), kPrepWarps);
-      mbar_init_u32(bar(kMatEmpty + s), 1 + kChainWarps);
+      mbar_init_u32(bar(kFull + s), 1);
+      mbar_init_u32(bar(kEmpty + s), 1 + kChainWarps);
+      mbar_init_u32(bar(kState + s), kChainWarps / 2);
+      mbar_init_u32(bar(kR + s), kChainWarps / 2);
+      mbar_init_u32(bar(kE + s), kChainWarps / 2);
+      for (int i : {kKs, kTr, kSu}) mbar_init_u32(bar(i + s), 1);
     }
-    mbar_init_u32(bar(kState), kChainWarps);
-    mbar_init_u32(bar(kR), kChainWarps);
-    mbar_init_u32(bar(kE), kChainWarps);
-    for (int i : {kKs, kTr, kQs, kSu, kOut}) mbar_init_u32(bar(i), 1);
+    mbar_init_u32(bar(kOutRead), kChainWarps);
+    for (int i : {kTail, kQs, kOut}) mbar_init_u32(bar(i), 1);
+    for (int i = 0; i < 8; ++i) mbar_init_u32(bar(kPair + i), 2);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffTmem);
-
-  if (warp < kChainWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
+  if (warp < kChainWarps)
     run_chain(a, it, smem, base, tmem);
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp < kMmaWarp) {
-      bool ok = true;
-      for (int c = 0; c < it.chunks; ++c) {
-        const uint32_t s = c & 1, pair = (c >> 1) & 1;
-        ok = wait_bar(bar(kKvFull + s), pair);
-        if (ok && c >= 2) ok = wait_bar(bar(kMatEmpty + s), pair ^ 1);
-        // all four warps go on or none does
-        int all;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-            "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-            : "=r"(all)
-            : "r"((int)ok)
-            : "memory");
-        ok = all != 0;
-        if (!ok) break;
-        prepare(smem, base, c);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_u32(bar(kMatFull + s));
-          mbar_arrive_u32(bar(kKvEmpty + s));
-        }
-      }
-      if (!ok && lane == 0) atomicOr(&g_give_up, 4u);
-    } else if (warp == kMmaWarp) {
-      issue_chunks(base, tmem, it);
-    } else {
-      const int tid = threadIdx.x - kLoadWarp * 32;
-      bool ok = true;
-      load_chunk(a, it, smem, base, 0, tid);
-      for (int c = 0; c < it.chunks; ++c) {
-        if (c + 1 < it.chunks) {
-          const uint32_t s = (c + 1) & 1;
-          if (c + 1 >= 2) ok = wait_bar(bar(kKvEmpty + s), (((c + 1) >> 1) & 1) ^ 1);
-          if (!ok) break;
-          load_chunk(a, it, smem, base, c + 1, tid);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        fence_async();
-        mbar_arrive_u32(bar(kKvFull + (c & 1)));
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!ok && lane == 0) atomicOr(&g_give_up, 8u);
-    }
-  }
+  else if (warp == kMmaWarp)
+    issue_chunks(base, tmem, it);
+  else
+    load_chunks(&kmap, &qmap, &vmap, blobs, a.H, it, smem, base);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -685,18 +844,57 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_chunk_kernel(const AdvanceArg
   }
 }
 
+// Rows [rows][heads][dim] in boxes of kC rows of one head.
+sv_status encode_rows(CUtensorMap *map, const void *p, long long row_stride, int rows, int heads,
+                      int dim, uint32_t box, CUtensorMapSwizzle swizzle) {
+  qmv::EncodeTiledFn enc = qmv::encode_tiled();
+  if (!enc) return fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  if (rows == 1) row_stride = (long long)heads * dim;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)row_stride * 2};
+  const cuuint32_t boxes[3] = {box, 1, kC}, ones[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides,
+                         boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SV_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
+  return SV_OK;
+}
+
 }  // namespace
 
-sv_status chunk_run(const AdvanceArgs &a, cudaStream_t stream) {
+size_t chunk_workspace_bytes(int rows, int B, int H) {
+  return (size_t)((long long)rows / kC + B) * H * kBlob;
+}
+
+sv_status chunk_run(const AdvanceArgs &a, void *workspace, cudaStream_t stream) {
   static PerDeviceOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(gdn_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kSmem);
+    const cudaError_t x = cudaFuncSetAttribute(
+        gdn_chunk_matrices, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrepSmem);
+    return x != cudaSuccess ? x
+                            : cudaFuncSetAttribute(gdn_chunk_states,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)kSmem);
   });
   if (e != cudaSuccess)
     return fail(SV_ERR_CUDA, "gdn_advance: cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+  CUtensorMap kmap, qmap, vmap;
+  sv_status st = encode_rows(&kmap, a.k, a.k_stride, a.rows, a.Hk, a.dk, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == SV_OK)
+    st = encode_rows(&qmap, a.q, a.q_stride, a.rows, a.Hk, a.dk, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == SV_OK)
+    st = encode_rows(&vmap, a.v, a.v_stride, a.rows, a.H, a.dv, kD, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st != SV_OK) return st;
+  uint8_t *blobs = static_cast<uint8_t *>(workspace);
+  const long long items = ((long long)a.rows / kC + a.B) * a.H;
+  if (items >= (1ll << 31)) return fail(SV_ERR_UNSUPPORTED, "gdn_advance: too many rows");
+  if (items > 0) {
+    gdn_chunk_matrices<<<(unsigned)items, kPrepThreads, kPrepSmem, stream>>>(a, blobs);
+    st = check_launch("gdn_advance");
+    if (st != SV_OK) return st;
+  }
   const dim3 grid((unsigned)a.H, (unsigned)a.B + 1);
-  gdn_chunk_kernel<<<grid, kThreads, kSmem, stream>>>(a);
+  gdn_chunk_states<<<grid, kThreads, kSmem, stream>>>(kmap, qmap, vmap, a, blobs);
   return check_launch("gdn_advance");
 }
 

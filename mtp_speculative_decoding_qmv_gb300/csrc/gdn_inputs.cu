@@ -60,24 +60,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
 // in the range that silu does not send to zero.
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-// The sequence b in [0, B] (B: the rows past the last) and the tile j of it that
-// tile number i is: b's first tile is number q_start[b] / tile + b, which leaves
-// room for the ceil(n / tile) tiles of every sequence before it.
-__device__ __forceinline__ int tile_owner(const InputsArgs &a, int i, int &j) {
-  const int lane = threadIdx.x & 31;
-  auto first = [&](int b) { return min(max(__ldg(a.q_start + b), 0), a.rows) / a.tile + b; };
-  int lo = 0, n = a.B + 1;  // the owner is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32, at = lo + lane * step;
-    const bool upto = at < lo + n && first(at) <= i;
-    const int found = max(__popc(__ballot_sync(0xffffffffu, upto)) - 1, 0);
-    n = min(step, n - found * step);
-    lo += found * step;
-  }
-  j = i - first(lo);
-  return lo;
-}
-
 template <class X, class Y, int kW>
 __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArgs a) {
   const int W = kW > 0 ? kW : a.W;
@@ -86,7 +68,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= a.tasks) return;
   int j;
-  const int b = tile_owner(a, blockIdx.y, j);
+  const int b = tile_owner(a.q_start, a.B, a.rows, a.tile, blockIdx.y, j);
   Rows s;
   int slot = -1;
   if (b < a.B) {

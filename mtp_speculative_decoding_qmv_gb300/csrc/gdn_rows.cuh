@@ -27,6 +27,27 @@ __device__ __forceinline__ int slot_of(const int32_t *index, int b, int slots) {
   return i >= 0 && i < slots ? i : -1;
 }
 
+// Tiles of `tile` rows that begin at the sequences' first rows, numbered so that
+// sequence b's first is q_start[b] / tile + b: room for the ceil(n / tile) tiles of
+// every sequence before it.  The owner of tile number i, in [0, B] (B: the rows past
+// the last sequence), and its place j among the owner's tiles (past its last: no
+// such tile).  By a whole warp.
+__device__ __forceinline__ int tile_owner(const int32_t *q_start, int B, int rows, int tile, int i,
+                                          int &j) {
+  const int lane = threadIdx.x & 31;
+  auto first = [&](int b) { return min(max(__ldg(q_start + b), 0), rows) / tile + b; };
+  int lo = 0, n = B + 1;  // the owner is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool upto = at < lo + n && first(at) <= i;
+    const int found = max(__popc(__ballot_sync(0xffffffffu, upto)) - 1, 0);
+    n = min(step, n - found * step);
+    lo += found * step;
+  }
+  j = i - first(lo);
+  return lo;
+}
+
 // Eight consecutive values, 32 bytes of fp32 or 16 of bf16, still as loaded.
 template <class T>
 struct Raw8;
@@ -86,7 +107,8 @@ struct AdvanceArgs {
 };
 
 // gdn_chunk.cu: bf16 rows in chunks on the tensor cores.
-sv_status chunk_run(const AdvanceArgs &a, cudaStream_t stream);
+size_t chunk_workspace_bytes(int rows, int B, int H);
+sv_status chunk_run(const AdvanceArgs &a, void *workspace, cudaStream_t stream);
 
 }  // namespace gdn
 }  // namespace sv

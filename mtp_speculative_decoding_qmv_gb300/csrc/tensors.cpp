@@ -323,12 +323,12 @@ PyObject *inputs(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 // gdn_advance(device, stream, q, k, v, alpha, beta, state, q_start, state_index or None, max_new,
-// out)
+// out, workspace or None)
 PyObject *advance(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Reader r;
   sv_stream_t stream;
-  if (!begin(args, n, 12, &r, &stream)) return nullptr;
+  if (!begin(args, n, 13, &r, &stream)) return nullptr;
   int max_new;
   if (!to_int(args[10], &max_new)) return nullptr;
   const at::Tensor *q = r.tensor(2), *state = r.tensor(7), *start = r.tensor(8);
@@ -347,6 +347,8 @@ PyObject *advance(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const auto *q_start = r.at<int32_t>(8, at::kInt, {b + 1});
   const auto *index = r.given(9) ? r.at<int32_t>(9, at::kInt, {b}) : nullptr;
   void *out = r.rows<void>(11, type, rows, hv, dv, &os);
+  int64_t bytes = 0;
+  void *workspace = r.given(12) ? r.any<void>(12, at::kByte, &bytes) : nullptr;
   if (!r.fits) Py_RETURN_NONE;
   int s[7];
   const int64_t sizes[7] = {b, rows, slots, hk, hv, dk, dv};
@@ -355,7 +357,7 @@ PyObject *advance(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return call([&] {
     return advance_fn(q_at, k_at, v_at, type == f32 ? SV_F32 : SV_BF16, qs, ks, vs, al, be,
                       state_at, q_start, index, s[0], s[1], max_new, s[2], s[3], s[4], s[5], s[6],
-                      out, os, stream);
+                      out, os, workspace, (size_t)bytes, stream);
   });
   END_HANDLE_TH_ERRORS
 }
