@@ -6,28 +6,30 @@
 //   e_i  = beta_i (v_i - G[i] S0 k_i - sum_{j<i} D[i][j] (k_i . k_j) e_j)
 //   o_i  = G[i] S0 q_i + sum_{j<=i} D[i][j] (q_i . k_j) e_j
 //   S    = G[63] S0 + sum_j D[63][j] e_j k_j^T
-// With L = tril(beta D K K^T, -1), T = (1 + L)^-1 and P = tril(D Q K^T), as columns
-// over the chunk's rows:
-//   R = beta (V - G S0 K^T);  E = R T^T;  O = G S0 Q^T + E P^T;  S = G[63] S0 + E' K
+// With L = tril(beta D K K^T, -1), T = (1 + L)^-1 beta and P = tril(D Q K^T), as
+// columns over the chunk's rows:
+//   E = V T^T + R T^T, R = -G S0 K^T;  O = G S0 Q^T + E P^T;  S = G[63] S0 + E' K
 // Two launches.  The first makes T and P of every chunk of every head, all chunks
 // side by side (mma.sync for K K^T and Q K^T, whose results are wanted in
 // registers; T by substitution in fp32).  The second follows the state from chunk
-// to chunk, a CTA a (sequence, head): five products a chunk, each with 128 rows
-// (dv) in tensor memory's lanes; S0, R and E are A operands in tensor memory, K, Q,
-// T and P (bf16, shared memory) are B.  K serves both as rows of dk (S0 K^T) and
-// with dk contiguous (E' K), from one copy.
+// to chunk, a CTA a (sequence, head): six products a chunk, each with 128 rows
+// (dv) in tensor memory's lanes; S0, R and E are A operands in tensor memory, V in
+// shared memory, K, Q, T and P (bf16, shared memory) are B.  K serves both as rows of
+// dk (S0 K^T) and with dk contiguous (E' K), from one copy.
 //
 // Precision: the state stays in fp32 registers.  An fp32 operand is cut into three
 // bf16 parts that add up to it exactly (8 bits of it each), so what reaches the
-// state is fp32-exact products of K (bf16 as given): S0 K^T and E' K with three
-// parts, R T^T with the six products of parts above 2^-24.  The output, bf16 in
-// the end, takes two parts of S0, E and P: 2^-16, far below its own rounding.
+// state is fp32-exact products of K and V (bf16 as given): S0 K^T, E' K and V T^T
+// with three parts, R T^T with the six products of parts above 2^-24.  The output,
+// bf16 in the end, takes two parts of S0 and P (2^-16) and E rounded to bf16: at
+// most its own rounding once more.
 //
 // What bounds the second is the chain from chunk to chunk: tensor-core time of S0
 // K^T, R T^T and E' K (about 2000 cycles a chunk), and between them the warps that
 // read a product, cut it and write the next operand.  The chunk's rows, and the
 // state's columns, go through in two halves, so that one half's products run while
-// the other half is cut.  S0 Q^T and E P^T run in the gaps.
+// the other half is cut.  S0 Q^T, V T^T and E P^T run in the gaps, and the outputs
+// leave by four warps of their own.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -44,13 +46,12 @@ constexpr int kD = 128;   // dk and dv, narrower ones padded with zeros
 
 // What the first launch leaves of a chunk of a head, as the second wants it in
 // shared memory: T in three parts and P in two ([64 rows][64 columns] bf16 each, in
-// the 128-byte swizzle), G, D[63] and beta.
+// the 128-byte swizzle), G and D[63].
 constexpr uint32_t kTile = kC * kD * 2;             // K, Q or V of a chunk
 constexpr uint32_t kPanel = kC * 128;               // 64 columns of it, 128-byte swizzle
 constexpr uint32_t kPart = kC * kC * 2;
 constexpr int kTParts = 3, kPParts = 2;
-constexpr uint32_t kOffP = kTParts * kPart, kOffG = kOffP + kPParts * kPart;
-constexpr uint32_t kOffLast = kOffG + kC * 4, kOffBeta = kOffLast + kC * 4;
+constexpr uint32_t kOffP = kTParts * kPart, kOffG = kOffP + kPParts * kPart;  // G, D[63], -G
 constexpr uint32_t kBlob = kOffG + 1024;
 
 __device__ unsigned int g_give_up;
@@ -70,11 +71,8 @@ __device__ __forceinline__ void cut(const float *x, uint32_t (&part)[kParts][kN]
       const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
       part[p][i] = prmt(ua, ub, 0x7632);
       if (p + 1 < kParts) {
-        const float2 rest =
-            __fadd2_rn(make_float2(a, b), make_float2(-__uint_as_float(ua & 0xFFFF0000u),
-                                                      -__uint_as_float(ub & 0xFFFF0000u)));
-        a = rest.x;
-        b = rest.y;
+        a -= __uint_as_float(ua & 0xFFFF0000u);
+        b -= __uint_as_float(ub & 0xFFFF0000u);
       }
     }
   }
@@ -90,7 +88,8 @@ constexpr int kPitch = kC + 4;  // floats a row of the scratch matrix
 // K lies where T's parts go, Q where P's go
 constexpr uint32_t kPrepQ = kOffP;
 constexpr uint32_t kPrepScratch = kBlob, kPrepAlpha = kPrepScratch + kC * kPitch * 4;
-constexpr uint32_t kPrepSmem = kPrepAlpha + kC * 4 + 1024;
+constexpr uint32_t kPrepBeta = kPrepAlpha + kC * 4;
+constexpr uint32_t kPrepSmem = kPrepBeta + kC * 4 + 1024;
 static_assert(kTile <= kOffP && kPParts * kPart == kTile, "K and Q under T and P");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
@@ -126,7 +125,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
   const long long row0 = s.start + c * kC;
   float *scratch = reinterpret_cast<float *>(smem + kPrepScratch);
   float *alpha = reinterpret_cast<float *>(smem + kPrepAlpha);
-  float *beta = reinterpret_cast<float *>(smem + kOffBeta);
+  float *beta = reinterpret_cast<float *>(smem + kPrepBeta);
   float *G = reinterpret_cast<float *>(smem + kOffG), *last = G + kC;
   {
     using B16 = __nv_bfloat16;
@@ -162,7 +161,9 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     }
     float before = __shfl_up_sync(0xffffffffu, upto, 1);
     if (lane == 0) before = 1.f;
-    *reinterpret_cast<float2 *>(G + 2 * lane) = make_float2(before * x.x, before * x.x * x.y);
+    const float2 g = make_float2(before * x.x, before * x.x * x.y);
+    *reinterpret_cast<float2 *>(G + 2 * lane) = g;
+    *reinterpret_cast<float2 *>(G + 2 * kC + 2 * lane) = make_float2(-g.x, -g.y);
   } else {
     const int j = warp == 3 ? 32 + lane : lane, low = warp ? 32 : 0;
     float al[32], d = 1.f;
@@ -242,9 +243,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     }
   }
   __syncthreads();  // L is there
-  // T: the four diagonal blocks of 16, one a warp, a column a lane, by substitution
+  // (1 + L)^-1: the four diagonal blocks of 16, one a warp, a column a lane, by
+  // substitution; T's columns take their beta as they are cut
   {
     const int col = lane & 15;
+    const float be = beta[16 * warp + col];
     float *block = scratch + 16 * warp * (kPitch + 1);
     float t[16];
     t[0] = col == 0 ? 1.f : 0.f;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       store_parts(smem, 16 * warp + (lane < 16 ? i : 8 + i), 16 * warp + col,
-                  lane < 16 ? t[i] : t[8 + i]);
+                  be * (lane < 16 ? t[i] : t[8 + i]));
   }
   __syncthreads();
   // the 16 x 16 blocks below them, -T11 (L10 T00) of each pair, four columns a thread
@@ -303,9 +306,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     const float v[4] = {-y.x, -y.y, -y.z, -y.w};
     __syncthreads();
     *reinterpret_cast<float4 *>(below + c4) = make_float4(v[0], v[1], v[2], v[3]);
-    uint32_t part[kTParts][2];
-    cut<2, kTParts>(v, part);
     const int row = 32 * (warp >> 1) + 16 + r, at = 32 * (warp >> 1) + c4;
+    const float4 be = *reinterpret_cast<const float4 *>(beta + at);
+    const float z[4] = {v[0] * be.x, v[1] * be.y, v[2] * be.z, v[3] * be.w};
+    uint32_t part[kTParts][2];
+    cut<2, kTParts>(z, part);
 #pragma unroll
     for (int p = 0; p < kTParts; ++p)
       *reinterpret_cast<uint2 *>(smem + p * kPart + swizzled(row, at >> 3) + (at & 7) * 2) =
@@ -345,7 +350,9 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     } else {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const float v[4] = {-x[y][0].x, -x[y][0].y, -x[y][1].x, -x[y][1].y};
+        const float4 be = *reinterpret_cast<const float4 *>(beta + c4);
+        const float v[4] = {-x[y][0].x * be.x, -x[y][0].y * be.y, -x[y][1].x * be.z,
+                            -x[y][1].y * be.w};
         uint32_t part[kTParts][2];
         cut<2, kTParts>(v, part);
 #pragma unroll
@@ -367,10 +374,13 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
 }
 
 // ---- the state from chunk to chunk ---------------------------------------------------
-constexpr int kChainWarps = 16, kMmaWarp = 16;  // and a loading warp
-constexpr int kThreads = 576;
+constexpr int kChainWarps = 16, kOutWarps = 4, kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kThreads = 768;
+// 512 x 96 + 128 x 64 + 128 x 32 = 768 x 80 registers
+constexpr int kChainRegs = 96, kOutRegs = 64, kOtherRegs = 32;
 constexpr uint32_t kStage = 3 * kTile + kBlob;  // K, Q, V, blob
-constexpr uint32_t kOffBars = 2 * kStage;
+constexpr uint32_t kOffOut = 2 * kStage;  // a chunk's outputs, [64 rows][128] bf16
+constexpr uint32_t kOffBars = kOffOut + kTile;
 enum Bar {
   kFull = 0,     // [2 stages] loaded
   kEmpty = 2,    // [2] read
@@ -384,24 +394,28 @@ enum Bar {
   kQs = 16,      // S0 Q^T is
   kSu = 17,      // [2 halves of dk] E' K is
   kOut = 19,     // E P^T is
-  kPair = 20,    // [8] the two warps that share a place of tensor memory have read it
-  kBars = 28
+  kBars = 20
 };
 constexpr uint32_t kOffTmem = kOffBars + 8 * kBars;
 constexpr uint32_t kSmem = kOffTmem + 16 + 1024;
 
-// Tensor memory (columns).  The state's parts: of each half of dk three parts of 32
-// columns; E' K of that half first lands in the same place.
+// Tensor memory (columns).  The state's parts: of each half of dk 12 pieces of 8
+// columns (16 of dk, one part); E' K of that half first lands in the first 64 of these
+// 96 columns, and the warp that reads 32 of them writes its own pieces over them.
 constexpr uint32_t kColState = 0, kColHalf = 96;
-constexpr uint32_t kColK = 192;   // S0 K^T, then E's two parts
+constexpr uint32_t kColK = 192;   // S0 K^T, then E
 constexpr uint32_t kColQ = 256;   // S0 Q^T
 constexpr uint32_t kColE = 320;   // R T^T, then E P^T
 constexpr uint32_t kColR = 384;   // R's parts, then those of E'
 constexpr uint32_t kTmemCols = 512;
+__host__ __device__ constexpr uint32_t state_col(int half, int part, int step) {
+  return kColState + kColHalf * half +
+         (part < 2 ? 32 * (step >> 1) + 16 * part : 64 + 16 * (step >> 1)) + 8 * (step & 1);
+}
 
-constexpr uint32_t idesc(int n, bool mn_major) {
+constexpr uint32_t idesc(int n, bool mn_major, bool a_mn_major = false) {
   return (1u << 4) | (1u << 7) | (1u << 10)  // D fp32; A, B bf16
-         | (mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
+         | (a_mn_major ? 1u << 15 : 0u) | (mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
                                             uint32_t bar) {
@@ -436,15 +450,30 @@ __device__ __forceinline__ void pin(uint32_t (&v)[kN]) {
                       "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7]));
 }
 
+// A warp's wait for a phase.  It begins with a non-blocking test: the blocking one
+// takes longer even when the phase is complete.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return true;
+  return __all_sync(0xffffffffu, mbar_wait_u32(bar, parity));
+}
+
 struct Item {
   int start, n, slot, h, hk, chunks;
   long long blob;  // of its first chunk; the next H further
 };
 
 // R T^T or E P^T, D[dv][64 rows] (+)= A parts x B parts, both lower triangular: the
-// 16 columns of step j reach the rows from 16 j on.  Steps [kJ0, kJ1); the product
-// begins with step 0.  Parts whose weights add up past `kLeast` are left out.
-template <int kNa, int kNb, int kLeast, int kJ0, int kJ1>
+// 16 columns of step j reach the rows from 16 j on.  Steps [kJ0, kJ1), begun by step
+// 0 unless kAdd.  Parts whose weights add up past `kLeast` are left out.
+template <int kNa, int kNb, int kLeast, int kJ0, int kJ1, bool kAdd>
 __device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int pa = 0; pa < kNa; ++pa)
@@ -455,8 +484,18 @@ __device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b) {
       for (int j = kJ0; j < kJ1; ++j)
         tc_mma_ts(d + 16 * j, a + 32 * pa + 8 * j,
                   smem_desc_sw128(b + pb * kPart + j * 2048 + j * 32), idesc(kC - 16 * j, false),
-                  pa + pb + j > 0);
+                  kAdd || pa + pb + j > 0);
     }
+}
+// V T^T, the same with V from shared memory, dv contiguous.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t t) {
+#pragma unroll
+  for (int p = 0; p < kTParts; ++p)
+#pragma unroll
+    for (int j = 0; j < kC / 16; ++j)
+      tc_mma_ss(d + 16 * j, smem_desc_sw128_mn(v + j * 2048, kPanel),
+                smem_desc_sw128(t + p * kPart + j * 2048 + j * 32),
+                idesc(kC - 16 * j, false, true), p + j > 0);
 }
 // S0 times kRows rows of K or Q, from half `half` of dk.
 template <int kParts, int kRowsOf>
@@ -465,7 +504,7 @@ __device__ __forceinline__ void mma_state(uint32_t d, uint32_t tmem, uint32_t b,
   for (int p = 0; p < kParts; ++p)
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks)
-      tc_mma_ts(d, tmem + kColState + half * kColHalf + 32 * p + 8 * ks,
+      tc_mma_ts(d, tmem + state_col(half, p, ks),
                 smem_desc_sw128(b + half * kPanel + ks * 32), idesc(kRowsOf, false),
                 half + p + ks > 0);
 }
@@ -483,16 +522,17 @@ __device__ __forceinline__ void mma_update(uint32_t tmem, uint32_t k_at, int hal
 __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
   auto bar = [&](int i) { return base + kOffBars + 8u * i; };
   const bool one = elect_one();
+  tmem = __reduce_max_sync(0xffffffffu, tmem);  // known to be the warp's: no move before every product
   bool ok = true;
   auto wait = [&](int i, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(i), parity));
+    ok = wait_phase(bar(i), parity);
     tc_fence_after();
     return ok;
   };
   for (int c = 0; c < it.chunks; ++c) {
     const uint32_t s = c & 1, odd = c & 1, pair = (c >> 1) & 1;
-    const uint32_t k_at = base + s * kStage, q_at = k_at + kTile;
-    const uint32_t t_at = k_at + 3 * kTile, p_at = t_at + kOffP;
+    const uint32_t k_at = base + s * kStage, q_at = k_at + kTile, v_at = q_at + kTile;
+    const uint32_t t_at = v_at + kTile, p_at = t_at + kOffP;
     if (c > 0 && !wait(kOut, odd ^ 1)) break;  // E P^T has read what S0 K^T overwrites
     if (!wait(kFull + s, pair) || !wait(kState, odd)) break;
     if (one) mma_state<3, 64>(tmem + kColK, tmem, k_at, 0);
@@ -504,24 +544,22 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
       mma_state<3, 32>(tmem + kColK + 32, tmem, k_at + 32 * 128, 1);
       tc_commit(bar(kKs + 1));
     }
-    __syncwarp();
     if (c > 0 && !wait(kOutRead, odd ^ 1)) break;
-    if (one) {
-      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 0);
-      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 1);
-      tc_commit(bar(kQs));
-    }
+    if (one) mma_values(tmem + kColE, v_at, t_at);
     __syncwarp();
     if (!wait(kR, odd)) break;
     if (one) {
-      mma_lower<3, 3, 2, 0, 2>(tmem + kColE, tmem + kColR, t_at);
+      mma_lower<3, 3, 2, 0, 2, true>(tmem + kColE, tmem + kColR, t_at);
       tc_commit(bar(kTr));
     }
     __syncwarp();
     if (!wait(kR + 1, odd)) break;
     if (one) {
-      mma_lower<3, 3, 2, 2, 4>(tmem + kColE, tmem + kColR, t_at);
+      mma_lower<3, 3, 2, 2, 4, true>(tmem + kColE, tmem + kColR, t_at);
       tc_commit(bar(kTr + 1));
+      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 0);
+      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 1);
+      tc_commit(bar(kQs));
     }
     __syncwarp();
     if (!wait(kQs, odd) || !wait(kE, odd)) break;  // S0 Q^T has read what E' K overwrites
@@ -536,7 +574,7 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
       tc_commit(bar(kSu));
       mma_update(tmem, k_at, 1, 2);
       tc_commit(bar(kSu + 1));
-      mma_lower<2, 2, 1, 0, 4>(tmem + kColE, tmem + kColK, p_at);
+      mma_lower<1, 2, 1, 0, 4, false>(tmem + kColE, tmem + kColK, p_at);
       tc_commit(bar(kOut));
       tc_commit(bar(kEmpty + s));
     }
@@ -560,7 +598,7 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
   };
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(b), parity));
+    ok = wait_phase(bar(b), parity);
     tc_fence_after();
     return ok;
   };
@@ -575,55 +613,45 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
     S[m + 2] = x.z;
     S[m + 3] = x.w;
   }
-  const uint32_t s_at = tmem + kColState + half * kColHalf;
   auto put_state = [&] {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       uint32_t part[3][8];
       cut<8, 3>(S + 16 * x, part);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) tc_st_x8(s_at + 32 * p + 16 * (g & 1) + 8 * x, part[p]);
+      for (int p = 0; p < 3; ++p)
+        tc_st_x8(tmem + kColHalf * half + (p < 2 ? 32 * (g & 1) + 16 * p : 64 + 16 * (g & 1)) + 8 * x,
+                 part[p]);
     }
     tc_wait_st();
     arrive(kState + half);
   };
   put_state();
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
-                       (long long)(it.start + 16 * g) * a.out_stride + (long long)it.h * a.dv + i;
   for (int c = 0; c < it.chunks; ++c) {
     const uint32_t s = c & 1, odd = c & 1, pair = (c >> 1) & 1;
-    const uint8_t *stage = smem + s * kStage, *blob = stage + 3 * kTile;
-    const float *G = reinterpret_cast<const float *>(blob + kOffG) + 16 * g;
-    const float *last = G + kC, *beta = last + kC;
-    const uint16_t *v = reinterpret_cast<const uint16_t *>(stage + 2 * kTile) + 16 * g * kD + i;
-    const int left = it.n - c * kC - 16 * g;  // rows of this warp's 16
-    // R = beta (v - G S0 k)
-    if (!wait(kFull + s, pair)) break;
-    float val[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) val[j] = __uint_as_float((uint32_t)v[j * kD] << 16);
-    if (!wait(kKs + half, odd)) break;
+    const float *G = reinterpret_cast<const float *>(smem + s * kStage + 3 * kTile + kOffG);
+    // R = -G S0 k
+    if (!wait(kFull + s, pair) || !wait(kKs + half, odd)) break;
     {
       uint32_t x[16];
       tc_ld_x16(tmem + kColK + 16 * g, x);
+      float r[16];
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4 *>(r + j) =
+            *reinterpret_cast<const float4 *>(G + 2 * kC + 16 * g + j);
       tc_wait_ld();
       pin(x);
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 be = *reinterpret_cast<const float4 *>(beta + j);
-        const float4 f = *reinterpret_cast<const float4 *>(G + j);
-        val[j] = be.x * fmaf(-f.x, __uint_as_float(x[j]), val[j]);
-        val[j + 1] = be.y * fmaf(-f.y, __uint_as_float(x[j + 1]), val[j + 1]);
-        val[j + 2] = be.z * fmaf(-f.z, __uint_as_float(x[j + 2]), val[j + 2]);
-        val[j + 3] = be.w * fmaf(-f.w, __uint_as_float(x[j + 3]), val[j + 3]);
-      }
-      if (left < 16) {  // no row: what lies there, or a state that is not finite, must not count
+      for (int j = 0; j < 16; ++j) r[j] *= __uint_as_float(x[j]);
+      const int left = it.n - c * kC - 16 * g;
+      if (left < 16) {  // no row: a state that is not finite must not count
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (j >= left) val[j] = 0.f;
+          if (j >= left) r[j] = 0.f;
       }
       uint32_t part[3][8];
-      cut<8, 3>(val, part);
+      cut<8, 3>(r, part);
 #pragma unroll
       for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
       tc_wait_st();
@@ -634,88 +662,49 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
     {
       uint32_t x[16];
       tc_ld_x16(tmem + kColE + 16 * g, x);
-      tc_wait_ld();
-      pin(x);
       float e[16];
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 d = *reinterpret_cast<const float4 *>(last + j);
-        e[j] = d.x * __uint_as_float(x[j]);
-        e[j + 1] = d.y * __uint_as_float(x[j + 1]);
-        e[j + 2] = d.z * __uint_as_float(x[j + 2]);
-        e[j + 3] = d.w * __uint_as_float(x[j + 3]);
-      }
-      {
-        uint32_t part[3][8];
-        cut<8, 3>(e, part);
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4 *>(e + j) = *reinterpret_cast<const float4 *>(G + kC + 16 * g + j);
+      tc_wait_ld();
+      pin(x);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
-      }
+      for (int j = 0; j < 16; ++j) e[j] *= __uint_as_float(x[j]);
+      uint32_t part[3][8];
+      cut<8, 3>(e, part);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) e[j] = __uint_as_float(x[j]);
-      {
-        uint32_t part[2][8];
-        cut<8, 2>(e, part);
+      for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
+      uint32_t whole[8];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) tc_st_x8(tmem + kColK + 32 * p + 8 * g, part[p]);
+      for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 y =
+            __floats2bfloat162_rn(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+        whole[j] = *reinterpret_cast<const uint32_t *>(&y);
       }
+      tc_st_x8(tmem + kColK + 8 * g, whole);
       tc_wait_st();
       arrive(kE + half);
     }
     // S = G[63] S0 + E' K
     if (!wait(kSu + half, odd)) break;
     {
-      const float all = reinterpret_cast<const float *>(blob + kOffG)[kC - 1];
-      const float2 all2 = make_float2(all, all);
+      const float2 all = make_float2(G[kC - 1], G[kC - 1]);
       uint32_t x[2][16];
-      tc_ld_x16(s_at + 32 * (g & 1), x[0]);
-      tc_ld_x16(s_at + 32 * (g & 1) + 16, x[1]);
+      tc_ld_x16(tmem + kColHalf * half + 32 * (g & 1), x[0]);
+      tc_ld_x16(tmem + kColHalf * half + 32 * (g & 1) + 16, x[1]);
       tc_wait_ld();
       pin(x[0]);
       pin(x[1]);
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
-        const float2 n = __ffma2_rn(all2, make_float2(S[j], S[j + 1]),
+        const float2 n = __ffma2_rn(all, make_float2(S[j], S[j + 1]),
                                     make_float2(__uint_as_float(x[j >> 4][j & 15]),
                                                 __uint_as_float(x[j >> 4][(j & 15) + 1])));
         S[j] = n.x;
         S[j + 1] = n.y;
       }
-      if (c + 1 < it.chunks) {
-        const int shared = kPair + 4 * half + (warp & 3);
-        arrive(shared);
-        if (!wait(shared, odd)) break;
-        put_state();
-      }
-    }
-    // o = G S0 q + E P
-    if (!wait(kOut, odd)) break;
-    {
-      uint32_t x[16], y[16];
-      tc_ld_x16(tmem + kColQ + 16 * g, x);
-      tc_ld_x16(tmem + kColE + 16 * g, y);
-      tc_wait_ld();
-      pin(x);
-      pin(y);
-      float o[16];
-#pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(G + j);
-        o[j] = fmaf(f.x, __uint_as_float(x[j]), __uint_as_float(y[j]));
-        o[j + 1] = fmaf(f.y, __uint_as_float(x[j + 1]), __uint_as_float(y[j + 1]));
-        o[j + 2] = fmaf(f.z, __uint_as_float(x[j + 2]), __uint_as_float(y[j + 2]));
-        o[j + 3] = fmaf(f.w, __uint_as_float(x[j + 3]), __uint_as_float(y[j + 3]));
-      }
-      arrive(kOutRead);
       if (lane == 0) mbar_arrive_u32(bar(kEmpty + s));
-      const int stored = i < a.dv ? left : 0;
-      __nv_bfloat16 *to = out;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (j < stored) *to = __float2bfloat16_rn(o[j]);
-        to += a.out_stride;
-      }
-      out += kC * a.out_stride;
+      if (c + 1 < it.chunks) put_state();
     }
   }
   if (!ok) {
@@ -728,6 +717,85 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
       if (32 * g + m < a.dk)
         *reinterpret_cast<float4 *>(state + m) = make_float4(S[m], S[m + 1], S[m + 2], S[m + 3]);
   }
+}
+
+// The outputs' warps: o = G S0 q + E P, lane = dv.
+__device__ void write_out(const AdvanceArgs &a, const CUtensorMap *omap, const Item &it,
+                          uint8_t *smem, uint32_t base, uint32_t tmem_base) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = 32 * (warp & 3) + lane;
+  const uint32_t tmem = tmem_base + ((uint32_t)(warp & 3) << 21);
+  auto bar = [&](int b) { return base + kOffBars + 8u * b; };
+  for (int c = 0; c < it.chunks; ++c) {
+    const uint32_t s = c & 1, odd = c & 1, pair = (c >> 1) & 1;
+    const float *G = reinterpret_cast<const float *>(smem + s * kStage + 3 * kTile + kOffG);
+    const bool ok = wait_phase(bar(kFull + s), pair) && wait_phase(bar(kOut), odd);
+    tc_fence_after();
+    // the copy of the chunk before has left shared memory; all four warps go on or none
+    if (threadIdx.x == kChainWarps * 32)
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((int)ok)
+        : "memory");
+    if (!all) {
+      if (lane == 0) atomicOr(&g_give_up, 8u);
+      break;
+    }
+    // all of it is read before any is stored: the next chunk waits for the place
+    uint32_t o[kC / 2];
+#pragma unroll
+    for (int x = 0; x < kC; x += 16) {
+      uint32_t q[16], e[16];
+      tc_ld_x16(tmem + kColQ + x, q);
+      tc_ld_x16(tmem + kColE + x, e);
+      tc_wait_ld();
+      pin(q);
+      pin(e);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float2 f = *reinterpret_cast<const float2 *>(G + x + j);
+        const __nv_bfloat162 y =
+            __floats2bfloat162_rn(fmaf(f.x, __uint_as_float(q[j]), __uint_as_float(e[j])),
+                                  fmaf(f.y, __uint_as_float(q[j + 1]), __uint_as_float(e[j + 1])));
+        o[(x + j) / 2] = *reinterpret_cast<const uint32_t *>(&y);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive_u32(bar(kOutRead));
+      mbar_arrive_u32(bar(kEmpty + s));
+    }
+    const int left = it.n - c * kC;
+    if (left >= kC) {
+      uint16_t *to = reinterpret_cast<uint16_t *>(smem + kOffOut) + i;
+#pragma unroll
+      for (int j = 0; j < kC; ++j) to[j * kD] = (uint16_t)(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+      fence_async();
+      asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+      if (threadIdx.x == kChainWarps * 32) {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                omap),
+            "r"(0), "r"(it.h), "r"(it.start + c * kC), "r"(base + kOffOut)
+            : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    } else if (i < a.dv) {  // the rows behind the sequence are another's
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                           (long long)(it.start + c * kC) * a.out_stride + (long long)it.h * a.dv + i;
+#pragma unroll
+      for (int j = 0; j < kC; ++j)
+        if (j < left)
+          reinterpret_cast<uint16_t *>(out)[j * a.out_stride] =
+              (uint16_t)(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+    }
+  }
+  if (threadIdx.x == kChainWarps * 32)
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, const CUtensorMap *vmap,
@@ -748,8 +816,8 @@ __device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, co
       for (int x = 0; x < 2; ++x) {
         tma_load_3d(at + x * kPanel, kmap, 64 * x, it.hk, row, full);
         tma_load_3d(at + kTile + x * kPanel, qmap, 64 * x, it.hk, row, full);
+        tma_load_3d(at + 2 * kTile + x * kPanel, vmap, 64 * x, it.h, row, full);
       }
-      tma_load_3d(at + 2 * kTile, vmap, 0, it.h, row, full);
       asm volatile(
           "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
               at + 3 * kTile),
@@ -758,12 +826,14 @@ __device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, co
     }
     __syncwarp();
     if (left < kC) {
-      // the rows behind the sequence are another's: as K's they must not meet E'
+      // the rows behind the sequence are another's: they must not meet the zeros of E' and T
       ok = __all_sync(0xffffffffu, mbar_wait_u32(full, 0));
       uint8_t *k = smem + s * kStage;
-      for (int x = lane; x < (kC - left) * 16; x += 32)
-        *reinterpret_cast<uint4 *>(k + (x & 1) * kPanel + (left + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
+      for (int x = lane; x < (kC - left) * 16; x += 32) {
+        uint8_t *to = k + (x & 1) * kPanel + (left + (x >> 4)) * 128 + ((x >> 1) & 7) * 16;
+        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<uint4 *>(to + 2 * kTile) =
             make_uint4(0, 0, 0, 0);
+      }
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive_u32(bar(kFull + s));
@@ -778,7 +848,8 @@ __device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, co
 
 __global__ void __launch_bounds__(kThreads, 1)
     gdn_chunk_states(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
-                     const __grid_constant__ CUtensorMap vmap, const AdvanceArgs a,
+                     const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ CUtensorMap omap, const AdvanceArgs a,
                      const uint8_t *blobs) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -814,27 +885,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init_u32(bar(kFull + s), 1);
-      mbar_init_u32(bar(kEmpty + s), 1 + kChainWarps);
+      mbar_init_u32(bar(kEmpty + s), 1 + kChainWarps + kOutWarps);
       mbar_init_u32(bar(kState + s), kChainWarps / 2);
       mbar_init_u32(bar(kR + s), kChainWarps / 2);
       mbar_init_u32(bar(kE + s), kChainWarps / 2);
       for (int i : {kKs, kTr, kSu}) mbar_init_u32(bar(i + s), 1);
     }
-    mbar_init_u32(bar(kOutRead), kChainWarps);
+    mbar_init_u32(bar(kOutRead), kOutWarps);
     for (int i : {kTail, kQs, kOut}) mbar_init_u32(bar(i), 1);
-    for (int i = 0; i < 8; ++i) mbar_init_u32(bar(kPair + i), 2);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffTmem);
-  if (warp < kChainWarps)
+  if (warp < kChainWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
     run_chain(a, it, smem, base, tmem);
-  else if (warp == kMmaWarp)
-    issue_chunks(base, tmem, it);
-  else
-    load_chunks(&kmap, &qmap, &vmap, blobs, a.H, it, smem, base);
+  } else if (warp < kChainWarps + kOutWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    write_out(a, &omap, it, smem, base, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp)
+      issue_chunks(base, tmem, it);
+    else if (warp == kLoadWarp)
+      load_chunks(&kmap, &qmap, &vmap, blobs, a.H, it, smem, base);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -844,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Rows [rows][heads][dim] in boxes of kC rows of one head.
+// Rows [rows][heads][dim] in boxes of kC rows of a head's columns: `box` of them.
 sv_status encode_rows(CUtensorMap *map, const void *p, long long row_stride, int rows, int heads,
                       int dim, uint32_t box, CUtensorMapSwizzle swizzle) {
   qmv::EncodeTiledFn enc = qmv::encode_tiled();
@@ -878,12 +955,14 @@ sv_status chunk_run(const AdvanceArgs &a, void *workspace, cudaStream_t stream) 
   });
   if (e != cudaSuccess)
     return fail(SV_ERR_CUDA, "gdn_advance: cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
-  CUtensorMap kmap, qmap, vmap;
+  CUtensorMap kmap, qmap, vmap, omap;
   sv_status st = encode_rows(&kmap, a.k, a.k_stride, a.rows, a.Hk, a.dk, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st == SV_OK)
     st = encode_rows(&qmap, a.q, a.q_stride, a.rows, a.Hk, a.dk, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st == SV_OK)
-    st = encode_rows(&vmap, a.v, a.v_stride, a.rows, a.H, a.dv, kD, CU_TENSOR_MAP_SWIZZLE_NONE);
+    st = encode_rows(&vmap, a.v, a.v_stride, a.rows, a.H, a.dv, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == SV_OK)
+    st = encode_rows(&omap, a.out, a.out_stride, a.rows, a.H, a.dv, kD, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (st != SV_OK) return st;
   uint8_t *blobs = static_cast<uint8_t *>(workspace);
   const long long items = ((long long)a.rows / kC + a.B) * a.H;
@@ -894,7 +973,7 @@ sv_status chunk_run(const AdvanceArgs &a, void *workspace, cudaStream_t stream) 
     if (st != SV_OK) return st;
   }
   const dim3 grid((unsigned)a.H, (unsigned)a.B + 1);
-  gdn_chunk_states<<<grid, kThreads, kSmem, stream>>>(kmap, qmap, vmap, a, blobs);
+  gdn_chunk_states<<<grid, kThreads, kSmem, stream>>>(kmap, qmap, vmap, omap, a, blobs);
   return check_launch("gdn_advance");
 }
 

@@ -52,43 +52,54 @@ def inputs(x, a, b, weight, window, a_log, dt_bias, q_start, k_heads, dk, index=
             (spread[0], spread[1], mag[:, 2 * Hk * dk:].reshape(rows, H, dv)))
 
 
-def advance(q, k, v, alpha, beta, state, q_start, index=None, reach=1):
-    """gdn_advance, token by token.  Returns out, state and bounds for their
-    fp32 arithmetic.
+def advance(q, k, v, alpha, beta, state, q_start, index=None, chunk=1, tol=0.0):
+    """gdn_advance, token by token.  Returns out, state and bounds for them: of
+    each output, and of each row of the state in norm.
 
     A step maps a row s of S to alpha s (1 - beta k k^T) + beta v k^T, which
     shrinks any error in s while beta |k|^2 <= 2, so the errors of the steps add
     up, each decayed by the gates after it.  A step's own: the decayed row, the
     dot product with k, e and the rank-1 term are each rounded a few times, and
-    in chunks of `reach` rows e is a sum over the rows e_j before it in the
-    chunk, with factors of norm at most 1.  Roundings are independent, so n of
-    them count sqrt(n): with dk + reach <= 256 terms and 6 operations on each
-    at most 40 half steps of (|s| + |v| + |e of the last rows|) |k|."""
+    in chunks e is a sum over the rows e_j before it in the chunk, with factors
+    of norm at most 1.  Roundings are independent, so n of them count sqrt(n):
+    with dk + chunk <= 256 terms and 6 operations on each at most 40 half steps
+    of (|s| + |v| + |e of the last rows|) |k|.
+
+    Of bf16 rows in chunks the output also takes every e_j rounded to bf16, and
+    the chunk's first state and the factors of the e_j cut off after 16 bits."""
     q, k, v, alpha, beta = (np.asarray(t, np.float64) for t in (q, k, v, alpha, beta))
     state = np.asarray(state, np.float64).copy()
     rows, Hk, dk = q.shape
     slots, H, dv, _ = state.shape
     G = H // Hk
     out, out_tol = np.zeros((rows, H, dv)), np.zeros((rows, H, dv))
-    tol = np.zeros((slots, H, dv))
+    tol = np.zeros((slots, H, dv)) + tol  # the state's own error before
     u = 40 * HALF_F32
     for s, (r0, r1) in enumerate(_spans(q_start, rows)):
         slot = s if index is None else int(index[s])
         if not 0 <= slot < slots:
             continue
         S, err = state[slot], tol[slot]
-        recent = np.zeros((reach, H, dv))
         for r in range(r0, r1):
+            if (r - r0) % chunk == 0:  # the chunk's rows so far, their gates, its first state
+                past_e, past_k, gates = [], [], []
+                first, g0 = np.linalg.norm(S, axis=-1), np.ones(H)
             kk, qq = np.repeat(k[r], G, 0), np.repeat(q[r], G, 0)
             S *= alpha[r][:, None, None]
             size = np.linalg.norm(S, axis=-1)
             e = beta[r][:, None] * (v[r] - np.einsum("hij,hj->hi", S, kk))
             S += e[..., None] * kk[:, None]
             out[r] = np.einsum("hij,hj->hi", S, qq)
-            recent[(r - r0) % reach] = e
+            gates = [g * alpha[r] for g in gates] + [np.ones(H)]
+            g0 = g0 * alpha[r]
+            past_e.append(np.abs(e))
+            past_k.append(kk)
             kn, qn = (np.linalg.norm(t, axis=-1)[:, None] for t in (kk, qq))
-            # within a chunk the rows before it enter e and o by their norm
-            near = np.sqrt((recent ** 2).sum(0)) if reach > 1 else np.abs(e)
+            near = np.sqrt((np.array(past_e) ** 2).sum(0))
             err[:] = err * alpha[r][:, None] + u * (size + (np.abs(v[r]) + near) * kn)
             out_tol[r] = err * qn + u * (np.linalg.norm(S, axis=-1) + near * kn) * qn
+            if chunk > 1:
+                factors = np.abs(np.einsum("jhd,hd->jh", np.array(past_k), qq)) * np.array(gates)
+                terms = np.einsum("jh,jhi->hi", factors, np.array(past_e))
+                out_tol[r] += (HALF_BF16 + 2.0 ** -15) * terms + 2.0 ** -15 * first * g0[:, None] * qn
     return out, state, out_tol, tol
