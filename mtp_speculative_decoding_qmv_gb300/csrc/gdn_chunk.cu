@@ -83,14 +83,14 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
 }
 
 // ---- T and P of a chunk: four warps ----------------------------------------------
+// Bound by latency (a chain of small steps), so as many chunks as fit share an SM:
+// the scratch matrix lies where K was, P where Q was.
 constexpr int kPrepThreads = 128;
 constexpr int kPitch = kC + 4;  // floats a row of the scratch matrix
-// K lies where T's parts go, Q where P's go
-constexpr uint32_t kPrepQ = kOffP;
-constexpr uint32_t kPrepScratch = kBlob, kPrepAlpha = kPrepScratch + kC * kPitch * 4;
-constexpr uint32_t kPrepBeta = kPrepAlpha + kC * 4;
+constexpr uint32_t kPrepQ = (kC * kPitch * 4 + 1023) / 1024 * 1024;
+constexpr uint32_t kPrepAlpha = kPrepQ + kTile, kPrepBeta = kPrepAlpha + kC * 4;
 constexpr uint32_t kPrepSmem = kPrepBeta + kC * 4 + 1024;
-static_assert(kTile <= kOffP && kPParts * kPart == kTile, "K and Q under T and P");
+static_assert(kTile <= kPrepQ && kPParts * kPart == kTile, "K under the scratch, Q under P");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
   // 16 bytes to shared memory, zeros where there is no source
@@ -98,18 +98,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
                "r"(real ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void store_parts(uint8_t *t, int i, int j, float x) {
-#pragma unroll
-  for (int p = 0; p < kTParts; ++p) {
-    const uint32_t u = __float_as_uint(x);
-    *reinterpret_cast<uint16_t *>(t + p * kPart + swizzled(i, j >> 3) + (j & 7) * 2) =
-        (uint16_t)(u >> 16);
-    x -= __uint_as_float(u & 0xFFFF0000u);
-  }
-}
 
-__global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const AdvanceArgs a,
-                                                                   uint8_t *blobs) {
+__global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const AdvanceArgs a,
+                                                                      uint8_t *blobs) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -123,10 +114,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
   if (c < 0 || c * kC >= s.n || slot_of(a.state_index, b, a.slots) < 0) return;
   const int left = min(kC, s.n - c * kC);
   const long long row0 = s.start + c * kC;
-  float *scratch = reinterpret_cast<float *>(smem + kPrepScratch);
+  float *scratch = reinterpret_cast<float *>(smem);
   float *alpha = reinterpret_cast<float *>(smem + kPrepAlpha);
   float *beta = reinterpret_cast<float *>(smem + kPrepBeta);
-  float *G = reinterpret_cast<float *>(smem + kOffG), *last = G + kC;
+  uint8_t *blob = blobs + (long long)blockIdx.x * kBlob;
+  float *G = reinterpret_cast<float *>(blob + kOffG), *last = G + kC;
   {
     using B16 = __nv_bfloat16;
     const B16 *k = static_cast<const B16 *>(a.k) + row0 * a.k_stride + (long long)hk * a.dk;
@@ -148,6 +140,34 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   __syncthreads();
+  // K K^T and Q K^T of the warp's 16 rows and the columns up to them
+  float kk[8][4], qk[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) kk[i][m] = qk[i][m] = 0.f;
+#pragma unroll 2
+  for (int ks = 0; ks < kD / 16; ++ks) {
+    const uint32_t panel = base + (ks >> 2) * kPanel;
+    const int piece = (ks & 3) * 2;
+    uint32_t ak[4], aq[4];
+    const uint32_t a_at = panel + swizzled(16 * warp + (lane & 15), piece + (lane >> 4));
+    qmv::ldmatrix_x4(ak, a_at);
+    qmv::ldmatrix_x4(aq, a_at + kPrepQ);
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      if (np <= warp) {
+        uint32_t x[4];
+        const int row = 16 * np + ((lane >> 4) << 3) + (lane & 7);
+        qmv::ldmatrix_x4(x, panel + swizzled(row, piece + ((lane >> 3) & 1)));
+        mma_bf16_m16n8k16(kk[2 * np], ak[0], ak[1], ak[2], ak[3], x[0], x[1]);
+        mma_bf16_m16n8k16(kk[2 * np + 1], ak[0], ak[1], ak[2], ak[3], x[2], x[3]);
+        mma_bf16_m16n8k16(qk[2 * np], aq[0], aq[1], aq[2], aq[3], x[0], x[1]);
+        mma_bf16_m16n8k16(qk[2 * np + 1], aq[0], aq[1], aq[2], aq[3], x[2], x[3]);
+      }
+    }
+  }
+  __syncthreads();  // K and Q have been read
   // D from the diagonal down, by products (a gate of 0 or gates whose product
   // underflows need no care): warp 0 rows 0..31 of columns 0..31, warps 2 and 3
   // rows 32..63, a column a thread; warp 1 G, by a scan
@@ -166,59 +186,33 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     *reinterpret_cast<float2 *>(G + 2 * kC + 2 * lane) = make_float2(-g.x, -g.y);
   } else {
     const int j = warp == 3 ? 32 + lane : lane, low = warp ? 32 : 0;
-    float al[32], d = 1.f;
+    float d = 1.f;
     if (warp == 2) {
 #pragma unroll
-      for (int i = 1; i < 32; ++i) {
-        const float x = alpha[i];
-        if (i > j) d *= x;
+      for (int i = 0; i < 32; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(alpha + i);
+        if (i > j) d *= x.x;
+        if (i + 1 > j) d *= x.y;
+        if (i + 2 > j) d *= x.z;
+        if (i + 3 > j) d *= x.w;
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(alpha + low + i);
-      al[i] = x.x;
-      al[i + 1] = x.y;
-      al[i + 2] = x.z;
-      al[i + 3] = x.w;
     }
     float *to = scratch + low * kPitch + j;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (low + i > j) d *= al[i];
-      to[i * kPitch] = d;  // 1 above the diagonal, where it is not used
+    for (int i = 0; i < 32; i += 4) {  // 1 above the diagonal, where it is not used
+      const float4 x = *reinterpret_cast<const float4 *>(alpha + low + i);
+      if (low + i > j) d *= x.x;
+      to[i * kPitch] = d;
+      if (low + i + 1 > j) d *= x.y;
+      to[(i + 1) * kPitch] = d;
+      if (low + i + 2 > j) d *= x.z;
+      to[(i + 2) * kPitch] = d;
+      if (low + i + 3 > j) d *= x.w;
+      to[(i + 3) * kPitch] = d;
     }
     if (warp) last[j] = d;
   }
-  // K K^T and Q K^T of the warp's 16 rows and the columns up to them
-  const uint32_t k_at = base, q_at = base + kPrepQ;
-  float kk[8][4], qk[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int m = 0; m < 4; ++m) kk[i][m] = qk[i][m] = 0.f;
-#pragma unroll 2
-  for (int ks = 0; ks < kD / 16; ++ks) {
-    const uint32_t panel = (ks >> 2) * kPanel;
-    const int piece = (ks & 3) * 2;
-    uint32_t ak[4], aq[4];
-    const uint32_t a_off = panel + swizzled(16 * warp + (lane & 15), piece + (lane >> 4));
-    qmv::ldmatrix_x4(ak, k_at + a_off);
-    qmv::ldmatrix_x4(aq, q_at + a_off);
-#pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      if (np <= warp) {
-        uint32_t x[4];
-        const int row = 16 * np + ((lane >> 4) << 3) + (lane & 7);
-        qmv::ldmatrix_x4(x, k_at + panel + swizzled(row, piece + ((lane >> 3) & 1)));
-        mma_bf16_m16n8k16(kk[2 * np], ak[0], ak[1], ak[2], ak[3], x[0], x[1]);
-        mma_bf16_m16n8k16(kk[2 * np + 1], ak[0], ak[1], ak[2], ak[3], x[2], x[3]);
-        mma_bf16_m16n8k16(qk[2 * np], aq[0], aq[1], aq[2], aq[3], x[0], x[1]);
-        mma_bf16_m16n8k16(qk[2 * np + 1], aq[0], aq[1], aq[2], aq[3], x[2], x[3]);
-      }
-    }
-  }
-  __syncthreads();  // D is there, K and Q have been read
+  __syncthreads();  // D is there
   const int g8 = lane >> 2, t4 = lane & 3;
   const float be2[2] = {beta[16 * warp + g8], beta[16 * warp + g8 + 8]};
 #pragma unroll
@@ -238,16 +232,22 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
       cut<1, kPParts>(p, part);
 #pragma unroll
       for (int x = 0; x < kPParts; ++x)
-        *reinterpret_cast<uint32_t *>(smem + kOffP + x * kPart + swizzled(i, nt) + t4 * 4) =
+        *reinterpret_cast<uint32_t *>(smem + kPrepQ + x * kPart + swizzled(i, nt) + t4 * 4) =
             part[x][0];
     }
   }
-  __syncthreads();  // L is there
+  fence_async();
+  __syncthreads();  // L and P are there
+  if (tid == 0) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(blob + kOffP),
+                 "r"(base + kPrepQ), "r"(kPParts * kPart)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
   // (1 + L)^-1: the four diagonal blocks of 16, one a warp, a column a lane, by
-  // substitution; T's columns take their beta as they are cut
+  // substitution
   {
     const int col = lane & 15;
-    const float be = beta[16 * warp + col];
     float *block = scratch + 16 * warp * (kPitch + 1);
     float t[16];
     t[0] = col == 0 ? 1.f : 0.f;
@@ -272,10 +272,6 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
 #pragma unroll
       for (int i = 0; i < 16; ++i) block[i * kPitch + lane] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      store_parts(smem, 16 * warp + (lane < 16 ? i : 8 + i), 16 * warp + col,
-                  be * (lane < 16 ? t[i] : t[8 + i]));
   }
   __syncthreads();
   // the 16 x 16 blocks below them, -T11 (L10 T00) of each pair, four columns a thread
@@ -303,21 +299,12 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
     *reinterpret_cast<float4 *>(below + c4) = x;
     __syncthreads();
     const float4 y = times(below + 16, pair + 16 * kPitch + c4);
-    const float v[4] = {-y.x, -y.y, -y.z, -y.w};
     __syncthreads();
-    *reinterpret_cast<float4 *>(below + c4) = make_float4(v[0], v[1], v[2], v[3]);
-    const int row = 32 * (warp >> 1) + 16 + r, at = 32 * (warp >> 1) + c4;
-    const float4 be = *reinterpret_cast<const float4 *>(beta + at);
-    const float z[4] = {v[0] * be.x, v[1] * be.y, v[2] * be.z, v[3] * be.w};
-    uint32_t part[kTParts][2];
-    cut<2, kTParts>(z, part);
-#pragma unroll
-    for (int p = 0; p < kTParts; ++p)
-      *reinterpret_cast<uint2 *>(smem + p * kPart + swizzled(row, at >> 3) + (at & 7) * 2) =
-          make_uint2(part[p][0], part[p][1]);
+    *reinterpret_cast<float4 *>(below + c4) = make_float4(-y.x, -y.y, -y.z, -y.w);
   }
   __syncthreads();
-  // the 32 x 32 block below, the same way, two rows by four columns a thread
+  // the 32 x 32 block below, the same way, two rows by four columns a thread; T's
+  // columns take their beta as they are cut
   const int r = 2 * (tid >> 3), c4 = 4 * (tid & 7);
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
@@ -348,29 +335,42 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_chunk_matrices(const Advance
             make_float4(x[y][0].x, x[y][0].y, x[y][1].x, x[y][1].y);
       __syncthreads();
     } else {
+      const float4 be = *reinterpret_cast<const float4 *>(beta + c4);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const float4 be = *reinterpret_cast<const float4 *>(beta + c4);
         const float v[4] = {-x[y][0].x * be.x, -x[y][0].y * be.y, -x[y][1].x * be.z,
                             -x[y][1].y * be.w};
         uint32_t part[kTParts][2];
         cut<2, kTParts>(v, part);
 #pragma unroll
         for (int p = 0; p < kTParts; ++p)
-          *reinterpret_cast<uint2 *>(smem + p * kPart + swizzled(32 + r + y, c4 >> 3) + (c4 & 7) * 2) =
+          *reinterpret_cast<uint2 *>(blob + p * kPart + swizzled(32 + r + y, c4 >> 3) + (c4 & 7) * 2) =
               make_uint2(part[p][0], part[p][1]);
       }
     }
   }
-  fence_async();
-  __syncthreads();
-  if (tid == 0) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                     blobs + (long long)blockIdx.x * kBlob),
-                 "r"(base), "r"(kBlob)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  // the two diagonal blocks of 32, eight columns of two rows a thread
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int row = (tid >> 2) + 32 * y, piece = (tid & 3) + 4 * y;
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; x += 4) {
+      const float4 t = *reinterpret_cast<const float4 *>(scratch + row * kPitch + 8 * piece + x);
+      const float4 be = *reinterpret_cast<const float4 *>(beta + 8 * piece + x);
+      v[x] = t.x * be.x;
+      v[x + 1] = t.y * be.y;
+      v[x + 2] = t.z * be.z;
+      v[x + 3] = t.w * be.w;
+    }
+    uint32_t part[kTParts][4];
+    cut<4, kTParts>(v, part);
+#pragma unroll
+    for (int p = 0; p < kTParts; ++p)
+      *reinterpret_cast<uint4 *>(blob + p * kPart + swizzled(row, piece)) =
+          make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- the state from chunk to chunk ---------------------------------------------------
