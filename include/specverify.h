@@ -15,6 +15,8 @@
  *   qmv_smallm        the target's 4-bit small-M quantised mat-vec (M = 1..16)
  *   qmv_plan_*        an ordered list of those mat-vecs in one persistent launch
  *   spec_accept       fp32 acceptance, residual resampling and bonus token
+ *   moe_smallm        a mixture-of-experts layer of a step's few rows: router,
+ *                     the chosen experts' 4-bit products, their weighted sum
  *   gdn_tape_capture  GatedDeltaNet recurrence over the verify tokens, with a
  *                     (gate, innovation, key) tape per token and head
  *   gdn_tape_replay   rebuild the recurrent state over an accepted prefix
@@ -312,6 +314,45 @@ size_t qmv_wide_workspace_bytes(int M, int K);
 sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint16_t *biases,
                    const uint16_t *x, float *y, int M, int N, int K, void *workspace,
                    size_t workspace_bytes, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_smallm: a mixture-of-experts layer for few rows.                      */
+/* ------------------------------------------------------------------------ */
+/* The feed-forward of a target model with experts ("MTP in llama.cpp", the MoE
+ * model of its benchmark), for the rows of a decode or verify step:
+ *   z_e = sum_i x[i] router[e][i];  the row's experts are the top_k largest z_e
+ *   (equal values: the lower e; NaN counts as below all others), in that order;
+ *   w_j = exp(z_ej) / sum over the chosen of exp(z), or with renormalize 0 over
+ *   all experts;
+ *   y = sum_j w_j Down_ej (silu(Gate_ej x) * (Up_ej x)),  silu(g) = g / (1 + exp(-g))
+ * x bf16 [rows][hidden], router bf16 [experts][hidden]; the experts' matrices in
+ * the layout of qmv_smallm, one after another: gate and up w_packed uint32
+ * [experts][inter][hidden / 8] with scales and biases bf16 bit patterns
+ * [experts][inter][hidden / 64], down [experts][hidden][inter / 8] and
+ * [experts][hidden][inter / 64].  y bf16 [rows][hidden], rounded once; ids int32
+ * and weights fp32 [rows][top_k] receive the choice when not NULL.  Accuracy:
+ * fp32 sums of exact products; the activations between the products are fp32,
+ * split into two bf16 parts as qmv_smallm does with fp32 x.  A row depends on no
+ * other row up to the order of its fp32 sums, and results do not depend on the run.
+ * Requires 0 <= rows <= 128 (0: no-op), 1 <= top_k <= 16, top_k <= experts <= 512,
+ * hidden and inter multiples of 128; x, router and the w_packed 16-byte, scales and
+ * biases 8-byte, y 8-byte aligned; no output overlaps an input or another output.
+ * workspace: moe_smallm_workspace_bytes(..) bytes on the current device (0 on
+ * invalid input; *zero_bytes, when given, is how many of the first are arrival
+ * counters: zero before its first call, every call leaves them zero), 256-byte
+ * aligned; it belongs to these sizes, and calls that run concurrently need
+ * workspaces of their own.  Three launches on `stream`, the second and third with a
+ * programmatic dependency on the one before.  A kernel wait that gives up sets a
+ * word read by sv_device_status; the counters are then undefined. */
+size_t moe_smallm_workspace_bytes(int rows, int hidden, int inter, int experts, int top_k,
+                                  size_t *zero_bytes);
+sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const uint32_t *gate_w,
+                     const uint16_t *gate_s, const uint16_t *gate_b, const uint32_t *up_w,
+                     const uint16_t *up_s, const uint16_t *up_b, const uint32_t *down_w,
+                     const uint16_t *down_s, const uint16_t *down_b, int rows, int hidden,
+                     int inter, int experts, int top_k, int renormalize, uint16_t *y,
+                     int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
+                     sv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* spec_accept: probability-ratio verification of K drafts per sequence.     */

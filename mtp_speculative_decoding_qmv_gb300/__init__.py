@@ -8,6 +8,7 @@ step, through a compiled extension (``csrc/tensors.cpp``).  All arithmetic runs 
 the library is missing, every call raises -- there is no fallback.
 
   qmv_smallm        4-bit affine group-64 mat-vec over M = 1..16 verify rows
+  moe_smallm        a mixture-of-experts layer for 1..128 rows, 4-bit experts
   spec_accept       fp32 probability-ratio acceptance, residual, bonus token
   gdn_tape_capture  GatedDeltaNet recurrence + innovation tape
   gdn_tape_replay   rebuild the recurrent state over an accepted prefix
@@ -35,6 +36,7 @@ __all__ = [
     "KvStep", "kv_pages_step", "rope_freqs", "rope_kv_append", "paged_attention",
     "make_attention_workspace", "paged_attention_workspace_bytes",
     "GdnInputs", "gdn_inputs", "gdn_advance", "gdn_advance_workspace_bytes",
+    "moe_smallm", "moe_smallm_workspace_bytes", "make_moe_workspace",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libspecverify.so"
@@ -154,6 +156,10 @@ def lib() -> ctypes.CDLL:
         L.gdn_advance.restype = I
         L.gdn_advance_workspace_bytes.argtypes = [I, I, I, I, I]
         L.gdn_advance_workspace_bytes.restype = Z
+        L.moe_smallm_workspace_bytes.argtypes = [I, I, I, I, I, ctypes.POINTER(Z)]
+        L.moe_smallm_workspace_bytes.restype = Z
+        L.moe_smallm.argtypes = [P] * 11 + [I] * 6 + [P, P, P, P, Z, P]
+        L.moe_smallm.restype = I
         _lib = L
     return _lib
 
@@ -679,7 +685,7 @@ def _load_direct():
                                "__graft_entry__.build())") from e
         built.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                      (lib().kv_pages_step, lib().rope_kv_append, lib().paged_attention,
-                      lib().gdn_inputs, lib().gdn_advance)))
+                      lib().gdn_inputs, lib().gdn_advance, lib().moe_smallm)))
         _direct = built
     return _direct
 
@@ -1031,4 +1037,70 @@ def gdn_advance(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.
         if workspace is not None:
             wanted.append((_need, workspace, "workspace", torch.uint8, None))
         _refuse("gdn_advance", st, [w + (q.device,) for w in wanted])
+    return out
+
+
+# ----------------------------------------------------------------------------
+def moe_smallm_workspace_bytes(rows: int, hidden: int, inter: int, experts: int,
+                               top_k: int) -> tuple[int, int]:
+    """Bytes of a workspace for moe_smallm on the current device, and how many of
+    the first have to be zero before its first call."""
+    zero = ctypes.c_size_t(0)
+    n = int(lib().moe_smallm_workspace_bytes(int(rows), int(hidden), int(inter), int(experts),
+                                             int(top_k), ctypes.byref(zero)))
+    if n == 0:
+        _check(SV_ERR_INVALID_ARG, "moe_smallm_workspace_bytes")
+    return n, int(zero.value)
+
+
+def make_moe_workspace(rows: int, hidden: int, inter: int, experts: int, top_k: int,
+                       device) -> torch.Tensor:
+    """A workspace (uint8) for moe_smallm with these sizes."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n, zero = moe_smallm_workspace_bytes(rows, hidden, inter, experts, top_k)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:zero].zero_()  # arrival counters; every call leaves them zero
+    return ws
+
+
+def moe_smallm(x: torch.Tensor, router: torch.Tensor, gate, up, down, top_k: int, *,
+               renormalize: bool = True, out: torch.Tensor | None = None,
+               ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts layer: x bf16 [rows, hidden] (1..128 rows), router bf16
+    [experts, hidden]; gate, up and down each a triple (w_packed int32 [experts, N,
+    K/8], scales, biases bf16 [experts, N, K/64]) with N, K = inter, hidden for gate
+    and up and hidden, inter for down.  Each row takes its ``top_k`` experts, weighted
+    by the softmax over them (over all experts without ``renormalize``).  Returns out
+    bf16 [rows, hidden]; ids int32 and weights fp32 [rows, top_k] receive the choice
+    when given.  ``workspace`` (from make_moe_workspace with these sizes) is made per
+    call when omitted."""
+    if x.dim() != 2 or gate[0].dim() != 3:
+        raise ValueError("x must be [rows, hidden] and the weights [experts, N, K/8]")
+    index = _on(x, "x")
+    rows, hidden = x.shape
+    E, inter = gate[0].shape[:2]
+    if out is None:
+        out = torch.empty_like(x)
+    if workspace is None:
+        workspace = make_moe_workspace(rows, hidden, inter, E, top_k, x.device)
+    st = _call(index, (_direct or _load_direct()).moe_smallm, x, router, *gate, *up, *down,
+               int(top_k), renormalize, out, ids, weights, workspace)
+    if st != SV_OK:
+        bf16, i32 = torch.bfloat16, torch.int32
+        wanted = [(_need, x, "x", bf16, (rows, hidden)),
+                  (_need, router, "router", bf16, (E, hidden))]
+        for name, w, N, K in (("gate", gate, inter, hidden), ("up", up, inter, hidden),
+                              ("down", down, hidden, inter)):
+            wanted += [(_need, w[0], name + " w_packed", i32, (E, N, K // 8)),
+                       (_need, w[1], name + " scales", bf16, (E, N, K // 64)),
+                       (_need, w[2], name + " biases", bf16, (E, N, K // 64))]
+        wanted.append((_need, out, "out", bf16, (rows, hidden)))
+        if ids is not None:
+            wanted.append((_need, ids, "ids", i32, (rows, top_k)))
+        if weights is not None:
+            wanted.append((_need, weights, "weights", torch.float32, (rows, top_k)))
+        wanted.append((_need, workspace, "workspace", torch.uint8, None))
+        _refuse("moe_smallm", st, [w + (x.device,) for w in wanted])
     return out

@@ -1,0 +1,733 @@
+// moe_smallm.cu -- a mixture-of-experts layer for few rows (1..128): router, the
+// chosen experts' 4-bit products, their weighted sum, sm_103a.
+//
+//   z_e = x . r_e;  the top_k largest z (ties: the lower expert) with weights
+//   w = softmax over them (or over all experts);
+//   y = sum_j w_j down_ej(silu(gate_ej x) * up_ej x)
+//
+// A few rows meet most of their experts once, so the layer streams the chosen
+// experts' weights (0.5625 bytes each) and is bound by memory.  Three launches,
+// the later two starting as the one before drains:
+//  * route: 8 experts a CTA, K over its warps, bf16 MMAs (exact products, fp32
+//    sums); the last CTA of 16 rows chooses their experts, the last of all sorts
+//    the (row, expert) pairs by expert and cuts each expert's rows into slots of
+//    up to 8, the columns of one MMA;
+//  * gate and up, then down: the stages of all slots' tiles laid out flat and cut
+//    evenly over the resident CTAs, so every SM streams the same number of bytes
+//    whichever experts were chosen.  A stage is 128 weight rows x 256 inputs: 64
+//    rows of gate and the same 64 of up (their product leaves in one place), or
+//    128 of down.  Four 64-groups x two blocks of 64 rows make a stage's work for
+//    eight warps, each as in qmv_smallm.  A producer warp keeps the ring of stages
+//    full across tiles.  A tile cut between CTAs leaves partial sums, which
+//    whichever CTA comes last adds in CTA order; nobody waits for another CTA, so
+//    the launches need not be resident together.
+// The activations between the products stay fp32 (two bf16 parts as operands).
+#include <algorithm>
+#include <atomic>
+
+#include "qmv_common.cuh"
+
+namespace sv {
+namespace {
+using namespace qmv;
+
+constexpr int kMaxRows = 128, kMaxTop = 16, kMaxExperts = 512;
+constexpr int kSlotRows = 8;       // pairs of a slot
+constexpr int kTileRows = 128;     // weight rows of a tile
+constexpr int kStageK = 256;       // inputs of a stage
+constexpr int kGroupsOf = kStageK / 64;
+constexpr int kWarps = 8;
+constexpr uint32_t kSb = 2 * kRows * 128;                   // scales, then biases
+constexpr uint32_t kSbBytes = kTileRows * kGroupsOf * 2;    // [128 rows][4 groups] bf16
+constexpr uint32_t kStageBytes = (kSb + 2 * kSbBytes + 1023) / 1024 * 1024;
+constexpr int kStages = 5;
+constexpr int kRedPitch = 68;      // floats: conflict-free both ways
+constexpr uint32_t kRedOff = kStages * kStageBytes;
+constexpr uint32_t kRedSize = kWarps * kSlotRows * kRedPitch * 4;
+constexpr uint32_t kBarOff = kRedOff + kRedSize;
+constexpr uint32_t kMoeSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;
+constexpr int kPartFloats = kTileRows * kSlotRows;
+
+__device__ unsigned int g_moe_device_error;
+
+struct Slot {
+  int expert, first, n, pad;
+};
+// What the caller's workspace holds.  The counters come first: zero before a call
+// and left zero by it.
+struct Space {
+  uint32_t *routed;   // [row tiles] CTAs of the router that are done, then row tiles that are
+  uint32_t *tiles;    // [slots][tiles] segments of a split tile
+  uint32_t *columns;  // [tiles of down] slots that are done
+  float *logits;      // [rows][experts]
+  int32_t *ids;       // [rows][top]
+  float *weights;     // [rows][top]
+  int32_t *order;     // the pairs row * top + j by expert
+  int32_t *n_slots;
+  Slot *slots;
+  float *h;           // [pairs][inter]
+  float *d;           // [pairs][hidden]
+  float *parts;       // [CTAs][2][kPartFloats]
+  size_t counters, total;  // bytes
+};
+inline int slots_most(int rows, int experts, int top) {
+  const int pairs = rows * top;
+  return std::min(experts, pairs) + pairs / kSlotRows;
+}
+Space space_of(void *base, int rows, int hidden, int inter, int experts, int top, int ctas) {
+  Space s = {};
+  size_t at = 0;
+  uint8_t *b = static_cast<uint8_t *>(base);
+  auto take = [&](auto *&p, size_t n) {
+    p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(b + at);
+    at += (n * sizeof(*p) + 255) / 256 * 256;
+  };
+  const size_t pairs = (size_t)rows * top, slots = (size_t)slots_most(rows, experts, top);
+  const size_t up = inter / 64, down = hidden / kTileRows;
+  take(s.routed, kMaxRows / 16 + 1);
+  take(s.tiles, slots * std::max(up, down));
+  take(s.columns, down);
+  s.counters = at;
+  take(s.logits, (size_t)rows * experts);
+  take(s.ids, pairs);
+  take(s.weights, pairs);
+  take(s.order, pairs);
+  take(s.n_slots, 1);
+  take(s.slots, slots);
+  take(s.h, pairs * inter);
+  take(s.d, pairs * hidden);
+  take(s.parts, (size_t)ctas * 2 * kPartFloats);
+  s.total = at;
+  return s;
+}
+
+struct MoeArgs {
+  const __nv_bfloat16 *x, *router;
+  const uint16_t *gate_s, *gate_b, *up_s, *up_b, *down_s, *down_b;
+  __nv_bfloat16 *y;
+  int32_t *ids_out;     // may be null
+  float *weights_out;   // may be null
+  Space ws;
+  int rows, hidden, inter, experts, top, renormalize;
+};
+
+// ---- router ---------------------------------------------------------------------
+constexpr int kRouteTile = 16;     // rows of x
+constexpr int kRouteExperts = 8;
+
+// Larger floats have larger keys; NaN has the smallest.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if (f != f) return 0u;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The experts of row t, by a warp: top times the largest key, of equal ones the
+// lowest expert.
+__device__ void choose(const MoeArgs &a, int t) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPer = kMaxExperts / 32;
+  const float *z = a.ws.logits + (size_t)t * a.experts;
+  float v[kPer];
+  uint32_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane + 32 * i;
+    v[i] = e < a.experts ? __ldcg(z + e) : 0.f;
+    key[i] = e < a.experts ? order_key(v[i]) + 1u : 0u;  // 0: none (a NaN is 1)
+  }
+  float mine = 0.f, most = 0.f;  // lane j: the logit of choice j
+  int id = 0;
+  for (int j = 0; j < a.top; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    uint32_t e = 0xffffffffu;
+#pragma unroll
+    for (int i = kPer - 1; i >= 0; --i)
+      if (key[i] == top) e = lane + 32 * i;
+    const int chosen = (int)__reduce_min_sync(0xffffffffu, e);
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i == chosen) {
+        x = v[i];
+        key[i] = 0u;
+      }
+    x = __shfl_sync(0xffffffffu, x, chosen & 31);
+    if (j == 0) most = x;
+    if (lane == j) {
+      mine = x;
+      id = chosen;
+    }
+  }
+  float w = lane < a.top ? expf(mine - most) : 0.f, sum = w;
+  if (!a.renormalize) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < a.experts) sum += expf(v[i] - most);
+  }
+  w /= warp_sum(sum);
+  if (lane < a.top) {
+    const int p = t * a.top + lane;
+    a.ws.ids[p] = id;
+    a.ws.weights[p] = w;
+    if (a.ids_out) a.ids_out[p] = id;
+    if (a.weights_out) a.weights_out[p] = w;
+  }
+}
+
+// The pairs by expert (rows ascending), and the slots.  A bit a row and expert
+// makes the order the same whoever sets the bits first.
+__device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, int *scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int pairs = a.rows * a.top;
+  for (int i = tid; i < kMaxExperts * 4; i += kWarps * 32) (&bits[0][0])[i] = 0u;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kWarps * 32) {
+    const int t = p / a.top, e = __ldcg(a.ws.ids + p);
+    atomicOr(&bits[e][t >> 5], 1u << (t & 31));
+  }
+  __syncthreads();
+  // two experts a thread: their pairs and slots in one scan (pairs << 16 | slots)
+  auto count = [&](int e) {
+    return __popc(bits[e][0]) + __popc(bits[e][1]) + __popc(bits[e][2]) + __popc(bits[e][3]);
+  };
+  const int n0 = count(2 * tid), n1 = count(2 * tid + 1);
+  const int s0 = (n0 + kSlotRows - 1) / kSlotRows, s1 = (n1 + kSlotRows - 1) / kSlotRows;
+  int upto = ((n0 + n1) << 16) | (s0 + s1);
+  const int own = upto;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  int before = upto - own;
+  for (int i = 0; i < warp; ++i) before += scan[i];
+  int at = before >> 16, slot = before & 0xffff;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int e = 2 * tid + x, n = x ? n1 : n0;
+    first[e] = at;
+    for (int i = 0; i < n; i += kSlotRows)
+      a.ws.slots[slot++] = Slot{e, at + i, min(kSlotRows, n - i), 0};
+    at += n;
+  }
+  if (tid == kWarps * 32 - 1) *a.ws.n_slots = slot;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kWarps * 32) {
+    const int t = p / a.top, e = __ldcg(a.ws.ids + p);
+    int rank = __popc(bits[e][t >> 5] & ((1u << (t & 31)) - 1u));
+    for (int i = 0; i < t >> 5; ++i) rank += __popc(bits[e][i]);
+    a.ws.order[first[e] + rank] = p;
+  }
+}
+
+__global__ void __launch_bounds__(kWarps * 32) moe_route_kernel(const MoeArgs a) {
+  __shared__ float red[kWarps][kRouteTile][kRouteExperts];
+  __shared__ uint32_t bits[kMaxExperts][4];
+  __shared__ int first[kMaxExperts], scan[kWarps];
+  __shared__ uint32_t s_old;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  const int e0 = blockIdx.x * kRouteExperts, t0 = blockIdx.y * kRouteTile;
+  pdl_launch_dependents();
+  pdl_wait();
+  // A: 16 rows of x, B: 8 experts.  A lane's 16 bytes are 8 inputs of a block of
+  // 32, in the same places of both, so their order within the block does not matter.
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 *ra = reinterpret_cast<const uint4 *>(a.x + (size_t)(t0 + g8) * a.hidden) + t4;
+  const uint4 *rb = reinterpret_cast<const uint4 *>(a.x + (size_t)(t0 + g8 + 8) * a.hidden) + t4;
+  const uint4 *we = reinterpret_cast<const uint4 *>(a.router + (size_t)(e0 + g8) * a.hidden) + t4;
+  const bool has_a = t0 + g8 < a.rows, has_b = t0 + g8 + 8 < a.rows, has_e = e0 + g8 < a.experts;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int blocks = a.hidden / 32;
+  constexpr int kFly = 4;
+  for (int b0 = warp; b0 < blocks; b0 += kWarps * kFly) {
+    uint4 xa[kFly], xb[kFly], w[kFly];
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      const int b = b0 + kWarps * i;
+      const bool in = b < blocks;
+      xa[i] = in && has_a ? __ldg(ra + 4 * b) : zero;
+      xb[i] = in && has_b ? __ldg(rb + 4 * b) : zero;
+      w[i] = in && has_e ? __ldg(we + 4 * b) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) {
+      mma_bf16_m16n8k16(acc, xa[i].x, xb[i].x, xa[i].y, xb[i].y, w[i].x, w[i].y);
+      mma_bf16_m16n8k16(acc, xa[i].z, xb[i].z, xa[i].w, xb[i].w, w[i].z, w[i].w);
+    }
+  }
+  red[warp][g8][2 * t4] = acc[0];
+  red[warp][g8][2 * t4 + 1] = acc[1];
+  red[warp][g8 + 8][2 * t4] = acc[2];
+  red[warp][g8 + 8][2 * t4 + 1] = acc[3];
+  __syncthreads();
+  if (tid < kRouteTile * kRouteExperts) {
+    const int t = tid / kRouteExperts, e = tid % kRouteExperts;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += red[w][t][e];
+    if (t0 + t < a.rows && e0 + e < a.experts)
+      a.ws.logits[(size_t)(t0 + t) * a.experts + e0 + e] = sum;
+  }
+  // the last CTA of these rows chooses their experts
+  auto last = [&](uint32_t *counter, uint32_t of) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      s_old = atomicAdd(counter, 1u);
+      __threadfence();
+    }
+    __syncthreads();
+    const bool is = s_old == of - 1u;
+    if (is && tid == 0) *counter = 0u;
+    return is;
+  };
+  if (!last(a.ws.routed + blockIdx.y, gridDim.x)) return;
+  for (int t = t0 + warp; t < min(t0 + kRouteTile, a.rows); t += kWarps) choose(a, t);
+  if (!last(a.ws.routed + kMaxRows / 16, gridDim.y)) return;
+  make_slots(a, bits, first, scan);
+}
+
+// ---- the experts' products ---------------------------------------------------------
+template <int kBytes>
+__device__ __forceinline__ void copy_small(uint32_t dst, const uint16_t *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+// (no eviction hint: an expert with more than 8 rows has its weights read again)
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// kDown false: h = silu(gate x) * (up x) of every slot; true: d = weight * (down h),
+// and y once a tile's slots are all there.
+template <bool kDown>
+__global__ void __launch_bounds__((kWarps + 1) * 32, 2)
+    moe_experts_kernel(const __grid_constant__ CUtensorMap map0,
+                       const __grid_constant__ CUtensorMap map1, const MoeArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw);
+  const uint32_t full0 = base + kBarOff, empty0 = full0 + 8 * kStages;
+  volatile uint32_t *s_old = reinterpret_cast<volatile uint32_t *>(smem + kBarOff + 16 * kStages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init_u32(full0 + 8u * i, 1 + 32);
+      mbar_init_u32(empty0 + 8u * i, kWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // The slots are the router's, finished before any CTA of the gate and up launch
+  // is past its wait; the down launch begins after that, and may read them and its
+  // weights while the launch before it still runs.
+  if (!kDown) pdl_wait();
+  pdl_launch_dependents();
+  const int K = kDown ? a.inter : a.hidden, N = kDown ? a.hidden : a.inter;
+  constexpr int kStep = kDown ? kTileRows : kTileRows / 2;  // outputs of a tile
+  const int tiles = N / kStep, stages = (K + kStageK - 1) / kStageK, groups = K / 64;
+  const int n_slots = __ldcg(a.ws.n_slots);
+  const long long W = (long long)n_slots * tiles * stages;
+  const int ctas = (int)min((long long)gridDim.x, W);
+  if ((int)blockIdx.x >= ctas) return;
+  const long long u_begin = W * blockIdx.x / ctas, u_end = W * (blockIdx.x + 1) / ctas;
+
+  struct Segment {
+    int tile, slot, n0, s0, s1;
+  };
+  auto segment = [&](long long u) {
+    Segment g;
+    g.tile = (int)(u / stages);
+    g.slot = g.tile / tiles;
+    g.n0 = (g.tile - g.slot * tiles) * kStep;
+    g.s0 = (int)(u - (long long)g.tile * stages);
+    g.s1 = (int)min((long long)stages, g.s0 + (u_end - u));
+    return g;
+  };
+
+  if (warp == kWarps) {
+    // ---- producer: weights by tensor copies, scales and biases by small ones -----
+    const uint16_t *s0p = kDown ? a.down_s : a.gate_s, *b0p = kDown ? a.down_b : a.gate_b;
+    const uint16_t *s1p = kDown ? a.down_s : a.up_s, *b1p = kDown ? a.down_b : a.up_b;
+    const bool wide = groups % 4 == 0;
+    int st = 0, ph = 0, issued = 0;
+    bool ok = true;
+    for (long long u = u_begin; ok && u < u_end;) {
+      const Segment g = segment(u);
+      u += g.s1 - g.s0;
+      const long long row0 = (long long)__ldcg(&a.ws.slots[g.slot].expert) * N + g.n0;
+      for (int c = g.s0; c < g.s1; ++c) {
+        if (issued >= kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait_u32(empty0 + 8u * st, ph ^ 1));
+        if (!ok) break;
+        const uint32_t at = base + st * kStageBytes, full = full0 + 8u * st;
+        if (lane == 0) {
+          mbar_arrive_expect_tx_u32(full, 2 * kRows * 128);
+          const int x = c * (kStageK / 8);
+          load_box(at, &map0, x, (int)row0, full);
+          load_box(at + kRows * 128, &map1, x, (int)row0 + (kDown ? kRows : 0), full);
+        }
+        const uint32_t sb = at + kSb;
+#pragma unroll
+        for (int i = 0; i < kTileRows / 32; ++i) {
+          const int r = lane + 32 * i;                       // row of the stage
+          const int n = kDown || r < kRows ? r : r - kRows;  // row of its matrix, from n0
+          const long long off = (row0 + n) * groups + c * kGroupsOf;
+          const uint16_t *sp = (!kDown && r >= kRows ? s1p : s0p) + off;
+          const uint16_t *bp = (!kDown && r >= kRows ? b1p : b0p) + off;
+          if (wide) {
+            copy_small<8>(sb + r * 8, sp);
+            copy_small<8>(sb + kSbBytes + r * 8, bp);
+          } else {  // an even number of groups, the last stage's two
+            copy_small<4>(sb + r * 8, sp);
+            copy_small<4>(sb + kSbBytes + r * 8, bp);
+            if (c * kGroupsOf + 2 < groups) {
+              copy_small<4>(sb + r * 8 + 4, sp + 2);
+              copy_small<4>(sb + kSbBytes + r * 8 + 4, bp + 2);
+            }
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full) : "memory");
+        ++issued;
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(&g_moe_device_error, 1u);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int i = max(0, issued - kStages); i < issued; ++i)  // the copies in flight
+        (void)mbar_wait_u32(full0 + 8u * (i % kStages), (i / kStages) & 1);
+    }
+    return;
+  }
+
+  // ---- consumers -----------------------------------------------------------------
+  const int tid = threadIdx.x, g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t ldm = ldmatrix_offset(warp, lane);
+  const uint32_t sb_off = kSb + (uint32_t)(((warp >> 2) * kRows + g8) * 8 + (warp & 3) * 2);
+  float *red = reinterpret_cast<float *>(smem + kRedOff);
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
+  if (kDown) pdl_wait();  // h is the launch before's
+  int st = 0, ph = 0;
+  bool ok = true;
+  for (long long u = u_begin; u < u_end;) {
+    const Segment g = segment(u);
+    u += g.s1 - g.s0;
+    const Slot slot = a.ws.slots[g.slot];
+    const int pair = g8 < slot.n ? __ldcg(a.ws.order + slot.first + g8) : 0;
+    const bool valid = g8 < slot.n;
+    const void *xrow = kDown ? static_cast<const void *>(a.ws.h + (size_t)pair * K)
+                             : static_cast<const void *>(a.x + (size_t)(pair / a.top) * K);
+    float acc[kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    int grp = g.s0 * kGroupsOf + (warp & 3);
+    XRaw<kDown> next = load_x<kDown>(xrow, valid, min(grp, groups - 1), t4);
+    for (int c = g.s0; c < g.s1; ++c, grp += kGroupsOf) {
+      const XRaw<kDown> cur = next;
+      next = load_x<kDown>(xrow, valid, min(grp + kGroupsOf, groups - 1), t4);
+      if (!warp_wait_stage(full0 + 8u * st, ph)) ok = false;
+      const uint32_t at = base + st * kStageBytes;
+      if (ok && grp < groups)
+        group_math<kDown>(acc, at + ldm, cur, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_u32(empty0 + 8u * st);
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    // the four warps' sums of each row, red[warp][column][row]
+    sync();
+#pragma unroll
+    for (int rt = 0; rt < kTiles; ++rt) {
+      float *p = red + (warp * kSlotRows + 2 * t4) * kRedPitch + rt * 16 + g8;
+      p[0] = acc[rt][0];
+      p[kRedPitch] = acc[rt][1];
+      p[8] = acc[rt][2];
+      p[kRedPitch + 8] = acc[rt][3];
+    }
+    sync();
+    // this thread: rows r and r + 64 of columns q and q + 4
+    const int r = tid & 63, q = tid >> 6;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float *p = red + (4 * (i & 1) * kSlotRows + q + 2 * (i & 2)) * kRedPitch + r;
+      v[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v[i] += p[w * kSlotRows * kRedPitch];
+    }
+    if (g.s0 > 0 || g.s1 < stages) {
+      // a part of the tile: whoever comes last adds them all, in CTA order
+      float *part = a.ws.parts + (size_t)(2 * blockIdx.x + (g.s0 == 0 ? 1 : 0)) * kPartFloats;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) __stcg(part + i * kWarps * 32 + tid, v[i]);
+      __threadfence();
+      sync();
+      const long long t0 = (long long)g.tile * stages;
+      const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
+      if (tid == 0) {
+        const uint32_t old = atomicAdd(a.ws.tiles + g.tile, 1u);
+        __threadfence();
+        const bool last = old == (uint32_t)(c1 - c0);
+        if (last) a.ws.tiles[g.tile] = 0u;
+        *s_old = last;
+      }
+      sync();
+      if (!*s_old) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float *from = a.ws.parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats + tid;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __ldcg(from + i * kWarps * 32);
+      }
+    }
+    if constexpr (!kDown) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = q + 4 * i;
+        if (col < slot.n) {
+          const float gate = v[2 * i], up = v[2 * i + 1];
+          a.ws.h[(size_t)__ldcg(a.ws.order + slot.first + col) * N + g.n0 + r] =
+              gate / (1.f + expf(-gate)) * up;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = q + 4 * i;
+        if (col >= slot.n) continue;
+        const int p = __ldcg(a.ws.order + slot.first + col);
+        const float w = __ldcg(a.ws.weights + p);
+        float *d = a.ws.d + (size_t)p * N + g.n0 + r;
+        __stcg(d, w * v[2 * i]);
+        __stcg(d + 64, w * v[2 * i + 1]);
+      }
+      __threadfence();
+      sync();
+      const int column = g.n0 / kStep;
+      if (tid == 0) {
+        const uint32_t old = atomicAdd(a.ws.columns + column, 1u);
+        __threadfence();
+        const bool last = old == (uint32_t)(n_slots - 1);
+        if (last) a.ws.columns[column] = 0u;
+        *s_old = last;
+      }
+      sync();
+      if (!*s_old) continue;
+      // the rows' sums over their experts, in the order of choice: four columns a lane
+      const int n = g.n0 + 4 * lane;
+      {
+        for (int t = warp; t < a.rows; t += 2 * kWarps) {
+          float4 sum[2] = {};
+          for (int j0 = 0; j0 < a.top; j0 += 4) {
+            float4 x[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                x[y][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j0 + j < a.top && t + y * kWarps < a.rows)
+                  x[y][j] = __ldcg(reinterpret_cast<const float4 *>(
+                      a.ws.d + (size_t)((t + y * kWarps) * a.top + j0 + j) * N + n));
+              }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                sum[y].x += x[y][j].x;
+                sum[y].y += x[y][j].y;
+                sum[y].z += x[y][j].z;
+                sum[y].w += x[y][j].w;
+              }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (t + y * kWarps < a.rows) {
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[y].x, sum[y].y);
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[y].z, sum[y].w);
+              *reinterpret_cast<uint2 *>(a.y + (size_t)(t + y * kWarps) * N + n) =
+                  make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                             *reinterpret_cast<const uint32_t *>(&hi));
+            }
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicOr(&g_moe_device_error, 2u);
+}
+
+int moe_ctas() { return 2 * device_sm_count(); }
+
+sv_status check_sizes(const char *who, int rows, int hidden, int inter, int experts, int top) {
+  if (rows < 0 || hidden < 1 || inter < 1 || experts < 1 || top < 1 || top > experts)
+    return fail(SV_ERR_INVALID_ARG, "%s: need rows >= 0, hidden, inter, experts >= 1, 1 <= top_k <= experts",
+                who);
+  if (rows > kMaxRows) return fail(SV_ERR_UNSUPPORTED, "%s: %d rows > %d", who, rows, kMaxRows);
+  if (experts > kMaxExperts)
+    return fail(SV_ERR_UNSUPPORTED, "%s: %d experts > %d", who, experts, kMaxExperts);
+  if (top > kMaxTop) return fail(SV_ERR_UNSUPPORTED, "%s: top_k=%d > %d", who, top, kMaxTop);
+  if (hidden % 128 || inter % 128)
+    return fail(SV_ERR_UNSUPPORTED, "%s: hidden and inter must be multiples of 128 (%d, %d)", who,
+                hidden, inter);
+  if (hidden > 65536 || inter > 65536 || (long long)experts * std::max(hidden, inter) > (1ll << 30))
+    return fail(SV_ERR_UNSUPPORTED, "%s: sizes too large", who);
+  return SV_OK;
+}
+
+}  // namespace
+
+unsigned take_device_error_moe() {
+  unsigned v = 0, zero = 0;
+  cudaMemcpyFromSymbol(&v, g_moe_device_error, sizeof v);
+  cudaMemcpyToSymbol(g_moe_device_error, &zero, sizeof zero);
+  return v;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t moe_smallm_workspace_bytes(int rows, int hidden, int inter, int experts, int top_k,
+                                             size_t *zero_bytes) {
+  clear_error();
+  if (check_sizes("moe_smallm_workspace_bytes", rows, hidden, inter, experts, top_k) != SV_OK) return 0;
+  const Space s = space_of(nullptr, std::max(rows, 1), hidden, inter, experts, top_k, moe_ctas());
+  if (zero_bytes) *zero_bytes = s.counters;
+  return s.total;
+}
+
+extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const uint32_t *gate_w,
+                                const uint16_t *gate_s, const uint16_t *gate_b,
+                                const uint32_t *up_w, const uint16_t *up_s, const uint16_t *up_b,
+                                const uint32_t *down_w, const uint16_t *down_s,
+                                const uint16_t *down_b, int rows, int hidden, int inter,
+                                int experts, int top_k, int renormalize, uint16_t *y, int32_t *ids,
+                                float *weights, void *workspace, size_t workspace_bytes,
+                                sv_stream_t stream) {
+  clear_error();
+  const char *who = "moe_smallm";
+  sv_status st = check_sizes(who, rows, hidden, inter, experts, top_k);
+  if (st != SV_OK) return st;
+  if (rows == 0) return SV_OK;
+  struct Buf {
+    const void *p;
+    size_t n;
+    size_t align;
+  };
+  const size_t gate_n = (size_t)experts * inter * hidden;
+  const Buf in[] = {{x, (size_t)rows * hidden * 2, 16},
+                    {router, (size_t)experts * hidden * 2, 16},
+                    {gate_w, gate_n / 2, 16},
+                    {gate_s, gate_n / 32, 8},
+                    {gate_b, gate_n / 32, 8},
+                    {up_w, gate_n / 2, 16},
+                    {up_s, gate_n / 32, 8},
+                    {up_b, gate_n / 32, 8},
+                    {down_w, gate_n / 2, 16},
+                    {down_s, gate_n / 32, 8},
+                    {down_b, gate_n / 32, 8}};
+  for (const Buf &b : in)
+    if (!b.p) return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!y || !workspace) return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
+  for (const Buf &b : in)
+    if (!aligned(b.p, b.align))
+      return fail(SV_ERR_INVALID_ARG,
+                  "%s: x, router and w_packed must be 16-byte, scales and biases 8-byte aligned", who);
+  if (!aligned(y, 8) || (ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4)) ||
+      !aligned(workspace, 256))
+    return fail(SV_ERR_INVALID_ARG, "%s: y must be 8-byte, the workspace 256-byte aligned", who);
+  const int ctas = moe_ctas();
+  const Space ws = space_of(workspace, rows, hidden, inter, experts, top_k, ctas);
+  if (workspace_bytes < ws.total)
+    return fail(SV_ERR_INVALID_ARG, "%s: the workspace has %zu bytes, %zu are needed", who,
+                workspace_bytes, ws.total);
+  const Buf out[] = {{y, (size_t)rows * hidden * 2, 8},
+                     {ids, ids ? (size_t)rows * top_k * 4 : 0, 4},
+                     {weights, weights ? (size_t)rows * top_k * 4 : 0, 4},
+                     {workspace, ws.total, 256}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Buf &b : in)
+      if (overlaps(out[i].p, out[i].n, b.p, b.n))
+        return fail(SV_ERR_INVALID_ARG, "%s: an output or the workspace overlaps an input", who);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(SV_ERR_INVALID_ARG, "%s: outputs and the workspace must not overlap", who);
+  }
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([] {
+    const cudaError_t x = cudaFuncSetAttribute(
+        moe_experts_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMoeSmem);
+    return x != cudaSuccess ? x
+                            : cudaFuncSetAttribute(moe_experts_kernel<true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)kMoeSmem);
+  });
+  if (e != cudaSuccess)
+    return fail(SV_ERR_CUDA, "%s: cudaFuncSetAttribute failed: %s", who, cudaGetErrorString(e));
+  CUtensorMap gate_map, up_map, down_map;
+  auto encode = [&](CUtensorMap *map, const uint32_t *w, int n, int k) {
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, w, (uint64_t)k / 8, (uint64_t)experts * n,
+                     (uint64_t)k / 2, kBoxWords, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  st = encode(&gate_map, gate_w, inter, hidden);
+  if (st == SV_OK) st = encode(&up_map, up_w, inter, hidden);
+  if (st == SV_OK) st = encode(&down_map, down_w, hidden, inter);
+  if (st != SV_OK) return st;
+  MoeArgs a = {};
+  a.x = reinterpret_cast<const __nv_bfloat16 *>(x);
+  a.router = reinterpret_cast<const __nv_bfloat16 *>(router);
+  a.gate_s = gate_s;
+  a.gate_b = gate_b;
+  a.up_s = up_s;
+  a.up_b = up_b;
+  a.down_s = down_s;
+  a.down_b = down_b;
+  a.y = reinterpret_cast<__nv_bfloat16 *>(y);
+  a.ids_out = ids;
+  a.weights_out = weights;
+  a.ws = ws;
+  a.rows = rows;
+  a.hidden = hidden;
+  a.inter = inter;
+  a.experts = experts;
+  a.top = top_k;
+  a.renormalize = renormalize;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = &early;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.gridDim = dim3((experts + kRouteExperts - 1) / kRouteExperts, (rows + kRouteTile - 1) / kRouteTile);
+  cfg.blockDim = dim3(kWarps * 32);
+  cudaError_t le = cudaLaunchKernelEx(&cfg, moe_route_kernel, a);
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3((kWarps + 1) * 32);
+  cfg.dynamicSmemBytes = kMoeSmem;
+  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<false>, gate_map, up_map, a);
+  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<true>, down_map, down_map, a);
+  if (le != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(SV_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(le));
+  }
+  return check_launch(who);
+}

@@ -82,9 +82,10 @@ extern "C" sv_status sv_device_status(void) {
   const unsigned p = sv::take_device_error_plan();
   const unsigned w = sv::take_device_error_wide();
   const unsigned t = sv::take_device_error_attn();
-  if (q | a | g | p | w | t)
+  const unsigned m = sv::take_device_error_moe();
+  if (q | a | g | p | w | t | m)
     return sv::fail(SV_ERR_DEVICE_FLAG,
-                    "device error words: qmv=%u accept=%u gdn=%u plan=%u wide=%u attention=%u", q,
-                    a, g, p, w, t);
+                    "device error words: qmv=%u accept=%u gdn=%u plan=%u wide=%u attention=%u experts=%u",
+                    q, a, g, p, w, t, m);
   return SV_OK;
 }

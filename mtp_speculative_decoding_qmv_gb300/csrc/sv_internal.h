@@ -54,5 +54,6 @@ unsigned take_device_error_gdn();
 unsigned take_device_error_plan();
 unsigned take_device_error_wide();
 unsigned take_device_error_attn();
+unsigned take_device_error_moe();
 
 }  // namespace sv

@@ -26,6 +26,7 @@ decltype(&rope_kv_append) append_fn = nullptr;
 decltype(&paged_attention) attend_fn = nullptr;
 decltype(&gdn_inputs) inputs_fn = nullptr;
 decltype(&gdn_advance) advance_fn = nullptr;
+decltype(&moe_smallm) experts_fn = nullptr;
 
 // What a call's arguments are read with.  `fits` turns false at the first
 // tensor that is not as wanted; later reads of that call then give null.
@@ -129,10 +130,10 @@ PyObject *call(F library) {
   return PyLong_FromLong(st);
 }
 
-// bind(kv_pages_step, rope_kv_append, paged_attention, gdn_inputs, gdn_advance): the
-// library's addresses
+// bind(kv_pages_step, rope_kv_append, paged_attention, gdn_inputs, gdn_advance, moe_smallm):
+// the library's addresses
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  constexpr int kCalls = 5;
+  constexpr int kCalls = 6;
   void *at[kCalls] = {};
   for (int i = 0; i < kCalls && n == kCalls; ++i) at[i] = PyLong_AsVoidPtr(args[i]);
   if (PyErr_Occurred()) return nullptr;
@@ -141,6 +142,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
   attend_fn = reinterpret_cast<decltype(attend_fn)>(at[2]);
   inputs_fn = reinterpret_cast<decltype(inputs_fn)>(at[3]);
   advance_fn = reinterpret_cast<decltype(advance_fn)>(at[4]);
+  experts_fn = reinterpret_cast<decltype(experts_fn)>(at[5]);
   Py_RETURN_NONE;
 }
 
@@ -362,11 +364,55 @@ PyObject *advance(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// moe_smallm(device, stream, x, router, gate w, s, b, up w, s, b, down w, s, b, top_k,
+// renormalize, out, ids or None, weights or None, workspace)
+PyObject *experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Reader r;
+  sv_stream_t stream;
+  if (!begin(args, n, 19, &r, &stream)) return nullptr;
+  int top;
+  if (!to_int(args[13], &top)) return nullptr;
+  const int renormalize = PyObject_IsTrue(args[14]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor *x = r.tensor(2), *gate = r.tensor(4);
+  if (!r.fits || x->dim() != 2 || gate->dim() != 3) Py_RETURN_NONE;
+  const auto bf16 = at::kBFloat16;
+  const int64_t rows = x->size(0), hidden = x->size(1), e = gate->size(0), inter = gate->size(1);
+  const auto *x_at = r.at<uint16_t>(2, bf16, {rows, hidden});
+  const auto *router = r.at<uint16_t>(3, bf16, {e, hidden});
+  const uint32_t *w[3];
+  const uint16_t *s[3], *b[3];
+  for (int i = 0; i < 3; ++i) {
+    const int64_t out = i < 2 ? inter : hidden, in = i < 2 ? hidden : inter;
+    w[i] = r.at<uint32_t>(4 + 3 * i, at::kInt, {e, out, in / 8});
+    s[i] = r.at<uint16_t>(5 + 3 * i, bf16, {e, out, in / 64});
+    b[i] = r.at<uint16_t>(6 + 3 * i, bf16, {e, out, in / 64});
+  }
+  auto *y = r.at<uint16_t>(15, bf16, {rows, hidden});
+  auto *ids = r.given(16) ? r.at<int32_t>(16, at::kInt, {rows, top}) : nullptr;
+  auto *weights = r.given(17) ? r.at<float>(17, at::kFloat, {rows, top}) : nullptr;
+  int64_t bytes = 0;
+  void *workspace = r.any<void>(18, at::kByte, &bytes);
+  if (!r.fits) Py_RETURN_NONE;
+  int v[4];
+  const int64_t sizes[4] = {rows, hidden, inter, e};
+  for (int i = 0; i < 4; ++i)
+    if (!to_int(sizes[i], &v[i])) return nullptr;
+  return call([&] {
+    return experts_fn(x_at, router, w[0], s[0], b[0], w[1], s[1], b[1], w[2], s[2], b[2], v[0],
+                      v[1], v[2], v[3], top, renormalize, y, ids, weights, workspace,
+                      (size_t)bytes, stream);
+  });
+  END_HANDLE_TH_ERRORS
+}
+
 #define METHOD(name, function) \
   {name, (PyCFunction)(void *)function, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD("bind", bind), METHOD("kv_pages_step", pages),
                          METHOD("rope_kv_append", append), METHOD("paged_attention", attend),
                          METHOD("gdn_inputs", inputs), METHOD("gdn_advance", advance),
+                         METHOD("moe_smallm", experts),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
