@@ -335,7 +335,7 @@ sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint1
  * split into two bf16 parts as qmv_smallm does with fp32 x.  A row depends on no
  * other row up to the order of its fp32 sums, and results do not depend on the run.
  * Requires 0 <= rows <= 128 (0: no-op), 1 <= top_k <= 16, top_k <= experts <= 512,
- * hidden and inter multiples of 128; x, router and the w_packed 16-byte, scales and
+ * hidden (at most 16384) and inter (at most 65536) multiples of 128; x, router and the w_packed 16-byte, scales and
  * biases 8-byte, y 8-byte aligned; no output overlaps an input or another output.
  * workspace: moe_smallm_workspace_bytes(..) bytes on the current device (0 on
  * invalid input; *zero_bytes, when given, is how many of the first are arrival

@@ -18,10 +18,14 @@
 //    rows of gate and the same 64 of up (their product leaves in one place), or
 //    128 of down.  Four 64-groups x two blocks of 64 rows make a stage's work for
 //    eight warps, each as in qmv_smallm.  A producer warp keeps the ring of stages
-//    full across tiles.  A tile cut between CTAs leaves partial sums, which
-//    whichever CTA comes last adds in CTA order; nobody waits for another CTA, so
-//    the launches need not be resident together.
-// The activations between the products stay fp32 (two bf16 parts as operands).
+//    full across tiles, and a warp of its own takes the sums of a finished tile, so
+//    that neither the copies nor the products wait for the fences below.  A tile cut
+//    between CTAs leaves partial sums, which whichever CTA comes last adds in CTA
+//    order; nobody waits for another CTA, so the launches need not be resident
+//    together.
+// The activations between the products are kept as two bf16 parts (2^-16 of their
+// sum).  As operands of down the parts of up to four rows share one MMA's eight
+// columns; five to eight rows take two MMAs.
 #include <algorithm>
 #include <atomic>
 
@@ -36,16 +40,20 @@ constexpr int kSlotRows = 8;       // pairs of a slot
 constexpr int kTileRows = 128;     // weight rows of a tile
 constexpr int kStageK = 256;       // inputs of a stage
 constexpr int kGroupsOf = kStageK / 64;
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;          // that multiply; then the producer, then the finisher
+constexpr int kMoeThreads = (kWarps + 2) * 32;
 constexpr uint32_t kSb = 2 * kRows * 128;                   // scales, then biases
 constexpr uint32_t kSbBytes = kTileRows * kGroupsOf * 2;    // [128 rows][4 groups] bf16
 constexpr uint32_t kStageBytes = (kSb + 2 * kSbBytes + 1023) / 1024 * 1024;
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kRedPitch = 68;      // floats: conflict-free both ways
 constexpr uint32_t kRedOff = kStages * kStageBytes;
-constexpr uint32_t kRedSize = kWarps * kSlotRows * kRedPitch * 4;
-constexpr uint32_t kBarOff = kRedOff + kRedSize;
-constexpr uint32_t kMoeSmem = kBarOff + 2 * kStages * 8 + 16 + 1024;
+constexpr uint32_t kRedSize = kWarps * kSlotRows * kRedPitch * 4;  // two of them
+constexpr int kMostColumns = 128;  // tiles of y that a CTA may come last at
+constexpr uint32_t kColumnsOff = kRedOff + 2 * kRedSize;  // their number, then they
+constexpr uint32_t kBarOff = kColumnsOff + (kMostColumns + 2) * 4;
+constexpr int kBarsOf = 2 * kStages + 5;
+constexpr uint32_t kMoeSmem = kBarOff + kBarsOf * 8 + 1024;
 constexpr int kPartFloats = kTileRows * kSlotRows;
 
 __device__ unsigned int g_moe_device_error;
@@ -65,7 +73,7 @@ struct Space {
   int32_t *order;     // the pairs row * top + j by expert
   int32_t *n_slots;
   Slot *slots;
-  float *h;           // [pairs][inter]
+  uint16_t *h;        // [2][pairs][inter]: the first bf16 part, the second
   float *d;           // [pairs][hidden]
   float *parts;       // [CTAs][2][kPartFloats]
   size_t counters, total;  // bytes
@@ -94,7 +102,7 @@ Space space_of(void *base, int rows, int hidden, int inter, int experts, int top
   take(s.order, pairs);
   take(s.n_slots, 1);
   take(s.slots, slots);
-  take(s.h, pairs * inter);
+  take(s.h, 2 * pairs * inter);
   take(s.d, pairs * hidden);
   take(s.parts, (size_t)ctas * 2 * kPartFloats);
   s.total = at;
@@ -134,8 +142,10 @@ __device__ void choose(const MoeArgs &a, int t) {
   for (int i = 0; i < kPer; ++i) {
     const int e = lane + 32 * i;
     v[i] = e < a.experts ? __ldcg(z + e) : 0.f;
-    key[i] = e < a.experts ? order_key(v[i]) + 1u : 0u;  // 0: none (a NaN is 1)
   }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)  // 0: none (a NaN is 1)
+    key[i] = lane + 32 * i < a.experts ? order_key(v[i]) + 1u : 0u;
   float mine = 0.f, most = 0.f;  // lane j: the logit of choice j
   int id = 0;
   for (int j = 0; j < a.top; ++j) {
@@ -181,23 +191,19 @@ __device__ void choose(const MoeArgs &a, int t) {
 
 // The pairs by expert (rows ascending), and the slots.  A bit a row and expert
 // makes the order the same whoever sets the bits first.
+constexpr int kRouteThreads = 512;
 __device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, int *scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = a.rows * a.top;
-  for (int i = tid; i < kMaxExperts * 4; i += kWarps * 32) (&bits[0][0])[i] = 0u;
-  __syncthreads();
-  for (int p = tid; p < pairs; p += kWarps * 32) {
+  for (int p = tid; p < pairs; p += kRouteThreads) {
     const int t = p / a.top, e = __ldcg(a.ws.ids + p);
     atomicOr(&bits[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
-  // two experts a thread: their pairs and slots in one scan (pairs << 16 | slots)
-  auto count = [&](int e) {
-    return __popc(bits[e][0]) + __popc(bits[e][1]) + __popc(bits[e][2]) + __popc(bits[e][3]);
-  };
-  const int n0 = count(2 * tid), n1 = count(2 * tid + 1);
-  const int s0 = (n0 + kSlotRows - 1) / kSlotRows, s1 = (n1 + kSlotRows - 1) / kSlotRows;
-  int upto = ((n0 + n1) << 16) | (s0 + s1);
+  // an expert a thread: its pairs and slots in one scan (pairs << 16 | slots)
+  static_assert(kRouteThreads == kMaxExperts, "an expert a thread");
+  const int n = __popc(bits[tid][0]) + __popc(bits[tid][1]) + __popc(bits[tid][2]) + __popc(bits[tid][3]);
+  int upto = (n << 16) | ((n + kSlotRows - 1) / kSlotRows);
   const int own = upto;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -208,18 +214,14 @@ __device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, in
   __syncthreads();
   int before = upto - own;
   for (int i = 0; i < warp; ++i) before += scan[i];
-  int at = before >> 16, slot = before & 0xffff;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int e = 2 * tid + x, n = x ? n1 : n0;
-    first[e] = at;
-    for (int i = 0; i < n; i += kSlotRows)
-      a.ws.slots[slot++] = Slot{e, at + i, min(kSlotRows, n - i), 0};
-    at += n;
-  }
-  if (tid == kWarps * 32 - 1) *a.ws.n_slots = slot;
+  const int at = before >> 16;
+  int slot = before & 0xffff;
+  first[tid] = at;
+  for (int i = 0; i < n; i += kSlotRows)
+    a.ws.slots[slot++] = Slot{tid, at + i, min(kSlotRows, n - i), 0};
+  if (tid == kRouteThreads - 1) *a.ws.n_slots = slot;
   __syncthreads();
-  for (int p = tid; p < pairs; p += kWarps * 32) {
+  for (int p = tid; p < pairs; p += kRouteThreads) {
     const int t = p / a.top, e = __ldcg(a.ws.ids + p);
     int rank = __popc(bits[e][t >> 5] & ((1u << (t & 31)) - 1u));
     for (int i = 0; i < t >> 5; ++i) rank += __popc(bits[e][i]);
@@ -227,14 +229,16 @@ __device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, in
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) moe_route_kernel(const MoeArgs a) {
-  __shared__ float red[kWarps][kRouteTile][kRouteExperts];
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const MoeArgs a) {
+  constexpr int kRouteWarps = kRouteThreads / 32;
+  __shared__ float red[kRouteWarps][kRouteTile][kRouteExperts];
   __shared__ uint32_t bits[kMaxExperts][4];
-  __shared__ int first[kMaxExperts], scan[kWarps];
+  __shared__ int first[kMaxExperts], scan[kRouteWarps];
   __shared__ uint32_t s_old;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
   const int e0 = blockIdx.x * kRouteExperts, t0 = blockIdx.y * kRouteTile;
   pdl_launch_dependents();
+  *reinterpret_cast<uint4 *>(bits[tid]) = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
   // A: 16 rows of x, B: 8 experts.  A lane's 16 bytes are 8 inputs of a block of
   // 32, in the same places of both, so their order within the block does not matter.
@@ -245,12 +249,12 @@ __global__ void __launch_bounds__(kWarps * 32) moe_route_kernel(const MoeArgs a)
   const bool has_a = t0 + g8 < a.rows, has_b = t0 + g8 + 8 < a.rows, has_e = e0 + g8 < a.experts;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const int blocks = a.hidden / 32;
-  constexpr int kFly = 4;
-  for (int b0 = warp; b0 < blocks; b0 += kWarps * kFly) {
+  constexpr int kFly = 5;
+  for (int b0 = warp; b0 < blocks; b0 += kRouteWarps * kFly) {
     uint4 xa[kFly], xb[kFly], w[kFly];
 #pragma unroll
     for (int i = 0; i < kFly; ++i) {
-      const int b = b0 + kWarps * i;
+      const int b = b0 + kRouteWarps * i;
       const bool in = b < blocks;
       xa[i] = in && has_a ? __ldg(ra + 4 * b) : zero;
       xb[i] = in && has_b ? __ldg(rb + 4 * b) : zero;
@@ -271,13 +275,13 @@ __global__ void __launch_bounds__(kWarps * 32) moe_route_kernel(const MoeArgs a)
     const int t = tid / kRouteExperts, e = tid % kRouteExperts;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += red[w][t][e];
+    for (int w = 0; w < kRouteWarps; ++w) sum += red[w][t][e];
     if (t0 + t < a.rows && e0 + e < a.experts)
-      a.ws.logits[(size_t)(t0 + t) * a.experts + e0 + e] = sum;
+      __stcg(a.ws.logits + (size_t)(t0 + t) * a.experts + e0 + e, sum);
+    __threadfence();
   }
   // the last CTA of these rows chooses their experts
   auto last = [&](uint32_t *counter, uint32_t of) {
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
       s_old = atomicAdd(counter, 1u);
@@ -289,8 +293,13 @@ __global__ void __launch_bounds__(kWarps * 32) moe_route_kernel(const MoeArgs a)
     return is;
   };
   if (!last(a.ws.routed + blockIdx.y, gridDim.x)) return;
-  for (int t = t0 + warp; t < min(t0 + kRouteTile, a.rows); t += kWarps) choose(a, t);
-  if (!last(a.ws.routed + kMaxRows / 16, gridDim.y)) return;
+  static_assert(kRouteWarps == kRouteTile, "a row a warp");
+  if (t0 + warp < a.rows) choose(a, t0 + warp);
+  __threadfence();
+  if (gridDim.y == 1)
+    __syncthreads();
+  else if (!last(a.ws.routed + kMaxRows / 16, gridDim.y))
+    return;
   make_slots(a, bits, first, scan);
 }
 
@@ -311,7 +320,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
 // kDown false: h = silu(gate x) * (up x) of every slot; true: d = weight * (down h),
 // and y once a tile's slots are all there.
 template <bool kDown>
-__global__ void __launch_bounds__((kWarps + 1) * 32, 2)
+__global__ void __launch_bounds__(kMoeThreads, 2)
     moe_experts_kernel(const __grid_constant__ CUtensorMap map0,
                        const __grid_constant__ CUtensorMap map1, const MoeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -319,13 +328,20 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw);
   const uint32_t full0 = base + kBarOff, empty0 = full0 + 8 * kStages;
-  volatile uint32_t *s_old = reinterpret_cast<volatile uint32_t *>(smem + kBarOff + 16 * kStages);
+  const uint32_t red_full0 = empty0 + 8 * kStages, red_empty0 = red_full0 + 16;
+  const uint32_t done = red_empty0 + 16;
+  volatile int *columns = reinterpret_cast<volatile int *>(smem + kColumnsOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init_u32(full0 + 8u * i, 1 + 32);
       mbar_init_u32(empty0 + 8u * i, kWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_u32(red_full0 + 8u * i, kWarps);
+      mbar_init_u32(red_empty0 + 8u * i, 1);
+    }
+    mbar_init_u32(done, 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2)
   const int K = kDown ? a.inter : a.hidden, N = kDown ? a.hidden : a.inter;
   constexpr int kStep = kDown ? kTileRows : kTileRows / 2;  // outputs of a tile
   const int tiles = N / kStep, stages = (K + kStageK - 1) / kStageK, groups = K / 64;
-  const int n_slots = __ldcg(a.ws.n_slots);
+  const int n_slots = __ldcg(a.ws.n_slots), pairs = a.rows * a.top;
   const long long W = (long long)n_slots * tiles * stages;
   const int ctas = (int)min((long long)gridDim.x, W);
   if ((int)blockIdx.x >= ctas) return;
@@ -415,35 +431,155 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2)
     return;
   }
 
-  // ---- consumers -----------------------------------------------------------------
-  const int tid = threadIdx.x, g8 = lane >> 2, t4 = lane & 3;
+  if (warp == kWarps + 1) {
+    // ---- finisher: rows 2 lane and 2 lane + 1 of both blocks of a tile -------------
+    if (kDown) pdl_wait();  // the tiles' counters and partials are the launch before's
+    int at_end = 0, k = 0;
+    bool ok = true;
+    for (long long u = u_begin; ok && u < u_end; ++k) {
+      const Segment g = segment(u);
+      u += g.s1 - g.s0;
+      const int first = __ldcg(&a.ws.slots[g.slot].first), n = __ldcg(&a.ws.slots[g.slot].n);
+      const bool whole = g.s0 == 0 && g.s1 == stages;
+      // down's slots of up to four rows have the second parts' sums in columns 4..7
+      const bool doubled = kDown && n <= 4;
+      float *part = a.ws.parts + (size_t)(2 * blockIdx.x + (g.s0 == 0 ? 1 : 0)) * kPartFloats + 2 * lane;
+      auto emit = [&](int col, float2 v0, float2 v1) {
+        const int p = __ldcg(a.ws.order + first + col);
+        if constexpr (!kDown) {
+          const float h0 = v0.x / (1.f + expf(-v0.x)) * v1.x, h1 = v0.y / (1.f + expf(-v0.y)) * v1.y;
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(h0, h1);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(h0 - __low2float(hi), h1 - __high2float(hi));
+          uint16_t *h = a.ws.h + (size_t)p * N + g.n0 + 2 * lane;
+          *reinterpret_cast<uint32_t *>(h) = *reinterpret_cast<const uint32_t *>(&hi);
+          *reinterpret_cast<uint32_t *>(h + (size_t)pairs * N) = *reinterpret_cast<const uint32_t *>(&lo);
+        } else {
+          const float w = __ldcg(a.ws.weights + p);
+          float *d = a.ws.d + (size_t)p * N + g.n0 + 2 * lane;
+          __stcg(reinterpret_cast<float2 *>(d), make_float2(w * v0.x, w * v0.y));
+          __stcg(reinterpret_cast<float2 *>(d + kRows), make_float2(w * v1.x, w * v1.y));
+        }
+      };
+      ok = __all_sync(0xffffffffu, mbar_wait_u32(red_full0 + 8u * (k & 1), (k >> 1) & 1));
+      if (!ok) break;
+      const float *red = reinterpret_cast<const float *>(smem + kRedOff + (k & 1) * kRedSize) + 2 * lane;
+      for (int col = 0; col < n; ++col) {
+        float2 v[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          v[x] = make_float2(0.f, 0.f);
+          for (int y = col; y < kSlotRows; y += 4) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 f = *reinterpret_cast<const float2 *>(
+                  red + ((4 * x + w) * kSlotRows + y) * kRedPitch);
+              v[x].x += f.x;
+              v[x].y += f.y;
+            }
+            if (!doubled) break;
+          }
+        }
+        if (whole) {
+          emit(col, v[0], v[1]);
+        } else {
+          __stcg(reinterpret_cast<float2 *>(part + col * kTileRows), v[0]);
+          __stcg(reinterpret_cast<float2 *>(part + col * kTileRows + kRows), v[1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_u32(red_empty0 + 8u * (k & 1));
+      // the warp's stores, then one of its lanes counts; the count's last adds up
+      auto count = [&](uint32_t *counter, uint32_t of) {
+        __threadfence();
+        __syncwarp();
+        uint32_t old = 0;
+        if (lane == 0) {
+          old = atomicAdd(counter, 1u);
+          if (old == of - 1u) *counter = 0u;
+        }
+        old = __shfl_sync(0xffffffffu, old, 0);
+        __threadfence();
+        return old == of - 1u;
+      };
+      if (!whole) {
+        // a part of the tile: whoever comes last adds them all, in CTA order
+        const long long t0 = (long long)g.tile * stages;
+        const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
+        if (!count(a.ws.tiles + g.tile, (uint32_t)(c1 - c0 + 1))) continue;
+        for (int col = 0; col < n; ++col) {
+          float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int c = c0; c <= c1; ++c) {
+            const float *from = a.ws.parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats +
+                                col * kTileRows + 2 * lane;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 f = __ldcg(reinterpret_cast<const float2 *>(from + x * kRows));
+              v[x].x += f.x;
+              v[x].y += f.y;
+            }
+          }
+          emit(col, v[0], v[1]);
+        }
+      }
+      if (kDown) {
+        const int column = g.n0 / kStep;
+        if (count(a.ws.columns + column, (uint32_t)n_slots)) {
+          if (lane == 0) columns[1 + at_end] = column;
+          ++at_end;
+        }
+      }
+    }
+    if (kDown) {
+      __syncwarp();
+      if (lane == 0) {
+        columns[0] = at_end;
+        mbar_arrive_u32(done);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&g_moe_device_error, 4u);
+    return;
+  }
+
+  // ---- the products ----------------------------------------------------------------
+  const int g8 = lane >> 2, t4 = lane & 3;
   const uint32_t ldm = ldmatrix_offset(warp, lane);
   const uint32_t sb_off = kSb + (uint32_t)(((warp >> 2) * kRows + g8) * 8 + (warp & 3) * 2);
-  float *red = reinterpret_cast<float *>(smem + kRedOff);
-  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
   if (kDown) pdl_wait();  // h is the launch before's
-  int st = 0, ph = 0;
+  int st = 0, ph = 0, k = 0;
   bool ok = true;
-  for (long long u = u_begin; u < u_end;) {
+  for (long long u = u_begin; ok && u < u_end; ++k) {
     const Segment g = segment(u);
     u += g.s1 - g.s0;
-    const Slot slot = a.ws.slots[g.slot];
-    const int pair = g8 < slot.n ? __ldcg(a.ws.order + slot.first + g8) : 0;
-    const bool valid = g8 < slot.n;
-    const void *xrow = kDown ? static_cast<const void *>(a.ws.h + (size_t)pair * K)
-                             : static_cast<const void *>(a.x + (size_t)(pair / a.top) * K);
+    const int first = __ldcg(&a.ws.slots[g.slot].first), n = __ldcg(&a.ws.slots[g.slot].n);
+    const bool both = kDown && n > 4;  // a column a row, its two parts one after the other
+    const int col = kDown && !both ? g8 & 3 : g8;
+    const bool valid = col < n;
+    const int pair = valid ? __ldcg(a.ws.order + first + col) : 0;
+    const uint16_t *xrow = kDown ? a.ws.h + ((size_t)pair + (!both && g8 >= 4 ? pairs : 0)) * K
+                                 : reinterpret_cast<const uint16_t *>(a.x) + (size_t)(pair / a.top) * K;
+    const uint16_t *xlow = kDown ? xrow + (size_t)pairs * K : nullptr;
     float acc[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     int grp = g.s0 * kGroupsOf + (warp & 3);
-    XRaw<kDown> next = load_x<kDown>(xrow, valid, min(grp, groups - 1), t4);
+    const int most = groups - 1;
+    XRaw<false> next = load_x<false>(xrow, valid, min(grp, most), t4), low = {};
+    if (both) low = load_x<false>(xlow, valid, min(grp, most), t4);
     for (int c = g.s0; c < g.s1; ++c, grp += kGroupsOf) {
-      const XRaw<kDown> cur = next;
-      next = load_x<kDown>(xrow, valid, min(grp + kGroupsOf, groups - 1), t4);
-      if (!warp_wait_stage(full0 + 8u * st, ph)) ok = false;
+      uint32_t hi[8], lo[8], none[8];
+      b_fragments<false>(next, hi, none);
+      if (both) b_fragments<false>(low, lo, none);
+      next = load_x<false>(xrow, valid, min(grp + kGroupsOf, most), t4);
+      if (both) low = load_x<false>(xlow, valid, min(grp + kGroupsOf, most), t4);
+      ok = warp_wait_stage(full0 + 8u * st, ph);
+      if (!ok) break;
       const uint32_t at = base + st * kStageBytes;
-      if (ok && grp < groups)
-        group_math<kDown>(acc, at + ldm, cur, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
+      if (grp < groups) {
+        if (both)
+          group_products<kDown>(acc, at + ldm, hi, lo, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
+        else
+          group_products<false>(acc, at + ldm, hi, lo, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive_u32(empty0 + 8u * st);
       if (++st == kStages) {
@@ -451,8 +587,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2)
         ph ^= 1;
       }
     }
-    // the four warps' sums of each row, red[warp][column][row]
-    sync();
+    // the sums to the finisher, red[warp][column][row]
+    if (ok && k >= 2)
+      ok = __all_sync(0xffffffffu, mbar_wait_u32(red_empty0 + 8u * (k & 1), ((k >> 1) & 1) ^ 1));
+    if (!ok) break;
+    float *red = reinterpret_cast<float *>(smem + kRedOff + (k & 1) * kRedSize);
 #pragma unroll
     for (int rt = 0; rt < kTiles; ++rt) {
       float *p = red + (warp * kSlotRows + 2 * t4) * kRedPitch + rt * 16 + g8;
@@ -461,112 +600,48 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2)
       p[8] = acc[rt][2];
       p[kRedPitch + 8] = acc[rt][3];
     }
-    sync();
-    // this thread: rows r and r + 64 of columns q and q + 4
-    const int r = tid & 63, q = tid >> 6;
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float *p = red + (4 * (i & 1) * kSlotRows + q + 2 * (i & 2)) * kRedPitch + r;
-      v[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) v[i] += p[w * kSlotRows * kRedPitch];
-    }
-    if (g.s0 > 0 || g.s1 < stages) {
-      // a part of the tile: whoever comes last adds them all, in CTA order
-      float *part = a.ws.parts + (size_t)(2 * blockIdx.x + (g.s0 == 0 ? 1 : 0)) * kPartFloats;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) __stcg(part + i * kWarps * 32 + tid, v[i]);
-      __threadfence();
-      sync();
-      const long long t0 = (long long)g.tile * stages;
-      const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
-      if (tid == 0) {
-        const uint32_t old = atomicAdd(a.ws.tiles + g.tile, 1u);
-        __threadfence();
-        const bool last = old == (uint32_t)(c1 - c0);
-        if (last) a.ws.tiles[g.tile] = 0u;
-        *s_old = last;
-      }
-      sync();
-      if (!*s_old) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float *from = a.ws.parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats + tid;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __ldcg(from + i * kWarps * 32);
-      }
-    }
-    if constexpr (!kDown) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = q + 4 * i;
-        if (col < slot.n) {
-          const float gate = v[2 * i], up = v[2 * i + 1];
-          a.ws.h[(size_t)__ldcg(a.ws.order + slot.first + col) * N + g.n0 + r] =
-              gate / (1.f + expf(-gate)) * up;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = q + 4 * i;
-        if (col >= slot.n) continue;
-        const int p = __ldcg(a.ws.order + slot.first + col);
-        const float w = __ldcg(a.ws.weights + p);
-        float *d = a.ws.d + (size_t)p * N + g.n0 + r;
-        __stcg(d, w * v[2 * i]);
-        __stcg(d + 64, w * v[2 * i + 1]);
-      }
-      __threadfence();
-      sync();
-      const int column = g.n0 / kStep;
-      if (tid == 0) {
-        const uint32_t old = atomicAdd(a.ws.columns + column, 1u);
-        __threadfence();
-        const bool last = old == (uint32_t)(n_slots - 1);
-        if (last) a.ws.columns[column] = 0u;
-        *s_old = last;
-      }
-      sync();
-      if (!*s_old) continue;
-      // the rows' sums over their experts, in the order of choice: four columns a lane
-      const int n = g.n0 + 4 * lane;
-      {
-        for (int t = warp; t < a.rows; t += 2 * kWarps) {
-          float4 sum[2] = {};
-          for (int j0 = 0; j0 < a.top; j0 += 4) {
-            float4 x[2][4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[y][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (j0 + j < a.top && t + y * kWarps < a.rows)
-                  x[y][j] = __ldcg(reinterpret_cast<const float4 *>(
-                      a.ws.d + (size_t)((t + y * kWarps) * a.top + j0 + j) * N + n));
-              }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                sum[y].x += x[y][j].x;
-                sum[y].y += x[y][j].y;
-                sum[y].z += x[y][j].z;
-                sum[y].w += x[y][j].w;
-              }
-          }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_u32(red_full0 + 8u * (k & 1));
+  }
+  if constexpr (kDown) {
+    // the tiles of y at which this CTA came last: the rows' sums over their experts, in
+    // the order of choice, four columns a lane
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_u32(done, 0));
+    const int count = ok ? columns[0] : 0;
+    for (int i = 0; i < count; ++i) {
+      const int n = columns[1 + i] * kTileRows + 4 * lane;
+      for (int t = warp; t < a.rows; t += 2 * kWarps) {
+        float4 sum[2] = {};
+        for (int j0 = 0; j0 < a.top; j0 += 4) {
+          float4 x[2][4];
 #pragma unroll
           for (int y = 0; y < 2; ++y)
-            if (t + y * kWarps < a.rows) {
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[y].x, sum[y].y);
-              const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[y].z, sum[y].w);
-              *reinterpret_cast<uint2 *>(a.y + (size_t)(t + y * kWarps) * N + n) =
-                  make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                             *reinterpret_cast<const uint32_t *>(&hi));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[y][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (j0 + j < a.top && t + y * kWarps < a.rows)
+                x[y][j] = __ldcg(reinterpret_cast<const float4 *>(
+                    a.ws.d + (size_t)((t + y * kWarps) * a.top + j0 + j) * N + n));
+            }
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              sum[y].x += x[y][j].x;
+              sum[y].y += x[y][j].y;
+              sum[y].z += x[y][j].z;
+              sum[y].w += x[y][j].w;
             }
         }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (t + y * kWarps < a.rows) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[y].x, sum[y].y);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[y].z, sum[y].w);
+            *reinterpret_cast<uint2 *>(a.y + (size_t)(t + y * kWarps) * N + n) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                           *reinterpret_cast<const uint32_t *>(&hi));
+          }
       }
     }
   }
@@ -586,7 +661,7 @@ sv_status check_sizes(const char *who, int rows, int hidden, int inter, int expe
   if (hidden % 128 || inter % 128)
     return fail(SV_ERR_UNSUPPORTED, "%s: hidden and inter must be multiples of 128 (%d, %d)", who,
                 hidden, inter);
-  if (hidden > 65536 || inter > 65536 || (long long)experts * std::max(hidden, inter) > (1ll << 30))
+  if (hidden > kMostColumns * kTileRows || inter > 65536 || (long long)experts * std::max(hidden, inter) > (1ll << 30))
     return fail(SV_ERR_UNSUPPORTED, "%s: sizes too large", who);
   return SV_OK;
 }
@@ -717,11 +792,11 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   cfg.attrs = &early;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   cfg.gridDim = dim3((experts + kRouteExperts - 1) / kRouteExperts, (rows + kRouteTile - 1) / kRouteTile);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kRouteThreads);
   cudaError_t le = cudaLaunchKernelEx(&cfg, moe_route_kernel, a);
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3((kWarps + 1) * 32);
+  cfg.blockDim = dim3(kMoeThreads);
   cfg.dynamicSmemBytes = kMoeSmem;
   if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<false>, gate_map, up_map, a);
   if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<true>, down_map, down_map, a);
