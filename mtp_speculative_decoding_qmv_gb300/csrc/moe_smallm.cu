@@ -9,25 +9,34 @@
 // experts' weights (0.5625 bytes each) and is bound by memory.  Three launches,
 // the later two starting as the one before drains:
 //  * route: 8 experts a CTA, K over its warps, bf16 MMAs (exact products, fp32
-//    sums); the last CTA of 16 rows chooses their experts, the last of all sorts
+//    sums), and the rows of x in the products' form; the last CTA of 16 rows chooses their experts, the last of all sorts
 //    the (row, expert) pairs by expert and cuts each expert's rows into slots of
 //    up to 8, the columns of one MMA;
 //  * gate and up, then down: the stages of all slots' tiles laid out flat and cut
 //    evenly over the resident CTAs, so every SM streams the same number of bytes
 //    whichever experts were chosen.  A stage is 128 weight rows x 256 inputs: 64
 //    rows of gate and the same 64 of up (their product leaves in one place), or
-//    128 of down.  Four 64-groups x two blocks of 64 rows make a stage's work for
-//    eight warps, each as in qmv_smallm.  A producer warp keeps the ring of stages
-//    full across tiles, and a warp of its own takes the sums of a finished tile, so
-//    that neither the copies nor the products wait for the fences below.  A tile cut
-//    between CTAs leaves partial sums, which whichever CTA comes last adds in CTA
-//    order; nobody waits for another CTA, so the launches need not be resident
-//    together.
-// The activations between the products are kept as two bf16 parts (2^-16 of their
-// sum).  As operands of down the parts of up to four rows share one MMA's eight
-// columns; five to eight rows take two MMAs.
+//    128 of down, with the rows' activations.  Eight warps take 32 rows by half of
+//    the inputs each.  A producer warp keeps the ring of stages full across tiles, and a warp of its
+//    own takes the sums of a finished tile, so that neither the copies nor the
+//    products wait for the fences below.  A tile cut between CTAs leaves partial
+//    sums, which whichever CTA comes last adds in CTA order; nobody waits for
+//    another CTA, so the launches need not be resident together.
+//
+// The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
+// the odd ones, left where they are, as 1024 + 16 q against activations divided by
+// 16: five integer operations a word of eight, where bf16 (128 + q, every nibble
+// shifted down) takes seven, and these operations are what the products are bound by.
+// The activations become fp16 once, before they are multiplied: per row and group of
+// 64 scaled by a power of two that brings the largest to 2^14 .. 2^15, which loses
+// nothing of a bf16 value down to 2^-28 of it.  Beside them lie the scale, what the
+// 1024s contribute (the sums start from its negative) and the group's sum, for the
+// bias.  The activations between the products are two such parts (2^-22).  As
+// operands of down the parts of up to four rows share one MMA's eight columns; five
+// to eight rows take two MMAs.
+#include <cuda_fp16.h>
+
 #include <algorithm>
-#include <atomic>
 
 #include "qmv_common.cuh"
 
@@ -42,18 +51,29 @@ constexpr int kStageK = 256;       // inputs of a stage
 constexpr int kGroupsOf = kStageK / 64;
 constexpr int kWarps = 8;          // that multiply; then the producer, then the finisher
 constexpr int kMoeThreads = (kWarps + 2) * 32;
-constexpr uint32_t kSb = 2 * kRows * 128;                   // scales, then biases
-constexpr uint32_t kSbBytes = kTileRows * kGroupsOf * 2;    // [128 rows][4 groups] bf16
-constexpr uint32_t kStageBytes = (kSb + 2 * kSbBytes + 1023) / 1024 * 1024;
-constexpr int kStages = 4;
-constexpr int kRedPitch = 68;      // floats: conflict-free both ways
-constexpr uint32_t kRedOff = kStages * kStageBytes;
-constexpr uint32_t kRedSize = kWarps * kSlotRows * kRedPitch * 4;  // two of them
+// A row's activations of a stage: four groups of 64 fp16, then a Group each.
+struct Group {
+  float f, start, sum, pad;  // 1 / scale; minus the 1024s' part; the inputs' sum
+};
+constexpr uint32_t kRecord = kGroupsOf * (128 + (uint32_t)sizeof(Group));  // 576
+constexpr uint32_t kSb = 2 * kRows * 128;                // [128 rows][4 scales, 4 biases]
+constexpr uint32_t kXOff = kSb + kTileRows * kGroupsOf * 4;
+template <bool kDown>
+struct Ring {  // down: the two parts of eight rows
+  static constexpr int kStages = kDown ? 3 : 4, kRecords = kDown ? 16 : 8;
+  static constexpr uint32_t kStage = (kXOff + kRecords * kRecord + 1023) / 1024 * 1024;
+  static constexpr uint32_t kRedOff = kStages * kStage;
+};
+constexpr int kRedPitch = kTileRows + 4;  // floats: conflict-free both ways
+constexpr uint32_t kRedPlane = kSlotRows * kRedPitch;      // floats: a half of the inputs
+constexpr uint32_t kRedSize = 2 * kRedPlane * 4;           // two of them
 constexpr int kMostColumns = 128;  // tiles of y that a CTA may come last at
-constexpr uint32_t kColumnsOff = kRedOff + 2 * kRedSize;  // their number, then they
-constexpr uint32_t kBarOff = kColumnsOff + (kMostColumns + 2) * 4;
-constexpr int kBarsOf = 2 * kStages + 5;
-constexpr uint32_t kMoeSmem = kBarOff + kBarsOf * 8 + 1024;
+template <bool kDown>
+struct Smem {
+  static constexpr uint32_t kColumnsOff = Ring<kDown>::kRedOff + 2 * kRedSize;  // number, then they
+  static constexpr uint32_t kBarOff = kColumnsOff + (kMostColumns + 2) * 4;
+  static constexpr uint32_t kTotal = kBarOff + (2 * Ring<kDown>::kStages + 5) * 8 + 1024;
+};
 constexpr int kPartFloats = kTileRows * kSlotRows;
 
 __device__ unsigned int g_moe_device_error;
@@ -73,7 +93,8 @@ struct Space {
   int32_t *order;     // the pairs row * top + j by expert
   int32_t *n_slots;
   Slot *slots;
-  uint16_t *h;        // [2][pairs][inter]: the first bf16 part, the second
+  uint8_t *x;         // [rows][stages of gate and up] records
+  uint8_t *h;         // [2][pairs][stages of down] records: the first parts, the second
   float *d;           // [pairs][hidden]
   float *parts;       // [CTAs][2][kPartFloats]
   size_t counters, total;  // bytes
@@ -102,7 +123,8 @@ Space space_of(void *base, int rows, int hidden, int inter, int experts, int top
   take(s.order, pairs);
   take(s.n_slots, 1);
   take(s.slots, slots);
-  take(s.h, 2 * pairs * inter);
+  take(s.x, (size_t)rows * ((hidden + kStageK - 1) / kStageK) * kRecord);
+  take(s.h, 2 * pairs * ((inter + kStageK - 1) / kStageK) * kRecord);
   take(s.d, pairs * hidden);
   take(s.parts, (size_t)ctas * 2 * kPartFloats);
   s.total = at;
@@ -118,6 +140,42 @@ struct MoeArgs {
   Space ws;
   int rows, hidden, inter, experts, top, renormalize;
 };
+
+// ---- activations in the products' form ----------------------------------------------
+// A group's 64 inputs, two a lane (2 lane and 2 lane + 1), to its place in a record:
+// scaled, the odd ones of each word of eight divided by 16, a word's in the order 0 4 1
+// 5 2 6 3 7 of the widened nibbles.  kParts 2: what the fp16 values leave goes to the
+// record `low` bytes further, the same way.  By a whole warp.
+template <int kParts>
+__device__ __forceinline__ void put_group(uint8_t *record, size_t low, int group, float2 v) {
+  const int lane = threadIdx.x & 31;
+  auto finite = [](float x) {
+    const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+    return u < 0x7f800000u ? u : 0u;
+  };
+  const uint32_t most = __reduce_max_sync(0xffffffffu, max(finite(v.x), finite(v.y)));
+  const int e = min(14 - ((int)(most >> 23) - 127), 126);
+  const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  float2 rest = make_float2(v.x * scale, v.y * scale);
+  // inputs 2 i and 2 i + 1 of a word: places i < 2: 4 i and 4 i + 2, else 4 i - 7 and 4 i - 5
+  const int i = lane & 3, place = i < 2 ? 4 * i : 4 * i - 7;
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) {
+    uint8_t *to = record + part * low;
+    const __half a = __float2half_rn(rest.x), b = __float2half_rn(rest.y * 0.0625f);
+    const float fa = __half2float(a), fb = __half2float(b);
+    __half *h = reinterpret_cast<__half *>(to + (group & 3) * 128) + (lane >> 2) * 8 + place;
+    h[0] = a;
+    h[2] = b;
+    const float sum = warp_sum(fa + 16.f * fb), start = warp_sum(fa + fb);
+    if (lane == 0)
+      *reinterpret_cast<float4 *>(to + kGroupsOf * 128 + (group & 3) * sizeof(Group)) =
+          make_float4(f, -1024.f * start, f * sum, 0.f);
+    rest.x -= fa;
+    rest.y -= 16.f * fb;
+  }
+}
 
 // ---- router ---------------------------------------------------------------------
 constexpr int kRouteTile = 16;     // rows of x
@@ -240,6 +298,15 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const MoeArgs 
   pdl_launch_dependents();
   *reinterpret_cast<uint4 *>(bits[tid]) = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
+  // this CTA's share of the rows' groups
+  if (t0 + warp < a.rows) {
+    const int t = t0 + warp, records = (a.hidden + kStageK - 1) / kStageK;
+    for (int g = blockIdx.x; g < a.hidden / 64; g += gridDim.x) {
+      const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(a.x + (size_t)t * a.hidden + 64 * g) + lane);
+      put_group<1>(a.ws.x + ((size_t)t * records + g / kGroupsOf) * kRecord, 0, g,
+                   make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)));
+    }
+  }
   // A: 16 rows of x, B: 8 experts.  A lane's 16 bytes are 8 inputs of a block of
   // 32, in the same places of both, so their order within the block does not matter.
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -305,7 +372,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const MoeArgs 
 
 // ---- the experts' products ---------------------------------------------------------
 template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t dst, const uint16_t *src) {
+__device__ __forceinline__ void copy_small(uint32_t dst, const uint8_t *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
 // (no eviction hint: an expert with more than 8 rows has its weights read again)
@@ -315,6 +382,51 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void load_record(uint32_t dst, const uint8_t *src, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(kRecord), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+// A group's products of 16 weight rows (w: ldmatrix of words t and 4 + t of rows g8 and
+// g8 + 8) with the rows of x in fragments x[2], added to d; kParts 2: with low as well.
+template <int kParts>
+__device__ __forceinline__ void group_f16(float (&d)[4], const uint32_t (&w)[4], const uint4 (&x)[2],
+                                          const uint4 (&low)[2]) {
+  constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u, k1024 = 0x64006400u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = w[2 * i], b = w[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
+    const uint32_t a0 = and_or(a, kEven, k1024), a1 = and_or(b, kEven, k1024),
+                   a2 = and_or(a, kOdd, k1024), a3 = and_or(b, kOdd, k1024);
+    mma_f16(d, a0, a1, a2, a3, x[i].x, x[i].y);
+    if constexpr (kParts == 2) mma_f16(d, a0, a1, a2, a3, low[i].x, low[i].y);
+    const uint32_t c0 = and_or(a8, kEven, k1024), c1 = and_or(b8, kEven, k1024),
+                   c2 = and_or(a8, kOdd, k1024), c3 = and_or(b8, kOdd, k1024);
+    mma_f16(d, c0, c1, c2, c3, x[i].z, x[i].w);
+    if constexpr (kParts == 2) mma_f16(d, c0, c1, c2, c3, low[i].z, low[i].w);
+  }
 }
 
 // kDown false: h = silu(gate x) * (up x) of every slot; true: d = weight * (down h),
@@ -327,10 +439,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw);
-  const uint32_t full0 = base + kBarOff, empty0 = full0 + 8 * kStages;
+  using R = Ring<kDown>;
+  using S = Smem<kDown>;
+  constexpr int kStages = R::kStages;
+  const uint32_t full0 = base + S::kBarOff, empty0 = full0 + 8 * kStages;
   const uint32_t red_full0 = empty0 + 8 * kStages, red_empty0 = red_full0 + 16;
   const uint32_t done = red_empty0 + 16;
-  volatile int *columns = reinterpret_cast<volatile int *>(smem + kColumnsOff);
+  volatile int *columns = reinterpret_cast<volatile int *>(smem + S::kColumnsOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -373,46 +488,81 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   };
 
   if (warp == kWarps) {
-    // ---- producer: weights by tensor copies, scales and biases by small ones -----
-    const uint16_t *s0p = kDown ? a.down_s : a.gate_s, *b0p = kDown ? a.down_b : a.gate_b;
-    const uint16_t *s1p = kDown ? a.down_s : a.up_s, *b1p = kDown ? a.down_b : a.up_b;
+    // ---- producer: weights by tensor copies, records by bulk copies, scales and
+    // biases, a row's few bytes at a time, by small ones ------------------------------
     const bool wide = groups % 4 == 0;
     int st = 0, ph = 0, issued = 0;
     bool ok = true;
+    // down's first stages begin with their weights: the records are the launch
+    // before's, and follow once it has ended
+    bool waited = !kDown;
+    const uint8_t *pending[kStages];
+    auto bring_pending = [&] {
+      pdl_wait();
+      waited = true;
+#pragma unroll
+      for (int i = 0; i < kStages; ++i)
+        if (i < issued && pending[i])
+          load_record(base + i * R::kStage + kXOff + lane * kRecord, pending[i], full0 + 8u * i);
+    };
     for (long long u = u_begin; ok && u < u_end;) {
       const Segment g = segment(u);
       u += g.s1 - g.s0;
       const long long row0 = (long long)__ldcg(&a.ws.slots[g.slot].expert) * N + g.n0;
+      // lane r brings record r: of row r, or of down's two parts r < n and the rest,
+      // from place 4 on (up to four rows) or 8
+      const int n = __ldcg(&a.ws.slots[g.slot].n), apart = n <= 4 ? 4 : 8;
+      const int col = kDown ? lane % apart : lane;
+      const bool brings = col < n && lane < (kDown ? 2 * apart : kSlotRows);
+      const int pair = brings ? __ldcg(a.ws.order + __ldcg(&a.ws.slots[g.slot].first) + col) : 0;
+      const uint8_t *from =
+          kDown ? a.ws.h + ((size_t)pair + (lane >= apart ? pairs : 0)) * stages * kRecord
+                : a.ws.x + (size_t)(pair / a.top) * stages * kRecord;
+      const uint8_t *sp[4], *bp[4];  // of rows lane + 32 i of the stage
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long off = ((row0 + (kDown ? 32 * i : 32 * (i & 1)) + lane) * groups + g.s0 * kGroupsOf) * 2;
+        sp[i] = reinterpret_cast<const uint8_t *>(kDown ? a.down_s : i < 2 ? a.gate_s : a.up_s) + off;
+        bp[i] = reinterpret_cast<const uint8_t *>(kDown ? a.down_b : i < 2 ? a.gate_b : a.up_b) + off;
+      }
+      const uint32_t bytes = 2 * kRows * 128 + (kDown ? 2 : 1) * n * kRecord;
       for (int c = g.s0; c < g.s1; ++c) {
+        if (!waited && issued == kStages) bring_pending();
         if (issued >= kStages)
           ok = __all_sync(0xffffffffu, mbar_wait_u32(empty0 + 8u * st, ph ^ 1));
         if (!ok) break;
-        const uint32_t at = base + st * kStageBytes, full = full0 + 8u * st;
+        const uint32_t at = base + st * R::kStage, full = full0 + 8u * st;
         if (lane == 0) {
-          mbar_arrive_expect_tx_u32(full, 2 * kRows * 128);
+          mbar_arrive_expect_tx_u32(full, bytes);
           const int x = c * (kStageK / 8);
           load_box(at, &map0, x, (int)row0, full);
           load_box(at + kRows * 128, &map1, x, (int)row0 + (kDown ? kRows : 0), full);
         }
-        const uint32_t sb = at + kSb;
+        __syncwarp();
+        const uint8_t *record = brings ? from + (size_t)c * kRecord : nullptr;
+        if (waited) {
+          if (record) load_record(at + kXOff + lane * kRecord, record, full);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kTileRows / 32; ++i) {
-          const int r = lane + 32 * i;                       // row of the stage
-          const int n = kDown || r < kRows ? r : r - kRows;  // row of its matrix, from n0
-          const long long off = (row0 + n) * groups + c * kGroupsOf;
-          const uint16_t *sp = (!kDown && r >= kRows ? s1p : s0p) + off;
-          const uint16_t *bp = (!kDown && r >= kRows ? b1p : b0p) + off;
+          for (int i = 0; i < kStages; ++i)
+            if (i == issued) pending[i] = record;
+        }
+        const uint32_t sb = at + kSb + lane * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           if (wide) {
-            copy_small<8>(sb + r * 8, sp);
-            copy_small<8>(sb + kSbBytes + r * 8, bp);
+            copy_small<8>(sb + i * 512, sp[i]);
+            copy_small<8>(sb + i * 512 + 8, bp[i]);
           } else {  // an even number of groups, the last stage's two
-            copy_small<4>(sb + r * 8, sp);
-            copy_small<4>(sb + kSbBytes + r * 8, bp);
+            copy_small<4>(sb + i * 512, sp[i]);
+            copy_small<4>(sb + i * 512 + 8, bp[i]);
             if (c * kGroupsOf + 2 < groups) {
-              copy_small<4>(sb + r * 8 + 4, sp + 2);
-              copy_small<4>(sb + kSbBytes + r * 8 + 4, bp + 2);
+              copy_small<4>(sb + i * 512 + 4, sp[i] + 4);
+              copy_small<4>(sb + i * 512 + 12, bp[i] + 4);
             }
           }
+          sp[i] += 8;
+          bp[i] += 8;
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full) : "memory");
         ++issued;
@@ -422,6 +572,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         }
       }
     }
+    if (!waited) bring_pending();
     if (!ok) {
       if (lane == 0) atomicOr(&g_moe_device_error, 1u);
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -447,12 +598,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       auto emit = [&](int col, float2 v0, float2 v1) {
         const int p = __ldcg(a.ws.order + first + col);
         if constexpr (!kDown) {
-          const float h0 = v0.x / (1.f + expf(-v0.x)) * v1.x, h1 = v0.y / (1.f + expf(-v0.y)) * v1.y;
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(h0, h1);
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(h0 - __low2float(hi), h1 - __high2float(hi));
-          uint16_t *h = a.ws.h + (size_t)p * N + g.n0 + 2 * lane;
-          *reinterpret_cast<uint32_t *>(h) = *reinterpret_cast<const uint32_t *>(&hi);
-          *reinterpret_cast<uint32_t *>(h + (size_t)pairs * N) = *reinterpret_cast<const uint32_t *>(&lo);
+          // a tile's 64 rows are one of down's groups
+          const float2 h = make_float2(v0.x / (1.f + expf(-v0.x)) * v1.x, v0.y / (1.f + expf(-v0.y)) * v1.y);
+          const int group = g.n0 / 64, records = (N + kStageK - 1) / kStageK;
+          put_group<2>(a.ws.h + ((size_t)p * records + group / kGroupsOf) * kRecord,
+                       (size_t)pairs * records * kRecord, group, h);
         } else {
           const float w = __ldcg(a.ws.weights + p);
           float *d = a.ws.d + (size_t)p * N + g.n0 + 2 * lane;
@@ -462,22 +612,19 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       };
       ok = __all_sync(0xffffffffu, mbar_wait_u32(red_full0 + 8u * (k & 1), (k >> 1) & 1));
       if (!ok) break;
-      const float *red = reinterpret_cast<const float *>(smem + kRedOff + (k & 1) * kRedSize) + 2 * lane;
+      const float *red = reinterpret_cast<const float *>(smem + R::kRedOff + (k & 1) * kRedSize) + 2 * lane;
       for (int col = 0; col < n; ++col) {
         float2 v[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           v[x] = make_float2(0.f, 0.f);
-          for (int y = col; y < kSlotRows; y += 4) {
+          for (int y = col; y < (doubled ? kSlotRows : col + 1); y += 4)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 f = *reinterpret_cast<const float2 *>(
-                  red + ((4 * x + w) * kSlotRows + y) * kRedPitch);
+            for (int plane = 0; plane < 2; ++plane) {
+              const float2 f = *reinterpret_cast<const float2 *>(red + plane * kRedPlane + y * kRedPitch + x * kRows);
               v[x].x += f.x;
               v[x].y += f.y;
             }
-            if (!doubled) break;
-          }
         }
         if (whole) {
           emit(col, v[0], v[1]);
@@ -541,44 +688,81 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   }
 
   // ---- the products ----------------------------------------------------------------
-  const int g8 = lane >> 2, t4 = lane & 3;
-  const uint32_t ldm = ldmatrix_offset(warp, lane);
-  const uint32_t sb_off = kSb + (uint32_t)(((warp >> 2) * kRows + g8) * 8 + (warp & 3) * 2);
-  if (kDown) pdl_wait();  // h is the launch before's
+  // Warp w: rows 32 (w % 4) .. of the stage and half w / 4 of its inputs.  Lane (g8, t4):
+  // weight rows g8 + 8 i; of the activations column (row) g8; of the sums columns 2 t4
+  // and 2 t4 + 1.
+  const int g8 = lane >> 2, t4 = lane & 3, rows0 = 32 * (warp & 3), half = warp >> 2;
+  const uint32_t w_at = (uint32_t)(rows0 + (lane & 15)) * 128;  // the second box follows the first
+  if (kDown) pdl_wait();  // the partials' places are the launch before's
   int st = 0, ph = 0, k = 0;
   bool ok = true;
   for (long long u = u_begin; ok && u < u_end; ++k) {
     const Segment g = segment(u);
     u += g.s1 - g.s0;
-    const int first = __ldcg(&a.ws.slots[g.slot].first), n = __ldcg(&a.ws.slots[g.slot].n);
+    const int n = __ldcg(&a.ws.slots[g.slot].n);
     const bool both = kDown && n > 4;  // a column a row, its two parts one after the other
-    const int col = kDown && !both ? g8 & 3 : g8;
-    const bool valid = col < n;
-    const int pair = valid ? __ldcg(a.ws.order + first + col) : 0;
-    const uint16_t *xrow = kDown ? a.ws.h + ((size_t)pair + (!both && g8 >= 4 ? pairs : 0)) * K
-                                 : reinterpret_cast<const uint16_t *>(a.x) + (size_t)(pair / a.top) * K;
-    const uint16_t *xlow = kDown ? xrow + (size_t)pairs * K : nullptr;
-    float acc[kTiles][4];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    int grp = g.s0 * kGroupsOf + (warp & 3);
-    const int most = groups - 1;
-    XRaw<false> next = load_x<false>(xrow, valid, min(grp, most), t4), low = {};
-    if (both) low = load_x<false>(xlow, valid, min(grp, most), t4);
-    for (int c = g.s0; c < g.s1; ++c, grp += kGroupsOf) {
-      uint32_t hi[8], lo[8], none[8];
-      b_fragments<false>(next, hi, none);
-      if (both) b_fragments<false>(low, lo, none);
-      next = load_x<false>(xrow, valid, min(grp + kGroupsOf, most), t4);
-      if (both) low = load_x<false>(xlow, valid, min(grp + kGroupsOf, most), t4);
+    const int apart = kDown && !both ? 4 : kSlotRows;
+    const bool valid = g8 % apart < n, real[2] = {2 * t4 % apart < n, (2 * t4 + 1) % apart < n};
+    float acc[2][4] = {};
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int c = g.s0; c < g.s1; ++c) {
       ok = warp_wait_stage(full0 + 8u * st, ph);
       if (!ok) break;
-      const uint32_t at = base + st * kStageBytes;
-      if (grp < groups) {
-        if (both)
-          group_products<kDown>(acc, at + ldm, hi, lo, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
-        else
-          group_products<false>(acc, at + ldm, hi, lo, at + sb_off, 16 * 8, 8 * 8, kSbBytes);
+      const uint32_t at = base + st * R::kStage;
+      const uint32_t sb_at = at + kSb + (uint32_t)(rows0 + g8) * 16 + half * 4;
+      const uint32_t x_at = at + kXOff + g8 * kRecord + half * 256 + t4 * 16;
+      const uint32_t group_at =
+          at + kXOff + 2 * t4 * kRecord + kGroupsOf * 128 + half * 2 * (uint32_t)sizeof(Group);
+      if (c * kGroupsOf + 2 * half < groups) {
+        uint32_t sw[4], bw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sw[i] = lds32(sb_at + i * 8 * 16);
+          bw[i] = lds32(sb_at + i * 8 * 16 + 8);
+        }
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+          uint32_t w[2][4];
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile)
+            ldmatrix_x4(w[tile], at + w_at + tile * 16 * 128 +
+                                     (((4 * half + 2 * gi + (lane >> 4)) ^ (lane & 7)) << 4));
+          uint4 x[2], low[2];
+          x[0] = valid ? lds128(x_at + gi * 128) : zero;
+          x[1] = valid ? lds128(x_at + gi * 128 + 64) : zero;
+          const uint4 r0 = real[0] ? lds128(group_at + gi * 16) : zero;
+          const uint4 r1 = real[1] ? lds128(group_at + kRecord + gi * 16) : zero;
+          float start0 = __uint_as_float(r0.y), start1 = __uint_as_float(r1.y);
+          float sum0 = __uint_as_float(r0.z), sum1 = __uint_as_float(r1.z);
+          if (both) {
+            low[0] = valid ? lds128(x_at + kSlotRows * kRecord + gi * 128) : zero;
+            low[1] = valid ? lds128(x_at + kSlotRows * kRecord + gi * 128 + 64) : zero;
+            const uint4 q0 = real[0] ? lds128(group_at + kSlotRows * kRecord + gi * 16) : zero;
+            const uint4 q1 = real[1] ? lds128(group_at + (kSlotRows + 1) * kRecord + gi * 16) : zero;
+            start0 += __uint_as_float(q0.y);
+            start1 += __uint_as_float(q1.y);
+            sum0 += __uint_as_float(q0.z);
+            sum1 += __uint_as_float(q1.z);
+          }
+          const float f0 = __uint_as_float(r0.x), f1 = __uint_as_float(r1.x);
+          auto of = [&](uint32_t word) {
+            return __uint_as_float(gi ? word & 0xFFFF0000u : word << 16);
+          };
+#pragma unroll
+          for (int tile = 0; tile < 2; ++tile) {
+            float d[4] = {start0, start1, start0, start1};
+            if (both)
+              group_f16<2>(d, w[tile], x, low);
+            else
+              group_f16<1>(d, w[tile], x, x);
+            const float s0 = of(sw[2 * tile]), s8 = of(sw[2 * tile + 1]);
+            const float b0 = of(bw[2 * tile]), b8 = of(bw[2 * tile + 1]);
+            acc[tile][0] = fmaf(s0, f0 * d[0], fmaf(b0, sum0, acc[tile][0]));
+            acc[tile][1] = fmaf(s0, f1 * d[1], fmaf(b0, sum1, acc[tile][1]));
+            acc[tile][2] = fmaf(s8, f0 * d[2], fmaf(b8, sum0, acc[tile][2]));
+            acc[tile][3] = fmaf(s8, f1 * d[3], fmaf(b8, sum1, acc[tile][3]));
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_u32(empty0 + 8u * st);
@@ -587,18 +771,18 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         ph ^= 1;
       }
     }
-    // the sums to the finisher, red[warp][column][row]
+    // the sums to the finisher, red[half][column][row]
     if (ok && k >= 2)
       ok = __all_sync(0xffffffffu, mbar_wait_u32(red_empty0 + 8u * (k & 1), ((k >> 1) & 1) ^ 1));
     if (!ok) break;
-    float *red = reinterpret_cast<float *>(smem + kRedOff + (k & 1) * kRedSize);
+    float *red = reinterpret_cast<float *>(smem + R::kRedOff + (k & 1) * kRedSize) + half * kRedPlane +
+                 2 * t4 * kRedPitch + rows0 + g8;
 #pragma unroll
-    for (int rt = 0; rt < kTiles; ++rt) {
-      float *p = red + (warp * kSlotRows + 2 * t4) * kRedPitch + rt * 16 + g8;
-      p[0] = acc[rt][0];
-      p[kRedPitch] = acc[rt][1];
-      p[8] = acc[rt][2];
-      p[kRedPitch + 8] = acc[rt][3];
+    for (int tile = 0; tile < 2; ++tile) {
+      red[16 * tile] = acc[tile][0];
+      red[16 * tile + kRedPitch] = acc[tile][1];
+      red[16 * tile + 8] = acc[tile][2];
+      red[16 * tile + 8 + kRedPitch] = acc[tile][3];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive_u32(red_full0 + 8u * (k & 1));
@@ -748,11 +932,11 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   static PerDeviceOnce once;
   const cudaError_t e = once.run([] {
     const cudaError_t x = cudaFuncSetAttribute(
-        moe_experts_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMoeSmem);
+        moe_experts_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<false>::kTotal);
     return x != cudaSuccess ? x
                             : cudaFuncSetAttribute(moe_experts_kernel<true>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)kMoeSmem);
+                                                   (int)Smem<true>::kTotal);
   });
   if (e != cudaSuccess)
     return fail(SV_ERR_CUDA, "%s: cudaFuncSetAttribute failed: %s", who, cudaGetErrorString(e));
@@ -797,8 +981,9 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kMoeThreads);
-  cfg.dynamicSmemBytes = kMoeSmem;
+  cfg.dynamicSmemBytes = Smem<false>::kTotal;
   if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<false>, gate_map, up_map, a);
+  cfg.dynamicSmemBytes = Smem<true>::kTotal;
   if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<true>, down_map, down_map, a);
   if (le != cudaSuccess) {
     (void)cudaGetLastError();

@@ -176,14 +176,15 @@ __device__ __forceinline__ void b_fragments(const XRaw<kXF32> &r, uint32_t (&hi)
 
 // One 64-group of one stage for the four 16-row tiles of a CTA:
 //   acc[rt] += s * D + (b - 128 s) * sum(x)
-// for B fragments of x = hi (+ lo).  `wbase` is the lane's ldmatrix address in the
-// stage for tile 0; the lane's scale of row g8 of tile rt is at sb + rt * sb_rt, of
-// row g8+8 at + sb_r8, and the biases at + sb_b.
-template <bool kLo>
-__device__ __forceinline__ void group_products(float (&acc)[kTiles][4], uint32_t wbase,
-                                               const uint32_t (&hi)[8], const uint32_t (&lo)[8],
-                                               uint32_t sb, uint32_t sb_rt, uint32_t sb_r8,
-                                               uint32_t sb_b) {
+// `wbase` is the lane's ldmatrix address in the stage for tile 0; the
+// lane's scale of row g8 of tile rt is at sb + rt * sb_rt, of row g8+8 at
+// + sb_r8, and the biases at + sb_b.
+template <bool kXF32>
+__device__ __forceinline__ void group_math(float (&acc)[kTiles][4], uint32_t wbase,
+                                           const XRaw<kXF32> &xcur, uint32_t sb, uint32_t sb_rt,
+                                           uint32_t sb_r8, uint32_t sb_b) {
+  uint32_t hi[8], lo[8];
+  b_fragments<kXF32>(xcur, hi, lo);
   // words t, 4+t of the group for rows g8 and g8+8 of each MMA tile
   uint32_t w[kTiles][4];
 #pragma unroll
@@ -201,7 +202,7 @@ __device__ __forceinline__ void group_products(float (&acc)[kTiles][4], uint32_t
       mma_bf16_zero(xs, kBf16One2, kBf16One2, kBf16One2, kBf16One2, b0, b1);
     else
       mma_bf16_m16n8k16(xs, kBf16One2, kBf16One2, kBf16One2, kBf16One2, b0, b1);
-    if constexpr (kLo)
+    if constexpr (kXF32)
       mma_bf16_m16n8k16(xs, kBf16One2, kBf16One2, kBf16One2, kBf16One2, lo[2 * ks],
                         lo[2 * ks + 1]);
 #pragma unroll
@@ -215,7 +216,7 @@ __device__ __forceinline__ void group_products(float (&acc)[kTiles][4], uint32_t
         mma_bf16_zero(d[rt], p0, p0r8, p1, p1r8, b0, b1);
       else
         mma_bf16_m16n8k16(d[rt], p0, p0r8, p1, p1r8, b0, b1);
-      if constexpr (kLo)
+      if constexpr (kXF32)
         mma_bf16_m16n8k16(d[rt], p0, p0r8, p1, p1r8, lo[2 * ks], lo[2 * ks + 1]);
     }
   }
@@ -231,15 +232,6 @@ __device__ __forceinline__ void group_products(float (&acc)[kTiles][4], uint32_t
     acc[rt][2] = fmaf(s1, d[rt][2], fmaf(c1, xs[0], acc[rt][2]));
     acc[rt][3] = fmaf(s1, d[rt][3], fmaf(c1, xs[1], acc[rt][3]));
   }
-}
-
-template <bool kXF32>
-__device__ __forceinline__ void group_math(float (&acc)[kTiles][4], uint32_t wbase,
-                                           const XRaw<kXF32> &xcur, uint32_t sb, uint32_t sb_rt,
-                                           uint32_t sb_r8, uint32_t sb_b) {
-  uint32_t hi[8], lo[8];
-  b_fragments<kXF32>(xcur, hi, lo);
-  group_products<kXF32>(acc, wbase, hi, lo, sb, sb_rt, sb_r8, sb_b);
 }
 
 // Sixteen activation rows (M = 9..16): the same per-group math with two
