@@ -335,13 +335,13 @@ sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint1
  * split into two bf16 parts as qmv_smallm does with fp32 x.  A row depends on no
  * other row up to the order of its fp32 sums, and results do not depend on the run.
  * Requires 0 <= rows <= 128 (0: no-op), 1 <= top_k <= 16, top_k <= experts <= 512,
- * hidden (at most 16384) and inter (at most 65536) multiples of 128; x, router and the w_packed 16-byte, scales and
- * biases 8-byte, y 8-byte aligned; no output overlaps an input or another output.
+ * hidden and inter multiples of 128, at most 65536; x, router, w_packed, scales
+ * and biases 16-byte, y 8-byte aligned; no output overlaps an input or another output.
  * workspace: moe_smallm_workspace_bytes(..) bytes on the current device (0 on
  * invalid input; *zero_bytes, when given, is how many of the first are arrival
  * counters: zero before its first call, every call leaves them zero), 256-byte
  * aligned; it belongs to these sizes, and calls that run concurrently need
- * workspaces of their own.  Three launches on `stream`, the second and third with a
+ * workspaces of their own.  Four launches on `stream`, all but the first with a
  * programmatic dependency on the one before.  A kernel wait that gives up sets a
  * word read by sv_device_status; the counters are then undefined. */
 size_t moe_smallm_workspace_bytes(int rows, int hidden, int inter, int experts, int top_k,

@@ -6,8 +6,8 @@
 //   y = sum_j w_j down_ej(silu(gate_ej x) * up_ej x)
 //
 // A few rows meet most of their experts once, so the layer streams the chosen
-// experts' weights (0.5625 bytes each) and is bound by memory.  Three launches,
-// the later two starting as the one before drains:
+// experts' weights (0.5625 bytes each) and is bound by memory.  Four launches,
+// the later ones starting as the one before drains:
 //  * route: 8 experts a CTA, K over its warps, bf16 MMAs (exact products, fp32
 //    sums), and the rows of x in the products' form; the last CTA of 16 rows chooses their experts, the last of all sorts
 //    the (row, expert) pairs by expert and cuts each expert's rows into slots of
@@ -56,23 +56,25 @@ struct Group {
   float f, start, sum, pad;  // 1 / scale; minus the 1024s' part; the inputs' sum
 };
 constexpr uint32_t kRecord = kGroupsOf * (128 + (uint32_t)sizeof(Group));  // 576
-constexpr uint32_t kSb = 2 * kRows * 128;                // [128 rows][4 scales, 4 biases]
-constexpr uint32_t kXOff = kSb + kTileRows * kGroupsOf * 4;
+constexpr uint32_t kXOff = 2 * kRows * 128;
+// Scales, then biases, of a block of two stages: [128 rows][8 groups] bf16.
+constexpr int kBlock = 2;
+constexpr uint32_t kSbRow = kBlock * kGroupsOf * 2, kSbBytes = kTileRows * kSbRow;
 template <bool kDown>
 struct Ring {  // down: the two parts of eight rows
   static constexpr int kStages = kDown ? 3 : 4, kRecords = kDown ? 16 : 8;
   static constexpr uint32_t kStage = (kXOff + kRecords * kRecord + 1023) / 1024 * 1024;
-  static constexpr uint32_t kRedOff = kStages * kStage;
+  static constexpr uint32_t kSbOff = kStages * kStage;  // two blocks
+  static constexpr uint32_t kRedOff = kSbOff + 2 * 2 * kSbBytes;
 };
 constexpr int kRedPitch = kTileRows + 4;  // floats: conflict-free both ways
 constexpr uint32_t kRedPlane = kSlotRows * kRedPitch;      // floats: a half of the inputs
 constexpr uint32_t kRedSize = 2 * kRedPlane * 4;           // two of them
-constexpr int kMostColumns = 128;  // tiles of y that a CTA may come last at
 template <bool kDown>
 struct Smem {
-  static constexpr uint32_t kColumnsOff = Ring<kDown>::kRedOff + 2 * kRedSize;  // number, then they
-  static constexpr uint32_t kBarOff = kColumnsOff + (kMostColumns + 2) * 4;
-  static constexpr uint32_t kTotal = kBarOff + (2 * Ring<kDown>::kStages + 5) * 8 + 1024;
+  static constexpr uint32_t kLastOff = Ring<kDown>::kRedOff + 2 * kRedSize;
+  static constexpr uint32_t kBarOff = kLastOff + 16;
+  static constexpr uint32_t kTotal = kBarOff + (2 * Ring<kDown>::kStages + 9) * 8 + 1024;
 };
 constexpr int kPartFloats = kTileRows * kSlotRows;
 
@@ -86,7 +88,6 @@ struct Slot {
 struct Space {
   uint32_t *routed;   // [row tiles] CTAs of the router that are done, then row tiles that are
   uint32_t *tiles;    // [slots][tiles] segments of a split tile
-  uint32_t *columns;  // [tiles of down] slots that are done
   float *logits;      // [rows][experts]
   int32_t *ids;       // [rows][top]
   float *weights;     // [rows][top]
@@ -115,7 +116,6 @@ Space space_of(void *base, int rows, int hidden, int inter, int experts, int top
   const size_t up = inter / 64, down = hidden / kTileRows;
   take(s.routed, kMaxRows / 16 + 1);
   take(s.tiles, slots * std::max(up, down));
-  take(s.columns, down);
   s.counters = at;
   take(s.logits, (size_t)rows * experts);
   take(s.ids, pairs);
@@ -189,46 +189,52 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 }
 
 // The experts of row t, by a warp: top times the largest key, of equal ones the
-// lowest expert.
-__device__ void choose(const MoeArgs &a, int t) {
+// lowest expert.  Lane l holds experts l + 32 i, and the best of them that is left;
+// only the lane whose best is taken looks for its next.
+template <int kPer>
+__device__ void choose(const MoeArgs &a, int t, int32_t *ids) {
   const int lane = threadIdx.x & 31;
-  constexpr int kPer = kMaxExperts / 32;
   const float *z = a.ws.logits + (size_t)t * a.experts;
   float v[kPer];
-  uint32_t key[kPer];
+  uint32_t key[kPer];  // 0: none (a NaN is 1)
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < a.experts ? __ldcg(z + e) : 0.f;
-  }
+  for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < a.experts ? __ldcg(z + lane + 32 * i) : 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)  // 0: none (a NaN is 1)
-    key[i] = lane + 32 * i < a.experts ? order_key(v[i]) + 1u : 0u;
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < a.experts ? order_key(v[i]) + 1u : 0u;
+  uint32_t best;
+  int at;
+  float value;
+  auto look = [&] {
+    best = key[0];
+    at = lane;
+    value = v[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+        value = v[i];
+      }
+  };
+  look();
   float mine = 0.f, most = 0.f;  // lane j: the logit of choice j
   int id = 0;
   for (int j = 0; j < a.top; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    uint32_t e = 0xffffffffu;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (key[i] == top) e = lane + 32 * i;
-    const int chosen = (int)__reduce_min_sync(0xffffffffu, e);
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i == chosen) {
-        x = v[i];
-        key[i] = 0u;
-      }
-    x = __shfl_sync(0xffffffffu, x, chosen & 31);
+    const int chosen = __reduce_min_sync(0xffffffffu, best == top ? at : kMaxExperts);
+    const float x = __shfl_sync(0xffffffffu, value, chosen & 31);
     if (j == 0) most = x;
     if (lane == j) {
       mine = x;
       id = chosen;
     }
+    if (lane == (chosen & 31)) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (lane + 32 * i == chosen) key[i] = 0u;
+      look();
+    }
+    __syncwarp();
   }
   float w = lane < a.top ? expf(mine - most) : 0.f, sum = w;
   if (!a.renormalize) {
@@ -242,6 +248,7 @@ __device__ void choose(const MoeArgs &a, int t) {
     const int p = t * a.top + lane;
     a.ws.ids[p] = id;
     a.ws.weights[p] = w;
+    ids[lane] = id;
     if (a.ids_out) a.ids_out[p] = id;
     if (a.weights_out) a.weights_out[p] = w;
   }
@@ -250,11 +257,16 @@ __device__ void choose(const MoeArgs &a, int t) {
 // The pairs by expert (rows ascending), and the slots.  A bit a row and expert
 // makes the order the same whoever sets the bits first.
 constexpr int kRouteThreads = 512;
-__device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, int *scan) {
+__device__ void make_slots(const MoeArgs &a, const int32_t (*chosen)[kMaxTop], uint32_t (*bits)[4],
+                           int *first, int *scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = a.rows * a.top;
+  // one CTA has chosen for up to 16 rows
+  auto expert = [&](int p, int t) {
+    return a.rows <= kRouteTile ? chosen[t][p - t * a.top] : __ldcg(a.ws.ids + p);
+  };
   for (int p = tid; p < pairs; p += kRouteThreads) {
-    const int t = p / a.top, e = __ldcg(a.ws.ids + p);
+    const int t = p / a.top, e = expert(p, t);
     atomicOr(&bits[e][t >> 5], 1u << (t & 31));
   }
   __syncthreads();
@@ -280,7 +292,7 @@ __device__ void make_slots(const MoeArgs &a, uint32_t (*bits)[4], int *first, in
   if (tid == kRouteThreads - 1) *a.ws.n_slots = slot;
   __syncthreads();
   for (int p = tid; p < pairs; p += kRouteThreads) {
-    const int t = p / a.top, e = __ldcg(a.ws.ids + p);
+    const int t = p / a.top, e = expert(p, t);
     int rank = __popc(bits[e][t >> 5] & ((1u << (t & 31)) - 1u));
     for (int i = 0; i < t >> 5; ++i) rank += __popc(bits[e][i]);
     a.ws.order[first[e] + rank] = p;
@@ -292,20 +304,31 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const MoeArgs 
   __shared__ float red[kRouteWarps][kRouteTile][kRouteExperts];
   __shared__ uint32_t bits[kMaxExperts][4];
   __shared__ int first[kMaxExperts], scan[kRouteWarps];
+  __shared__ int32_t chosen[kRouteTile][kMaxTop];
   __shared__ uint32_t s_old;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  const int routers = (a.experts + kRouteExperts - 1) / kRouteExperts;
   const int e0 = blockIdx.x * kRouteExperts, t0 = blockIdx.y * kRouteTile;
   pdl_launch_dependents();
   *reinterpret_cast<uint4 *>(bits[tid]) = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
-  // this CTA's share of the rows' groups
-  if (t0 + warp < a.rows) {
-    const int t = t0 + warp, records = (a.hidden + kStageK - 1) / kStageK;
-    for (int g = blockIdx.x; g < a.hidden / 64; g += gridDim.x) {
-      const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(a.x + (size_t)t * a.hidden + 64 * g) + lane);
-      put_group<1>(a.ws.x + ((size_t)t * records + g / kGroupsOf) * kRecord, 0, g,
-                   make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)));
+  if ((int)blockIdx.x >= routers) {
+    // a row a warp: one record of the rows' form for the products
+    const int t = t0 + warp, record = blockIdx.x - routers, records = gridDim.x - routers;
+    if (t >= a.rows) return;
+    uint32_t u[kGroupsOf];
+#pragma unroll
+    for (int i = 0; i < kGroupsOf; ++i) {
+      const int g = record * kGroupsOf + i;
+      u[i] = 64 * g < a.hidden
+                 ? __ldg(reinterpret_cast<const uint32_t *>(a.x + (size_t)t * a.hidden + 64 * g) + lane)
+                 : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < kGroupsOf; ++i)
+      put_group<1>(a.ws.x + ((size_t)t * records + record) * kRecord, 0, i,
+                   make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)));
+    return;
   }
   // A: 16 rows of x, B: 8 experts.  A lane's 16 bytes are 8 inputs of a block of
   // 32, in the same places of both, so their order within the block does not matter.
@@ -359,15 +382,22 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const MoeArgs 
     if (is && tid == 0) *counter = 0u;
     return is;
   };
-  if (!last(a.ws.routed + blockIdx.y, gridDim.x)) return;
+  if (!last(a.ws.routed + blockIdx.y, routers)) return;
   static_assert(kRouteWarps == kRouteTile, "a row a warp");
-  if (t0 + warp < a.rows) choose(a, t0 + warp);
+  if (t0 + warp < a.rows) {
+    if (a.experts <= 64)
+      choose<2>(a, t0 + warp, chosen[warp]);
+    else if (a.experts <= 256)
+      choose<8>(a, t0 + warp, chosen[warp]);
+    else
+      choose<kMaxExperts / 32>(a, t0 + warp, chosen[warp]);
+  }
   __threadfence();
   if (gridDim.y == 1)
     __syncthreads();
   else if (!last(a.ws.routed + kMaxRows / 16, gridDim.y))
     return;
-  make_slots(a, bits, first, scan);
+  make_slots(a, chosen, bits, first, scan);
 }
 
 // ---- the experts' products ---------------------------------------------------------
@@ -409,32 +439,137 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-// A group's products of 16 weight rows (w: ldmatrix of words t and 4 + t of rows g8 and
-// g8 + 8) with the rows of x in fragments x[2], added to d; kParts 2: with low as well.
+// A group's products of two tiles of 16 weight rows (w: ldmatrix of words t and 4 + t of
+// rows g8 and g8 + 8) with the rows of x in fragments x[2], added to d; kParts 2: with
+// low as well.  The tiles' chains alternate, so that no MMA waits for the one just issued.
 template <int kParts>
-__device__ __forceinline__ void group_f16(float (&d)[4], const uint32_t (&w)[4], const uint4 (&x)[2],
+__device__ __forceinline__ void group_f16(float (&d)[2][4], const uint32_t (&w)[2][4], const uint4 (&x)[2],
                                           const uint4 (&low)[2]) {
   constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u, k1024 = 0x64006400u;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t a = w[2 * i], b = w[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
-    const uint32_t a0 = and_or(a, kEven, k1024), a1 = and_or(b, kEven, k1024),
-                   a2 = and_or(a, kOdd, k1024), a3 = and_or(b, kOdd, k1024);
-    mma_f16(d, a0, a1, a2, a3, x[i].x, x[i].y);
-    if constexpr (kParts == 2) mma_f16(d, a0, a1, a2, a3, low[i].x, low[i].y);
-    const uint32_t c0 = and_or(a8, kEven, k1024), c1 = and_or(b8, kEven, k1024),
-                   c2 = and_or(a8, kOdd, k1024), c3 = and_or(b8, kOdd, k1024);
-    mma_f16(d, c0, c1, c2, c3, x[i].z, x[i].w);
-    if constexpr (kParts == 2) mma_f16(d, c0, c1, c2, c3, low[i].z, low[i].w);
-  }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      const uint32_t b0 = step ? x[i].z : x[i].x, b1 = step ? x[i].w : x[i].y;
+      uint32_t q[2][4];
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        const uint32_t a = w[tile][2 * i] >> (8 * step), b = w[tile][2 * i + 1] >> (8 * step);
+        q[tile][0] = and_or(a, kEven, k1024);
+        q[tile][1] = and_or(b, kEven, k1024);
+        q[tile][2] = and_or(a, kOdd, k1024);
+        q[tile][3] = and_or(b, kOdd, k1024);
+        mma_f16(d[tile], q[tile][0], q[tile][1], q[tile][2], q[tile][3], b0, b1);
+      }
+      if constexpr (kParts == 2) {
+        const uint32_t c0 = step ? low[i].z : low[i].x, c1 = step ? low[i].w : low[i].y;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+          mma_f16(d[tile], q[tile][0], q[tile][1], q[tile][2], q[tile][3], c0, c1);
+      }
+    }
 }
 
-// kDown false: h = silu(gate x) * (up x) of every slot; true: d = weight * (down h),
-// and y once a tile's slots are all there.
+// A warp's part of stages [s0, s1) of a tile: rows 32 (w % 4) .. of the stage and half
+// w / 4 of its inputs.  Lane (g8, t4): weight rows g8 + 8 i; of the activations column
+// (row) g8; of the sums columns 2 t4 and 2 t4 + 1.  kBoth: a column a row, its two parts
+// one after the other; else down's second parts are columns of their own.
+template <bool kDown, bool kBoth>
+__device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint32_t full0,
+                                         uint32_t empty0, uint32_t sb_full0, uint32_t sb_empty0,
+                                         int &st, int &ph, int &blocks, int s0, int s1, int groups,
+                                         int n) {
+  using R = Ring<kDown>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g8 = lane >> 2, t4 = lane & 3, rows0 = 32 * (warp & 3), half = warp >> 2;
+  constexpr int apart = kDown && !kBoth ? 4 : kSlotRows;
+  const bool valid = g8 % apart < n, real0 = 2 * t4 % apart < n, real1 = (2 * t4 + 1) % apart < n;
+  const uint32_t w_at = (uint32_t)(rows0 + (lane & 15)) * 128;  // the second box follows the first
+  const uint32_t x_at = kXOff + g8 * kRecord + half * 256 + t4 * 16;
+  const uint32_t group_at =
+      kXOff + 2 * t4 * kRecord + kGroupsOf * 128 + half * 2 * (uint32_t)sizeof(Group);
+  constexpr uint32_t kLow = kSlotRows * kRecord;  // to a row's second part
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int c = s0; c < s1; ++c) {
+    if ((c == s0 || c % kBlock == 0) && !warp_wait_stage(sb_full0 + 8u * (blocks & 1), (blocks >> 1) & 1))
+      return false;
+    if (!warp_wait_stage(full0 + 8u * st, ph)) return false;
+    const uint32_t at = base + st * R::kStage;
+    const uint32_t sb_at = base + R::kSbOff + (blocks & 1) * 2 * kSbBytes + (rows0 + g8) * kSbRow +
+                           (c % kBlock) * 8 + half * 4;
+    if (c * kGroupsOf + 2 * half < groups) {
+      uint4 x[2][2], r[2][2], low[2][2];
+      uint32_t w[2][2][4], sw[4], bw[4];
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+          ldmatrix_x4(w[gi][tile], at + w_at + tile * 16 * 128 +
+                                       (((4 * half + 2 * gi + (lane >> 4)) ^ (lane & 7)) << 4));
+        x[gi][0] = valid ? lds128(at + x_at + gi * 128) : zero;
+        x[gi][1] = valid ? lds128(at + x_at + gi * 128 + 64) : zero;
+        r[gi][0] = real0 ? lds128(at + group_at + gi * 16) : zero;
+        r[gi][1] = real1 ? lds128(at + group_at + kRecord + gi * 16) : zero;
+        if constexpr (kBoth) {
+          low[gi][0] = valid ? lds128(at + x_at + kLow + gi * 128) : zero;
+          low[gi][1] = valid ? lds128(at + x_at + kLow + gi * 128 + 64) : zero;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sw[i] = lds32(sb_at + i * 8 * kSbRow);
+        bw[i] = lds32(sb_at + kSbBytes + i * 8 * kSbRow);
+      }
+#pragma unroll
+      for (int gi = 0; gi < 2; ++gi) {
+        const float f0 = __uint_as_float(r[gi][0].x), f1 = __uint_as_float(r[gi][1].x);
+        float start0 = __uint_as_float(r[gi][0].y), start1 = __uint_as_float(r[gi][1].y);
+        float sum0 = __uint_as_float(r[gi][0].z), sum1 = __uint_as_float(r[gi][1].z);
+        if constexpr (kBoth) {
+          const uint4 q0 = real0 ? lds128(at + group_at + kLow + gi * 16) : zero;
+          const uint4 q1 = real1 ? lds128(at + group_at + kLow + kRecord + gi * 16) : zero;
+          start0 += __uint_as_float(q0.y);
+          start1 += __uint_as_float(q1.y);
+          sum0 += __uint_as_float(q0.z);
+          sum1 += __uint_as_float(q1.z);
+        }
+        float d[2][4] = {{start0, start1, start0, start1}, {start0, start1, start0, start1}};
+        group_f16<kBoth ? 2 : 1>(d, w[gi], x[gi], kBoth ? low[gi] : x[gi]);
+        auto of = [&](uint32_t word) { return __uint_as_float(gi ? word & 0xFFFF0000u : word << 16); };
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          const float s0r = of(sw[2 * tile]), s8r = of(sw[2 * tile + 1]);
+          const float b0r = of(bw[2 * tile]), b8r = of(bw[2 * tile + 1]);
+          acc[tile][0] = fmaf(s0r, f0 * d[tile][0], fmaf(b0r, sum0, acc[tile][0]));
+          acc[tile][1] = fmaf(s0r, f1 * d[tile][1], fmaf(b0r, sum1, acc[tile][1]));
+          acc[tile][2] = fmaf(s8r, f0 * d[tile][2], fmaf(b8r, sum0, acc[tile][2]));
+          acc[tile][3] = fmaf(s8r, f1 * d[tile][3], fmaf(b8r, sum1, acc[tile][3]));
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_u32(empty0 + 8u * st);
+    if (c + 1 == s1 || c % kBlock == kBlock - 1) {
+      if (lane == 0) mbar_arrive_u32(sb_empty0 + 8u * (blocks & 1));
+      ++blocks;
+    }
+    if (++st == R::kStages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  return true;
+}
+
+// The weights of a stage's two blocks of 64 rows.
+struct Maps {
+  CUtensorMap w[2];
+};
+
+// kDown false: h = silu(gate x) * (up x) of every slot; true: d = weight * (down h).
 template <bool kDown>
 __global__ void __launch_bounds__(kMoeThreads, 2)
-    moe_experts_kernel(const __grid_constant__ CUtensorMap map0,
-                       const __grid_constant__ CUtensorMap map1, const MoeArgs a) {
+    moe_experts_kernel(const __grid_constant__ Maps maps, const MoeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -444,17 +579,18 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   constexpr int kStages = R::kStages;
   const uint32_t full0 = base + S::kBarOff, empty0 = full0 + 8 * kStages;
   const uint32_t red_full0 = empty0 + 8 * kStages, red_empty0 = red_full0 + 16;
-  const uint32_t done = red_empty0 + 16;
-  volatile int *columns = reinterpret_cast<volatile int *>(smem + S::kColumnsOff);
+  const uint32_t sb_full0 = red_empty0 + 16, sb_empty0 = sb_full0 + 16, done = sb_empty0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init_u32(full0 + 8u * i, 1 + 32);
+      mbar_init_u32(full0 + 8u * i, 1);
       mbar_init_u32(empty0 + 8u * i, kWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_u32(red_full0 + 8u * i, kWarps);
       mbar_init_u32(red_empty0 + 8u * i, 1);
+      mbar_init_u32(sb_full0 + 8u * i, 32);
+      mbar_init_u32(sb_empty0 + 8u * i, kWarps);
     }
     mbar_init_u32(done, 1);
     fence_mbar_init();
@@ -487,11 +623,35 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     return g;
   };
 
+  // lane c: pair and weight of column c of a slot
+  auto columns_of = [&](const Segment &g, int &n, int &pair, float &weight) {
+    n = __ldcg(&a.ws.slots[g.slot].n);
+    pair = lane < n ? __ldcg(a.ws.order + __ldcg(&a.ws.slots[g.slot].first) + lane) : 0;
+    weight = kDown && lane < n ? __ldcg(a.ws.weights + pair) : 0.f;
+  };
+  // a column's sums, rows 2 lane and 2 lane + 1 of both blocks of a tile
+  auto emit = [&](const Segment &g, int p, float weight, float2 v0, float2 v1) {
+    if constexpr (!kDown) {
+      // a tile's 64 rows are one of down's groups
+      const float2 h = make_float2(v0.x / (1.f + expf(-v0.x)) * v1.x, v0.y / (1.f + expf(-v0.y)) * v1.y);
+      const int group = g.n0 / 64, records = (N + kStageK - 1) / kStageK;
+      put_group<2>(a.ws.h + ((size_t)p * records + group / kGroupsOf) * kRecord,
+                   (size_t)pairs * records * kRecord, group, h);
+    } else {
+      float *d = a.ws.d + (size_t)p * N + g.n0 + 2 * lane;
+      __stcg(reinterpret_cast<float2 *>(d), make_float2(weight * v0.x, weight * v0.y));
+      __stcg(reinterpret_cast<float2 *>(d + kRows), make_float2(weight * v1.x, weight * v1.y));
+    }
+  };
+
   if (warp == kWarps) {
     // ---- producer: weights by tensor copies, records by bulk copies, scales and
-    // biases, a row's few bytes at a time, by small ones ------------------------------
+    // biases by small copies of four lanes (or eight) a row, four stages at a time: a
+    // row's 32 bytes are one sector or two then, where a stage's 8 bytes of a row at a
+    // time held the loads in flight up (gate and up of 4 rows, 5120 x 1024: 32 us against
+    // 25 without these copies; as tensor boxes of 16-byte rows 39) ---------------------
     const bool wide = groups % 4 == 0;
-    int st = 0, ph = 0, issued = 0;
+    int st = 0, ph = 0, issued = 0, blocks = 0;
     bool ok = true;
     // down's first stages begin with their weights: the records are the launch
     // before's, and follow once it has ended
@@ -518,16 +678,46 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       const uint8_t *from =
           kDown ? a.ws.h + ((size_t)pair + (lane >= apart ? pairs : 0)) * stages * kRecord
                 : a.ws.x + (size_t)(pair / a.top) * stages * kRecord;
-      const uint8_t *sp[4], *bp[4];  // of rows lane + 32 i of the stage
+      auto bring_block = [&](int block) {
+        const uint32_t at = base + R::kSbOff + (blocks & 1) * 2 * kSbBytes;
+        const uint16_t *from[4] = {kDown ? a.down_s : a.gate_s, kDown ? a.down_s : a.up_s,
+                                   kDown ? a.down_b : a.gate_b, kDown ? a.down_b : a.up_b};
+        constexpr int kLanes = kBlock * kGroupsOf / 4;  // a row's 8-byte pieces
+        const int pieces = wide ? kLanes : 2 * kLanes, piece = lane % pieces, r = lane / pieces;
+        const int group = block * kBlock * kGroupsOf + piece * (wide ? 4 : 2);
+        if (group < groups) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long off = ((row0 + (kDown ? 32 * i : 32 * (i & 1)) + lane) * groups + g.s0 * kGroupsOf) * 2;
-        sp[i] = reinterpret_cast<const uint8_t *>(kDown ? a.down_s : i < 2 ? a.gate_s : a.up_s) + off;
-        bp[i] = reinterpret_cast<const uint8_t *>(kDown ? a.down_b : i < 2 ? a.gate_b : a.up_b) + off;
-      }
+          for (int m = 0; m < 4; ++m) {  // scales of the two blocks of rows, biases
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(
+                from[m] + (row0 + (kDown ? kRows * (m & 1) : 0) + r) * groups + group);
+            uint32_t to = at + m * (kRows * kSbRow) + r * kSbRow + piece * (wide ? 8 : 4);
+            if (wide) {
+#pragma unroll
+              for (int i = 0; i < kRows; i += 32 / kLanes, p += 64 / kLanes * groups, to += 32 / kLanes * kSbRow)
+                copy_small<8>(to, p);
+            } else {
+#pragma unroll 4
+              for (int i = 0; i < kRows; i += 16 / kLanes, p += 32 / kLanes * groups, to += 16 / kLanes * kSbRow)
+                copy_small<4>(to, p);
+            }
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(sb_full0 + 8u * (blocks & 1))
+                     : "memory");
+        ++blocks;
+      };
       const uint32_t bytes = 2 * kRows * 128 + (kDown ? 2 : 1) * n * kRecord;
       for (int c = g.s0; c < g.s1; ++c) {
-        if (!waited && issued == kStages) bring_pending();
+        // (nothing is given free before the records are there)
+        const bool new_block = c == g.s0 || c % kBlock == 0;
+        if (!waited && (issued == kStages || (new_block && blocks == 2))) bring_pending();
+        if (new_block) {
+          if (blocks >= 2)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_u32(sb_empty0 + 8u * (blocks & 1), ((blocks >> 1) & 1) ^ 1));
+          if (!ok) break;
+          bring_block(c / kBlock);
+        }
         if (issued >= kStages)
           ok = __all_sync(0xffffffffu, mbar_wait_u32(empty0 + 8u * st, ph ^ 1));
         if (!ok) break;
@@ -535,8 +725,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         if (lane == 0) {
           mbar_arrive_expect_tx_u32(full, bytes);
           const int x = c * (kStageK / 8);
-          load_box(at, &map0, x, (int)row0, full);
-          load_box(at + kRows * 128, &map1, x, (int)row0 + (kDown ? kRows : 0), full);
+          load_box(at, &maps.w[0], x, (int)row0, full);
+          load_box(at + kRows * 128, &maps.w[1], x, (int)row0 + (kDown ? kRows : 0), full);
         }
         __syncwarp();
         const uint8_t *record = brings ? from + (size_t)c * kRecord : nullptr;
@@ -547,24 +737,6 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
           for (int i = 0; i < kStages; ++i)
             if (i == issued) pending[i] = record;
         }
-        const uint32_t sb = at + kSb + lane * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (wide) {
-            copy_small<8>(sb + i * 512, sp[i]);
-            copy_small<8>(sb + i * 512 + 8, bp[i]);
-          } else {  // an even number of groups, the last stage's two
-            copy_small<4>(sb + i * 512, sp[i]);
-            copy_small<4>(sb + i * 512 + 8, bp[i]);
-            if (c * kGroupsOf + 2 < groups) {
-              copy_small<4>(sb + i * 512 + 4, sp[i] + 4);
-              copy_small<4>(sb + i * 512 + 12, bp[i] + 4);
-            }
-          }
-          sp[i] += 8;
-          bp[i] += 8;
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full) : "memory");
         ++issued;
         if (++st == kStages) {
           st = 0;
@@ -583,33 +755,20 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   }
 
   if (warp == kWarps + 1) {
-    // ---- finisher: rows 2 lane and 2 lane + 1 of both blocks of a tile -------------
-    if (kDown) pdl_wait();  // the tiles' counters and partials are the launch before's
-    int at_end = 0, k = 0;
+    // ---- finisher: a tile's sums to where they go -----------------------------------
+    if (kDown) pdl_wait();  // the partials' places are the launch before's
+    int k = 0;
     bool ok = true;
     for (long long u = u_begin; ok && u < u_end; ++k) {
       const Segment g = segment(u);
       u += g.s1 - g.s0;
-      const int first = __ldcg(&a.ws.slots[g.slot].first), n = __ldcg(&a.ws.slots[g.slot].n);
+      int n, pair;
+      float weight;
+      columns_of(g, n, pair, weight);
       const bool whole = g.s0 == 0 && g.s1 == stages;
       // down's slots of up to four rows have the second parts' sums in columns 4..7
       const bool doubled = kDown && n <= 4;
       float *part = a.ws.parts + (size_t)(2 * blockIdx.x + (g.s0 == 0 ? 1 : 0)) * kPartFloats + 2 * lane;
-      auto emit = [&](int col, float2 v0, float2 v1) {
-        const int p = __ldcg(a.ws.order + first + col);
-        if constexpr (!kDown) {
-          // a tile's 64 rows are one of down's groups
-          const float2 h = make_float2(v0.x / (1.f + expf(-v0.x)) * v1.x, v0.y / (1.f + expf(-v0.y)) * v1.y);
-          const int group = g.n0 / 64, records = (N + kStageK - 1) / kStageK;
-          put_group<2>(a.ws.h + ((size_t)p * records + group / kGroupsOf) * kRecord,
-                       (size_t)pairs * records * kRecord, group, h);
-        } else {
-          const float w = __ldcg(a.ws.weights + p);
-          float *d = a.ws.d + (size_t)p * N + g.n0 + 2 * lane;
-          __stcg(reinterpret_cast<float2 *>(d), make_float2(w * v0.x, w * v0.y));
-          __stcg(reinterpret_cast<float2 *>(d + kRows), make_float2(w * v1.x, w * v1.y));
-        }
-      };
       ok = __all_sync(0xffffffffu, mbar_wait_u32(red_full0 + 8u * (k & 1), (k >> 1) & 1));
       if (!ok) break;
       const float *red = reinterpret_cast<const float *>(smem + R::kRedOff + (k & 1) * kRedSize) + 2 * lane;
@@ -627,7 +786,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
             }
         }
         if (whole) {
-          emit(col, v[0], v[1]);
+          emit(g, __shfl_sync(0xffffffffu, pair, col), __shfl_sync(0xffffffffu, weight, col), v[0], v[1]);
         } else {
           __stcg(reinterpret_cast<float2 *>(part + col * kTileRows), v[0]);
           __stcg(reinterpret_cast<float2 *>(part + col * kTileRows + kRows), v[1]);
@@ -635,148 +794,35 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_u32(red_empty0 + 8u * (k & 1));
-      // the warp's stores, then one of its lanes counts; the count's last adds up
-      auto count = [&](uint32_t *counter, uint32_t of) {
-        __threadfence();
-        __syncwarp();
-        uint32_t old = 0;
-        if (lane == 0) {
-          old = atomicAdd(counter, 1u);
-          if (old == of - 1u) *counter = 0u;
-        }
-        old = __shfl_sync(0xffffffffu, old, 0);
-        __threadfence();
-        return old == of - 1u;
-      };
-      if (!whole) {
-        // a part of the tile: whoever comes last adds them all, in CTA order
-        const long long t0 = (long long)g.tile * stages;
-        const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
-        if (!count(a.ws.tiles + g.tile, (uint32_t)(c1 - c0 + 1))) continue;
-        for (int col = 0; col < n; ++col) {
-          float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          for (int c = c0; c <= c1; ++c) {
-            const float *from = a.ws.parts + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats +
-                                col * kTileRows + 2 * lane;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 f = __ldcg(reinterpret_cast<const float2 *>(from + x * kRows));
-              v[x].x += f.x;
-              v[x].y += f.y;
-            }
-          }
-          emit(col, v[0], v[1]);
-        }
-      }
-      if (kDown) {
-        const int column = g.n0 / kStep;
-        if (count(a.ws.columns + column, (uint32_t)n_slots)) {
-          if (lane == 0) columns[1 + at_end] = column;
-          ++at_end;
-        }
-      }
     }
-    if (kDown) {
-      __syncwarp();
-      if (lane == 0) {
-        columns[0] = at_end;
-        mbar_arrive_u32(done);
-      }
-    }
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_u32(done);
     if (!ok && lane == 0) atomicOr(&g_moe_device_error, 4u);
     return;
   }
 
   // ---- the products ----------------------------------------------------------------
-  // Warp w: rows 32 (w % 4) .. of the stage and half w / 4 of its inputs.  Lane (g8, t4):
-  // weight rows g8 + 8 i; of the activations column (row) g8; of the sums columns 2 t4
-  // and 2 t4 + 1.
-  const int g8 = lane >> 2, t4 = lane & 3, rows0 = 32 * (warp & 3), half = warp >> 2;
-  const uint32_t w_at = (uint32_t)(rows0 + (lane & 15)) * 128;  // the second box follows the first
-  if (kDown) pdl_wait();  // the partials' places are the launch before's
-  int st = 0, ph = 0, k = 0;
+  const int rows0 = 32 * (warp & 3), half = warp >> 2;
+  int st = 0, ph = 0, blocks = 0, k = 0;
   bool ok = true;
   for (long long u = u_begin; ok && u < u_end; ++k) {
     const Segment g = segment(u);
     u += g.s1 - g.s0;
     const int n = __ldcg(&a.ws.slots[g.slot].n);
-    const bool both = kDown && n > 4;  // a column a row, its two parts one after the other
-    const int apart = kDown && !both ? 4 : kSlotRows;
-    const bool valid = g8 % apart < n, real[2] = {2 * t4 % apart < n, (2 * t4 + 1) % apart < n};
     float acc[2][4] = {};
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int c = g.s0; c < g.s1; ++c) {
-      ok = warp_wait_stage(full0 + 8u * st, ph);
-      if (!ok) break;
-      const uint32_t at = base + st * R::kStage;
-      const uint32_t sb_at = at + kSb + (uint32_t)(rows0 + g8) * 16 + half * 4;
-      const uint32_t x_at = at + kXOff + g8 * kRecord + half * 256 + t4 * 16;
-      const uint32_t group_at =
-          at + kXOff + 2 * t4 * kRecord + kGroupsOf * 128 + half * 2 * (uint32_t)sizeof(Group);
-      if (c * kGroupsOf + 2 * half < groups) {
-        uint32_t sw[4], bw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sw[i] = lds32(sb_at + i * 8 * 16);
-          bw[i] = lds32(sb_at + i * 8 * 16 + 8);
-        }
-#pragma unroll
-        for (int gi = 0; gi < 2; ++gi) {
-          uint32_t w[2][4];
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile)
-            ldmatrix_x4(w[tile], at + w_at + tile * 16 * 128 +
-                                     (((4 * half + 2 * gi + (lane >> 4)) ^ (lane & 7)) << 4));
-          uint4 x[2], low[2];
-          x[0] = valid ? lds128(x_at + gi * 128) : zero;
-          x[1] = valid ? lds128(x_at + gi * 128 + 64) : zero;
-          const uint4 r0 = real[0] ? lds128(group_at + gi * 16) : zero;
-          const uint4 r1 = real[1] ? lds128(group_at + kRecord + gi * 16) : zero;
-          float start0 = __uint_as_float(r0.y), start1 = __uint_as_float(r1.y);
-          float sum0 = __uint_as_float(r0.z), sum1 = __uint_as_float(r1.z);
-          if (both) {
-            low[0] = valid ? lds128(x_at + kSlotRows * kRecord + gi * 128) : zero;
-            low[1] = valid ? lds128(x_at + kSlotRows * kRecord + gi * 128 + 64) : zero;
-            const uint4 q0 = real[0] ? lds128(group_at + kSlotRows * kRecord + gi * 16) : zero;
-            const uint4 q1 = real[1] ? lds128(group_at + (kSlotRows + 1) * kRecord + gi * 16) : zero;
-            start0 += __uint_as_float(q0.y);
-            start1 += __uint_as_float(q1.y);
-            sum0 += __uint_as_float(q0.z);
-            sum1 += __uint_as_float(q1.z);
-          }
-          const float f0 = __uint_as_float(r0.x), f1 = __uint_as_float(r1.x);
-          auto of = [&](uint32_t word) {
-            return __uint_as_float(gi ? word & 0xFFFF0000u : word << 16);
-          };
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile) {
-            float d[4] = {start0, start1, start0, start1};
-            if (both)
-              group_f16<2>(d, w[tile], x, low);
-            else
-              group_f16<1>(d, w[tile], x, x);
-            const float s0 = of(sw[2 * tile]), s8 = of(sw[2 * tile + 1]);
-            const float b0 = of(bw[2 * tile]), b8 = of(bw[2 * tile + 1]);
-            acc[tile][0] = fmaf(s0, f0 * d[0], fmaf(b0, sum0, acc[tile][0]));
-            acc[tile][1] = fmaf(s0, f1 * d[1], fmaf(b0, sum1, acc[tile][1]));
-            acc[tile][2] = fmaf(s8, f0 * d[2], fmaf(b8, sum0, acc[tile][2]));
-            acc[tile][3] = fmaf(s8, f1 * d[3], fmaf(b8, sum1, acc[tile][3]));
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_u32(empty0 + 8u * st);
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1;
-      }
-    }
+    if (kDown && n > 4)
+      ok = multiply<kDown, kDown>(acc, base, full0, empty0, sb_full0, sb_empty0, st, ph, blocks, g.s0, g.s1,
+                                   groups, n);
+    else
+      ok = multiply<kDown, false>(acc, base, full0, empty0, sb_full0, sb_empty0, st, ph, blocks, g.s0, g.s1,
+                                   groups, n);
     // the sums to the finisher, red[half][column][row]
     if (ok && k >= 2)
       ok = __all_sync(0xffffffffu, mbar_wait_u32(red_empty0 + 8u * (k & 1), ((k >> 1) & 1) ^ 1));
     if (!ok) break;
     float *red = reinterpret_cast<float *>(smem + R::kRedOff + (k & 1) * kRedSize) + half * kRedPlane +
-                 2 * t4 * kRedPitch + rows0 + g8;
+                 2 * (lane & 3) * kRedPitch + rows0 + (lane >> 2);
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
       red[16 * tile] = acc[tile][0];
@@ -787,49 +833,95 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     __syncwarp();
     if (lane == 0) mbar_arrive_u32(red_full0 + 8u * (k & 1));
   }
-  if constexpr (kDown) {
-    // the tiles of y at which this CTA came last: the rows' sums over their experts, in
-    // the order of choice, four columns a lane
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_u32(done, 0));
-    const int count = ok ? columns[0] : 0;
-    for (int i = 0; i < count; ++i) {
-      const int n = columns[1 + i] * kTileRows + 4 * lane;
-      for (int t = warp; t < a.rows; t += 2 * kWarps) {
-        float4 sum[2] = {};
-        for (int j0 = 0; j0 < a.top; j0 += 4) {
-          float4 x[2][4];
+  // ---- the end: what others count on, and what counts on others.  Once, when this
+  // CTA's segments are all done: a fence and an atomic a segment took longer than a short
+  // segment's products.
+  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_u32(done, 0));
+  if (kDown) pdl_wait();  // (over by now)
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
+  // a split tile at the beginning, one at the end: whoever comes last adds all of
+  // their parts, in CTA order
+  const int tile0 = (int)(u_begin / stages), tile1 = (int)((u_end - 1) / stages);
+  const bool split0 = u_begin % stages != 0 || (tile0 == tile1 && u_end % stages != 0);
+  const bool split1 = tile1 != tile0 && u_end % stages != 0;
+  volatile int *last = reinterpret_cast<volatile int *>(smem + S::kLastOff);
+  if (threadIdx.x < 2) {
+    const int tile = threadIdx.x ? tile1 : tile0;
+    bool is = false;
+    if (ok && (threadIdx.x ? split1 : split0)) {
+      const long long t0 = (long long)tile * stages;
+      const uint32_t others = (uint32_t)(((t0 + stages) * ctas - 1) / W - ((t0 + 1) * ctas - 1) / W);
+      is = atomicAdd(a.ws.tiles + tile, 1u) == others;
+      if (is) a.ws.tiles[tile] = 0u;
+      __threadfence();
+    }
+    last[threadIdx.x] = is;
+  }
+  sync();
+  const bool last0 = last[0], last1 = last[1];
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+  for (int i = 0; i < 2; ++i) {
+    if (!(i ? last1 : last0)) continue;
+    const long long t0 = (long long)(i ? tile1 : tile0) * stages;
+    const Segment g = segment(t0);
+    const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
+    int n, pair;
+    float weight;
+    columns_of(g, n, pair, weight);
+    if (warp < n) {  // a column a warp
+      float2 v[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int c = c0; c <= c1; c += 4) {  // four CTAs' in flight
+        float2 f[4][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[y][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (j0 + j < a.top && t + y * kWarps < a.rows)
-                x[y][j] = __ldcg(reinterpret_cast<const float4 *>(
-                    a.ws.d + (size_t)((t + y * kWarps) * a.top + j0 + j) * N + n));
-            }
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+          for (int x = 0; x < 2; ++x) {
+            const float *from = a.ws.parts + (size_t)(2 * (c + y) + (c + y == c0 ? 1 : 0)) * kPartFloats +
+                                warp * kTileRows + x * kRows + 2 * lane;
+            f[y][x] = c + y <= c1 ? __ldcg(reinterpret_cast<const float2 *>(from)) : make_float2(0.f, 0.f);
+          }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              sum[y].x += x[y][j].x;
-              sum[y].y += x[y][j].y;
-              sum[y].z += x[y][j].z;
-              sum[y].w += x[y][j].w;
-            }
-        }
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (t + y * kWarps < a.rows) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[y].x, sum[y].y);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(sum[y].z, sum[y].w);
-            *reinterpret_cast<uint2 *>(a.y + (size_t)(t + y * kWarps) * N + n) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
-                           *reinterpret_cast<const uint32_t *>(&hi));
+          for (int x = 0; x < 2; ++x) {
+            v[x].x += f[y][x].x;
+            v[x].y += f[y][x].y;
           }
       }
+      emit(g, __shfl_sync(0xffffffffu, pair, warp), __shfl_sync(0xffffffffu, weight, warp), v[0], v[1]);
     }
   }
   if (!ok && lane == 0) atomicOr(&g_moe_device_error, 2u);
+}
+
+// y: a row's sums over its experts, in the order of choice; four columns a thread.
+// (By whichever CTA of the launch before came last at a tile of y, without this launch:
+// most tiles' last slots end together, and one CTA was left with nearly all of them.)
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(const MoeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n = 4 * (blockIdx.x * kSumThreads + threadIdx.x);
+  if (n >= a.hidden) return;
+  const float *d = a.ws.d + (size_t)blockIdx.y * a.top * a.hidden + n;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < a.top; j0 += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = j0 + j < a.top ? __ldcg(reinterpret_cast<const float4 *>(d + (size_t)(j0 + j) * a.hidden))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum.x += x[j].x;
+      sum.y += x[j].y;
+      sum.z += x[j].z;
+      sum.w += x[j].w;
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
+  *reinterpret_cast<uint2 *>(a.y + (size_t)blockIdx.y * a.hidden + n) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
 int moe_ctas() { return 2 * device_sm_count(); }
@@ -845,7 +937,7 @@ sv_status check_sizes(const char *who, int rows, int hidden, int inter, int expe
   if (hidden % 128 || inter % 128)
     return fail(SV_ERR_UNSUPPORTED, "%s: hidden and inter must be multiples of 128 (%d, %d)", who,
                 hidden, inter);
-  if (hidden > kMostColumns * kTileRows || inter > 65536 || (long long)experts * std::max(hidden, inter) > (1ll << 30))
+  if (hidden > 65536 || inter > 65536 || (long long)experts * std::max(hidden, inter) > (1ll << 30))
     return fail(SV_ERR_UNSUPPORTED, "%s: sizes too large", who);
   return SV_OK;
 }
@@ -894,21 +986,21 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   const Buf in[] = {{x, (size_t)rows * hidden * 2, 16},
                     {router, (size_t)experts * hidden * 2, 16},
                     {gate_w, gate_n / 2, 16},
-                    {gate_s, gate_n / 32, 8},
-                    {gate_b, gate_n / 32, 8},
+                    {gate_s, gate_n / 32, 16},
+                    {gate_b, gate_n / 32, 16},
                     {up_w, gate_n / 2, 16},
-                    {up_s, gate_n / 32, 8},
-                    {up_b, gate_n / 32, 8},
+                    {up_s, gate_n / 32, 16},
+                    {up_b, gate_n / 32, 16},
                     {down_w, gate_n / 2, 16},
-                    {down_s, gate_n / 32, 8},
-                    {down_b, gate_n / 32, 8}};
+                    {down_s, gate_n / 32, 16},
+                    {down_b, gate_n / 32, 16}};
   for (const Buf &b : in)
     if (!b.p) return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!y || !workspace) return fail(SV_ERR_INVALID_ARG, "%s: null pointer", who);
   for (const Buf &b : in)
     if (!aligned(b.p, b.align))
       return fail(SV_ERR_INVALID_ARG,
-                  "%s: x, router and w_packed must be 16-byte, scales and biases 8-byte aligned", who);
+                  "%s: x, router, w_packed, scales and biases must be 16-byte aligned", who);
   if (!aligned(y, 8) || (ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4)) ||
       !aligned(workspace, 256))
     return fail(SV_ERR_INVALID_ARG, "%s: y must be 8-byte, the workspace 256-byte aligned", who);
@@ -940,15 +1032,16 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   });
   if (e != cudaSuccess)
     return fail(SV_ERR_CUDA, "%s: cudaFuncSetAttribute failed: %s", who, cudaGetErrorString(e));
-  CUtensorMap gate_map, up_map, down_map;
+  Maps up_maps, down_maps;
   auto encode = [&](CUtensorMap *map, const uint32_t *w, int n, int k) {
     return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, w, (uint64_t)k / 8, (uint64_t)experts * n,
                      (uint64_t)k / 2, kBoxWords, kRows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  st = encode(&gate_map, gate_w, inter, hidden);
-  if (st == SV_OK) st = encode(&up_map, up_w, inter, hidden);
-  if (st == SV_OK) st = encode(&down_map, down_w, hidden, inter);
+  st = encode(&up_maps.w[0], gate_w, inter, hidden);
+  if (st == SV_OK) st = encode(&up_maps.w[1], up_w, inter, hidden);
+  if (st == SV_OK) st = encode(&down_maps.w[0], down_w, hidden, inter);
   if (st != SV_OK) return st;
+  down_maps.w[1] = down_maps.w[0];
   MoeArgs a = {};
   a.x = reinterpret_cast<const __nv_bfloat16 *>(x);
   a.router = reinterpret_cast<const __nv_bfloat16 *>(router);
@@ -975,16 +1068,21 @@ extern "C" sv_status moe_smallm(const uint16_t *x, const uint16_t *router, const
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = &early;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  cfg.gridDim = dim3((experts + kRouteExperts - 1) / kRouteExperts, (rows + kRouteTile - 1) / kRouteTile);
+  cfg.gridDim = dim3((experts + kRouteExperts - 1) / kRouteExperts + (hidden + kStageK - 1) / kStageK,
+                     (rows + kRouteTile - 1) / kRouteTile);
   cfg.blockDim = dim3(kRouteThreads);
   cudaError_t le = cudaLaunchKernelEx(&cfg, moe_route_kernel, a);
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kMoeThreads);
   cfg.dynamicSmemBytes = Smem<false>::kTotal;
-  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<false>, gate_map, up_map, a);
+  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<false>, up_maps, a);
   cfg.dynamicSmemBytes = Smem<true>::kTotal;
-  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<true>, down_map, down_map, a);
+  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_experts_kernel<true>, down_maps, a);
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3((hidden + 4 * kSumThreads - 1) / (4 * kSumThreads), rows);
+  cfg.blockDim = dim3(kSumThreads);
+  if (le == cudaSuccess) le = cudaLaunchKernelEx(&cfg, moe_sum_kernel, a);
   if (le != cudaSuccess) {
     (void)cudaGetLastError();
     return fail(SV_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(le));
