@@ -41,7 +41,7 @@ namespace sv {
 namespace gdn {
 namespace {
 
-constexpr int kC = 64;    // rows a chunk
+constexpr int kC = 64;    // rows a chunk (1 << 6)
 constexpr int kD = 128;   // dk and dv, narrower ones padded with zeros
 
 // What the first launch leaves of a chunk of a head, as the second wants it in
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const Adva
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, place = blockIdx.x / a.H, hk = h / (a.H / a.Hk);
   int c;
-  const int b = tile_owner(a.q_start, a.B, a.rows, kC, place, c);
+  const int b = tile_owner(a.q_start, a.B, a.rows, 6, place, c);
   if (b >= a.B) return;
   const Rows s = rows_of(a.q_start, b, a.rows);
   if (c < 0 || c * kC >= s.n || slot_of(a.state_index, b, a.slots) < 0) return;

@@ -8,9 +8,9 @@
 // Bound by memory: every input is read once and every output written once (the
 // rows before a tile are read twice).  A warp takes one head (up to 128
 // channels, four a lane) of a tile of rows of one sequence and slides the
-// window along in registers, so the W taps cost no loads; eight rows' loads are
-// in flight a warp.  The heads of a row are neighbouring warps, so a CTA reads
-// and writes runs of 2 KB.  The tiles begin at the sequences' first rows: a
+// window along in registers, so the W taps cost no loads; four to eight rows' loads
+// are in flight a warp, 24 warps an SM.  The heads of a row are neighbouring warps, so
+// a CTA reads and writes runs of 1 KB.  The tiles begin at the sequences' first rows: a
 // sequence's first tile alone reads its window, and the same warp writes it, so
 // one launch needs no order among its CTAs.
 #include <cuda_runtime.h>
@@ -21,9 +21,9 @@ namespace sv {
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kMaxW = 8;
-constexpr int kBatch = 8;  // rows whose loads are in flight together
+constexpr int kBatch = 4;  // rows whose loads go together, a batch ahead
 
 struct InputsArgs {
   const void *x, *a, *b;
@@ -35,7 +35,7 @@ struct InputsArgs {
   void *q, *k, *v;
   float *alpha, *beta;
   float q_scale, eps;
-  int B, rows, slots, W, Hk, H, dk, dv, C, tile, update, heads, tasks;
+  int B, rows, slots, W, Hk, H, dk, dv, C, shift, update, heads, tasks;
 };
 
 // Four consecutive values.
@@ -56,19 +56,38 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
                                              *reinterpret_cast<const uint32_t *>(&b));
 }
-// The approximate exponential and division are off by a few 2^-23 of the value
-// in the range that silu does not send to zero.
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+// y / (1 + 2^(-y log2 e)) by the approximate power and reciprocal: each off by about
+// 2^-22 of the value, and the exponent by its rounding, in the range that silu does not
+// send to zero; below y = -87 it is zero.
+__device__ __forceinline__ float silu(float y) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return y * r;
+}
 
 template <class X, class Y, int kW>
-__global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel(const InputsArgs a) {
   const int W = kW > 0 ? kW : a.W;
   constexpr int kTaps = kW > 0 ? kW : kMaxW;
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= a.tasks) return;
+  // head `unit` of the row: q heads, then k heads, then v heads
+  const int kind = unit < a.Hk ? 0 : unit < 2 * a.Hk ? 1 : 2;
+  const int head = kind == 2 ? unit - 2 * a.Hk : kind == 1 ? unit - a.Hk : unit;
+  const int d = kind == 2 ? a.dv : a.dk;
+  const int c0 = (kind == 2 ? 2 * a.Hk * a.dk + head * a.dv : unit * a.dk) + 4 * lane;
+  const bool mine = 4 * lane < d && unit < a.heads;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 w[kTaps], h[kTaps];  // h[i]: the input W - 1 - i places back; h[W - 1] the newest
+#pragma unroll
+  for (int i = 0; i < kTaps; ++i) {  // on their way while the tile is looked for
+    w[i] = h[i] = zero;
+    if (i < W && mine) w[i] = load4(a.weight + (long long)i * a.C + c0);
+  }
   int j;
-  const int b = tile_owner(a.q_start, a.B, a.rows, a.tile, blockIdx.y, j);
+  const int b = tile_owner(a.q_start, a.B, a.rows, a.shift, blockIdx.y, j);
   Rows s;
   int slot = -1;
   if (b < a.B) {
@@ -78,9 +97,9 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
     s.start = min(max(__ldg(a.q_start + a.B), 0), a.rows);
     s.n = a.rows - s.start;
   }
-  const int t0 = j * a.tile;
+  const int t0 = j << a.shift;
   if (j < 0 || t0 >= s.n) return;
-  const int n = min(a.tile, s.n - t0);  // rows of this tile
+  const int n = min(1 << a.shift, s.n - t0);  // rows of this tile
   const bool real = slot >= 0;
 
   if (unit >= a.heads) {  // the gates of 32 heads
@@ -103,16 +122,9 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
     return;
   }
 
-  // head `unit` of the row: q heads, then k heads, then v heads
-  const int kind = unit < a.Hk ? 0 : unit < 2 * a.Hk ? 1 : 2;
-  const int head = kind == 2 ? unit - 2 * a.Hk : kind == 1 ? unit - a.Hk : unit;
-  const int d = kind == 2 ? a.dv : a.dk;
-  const int c0 = (kind == 2 ? 2 * a.Hk * a.dk + head * a.dv : unit * a.dk) + 4 * lane;
-  const bool mine = 4 * lane < d;
   Y *to = static_cast<Y *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
   const long long to_row = (long long)(kind == 2 ? a.H : a.Hk) * d;
   to += head * d + 4 * lane + (s.start + t0) * to_row;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   if (!real) {
     for (int t = 0; t < n; ++t)
       if (mine) store4(to + t * to_row, zero);
@@ -120,16 +132,11 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
   }
   const X *x = static_cast<const X *>(a.x) + (s.start + t0) * a.x_stride + c0;
   float *window = a.window + (long long)slot * (W - 1) * a.C + c0;
-  float4 w[kTaps], h[kTaps];  // h[i]: the input W - 1 - i places back; h[W - 1] the newest
 #pragma unroll
-  for (int i = 0; i < kTaps; ++i) w[i] = h[i] = zero;
-#pragma unroll
-  for (int i = 0; i < kTaps; ++i) {
-    if (i < W && mine) w[i] = load4(a.weight + (long long)i * a.C + c0);
+  for (int i = 0; i < kTaps - 1; ++i)
     if (i < W - 1 && mine)
       h[i + 1] = t0 == 0 ? *reinterpret_cast<const float4 *>(window + (long long)i * a.C)
                          : widen4(load4(x + (long long)(i - (W - 1)) * a.x_stride));
-  }
   if (t0 == 0 && a.update && mine) {
     // entry i of the next window: the input of row n - (W - 1) + i, or the old
     // window's where that is before the first row
@@ -147,11 +154,20 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
     for (int i = 0; i < kTaps - 1; ++i)
       if (i < W - 1) *reinterpret_cast<float4 *>(window + (long long)i * a.C) = next[i];
   }
+  decltype(load4(x)) next[kBatch];
+  auto load = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (t + i < n && mine) next[i] = load4(x + (long long)i * a.x_stride);
+    x += (long long)kBatch * a.x_stride;
+  };
+  load(0);
+  const float scale = kind == 0 ? a.q_scale : 1.f;
   for (int t = 0; t < n; t += kBatch) {
     decltype(load4(x)) raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (t + i < n && mine) raw[i] = load4(x + (long long)(t + i) * a.x_stride);
+    for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+    load(t + kBatch);
     float4 y[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -183,20 +199,21 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_inputs_kernel(const InputsArg
         for (int i = 0; i < kBatch; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float f = rsqrtf(ss[i] + a.eps) * (kind == 0 ? a.q_scale : 1.f);
+        const float f = rsqrtf(ss[i] + a.eps) * scale;
         y[i] = make_float4(y[i].x * f, y[i].y * f, y[i].z * f, y[i].w * f);
       }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (t + i < n && mine) store4(to + (t + i) * to_row, y[i]);
+      if (t + i < n && mine) store4(to + i * to_row, y[i]);
+    to += kBatch * to_row;
   }
 }
 
 using Kernel = void (*)(InputsArgs);
 template <class X, class Y>
 Kernel pick(int W) {
-  return W == 4 ? gdn_inputs_kernel<X, Y, 4> : gdn_inputs_kernel<X, Y, 0>;
+  return W == 4 ? gdn_inputs_kernel<X, Y, 4> : W == 2 ? gdn_inputs_kernel<X, Y, 2> : gdn_inputs_kernel<X, Y, 0>;
 }
 
 }  // namespace
@@ -311,15 +328,12 @@ extern "C" sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_
   p.heads = 2 * Hk + Hv;
   p.tasks = p.heads + (Hv + 31) / 32;
   // at least kMaxW rows a tile: a later tile's taps are then all rows of x
-  p.tile = max_new <= 16 ? 16 : 32;
-  const long long tiles = rows / p.tile + (long long)B + 1;
-  if (tiles > 65535) {  // grid.y
-    while (rows / p.tile + (long long)B + 1 > 65535 && p.tile < (1 << 20)) p.tile *= 2;
-    if (rows / p.tile + (long long)B + 1 > 65535)
-      return fail(SV_ERR_UNSUPPORTED, "%s: too many sequences", who);
-  }
+  p.shift = max_new <= 16 ? 4 : 5;
+  auto tiles = [&] { return ((long long)rows >> p.shift) + B + 1; };
+  while (tiles() > 65535 && p.shift < 20) ++p.shift;  // grid.y
+  if (tiles() > 65535) return fail(SV_ERR_UNSUPPORTED, "%s: too many sequences", who);
   const dim3 grid((unsigned)((p.tasks + kWarps - 1) / kWarps),
-                  (unsigned)(rows / p.tile + (long long)B + 1));
+                  (unsigned)tiles());
   const Kernel kernel =
       x_dtype == SV_F32
           ? (out_dtype == SV_F32 ? pick<float, float>(W) : pick<float, __nv_bfloat16>(W))

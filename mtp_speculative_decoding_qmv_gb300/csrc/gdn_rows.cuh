@@ -27,15 +27,15 @@ __device__ __forceinline__ int slot_of(const int32_t *index, int b, int slots) {
   return i >= 0 && i < slots ? i : -1;
 }
 
-// Tiles of `tile` rows that begin at the sequences' first rows, numbered so that
-// sequence b's first is q_start[b] / tile + b: room for the ceil(n / tile) tiles of
-// every sequence before it.  The owner of tile number i, in [0, B] (B: the rows past
+// Tiles of 1 << shift rows that begin at the sequences' first rows, numbered so that
+// sequence b's first is (q_start[b] >> shift) + b: room for the tiles of every sequence
+// before it, those that are not full included.  The owner of tile number i, in [0, B] (B: the rows past
 // the last sequence), and its place j among the owner's tiles (past its last: no
 // such tile).  By a whole warp.
-__device__ __forceinline__ int tile_owner(const int32_t *q_start, int B, int rows, int tile, int i,
+__device__ __forceinline__ int tile_owner(const int32_t *q_start, int B, int rows, int shift, int i,
                                           int &j) {
   const int lane = threadIdx.x & 31;
-  auto first = [&](int b) { return min(max(__ldg(q_start + b), 0), rows) / tile + b; };
+  auto first = [&](int b) { return (min(max(__ldg(q_start + b), 0), rows) >> shift) + b; };
   int lo = 0, n = B + 1;  // the owner is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32, at = lo + lane * step;
