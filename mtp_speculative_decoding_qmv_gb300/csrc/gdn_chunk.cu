@@ -99,6 +99,44 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
                : "memory");
 }
 
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// d (+)= 16 x kK floats at `left` times kK x 8 at `right`, both of the scratch matrix, by
+// a warp.  Each factor is cut into two tf32 parts (its upper 11 bits, and 11 of what
+// they leave), three products of them: 2^-21 of the terms.  As sums of fp32 products,
+// the loads from shared memory (four values a lane for a product each) bound the launch.
+template <int kK>
+__device__ __forceinline__ void times(float (&d)[4], const float *left, const float *right) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int k = 0; k < kK; k += 8) {
+    uint32_t a[2][4], b[2][2];
+    auto cut_tf32 = [](float x, uint32_t &high, uint32_t &low) {
+      high = __float_as_uint(x) & 0xFFFFE000u;
+      low = __float_as_uint(x - __uint_as_float(high)) & 0xFFFFE000u;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      cut_tf32(left[(g8 + 8 * (i & 1)) * kPitch + k + t4 + 4 * (i >> 1)], a[0][i], a[1][i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) cut_tf32(right[(k + t4 + 4 * i) * kPitch + g8], b[0][i], b[1][i]);
+    mma_tf32(d, a[0], b[1]);
+    mma_tf32(d, a[1], b[0]);
+    mma_tf32(d, a[0], b[0]);
+  }
+}
+// A product's 16 x 8 values to the scratch matrix, times `sign`.
+__device__ __forceinline__ void put_product(float *to, const float (&d)[4], float sign) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  *reinterpret_cast<float2 *>(to + g8 * kPitch + 2 * t4) = make_float2(sign * d[0], sign * d[1]);
+  *reinterpret_cast<float2 *>(to + (g8 + 8) * kPitch + 2 * t4) = make_float2(sign * d[2], sign * d[3]);
+}
+
 __global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const AdvanceArgs a,
                                                                       uint8_t *blobs) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -274,85 +312,45 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const Adva
     }
   }
   __syncthreads();
-  // the 16 x 16 blocks below them, -T11 (L10 T00) of each pair, four columns a thread
+  // the 16 x 16 blocks below them, -T11 (L10 T00) of each pair, eight columns a warp
   {
-    float *pair = scratch + 32 * (warp >> 1) * (kPitch + 1);
-    const int r = (tid & 63) >> 2, c4 = 4 * (tid & 3);
-    auto times = [&](const float *left_of, const float *right) {
-      float2 x0 = make_float2(0.f, 0.f), x1 = x0;
-#pragma unroll
-      for (int m = 0; m < 16; m += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(left_of + m);
-        const float w[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4 t = *reinterpret_cast<const float4 *>(right + (m + y) * kPitch);
-          x0 = __ffma2_rn(make_float2(w[y], w[y]), make_float2(t.x, t.y), x0);
-          x1 = __ffma2_rn(make_float2(w[y], w[y]), make_float2(t.z, t.w), x1);
-        }
-      }
-      return make_float4(x0.x, x0.y, x1.x, x1.y);
-    };
-    float *below = pair + (16 + r) * kPitch;
-    const float4 x = times(below, pair + c4);
-    __syncwarp();  // the rows of L10 that this warp reads are its own
-    *reinterpret_cast<float4 *>(below + c4) = x;
+    float *pair = scratch + 32 * (warp >> 1) * (kPitch + 1), *below = pair + 16 * kPitch;
+    const int col = 8 * (warp & 1);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    times<16>(d, below, pair + col);
+    __syncthreads();  // L10 has been read
+    put_product(below + col, d, 1.f);
     __syncthreads();
-    const float4 y = times(below + 16, pair + 16 * kPitch + c4);
+    float e[4] = {0.f, 0.f, 0.f, 0.f};
+    times<16>(e, below + 16, below + col);
     __syncthreads();
-    *reinterpret_cast<float4 *>(below + c4) = make_float4(-y.x, -y.y, -y.z, -y.w);
+    put_product(below + col, e, -1.f);
   }
   __syncthreads();
-  // the 32 x 32 block below, the same way, two rows by four columns a thread; T's
-  // columns take their beta as they are cut
-  const int r = 2 * (tid >> 3), c4 = 4 * (tid & 7);
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    // pass 0: X = L10 T00 in L10's place; pass 1: T11 X
-    const float *left_of = scratch + (32 + r) * kPitch + (pass ? 32 : 0);
-    const float *right = scratch + (pass ? 32 * kPitch : 0) + c4;
-    float2 x[2][2] = {};
-#pragma unroll
-    for (int m = 0; m < 32; m += 4) {
-      const float4 l0 = *reinterpret_cast<const float4 *>(left_of + m);
-      const float4 l1 = *reinterpret_cast<const float4 *>(left_of + kPitch + m);
-      const float w0[4] = {l0.x, l0.y, l0.z, l0.w}, w1[4] = {l1.x, l1.y, l1.z, l1.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float4 t = *reinterpret_cast<const float4 *>(right + (m + y) * kPitch);
-        const float2 lo = make_float2(t.x, t.y), hi = make_float2(t.z, t.w);
-        x[0][0] = __ffma2_rn(make_float2(w0[y], w0[y]), lo, x[0][0]);
-        x[0][1] = __ffma2_rn(make_float2(w0[y], w0[y]), hi, x[0][1]);
-        x[1][0] = __ffma2_rn(make_float2(w1[y], w1[y]), lo, x[1][0]);
-        x[1][1] = __ffma2_rn(make_float2(w1[y], w1[y]), hi, x[1][1]);
-      }
-    }
-    if (pass == 0) {
-      __syncwarp();
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        *reinterpret_cast<float4 *>(scratch + (32 + r + y) * kPitch + c4) =
-            make_float4(x[y][0].x, x[y][0].y, x[y][1].x, x[y][1].y);
-      __syncthreads();
-    } else {
-      const float4 be = *reinterpret_cast<const float4 *>(beta + c4);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const float v[4] = {-x[y][0].x * be.x, -x[y][0].y * be.y, -x[y][1].x * be.z,
-                            -x[y][1].y * be.w};
-        uint32_t part[kTParts][2];
-        cut<2, kTParts>(v, part);
-#pragma unroll
-        for (int p = 0; p < kTParts; ++p)
-          *reinterpret_cast<uint2 *>(blob + p * kPart + swizzled(32 + r + y, c4 >> 3) + (c4 & 7) * 2) =
-              make_uint2(part[p][0], part[p][1]);
-      }
-    }
+  // the 32 x 32 block below, the same way: 16 rows by 16 columns a warp
+  {
+    float *rows = scratch + (32 + 16 * (warp >> 1)) * kPitch;
+    const int col = 16 * (warp & 1);
+    float d[2][4] = {};
+    times<32>(d[0], rows, scratch + col);
+    times<32>(d[1], rows, scratch + col + 8);
+    __syncthreads();
+    put_product(rows + col, d[0], 1.f);
+    put_product(rows + col + 8, d[1], 1.f);
+    __syncthreads();
+    float e[2][4] = {};
+    times<32>(e[0], rows + 32, scratch + 32 * kPitch + col);
+    times<32>(e[1], rows + 32, scratch + 32 * kPitch + col + 8);
+    __syncthreads();
+    put_product(rows + col, e[0], -1.f);
+    put_product(rows + col + 8, e[1], -1.f);
   }
-  // the two diagonal blocks of 32, eight columns of two rows a thread
+  __syncthreads();
+  // T, its columns times their beta, in parts: eight columns of three rows a thread
 #pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    const int row = (tid >> 2) + 32 * y, piece = (tid & 3) + 4 * y;
+  for (int y = 0; y < 3; ++y) {
+    const int i = tid + y * kPrepThreads;  // rows 0..31: four pieces, 32..63: eight
+    const int row = i < 128 ? i >> 2 : 32 + ((i - 128) >> 3), piece = i < 128 ? i & 3 : i & 7;
     float v[8];
 #pragma unroll
     for (int x = 0; x < 8; x += 4) {
