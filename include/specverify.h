@@ -41,9 +41,9 @@
  * Conventions (all entry points):
  *  - Every tensor argument is a DEVICE pointer owned by the caller, to
  *    contiguous row-major memory (rope_kv_append, paged_attention, gdn_inputs
- *    and gdn_advance take a row stride for their packed rows).  The library allocates no device memory and
- *    keeps no pointer after a call returns, except a qmv plan (below), which
- *    holds the pointers it was created with.
+ *    and gdn_advance take a row stride for their packed rows).  The library
+ *    allocates no device memory and keeps no pointer after a call returns,
+ *    except a qmv plan (below), which holds the pointers it was created with.
  *  - Calls are asynchronous on `stream` (NULL = the legacy default stream) and
  *    never synchronise with the host -- except qmv_plan_create and the
  *    start-up probe qmv_identity_probe, which say so.
@@ -331,9 +331,12 @@ sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint1
  * [experts][inter][hidden / 64], down [experts][hidden][inter / 8] and
  * [experts][hidden][inter / 64].  y bf16 [rows][hidden], rounded once; ids int32
  * and weights fp32 [rows][top_k] receive the choice when not NULL.  Accuracy:
- * fp32 sums of exact products; the activations between the products are fp32,
- * split into two bf16 parts as qmv_smallm does with fp32 x.  A row depends on no
- * other row up to the order of its fp32 sums, and results do not depend on the run.
+ * fp32 sums of exact products of x, whose 64 inputs of a group are scaled by one
+ * power of two (a value below 2^-28 of its group's largest keeps fewer bits than
+ * bf16's); the activations between the products are fp32, split into two fp16 parts
+ * (2^-22 of their group's largest).  An infinity or a NaN in x reaches its own row
+ * alone.  A row depends on no other row up to the order of its fp32 sums, and
+ * results do not depend on the run.
  * Requires 0 <= rows <= 128 (0: no-op), 1 <= top_k <= 16, top_k <= experts <= 512,
  * hidden and inter multiples of 128, at most 65536; x, router, w_packed, scales
  * and biases 16-byte, y 8-byte aligned; no output overlaps an input or another output.
@@ -593,6 +596,9 @@ sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_dtype x_dty
  * [rows][Hk][dk], v and out [rows][Hv][dv], all fp32 or all bf16, their rows
  * q_row_stride etc. elements apart; alpha, beta fp32 [rows][Hv].  States and
  * sums are fp32, out is rounded once.
+ * bf16 rows with max_new from 32 on go 64 at a time: infinities and NaN among them
+ * then reach all 64 rows of their sequence and head that go together, and what
+ * follows; no other sequence.
  * Requires q, k, v, state and out 16-byte aligned, row strides multiples of 8
  * elements; neither out nor state overlaps an input or the other.  Results do
  * not depend on the run.

@@ -8,20 +8,26 @@
 // A few rows meet most of their experts once, so the layer streams the chosen
 // experts' weights (0.5625 bytes each) and is bound by memory.  Four launches,
 // the later ones starting as the one before drains:
-//  * route: 8 experts a CTA, K over its warps, bf16 MMAs (exact products, fp32
-//    sums), and the rows of x in the products' form; the last CTA of 16 rows chooses their experts, the last of all sorts
-//    the (row, expert) pairs by expert and cuts each expert's rows into slots of
-//    up to 8, the columns of one MMA;
+//  * route: 8 experts a CTA, K over its warps, bf16 MMAs (exact products, fp32 sums),
+//    and the rows of x in the products' form; the last CTA of 16 rows chooses their
+//    experts, the last of all sorts the (row, expert) pairs by expert and cuts each
+//    expert's rows into slots of up to 8, the columns of one MMA;
 //  * gate and up, then down: the stages of all slots' tiles laid out flat and cut
 //    evenly over the resident CTAs, so every SM streams the same number of bytes
 //    whichever experts were chosen.  A stage is 128 weight rows x 256 inputs: 64
 //    rows of gate and the same 64 of up (their product leaves in one place), or
 //    128 of down, with the rows' activations.  Eight warps take 32 rows by half of
-//    the inputs each.  A producer warp keeps the ring of stages full across tiles, and a warp of its
-//    own takes the sums of a finished tile, so that neither the copies nor the
-//    products wait for the fences below.  A tile cut between CTAs leaves partial
-//    sums, which whichever CTA comes last adds in CTA order; nobody waits for
-//    another CTA, so the launches need not be resident together.
+//    the inputs each.  A producer warp keeps the ring of stages full across tiles, and
+//    a warp of its own takes the sums of a finished tile, so that neither the copies
+//    nor the products wait for it.  A tile cut between CTAs leaves partial sums, which
+//    whichever CTA comes last adds in CTA order; nobody waits for another CTA, so the
+//    launches need not be resident together;
+//  * the sum of a row's experts, in the order of choice.
+// Measured (us, in a graph): one row of 2048 inputs, 8 of 256 experts of 512, 30.5 (7
+// MB, 4 launches of 4 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
+// experts of 1024, 75 (2.5 TB/s: the last launches 42, 30 and 4 us, of which 8 .. 10 us
+// each are the first loads, the merge of the split tiles and the launch); 128 rows of
+// 2048, 6 of 96 experts of 1024, 168 (2.0 TB/s: products and the widening of nibbles).
 //
 // The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
 // the odd ones, left where they are, as 1024 + 16 q against activations divided by
@@ -57,12 +63,12 @@ struct Group {
 };
 constexpr uint32_t kRecord = kGroupsOf * (128 + (uint32_t)sizeof(Group));  // 576
 constexpr uint32_t kXOff = 2 * kRows * 128;
-// Scales, then biases, of a block of two stages: [128 rows][8 groups] bf16.
-constexpr int kBlock = 2;
+// Scales, then biases, of a block of four stages: [128 rows][16 groups] bf16.
+constexpr int kBlock = 4;
 constexpr uint32_t kSbRow = kBlock * kGroupsOf * 2, kSbBytes = kTileRows * kSbRow;
 template <bool kDown>
 struct Ring {  // down: the two parts of eight rows
-  static constexpr int kStages = kDown ? 3 : 4, kRecords = kDown ? 16 : 8;
+  static constexpr int kStages = kDown ? 2 : 3, kRecords = kDown ? 16 : 8;
   static constexpr uint32_t kStage = (kXOff + kRecords * kRecord + 1023) / 1024 * 1024;
   static constexpr uint32_t kSbOff = kStages * kStage;  // two blocks
   static constexpr uint32_t kRedOff = kSbOff + 2 * 2 * kSbBytes;
@@ -646,10 +652,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 
   if (warp == kWarps) {
     // ---- producer: weights by tensor copies, records by bulk copies, scales and
-    // biases by small copies of four lanes (or eight) a row, four stages at a time: a
-    // row's 32 bytes are one sector or two then, where a stage's 8 bytes of a row at a
-    // time held the loads in flight up (gate and up of 4 rows, 5120 x 1024: 32 us against
-    // 25 without these copies; as tensor boxes of 16-byte rows 39) ---------------------
+    // biases by small copies of a lane 8 (or 4) bytes, a block of four stages at a time: a
+    // row's 32 bytes.  (Gate and up of 4 rows, 5120 x 1024, take 32 us with these copies
+    // and 25 without; as tensor boxes of 16-byte rows 39.  Two stages a block and rings
+    // of 4 and 3 stages: 128 rows in 177 us, as against 168.)  ---------------------------
     const bool wide = groups % 4 == 0;
     int st = 0, ph = 0, issued = 0, blocks = 0;
     bool ok = true;
@@ -851,6 +857,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     if (ok && (threadIdx.x ? split1 : split0)) {
       const long long t0 = (long long)tile * stages;
       const uint32_t others = (uint32_t)(((t0 + stages) * ctas - 1) / W - ((t0 + 1) * ctas - 1) / W);
+      __threadfence();  // the finisher's partial sums before the count
       is = atomicAdd(a.ws.tiles + tile, 1u) == others;
       if (is) a.ws.tiles[tile] = 0u;
       __threadfence();
