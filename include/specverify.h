@@ -605,7 +605,8 @@ sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_dtype x_dty
  * workspace: gdn_advance_workspace_bytes(..) bytes (0 where none is needed, as for
  * single tokens and fp32 rows; else 41984 a head and 64 rows begun), 256-byte
  * aligned, with no required contents; it overlaps no other argument.  Calls that
- * run concurrently need workspaces of their own.  One launch on `stream`, or two. */
+ * run concurrently need workspaces of their own.  One launch on `stream`, or two, the
+ * second with a programmatic dependency on the first. */
 size_t gdn_advance_workspace_bytes(sv_dtype dtype, int B, int rows, int max_new, int Hv);
 sv_status gdn_advance(const void *q, const void *k, const void *v, sv_dtype dtype,
                       long long q_row_stride, long long k_row_stride, long long v_row_stride,

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const Adva
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw);
+  pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, place = blockIdx.x / a.H, hk = h / (a.H / a.Hk);
   int c;
@@ -808,6 +809,7 @@ __device__ void load_chunks(const CUtensorMap *kmap, const CUtensorMap *qmap, co
   auto bar = [&](int i) { return base + kOffBars + 8u * i; };
   bool ok = true;
   int c = 0;
+  pdl_wait();  // T and P are the launch before's; what all others read is older
   for (; c < it.chunks; ++c) {
     const uint32_t s = c & 1, at = base + s * kStage;
     if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait_u32(bar(kEmpty + s), ((c >> 1) & 1) ^ 1));
@@ -874,13 +876,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.n = s.n;
     it.slot = slot_of(a.state_index, b, a.slots);
   }
-  if (it.n == 0) return;
+  if (it.n == 0) return pdl_wait();
   if (it.slot < 0) {  // zeros
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (long long)it.start * a.out_stride +
                          (long long)it.h * a.dv;
     for (long long i = threadIdx.x; i < (long long)it.n * a.dv; i += kThreads)
       out[i / a.dv * a.out_stride + i % a.dv] = __float2bfloat16_rn(0.f);
-    return;
+    return pdl_wait();
   }
   it.chunks = (it.n + kC - 1) / kC;
   it.blob = (long long)(it.start / kC + b) * a.H + it.h;
@@ -976,8 +978,23 @@ sv_status chunk_run(const AdvanceArgs &a, void *workspace, cudaStream_t stream) 
     st = check_launch("gdn_advance");
     if (st != SV_OK) return st;
   }
-  const dim3 grid((unsigned)a.H, (unsigned)a.B + 1);
-  gdn_chunk_states<<<grid, kThreads, kSmem, stream>>>(kmap, qmap, vmap, omap, a, blobs);
+  // The states' launch begins as the matrices' drains.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.H, (unsigned)a.B + 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = items > 0 ? 1 : 0;
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, gdn_chunk_states, kmap, qmap, vmap, omap, a,
+                                            static_cast<const uint8_t *>(blobs));
+  if (le != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(SV_ERR_CUDA, "gdn_advance: launch failed: %s", cudaGetErrorString(le));
+  }
   return check_launch("gdn_advance");
 }
 
