@@ -13,6 +13,11 @@
 // a CTA reads and writes runs of 1 KB.  The tiles begin at the sequences' first rows: a
 // sequence's first tile alone reads its window, and the same warp writes it, so
 // one launch needs no order among its CTAs.
+// Measured, 10240 channels and 48 heads, bf16, W = 4: three prompts of 7519 rows in all
+// 81 us (313 MB, 3.9 TB/s; ncu: issue 51 %, DRAM 43 %: a batch's loads, then its
+// arithmetic; with fewer warps and no batch ahead 236 us), 256 single tokens with
+// their windows 27 us (74 MB); four rows of one sequence 5 us, a launch and its
+// dependent loads.
 #include <cuda_runtime.h>
 
 #include "gdn_rows.cuh"

@@ -29,9 +29,9 @@ __device__ __forceinline__ int slot_of(const int32_t *index, int b, int slots) {
 
 // Tiles of 1 << shift rows that begin at the sequences' first rows, numbered so that
 // sequence b's first is (q_start[b] >> shift) + b: room for the tiles of every sequence
-// before it, those that are not full included.  The owner of tile number i, in [0, B] (B: the rows past
-// the last sequence), and its place j among the owner's tiles (past its last: no
-// such tile).  By a whole warp.
+// before it, those that are not full included.  The owner of tile number i, in [0, B]
+// (B: the rows past the last sequence), and its place j among the owner's tiles (past
+// its last: no such tile).  By a whole warp.
 __device__ __forceinline__ int tile_owner(const int32_t *q_start, int B, int rows, int shift, int i,
                                           int &j) {
   const int lane = threadIdx.x & 31;
