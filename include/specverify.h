@@ -343,8 +343,8 @@ sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint1
  * workspace: moe_smallm_workspace_bytes(..) bytes on the current device (0 on
  * invalid input; *zero_bytes, when given, is how many of the first are arrival
  * counters: zero before its first call, every call leaves them zero), 256-byte
- * aligned; it belongs to these sizes, and calls that run concurrently need
- * workspaces of their own.  Four launches on `stream`, all but the first with a
+ * aligned; it belongs to these sizes and any fewer rows of them, and calls that run
+ * concurrently need workspaces of their own.  Four launches on `stream`, all but the first with a
  * programmatic dependency on the one before.  A kernel wait that gives up sets a
  * word read by sv_device_status; the counters are then undefined. */
 size_t moe_smallm_workspace_bytes(int rows, int hidden, int inter, int experts, int top_k,

@@ -1055,7 +1055,7 @@ def moe_smallm_workspace_bytes(rows: int, hidden: int, inter: int, experts: int,
 
 def make_moe_workspace(rows: int, hidden: int, inter: int, experts: int, top_k: int,
                        device) -> torch.Tensor:
-    """A workspace (uint8) for moe_smallm with these sizes."""
+    """A workspace (uint8) for moe_smallm with these sizes, and any fewer rows."""
     device = torch.device(device)
     with torch.cuda.device(device):
         n, zero = moe_smallm_workspace_bytes(rows, hidden, inter, experts, top_k)
@@ -1074,8 +1074,8 @@ def moe_smallm(x: torch.Tensor, router: torch.Tensor, gate, up, down, top_k: int
     and up and hidden, inter for down.  Each row takes its ``top_k`` experts, weighted
     by the softmax over them (over all experts without ``renormalize``).  Returns out
     bf16 [rows, hidden]; ids int32 and weights fp32 [rows, top_k] receive the choice
-    when given.  ``workspace`` (from make_moe_workspace with these sizes) is made per
-    call when omitted."""
+    when given.  ``workspace`` (from make_moe_workspace with these sizes, or more rows) is
+    made per call when omitted."""
     if x.dim() != 2 or gate[0].dim() != 3:
         raise ValueError("x must be [rows, hidden] and the weights [experts, N, K/8]")
     index = _on(x, "x")

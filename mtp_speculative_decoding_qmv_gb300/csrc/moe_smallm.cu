@@ -86,7 +86,7 @@ constexpr int kPartFloats = kTileRows * kSlotRows;
 
 __device__ unsigned int g_moe_device_error;
 
-struct Slot {
+struct alignas(16) Slot {
   int expert, first, n, pad;
 };
 // What the caller's workspace holds.  The counters come first: zero before a call
@@ -120,8 +120,9 @@ Space space_of(void *base, int rows, int hidden, int inter, int experts, int top
   };
   const size_t pairs = (size_t)rows * top, slots = (size_t)slots_most(rows, experts, top);
   const size_t up = inter / 64, down = hidden / kTileRows;
+  // the counters' place is that of the most rows, so that a workspace serves any fewer
   take(s.routed, kMaxRows / 16 + 1);
-  take(s.tiles, slots * std::max(up, down));
+  take(s.tiles, (size_t)slots_most(kMaxRows, experts, top) * std::max(up, down));
   s.counters = at;
   take(s.logits, (size_t)rows * experts);
   take(s.ids, pairs);
@@ -631,8 +632,9 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 
   // lane c: pair and weight of column c of a slot
   auto columns_of = [&](const Segment &g, int &n, int &pair, float &weight) {
-    n = __ldcg(&a.ws.slots[g.slot].n);
-    pair = lane < n ? __ldcg(a.ws.order + __ldcg(&a.ws.slots[g.slot].first) + lane) : 0;
+    const int4 facts = __ldcg(reinterpret_cast<const int4 *>(a.ws.slots + g.slot));
+    n = facts.z;
+    pair = lane < n ? __ldcg(a.ws.order + facts.y + lane) : 0;
     weight = kDown && lane < n ? __ldcg(a.ws.weights + pair) : 0.f;
   };
   // a column's sums, rows 2 lane and 2 lane + 1 of both blocks of a tile
@@ -671,19 +673,28 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
         if (i < issued && pending[i])
           load_record(base + i * R::kStage + kXOff + lane * kRecord, pending[i], full0 + 8u * i);
     };
+    // a slot's facts, read again where the slot changes: two trips to memory
+    int slot = -1, n = 0;
+    long long expert0 = 0;
+    bool brings = false;
+    const uint8_t *from = nullptr;
     for (long long u = u_begin; ok && u < u_end;) {
       const Segment g = segment(u);
       u += g.s1 - g.s0;
-      const long long row0 = (long long)__ldcg(&a.ws.slots[g.slot].expert) * N + g.n0;
-      // lane r brings record r: of row r, or of down's two parts r < n and the rest,
-      // from place 4 on (up to four rows) or 8
-      const int n = __ldcg(&a.ws.slots[g.slot].n), apart = n <= 4 ? 4 : 8;
-      const int col = kDown ? lane % apart : lane;
-      const bool brings = col < n && lane < (kDown ? 2 * apart : kSlotRows);
-      const int pair = brings ? __ldcg(a.ws.order + __ldcg(&a.ws.slots[g.slot].first) + col) : 0;
-      const uint8_t *from =
-          kDown ? a.ws.h + ((size_t)pair + (lane >= apart ? pairs : 0)) * stages * kRecord
-                : a.ws.x + (size_t)(pair / a.top) * stages * kRecord;
+      if (g.slot != slot) {
+        slot = g.slot;
+        const int4 facts = __ldcg(reinterpret_cast<const int4 *>(a.ws.slots + slot));
+        expert0 = (long long)facts.x * N;
+        n = facts.z;
+        // lane r brings record r: of row r, or of down's two parts r < n and the rest,
+        // from place 4 on (up to four rows) or 8
+        const int apart = n <= 4 ? 4 : 8, col = kDown ? lane % apart : lane;
+        brings = col < n && lane < (kDown ? 2 * apart : kSlotRows);
+        const int pair = brings ? __ldcg(a.ws.order + facts.y + col) : 0;
+        from = kDown ? a.ws.h + ((size_t)pair + (lane >= apart ? pairs : 0)) * stages * kRecord
+                     : a.ws.x + (size_t)(pair / a.top) * stages * kRecord;
+      }
+      const long long row0 = expert0 + g.n0;
       auto bring_block = [&](int block) {
         const uint32_t at = base + R::kSbOff + (blocks & 1) * 2 * kSbBytes;
         const uint16_t *from[4] = {kDown ? a.down_s : a.gate_s, kDown ? a.down_s : a.up_s,
@@ -763,14 +774,14 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   if (warp == kWarps + 1) {
     // ---- finisher: a tile's sums to where they go -----------------------------------
     if (kDown) pdl_wait();  // the partials' places are the launch before's
-    int k = 0;
+    int k = 0, slot = -1, n = 0, pair = 0;
+    float weight = 0.f;
     bool ok = true;
     for (long long u = u_begin; ok && u < u_end; ++k) {
       const Segment g = segment(u);
       u += g.s1 - g.s0;
-      int n, pair;
-      float weight;
-      columns_of(g, n, pair, weight);
+      if (g.slot != slot) columns_of(g, n, pair, weight);
+      slot = g.slot;
       const bool whole = g.s0 == 0 && g.s1 == stages;
       // down's slots of up to four rows have the second parts' sums in columns 4..7
       const bool doubled = kDown && n <= 4;
@@ -810,12 +821,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 
   // ---- the products ----------------------------------------------------------------
   const int rows0 = 32 * (warp & 3), half = warp >> 2;
-  int st = 0, ph = 0, blocks = 0, k = 0;
+  int st = 0, ph = 0, blocks = 0, k = 0, slot = -1, n = 0;
   bool ok = true;
   for (long long u = u_begin; ok && u < u_end; ++k) {
     const Segment g = segment(u);
     u += g.s1 - g.s0;
-    const int n = __ldcg(&a.ws.slots[g.slot].n);
+    if (g.slot != slot) n = __ldcg(&a.ws.slots[g.slot].n);
+    slot = g.slot;
     float acc[2][4] = {};
     if (kDown && n > 4)
       ok = multiply<kDown, kDown>(acc, base, full0, empty0, sb_full0, sb_empty0, st, ph, blocks, g.s0, g.s1,

@@ -267,6 +267,16 @@ def test_experts_largest_sizes(sv, rows, hidden, inter, experts, top):
     sv.device_status()
 
 
+def test_a_workspace_of_more_rows_serves_fewer(sv):
+    layers = [Experts(rows, 512, 384, 20, 3, seed=rows) for rows in (128, 3, 100, 1, 17, 128)]
+    ws = sv.make_moe_workspace(128, 512, 384, 20, 3, dev())
+    for e in layers:
+        check_experts(e, e.run(sv, workspace=ws))
+    n, zero = sv.moe_smallm_workspace_bytes(128, 512, 384, 20, 3)
+    assert not ws[:zero].any()
+    sv.device_status()
+
+
 @pytest.mark.parametrize("rows", [1, 7, 40])
 def test_experts_of_zero_inputs_and_wide_ranges(sv, rows):
     """Groups of zeros, and groups whose values span 2^24."""

@@ -59,7 +59,7 @@ def test_inputs_refuses(L, kw):
 
 
 @pytest.mark.parametrize("kw", [
-    {"dk": 4}, {"dv": 0}, {"dk": 12}, {"dv": 136}, {"W": 1}, {"W": 9}, {"Hk": 1, "Hv": 16385},
+    {"dk": 4}, {"dv": 0}, {"dk": 12}, {"dv": 136}, {"W": 1}, {"W": 9}, {"Hk": 1, "Hv": 16385}, {"B": 70000, "slots": 70000},
 ], ids=str)
 def test_inputs_does_not_support(L, kw):
     assert inputs(L, **kw) == UNSUPPORTED
@@ -155,6 +155,9 @@ def test_moe_workspace_bytes(L):
     assert L.moe_smallm_workspace_bytes(0, 256, 128, 8, 2, None) > 0
     for sizes in ((1, 128, 128, 1, 1), (128, 2048, 1024, 96, 6), (128, 65536, 128, 512, 16)):
         n = L.moe_smallm_workspace_bytes(*sizes, ctypes.byref(zero))
+        # one for more rows serves fewer: no more bytes, and the counters' place is the same
+        counters, least = zero.value, L.moe_smallm_workspace_bytes(1, *sizes[1:], ctypes.byref(zero))
+        assert least <= n and zero.value == counters
         assert 0 < zero.value < n and zero.value % 256 == n % 256 == 0
         rows, hidden, _, _, top = sizes
         assert n > rows * top * hidden * 4
