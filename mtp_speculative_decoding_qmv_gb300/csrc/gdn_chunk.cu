@@ -21,8 +21,8 @@
 // bf16 parts that add up to it exactly (8 bits of it each), so what reaches the
 // state is fp32-exact products of K and V (bf16 as given): S0 K^T, E' K and V T^T
 // with three parts, R T^T with the six products of parts above 2^-24.  The output,
-// bf16 in the end, takes two parts of S0 and P (2^-16) and E rounded to bf16: at
-// most its own rounding once more.
+// bf16 in the end, takes two parts of S0, P and E (2^-15).  (E rounded to bf16: 5 %
+// faster, but outputs were off by 1.2 to 1.45 times their own rounding.)
 //
 // What bounds the second is the chain from chunk to chunk: tensor-core time of S0
 // K^T, R T^T and E' K (about 2000 cycles a chunk), and between them the warps that
@@ -31,9 +31,9 @@
 // the other half is cut.  S0 Q^T, V T^T and E P^T run in the gaps, and the outputs
 // leave by four warps of their own.
 //
-// Measured, 48 heads of 128 x 128: a prompt of 5000 rows 300 us in a graph (matrices
-// 60, states 242: 3.1 us a chunk; 79 TFLOP/s of the recurrence's own operations), five
-// prompts of 77 to 2000 rows 186 us, 64 rows 15 us.  The second launch begins as the
+// Measured, 48 heads of 128 x 128: a prompt of 5000 rows 317 us in a graph (matrices
+// 60, states 257: 3.2 us a chunk; 74 TFLOP/s of the recurrence's own operations), five
+// prompts of 77 to 2000 rows 192 us, 64 rows 15 us.  The second launch begins as the
 // first drains (4 to 5 us less).  Both in one launch, chains waiting for each chunk's
 // matrices: 338 us, as the matrices' code costs the chains registers.
 #include <cuda.h>
@@ -419,6 +419,11 @@ __host__ __device__ constexpr uint32_t state_col(int half, int part, int step) {
          (part < 2 ? 32 * (step >> 1) + 16 * part : 64 + 16 * (step >> 1)) + 8 * (step & 1);
 }
 
+// E's parts over S0 K^T: each half's over the columns that the warps of that half have read.
+__host__ __device__ constexpr uint32_t e_col(int part, int step) {
+  return 32 * (step >> 1) + 16 * part + 8 * (step & 1);
+}
+
 constexpr uint32_t idesc(int n, bool mn_major, bool a_mn_major = false) {
   return (1u << 4) | (1u << 7) | (1u << 10)  // D fp32; A, B bf16
          | (a_mn_major ? 1u << 15 : 0u) | (mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kD >> 4) << 24);
@@ -476,27 +481,34 @@ struct Item {
   long long blob;  // of its first chunk; the next H further
 };
 
-// R T^T or E P^T, D[dv][64 rows] (+)= A parts x B parts, both lower triangular: the
-// 16 columns of step j reach the rows from 16 j on.  Steps [kJ0, kJ1), begun by step
-// 0 unless kAdd.  Parts whose weights add up past `kLeast` are left out.  Here and
-// below the least parts come first: a sum in tensor memory is cut off, not rounded, at
-// each step, and a small sum loses less by it (the states of a prompt: 7e-7, as
-// against 11e-7, relative to their norm).
-template <int kNa, int kNb, int kLeast, int kJ0, int kJ1, bool kAdd>
+// R T^T, D[dv][64 rows] += A parts x B parts, both lower triangular: the 16 columns of
+// step j reach the rows from 16 j on.  Steps [kJ0, kJ1).  Parts whose weights add up past
+// 2 are left out.  Here and below the least parts come first: a sum in tensor memory is
+// cut off, not rounded, at each step, and a small sum loses less by it (the states of a
+// prompt: 7e-7, as against 11e-7, relative to their norm).
+template <int kJ0, int kJ1>
 __device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b) {
-  static_assert(kAdd || (kJ0 == 0 && kLeast < kNb), "the first product is that of A's part 0");
 #pragma unroll
-  for (int weight = kLeast; weight >= 0; --weight)
+  for (int weight = 2; weight >= 0; --weight)
 #pragma unroll
-    for (int pa = 0; pa < kNa; ++pa) {
-      const int pb = weight - pa;
-      if (pb < 0 || pb >= kNb) continue;
+    for (int pa = 0; pa <= weight; ++pa)
 #pragma unroll
       for (int j = kJ0; j < kJ1; ++j)
         tc_mma_ts(d + 16 * j, a + 32 * pa + 8 * j,
-                  smem_desc_sw128(b + pb * kPart + j * 2048 + j * 32), idesc(kC - 16 * j, false),
-                  kAdd || weight < kLeast || pa + j > 0);
-    }
+                  smem_desc_sw128(b + (weight - pa) * kPart + j * 2048 + j * 32),
+                  idesc(kC - 16 * j, false), true);
+}
+// E P^T, the same, of two parts each.
+__device__ __forceinline__ void mma_out(uint32_t d, uint32_t e, uint32_t p) {
+#pragma unroll
+  for (int weight = 1; weight >= 0; --weight)
+#pragma unroll
+    for (int pa = 0; pa <= weight; ++pa)
+#pragma unroll
+      for (int j = 0; j < kC / 16; ++j)
+        tc_mma_ts(d + 16 * j, e + e_col(pa, j),
+                  smem_desc_sw128(p + (weight - pa) * kPart + j * 2048 + j * 32),
+                  idesc(kC - 16 * j, false), weight == 0 || pa + j > 0);
 }
 // V T^T, the same with V from shared memory, dv contiguous.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t t) {
@@ -560,13 +572,13 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
     __syncwarp();
     if (!wait(kR, odd)) break;
     if (one) {
-      mma_lower<3, 3, 2, 0, 2, true>(tmem + kColE, tmem + kColR, t_at);
+      mma_lower<0, 2>(tmem + kColE, tmem + kColR, t_at);
       tc_commit(bar(kTr));
     }
     __syncwarp();
     if (!wait(kR + 1, odd)) break;
     if (one) {
-      mma_lower<3, 3, 2, 2, 4, true>(tmem + kColE, tmem + kColR, t_at);
+      mma_lower<2, 4>(tmem + kColE, tmem + kColR, t_at);
       tc_commit(bar(kTr + 1));
       mma_state<2, 64>(tmem + kColQ, tmem, q_at, 0);
       mma_state<2, 64>(tmem + kColQ, tmem, q_at, 1);
@@ -585,7 +597,7 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
       tc_commit(bar(kSu));
       mma_update(tmem, k_at, 1, 2);
       tc_commit(bar(kSu + 1));
-      mma_lower<1, 2, 1, 0, 4, false>(tmem + kColE, tmem + kColK, p_at);
+      mma_out(tmem + kColE, tmem + kColK, p_at);
       tc_commit(bar(kOut));
       tc_commit(bar(kEmpty + s));
     }
@@ -685,14 +697,10 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
       cut<8, 3>(e, part);
 #pragma unroll
       for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
-      uint32_t whole[8];
+      uint32_t whole[2][8];
+      cut<8, 2>(reinterpret_cast<const float *>(x), whole);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 y =
-            __floats2bfloat162_rn(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-        whole[j] = *reinterpret_cast<const uint32_t *>(&y);
-      }
-      tc_st_x8(tmem + kColK + 8 * g, whole);
+      for (int p = 0; p < 2; ++p) tc_st_x8(tmem + kColK + e_col(p, g), whole[p]);
       tc_wait_st();
       arrive(kE + half);
     }

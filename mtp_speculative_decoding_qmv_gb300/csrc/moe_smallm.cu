@@ -25,9 +25,9 @@
 //  * the sum of a row's experts, in the order of choice.
 // Measured (us, in a graph): one row of 2048 inputs, 8 of 256 experts of 512, 30.5 (7
 // MB, 4 launches of 4 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
-// experts of 1024, 75 (2.5 TB/s: the last launches 42, 30 and 4 us, of which 8 .. 10 us
+// experts of 1024, 72 .. 76 (2.5 TB/s: the last launches 42, 30 and 4 us, of which 8 .. 10 us
 // each are the first loads, the merge of the split tiles and the launch); 128 rows of
-// 2048, 6 of 96 experts of 1024, 168 (2.0 TB/s: products and the widening of nibbles).
+// 2048, 6 of 96 experts of 1024, 163 (2.1 TB/s: products and the widening of nibbles).
 //
 // The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
 // the odd ones, left where they are, as 1024 + 16 q against activations divided by
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     // biases by small copies of a lane 8 (or 4) bytes, a block of four stages at a time: a
     // row's 32 bytes.  (Gate and up of 4 rows, 5120 x 1024, take 32 us with these copies
     // and 25 without; as tensor boxes of 16-byte rows 39.  Two stages a block and rings
-    // of 4 and 3 stages: 128 rows in 177 us, as against 168.)  ---------------------------
+    // of 4 and 3 stages: 128 rows in 177 us, as against 173.)  ---------------------------
     const bool wide = groups % 4 == 0;
     int st = 0, ph = 0, issued = 0, blocks = 0;
     bool ok = true;
