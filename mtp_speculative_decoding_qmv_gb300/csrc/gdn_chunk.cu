@@ -21,7 +21,7 @@
 // bf16 parts that add up to it exactly (8 bits of it each), so what reaches the
 // state is fp32-exact products of K and V (bf16 as given): S0 K^T, E' K and V T^T
 // with three parts, R T^T with the six products of parts above 2^-24.  The output,
-// bf16 in the end, takes two parts of S0, P and E (2^-15).  (E rounded to bf16: 5 %
+// bf16 in the end, takes two parts of S0, P and E (2^-13 of the terms).  (E rounded to bf16: 5 %
 // faster, but outputs were off by 1.2 to 1.45 times their own rounding.)
 //
 // What bounds the second is the chain from chunk to chunk: tensor-core time of S0

@@ -27,7 +27,7 @@
 // MB, 4 launches of 4 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
 // experts of 1024, 72 .. 76 (2.5 TB/s: the last launches 42, 30 and 4 us, of which 8 .. 10 us
 // each are the first loads, the merge of the split tiles and the launch); 128 rows of
-// 2048, 6 of 96 experts of 1024, 163 (2.1 TB/s: products and the widening of nibbles).
+// 2048, 6 of 96 experts of 1024, 163 .. 168 (2.1 TB/s: products and the widening of nibbles).
 //
 // The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
 // the odd ones, left where they are, as 1024 + 16 q against activations divided by

@@ -65,8 +65,9 @@ def advance(q, k, v, alpha, beta, state, q_start, index=None, chunk=1, tol=0.0):
     with dk + chunk <= 256 terms and 6 operations on each at most 40 half steps
     of (|s| + |v| + |e of the last rows|) |k|.
 
-    Of bf16 rows in chunks the output also takes every e_j rounded to bf16, and
-    the chunk's first state and the factors of the e_j cut off after 16 bits."""
+    Of bf16 rows in chunks the output takes the chunk's first state, every e_j and
+    their factors in two bf16 parts each, cut off: 2^-15 of the value is left out, and
+    the product of two second parts, below 2^-14 of theirs."""
     q, k, v, alpha, beta = (np.asarray(t, np.float64) for t in (q, k, v, alpha, beta))
     state = np.asarray(state, np.float64).copy()
     rows, Hk, dk = q.shape
@@ -101,5 +102,5 @@ def advance(q, k, v, alpha, beta, state, q_start, index=None, chunk=1, tol=0.0):
             if chunk > 1:
                 factors = np.abs(np.einsum("jhd,hd->jh", np.array(past_k), qq)) * np.array(gates)
                 terms = np.einsum("jh,jhi->hi", factors, np.array(past_e))
-                out_tol[r] += (HALF_BF16 + 2.0 ** -15) * terms + 2.0 ** -15 * first * g0[:, None] * qn
+                out_tol[r] += 2.0 ** -13 * terms + 2.0 ** -15 * first * g0[:, None] * qn
     return out, state, out_tol, tol
