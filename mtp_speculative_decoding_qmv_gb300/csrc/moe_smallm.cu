@@ -23,10 +23,10 @@
 //    whichever CTA comes last adds in CTA order; nobody waits for another CTA, so the
 //    launches need not be resident together;
 //  * the sum of a row's experts, in the order of choice.
-// Measured (us, in a graph): one row of 2048 inputs, 8 of 256 experts of 512, 30.5 (7
-// MB, 4 launches of 4 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
-// experts of 1024, 72 .. 76 (2.5 TB/s: the last launches 42, 30 and 4 us, of which 8 .. 10 us
-// each are the first loads, the merge of the split tiles and the launch); 128 rows of
+// Measured (us, in a graph): one row of 2048 inputs, 8 of 256 experts of 512, 27 (15
+// MB, 4 launches of 3 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
+// experts of 1024, 68 (2.7 TB/s: the later launches' first loads, the merge of the
+// split tiles and the launch itself are 8 .. 10 us each); 128 rows of
 // 2048, 6 of 96 experts of 1024, 163 .. 168 (2.1 TB/s: products and the widening of nibbles).
 //
 // The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
@@ -613,9 +613,17 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
   const int tiles = N / kStep, stages = (K + kStageK - 1) / kStageK, groups = K / 64;
   const int n_slots = __ldcg(a.ws.n_slots), pairs = a.rows * a.top;
   const long long W = (long long)n_slots * tiles * stages;
-  const int ctas = (int)min((long long)gridDim.x, W);
-  if ((int)blockIdx.x >= ctas) return;
-  const long long u_begin = W * blockIdx.x / ctas, u_end = W * (blockIdx.x + 1) / ctas;
+  // Units a CTA: as few as the CTAs allow, or up to a quarter more where a tile is then
+  // cut evenly, or not at all (W is below 2^28): a CTA with ends of two tiles joins both
+  // of them.  (Us, without and with: one row, 8 of 256 experts, 2048 x 512, 30.5 and
+  // 27.1; 4 rows, 6 of 64, 5120 x 1024, 72.7 and 67.9; 19 rows, 4 of 60, 2560 x 896, 73.7
+  // and 69.8.  Up to half more: 27.7, 69.8, 70.1, and 128 rows 172 as against 167.)
+  const int least = (int)((W + gridDim.x - 1) / gridDim.x);
+  int p = least;
+  while (4 * p <= 5 * least && (p < stages ? stages % p : p % stages) != 0) ++p;
+  if (4 * p > 5 * least) p = least;
+  const long long u_begin = (long long)p * blockIdx.x, u_end = min(W, u_begin + p);
+  if (u_begin >= W) return;
 
   struct Segment {
     int tile, slot, n0, s0, s1;
@@ -868,7 +876,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     bool is = false;
     if (ok && (threadIdx.x ? split1 : split0)) {
       const long long t0 = (long long)tile * stages;
-      const uint32_t others = (uint32_t)(((t0 + stages) * ctas - 1) / W - ((t0 + 1) * ctas - 1) / W);
+      const uint32_t others = (uint32_t)(((int)t0 + stages - 1) / p - (int)t0 / p);
       __threadfence();  // the finisher's partial sums before the count
       is = atomicAdd(a.ws.tiles + tile, 1u) == others;
       if (is) a.ws.tiles[tile] = 0u;
@@ -883,7 +891,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     if (!(i ? last1 : last0)) continue;
     const long long t0 = (long long)(i ? tile1 : tile0) * stages;
     const Segment g = segment(t0);
-    const int c0 = (int)(((t0 + 1) * ctas - 1) / W), c1 = (int)(((t0 + stages) * ctas - 1) / W);
+    const int c0 = (int)t0 / p, c1 = ((int)t0 + stages - 1) / p;
     int n, pair;
     float weight;
     columns_of(g, n, pair, weight);
