@@ -11,18 +11,21 @@
 //   E = V T^T + R T^T, R = -G S0 K^T;  O = G S0 Q^T + E P^T;  S = G[63] S0 + E' K
 // Two launches.  The first makes T and P of every chunk of every head, all chunks
 // side by side (mma.sync for K K^T and Q K^T, whose results are wanted in
-// registers; T by substitution in fp32).  The second follows the state from chunk
+// registers; T by substitution).  The second follows the state from chunk
 // to chunk, a CTA a (sequence, head): six products a chunk, each with 128 rows
 // (dv) in tensor memory's lanes; S0, R and E are A operands in tensor memory, V in
 // shared memory, K, Q, T and P (bf16, shared memory) are B.  K serves both as rows of
 // dk (S0 K^T) and with dk contiguous (E' K), from one copy.
 //
-// Precision: the state stays in fp32 registers.  An fp32 operand is cut into three
-// bf16 parts that add up to it exactly (8 bits of it each), so what reaches the
-// state is fp32-exact products of K and V (bf16 as given): S0 K^T, E' K and V T^T
-// with three parts, R T^T with the six products of parts above 2^-24.  The output,
-// bf16 in the end, takes two parts of S0, P and E (2^-13 of the terms).  (E rounded to bf16: 5 %
-// faster, but outputs were off by 1.2 to 1.45 times their own rounding.)
+// Precision: the state stays in fp32 registers, and outputs are sums to fp32 rounded
+// once.  An fp32 operand is cut into three bf16 parts that add up to it exactly (8 bits
+// of it each): S0 K^T, S0 Q^T, E' K and V T^T take all three (K, Q and V are bf16 as
+// given), R T^T and E P^T the six products of parts above 2^-24.  T's diagonal blocks
+// of 16 are made in fp32, those below by products of two tf32 parts (2^-21 of the
+// terms).  Sums in tensor memory are cut off at each step, which leaves a prompt's
+// states off by 7e-7.  (S0, P and E in two parts for the outputs: 317 us where three
+// take 328, but 1 % of the outputs of a chunk were not the bf16 nearest to the exact
+// value, as against 0.03 %.)
 //
 // What bounds the second is the chain from chunk to chunk: tensor-core time of S0
 // K^T, R T^T and E' K (about 2000 cycles a chunk), and between them the warps that
@@ -31,9 +34,9 @@
 // the other half is cut.  S0 Q^T, V T^T and E P^T run in the gaps, and the outputs
 // leave by four warps of their own.
 //
-// Measured, 48 heads of 128 x 128: a prompt of 5000 rows 317 us in a graph (matrices
-// 60, states 257: 3.2 us a chunk; 74 TFLOP/s of the recurrence's own operations), five
-// prompts of 77 to 2000 rows 192 us, 64 rows 15 us.  The second launch begins as the
+// Measured, 48 heads of 128 x 128: a prompt of 5000 rows 328 us (matrices
+// 60, states 268: 3.4 us a chunk; 72 TFLOP/s of the recurrence's own operations), five
+// prompts of 77 to 2000 rows 198 us, 64 rows 15 us.  The second launch begins as the
 // first drains (4 to 5 us less).  Both in one launch, chains waiting for each chunk's
 // matrices: 338 us, as the matrices' code costs the chains registers.
 #include <cuda.h>
@@ -51,13 +54,13 @@ constexpr int kC = 64;    // rows a chunk (1 << 6)
 constexpr int kD = 128;   // dk and dv, narrower ones padded with zeros
 
 // What the first launch leaves of a chunk of a head, as the second wants it in
-// shared memory: T in three parts and P in two ([64 rows][64 columns] bf16 each, in
-// the 128-byte swizzle), G and D[63].
+// shared memory: T and P in three parts ([64 rows][64 columns] bf16 each, in the
+// 128-byte swizzle; P's third where its first two are not read), G and D[63].
 constexpr uint32_t kTile = kC * kD * 2;             // K, Q or V of a chunk
 constexpr uint32_t kPanel = kC * 128;               // 64 columns of it, 128-byte swizzle
 constexpr uint32_t kPart = kC * kC * 2;
-constexpr int kTParts = 3, kPParts = 2;
-constexpr uint32_t kOffP = kTParts * kPart, kOffG = kOffP + kPParts * kPart;  // G, D[63], -G
+constexpr int kTParts = 3, kPTiles = 2;
+constexpr uint32_t kOffP = kTParts * kPart, kOffG = kOffP + kPTiles * kPart;  // G, D[63], -G
 constexpr uint32_t kBlob = kOffG + 1024;
 
 __device__ unsigned int g_give_up;
@@ -88,6 +91,19 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
   return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
+// P's third part.  P is lower triangular: of the 16 columns of step j the rows from 16 j
+// on are read, so the rows above are free in the tiles of the first two parts.  Rows
+// [16 j, 64) of step j lie there as rows [0, 64 - 16 j) of another step (step 0's last 16
+// rows apart, as no step has 64 rows free).  The moves are by 16 rows, so the swizzle's
+// order within eight rows is kept.
+struct Place {
+  int tile, step;
+};
+__host__ __device__ constexpr Place third_of_p(int j, bool last_rows) {
+  return j == 0 ? Place{0, last_rows ? 1 : 3}
+                : j == 1 ? Place{1, 3} : j == 2 ? Place{0, 2} : Place{1, 1};
+}
+
 // ---- T and P of a chunk: four warps ----------------------------------------------
 // Bound by latency (a chain of small steps; issue 47 %, DRAM 43 %), so as many chunks
 // as fit share an SM: the scratch matrix lies where K was, P where Q was.
@@ -96,7 +112,7 @@ constexpr int kPitch = kC + 4;  // floats a row of the scratch matrix
 constexpr uint32_t kPrepQ = (kC * kPitch * 4 + 1023) / 1024 * 1024;
 constexpr uint32_t kPrepAlpha = kPrepQ + kTile, kPrepBeta = kPrepAlpha + kC * 4;
 constexpr uint32_t kPrepSmem = kPrepBeta + kC * 4 + 1024;
-static_assert(kTile <= kPrepQ && kPParts * kPart == kTile, "K under the scratch, Q under P");
+static_assert(kTile <= kPrepQ && kPTiles * kPart == kTile, "K under the scratch, Q under P");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
   // 16 bytes to shared memory, zeros where there is no source
@@ -274,19 +290,25 @@ __global__ void __launch_bounds__(kPrepThreads, 5) gdn_chunk_matrices(const Adva
                           j < i ? qk[nt][2 * half + 1] * w.y : 0.f};
       *d = make_float2(j < i ? be2[half] * (kk[nt][2 * half] * w.x) : 0.f,
                        j + 1 < i ? be2[half] * (kk[nt][2 * half + 1] * w.y) : 0.f);
-      uint32_t part[kPParts][1];
-      cut<1, kPParts>(p, part);
+      uint32_t part[3][1];
+      cut<1, 3>(p, part);
 #pragma unroll
-      for (int x = 0; x < kPParts; ++x)
+      for (int x = 0; x < kPTiles; ++x)
         *reinterpret_cast<uint32_t *>(smem + kPrepQ + x * kPart + swizzled(i, nt) + t4 * 4) =
             part[x][0];
+      const int step = nt >> 1;
+      const bool last_rows = step == 0 && warp == 3;
+      const Place to = third_of_p(step, last_rows);
+      *reinterpret_cast<uint32_t *>(smem + kPrepQ + to.tile * kPart + t4 * 4 +
+                                    swizzled(i - (last_rows ? 48 : 16 * step), 2 * to.step + (nt & 1))) =
+          part[2][0];
     }
   }
   fence_async();
   __syncthreads();  // L and P are there
   if (tid == 0) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(blob + kOffP),
-                 "r"(base + kPrepQ), "r"(kPParts * kPart)
+                 "r"(base + kPrepQ), "r"(kPTiles * kPart)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
@@ -413,15 +435,17 @@ constexpr uint32_t kColK = 192;   // S0 K^T, then E
 constexpr uint32_t kColQ = 256;   // S0 Q^T
 constexpr uint32_t kColE = 320;   // R T^T, then E P^T
 constexpr uint32_t kColR = 384;   // R's parts, then those of E'
+constexpr uint32_t kColLow = 480; // E's third part
 constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t state_col(int half, int part, int step) {
   return kColState + kColHalf * half +
          (part < 2 ? 32 * (step >> 1) + 16 * part : 64 + 16 * (step >> 1)) + 8 * (step & 1);
 }
 
-// E's parts over S0 K^T: each half's over the columns that the warps of that half have read.
+// E's first two parts lie over S0 K^T, each half's over the columns that the warps of that
+// half have read; the third behind all else.
 __host__ __device__ constexpr uint32_t e_col(int part, int step) {
-  return 32 * (step >> 1) + 16 * part + 8 * (step & 1);
+  return part < 2 ? kColK + 32 * (step >> 1) + 16 * part + 8 * (step & 1) : kColLow + 8 * step;
 }
 
 constexpr uint32_t idesc(int n, bool mn_major, bool a_mn_major = false) {
@@ -498,17 +522,28 @@ __device__ __forceinline__ void mma_lower(uint32_t d, uint32_t a, uint32_t b) {
                   smem_desc_sw128(b + (weight - pa) * kPart + j * 2048 + j * 32),
                   idesc(kC - 16 * j, false), true);
 }
-// E P^T, the same, of two parts each.
-__device__ __forceinline__ void mma_out(uint32_t d, uint32_t e, uint32_t p) {
+// E P^T, the same: E's third part first, whose product sets the sum.
+__device__ __forceinline__ void mma_out(uint32_t d, uint32_t tmem, uint32_t p) {
 #pragma unroll
-  for (int weight = 1; weight >= 0; --weight)
+  for (int weight = 2; weight >= 0; --weight)
 #pragma unroll
-    for (int pa = 0; pa <= weight; ++pa)
+    for (int pa = weight; pa >= 0; --pa)
 #pragma unroll
-      for (int j = 0; j < kC / 16; ++j)
-        tc_mma_ts(d + 16 * j, e + e_col(pa, j),
-                  smem_desc_sw128(p + (weight - pa) * kPart + j * 2048 + j * 32),
-                  idesc(kC - 16 * j, false), weight == 0 || pa + j > 0);
+      for (int j = 0; j < kC / 16; ++j) {
+        const uint32_t e = tmem + e_col(pa, j);
+        if (weight - pa < kPTiles) {
+          tc_mma_ts(d + 16 * j, e, smem_desc_sw128(p + (weight - pa) * kPart + j * 2048 + j * 32),
+                    idesc(kC - 16 * j, false), weight < 2 || pa < 2 || j > 0);
+        } else {
+          const Place at = third_of_p(j, false);
+          tc_mma_ts(d + 16 * j, e, smem_desc_sw128(p + at.tile * kPart + at.step * 32),
+                    idesc(j == 0 ? 48 : kC - 16 * j, false), true);
+          const Place rest = third_of_p(0, true);
+          if (j == 0)
+            tc_mma_ts(d + 48, e, smem_desc_sw128(p + rest.tile * kPart + rest.step * 32),
+                      idesc(16, false), true);
+        }
+      }
 }
 // V T^T, the same with V from shared memory, dv contiguous.
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t v, uint32_t t) {
@@ -580,8 +615,8 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
     if (one) {
       mma_lower<2, 4>(tmem + kColE, tmem + kColR, t_at);
       tc_commit(bar(kTr + 1));
-      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 0);
-      mma_state<2, 64>(tmem + kColQ, tmem, q_at, 1);
+      mma_state<3, 64>(tmem + kColQ, tmem, q_at, 0);
+      mma_state<3, 64>(tmem + kColQ, tmem, q_at, 1);
       tc_commit(bar(kQs));
     }
     __syncwarp();
@@ -597,7 +632,7 @@ __device__ void issue_chunks(uint32_t base, uint32_t tmem, const Item &it) {
       tc_commit(bar(kSu));
       mma_update(tmem, k_at, 1, 2);
       tc_commit(bar(kSu + 1));
-      mma_out(tmem + kColE, tmem + kColK, p_at);
+      mma_out(tmem + kColE, tmem, p_at);
       tc_commit(bar(kOut));
       tc_commit(bar(kEmpty + s));
     }
@@ -697,10 +732,9 @@ __device__ void run_chain(const AdvanceArgs &a, const Item &it, uint8_t *smem, u
       cut<8, 3>(e, part);
 #pragma unroll
       for (int p = 0; p < 3; ++p) tc_st_x8(tmem + kColR + 32 * p + 8 * g, part[p]);
-      uint32_t whole[2][8];
-      cut<8, 2>(reinterpret_cast<const float *>(x), whole);
+      cut<8, 3>(reinterpret_cast<const float *>(x), part);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) tc_st_x8(tmem + kColK + e_col(p, g), whole[p]);
+      for (int p = 0; p < 3; ++p) tc_st_x8(tmem + e_col(p, g), part[p]);
       tc_wait_st();
       arrive(kE + half);
     }
