@@ -27,19 +27,20 @@
 // MB, 4 launches of 3 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
 // experts of 1024, 68 (2.7 TB/s: the later launches' first loads, the merge of the
 // split tiles and the launch itself are 8 .. 10 us each); 128 rows of
-// 2048, 6 of 96 experts of 1024, 163 .. 168 (2.1 TB/s: products and the widening of nibbles).
+// 2048, 6 of 96 experts of 1024, 153 .. 158 (2.2 TB/s: products and the masking of nibbles).
 //
-// The nibbles are widened to fp16: of a word, the even ones of each half as 1024 + q,
-// the odd ones, left where they are, as 1024 + 16 q against activations divided by
-// 16: five integer operations a word of eight, where bf16 (128 + q, every nibble
-// shifted down) takes seven, and these operations are what the products are bound by.
+// The nibbles are fp16 numbers as they stand: of a word, the even ones of each half
+// masked are the subnormals q 2^-24, the odd ones 16 q 2^-24 against activations divided by
+// 16, which the MMAs multiply exactly.  Five integer operations a word of eight, and
+// nothing is added to a nibble that would have to be taken off a sum again.  (As 1024 + q,
+// the form of a normal number, 1 to 2 % of the outputs were not the bf16 nearest to the
+// exact value, now 0.1 to 0.3 %; 128 rows took 166 us, now 153 to 158.)
 // The activations become fp16 once, before they are multiplied: per row and group of
 // 64 scaled by a power of two that brings the largest to 2^14 .. 2^15, which loses
-// nothing of a bf16 value down to 2^-28 of it.  Beside them lie the scale, what the
-// 1024s contribute (the sums start from its negative) and the group's sum, for the
-// bias.  The activations between the products are two such parts (2^-22).  As
-// operands of down the parts of up to four rows share one MMA's eight columns; five
-// to eight rows take two MMAs.
+// nothing of a bf16 value down to 2^-28 of it.  Beside them lie the scale and the
+// group's sum, for the bias.  The activations between the products are two such parts
+// (2^-22).  As operands of down the parts of up to four rows share one MMA's eight
+// columns; five to eight rows take two MMAs.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -58,8 +59,8 @@ constexpr int kGroupsOf = kStageK / 64;
 constexpr int kWarps = 8;          // that multiply; then the producer, then the finisher
 constexpr int kMoeThreads = (kWarps + 2) * 32;
 // A row's activations of a stage: four groups of 64 fp16, then a Group each.
-struct Group {
-  float f, start, sum, pad;  // 1 / scale; minus the 1024s' part; the inputs' sum
+struct alignas(16) Group {
+  float f, sum;  // 1 / scale; the inputs' sum
 };
 constexpr uint32_t kRecord = kGroupsOf * (128 + (uint32_t)sizeof(Group));  // 576
 constexpr uint32_t kXOff = 2 * kRows * 128;
@@ -151,7 +152,7 @@ struct MoeArgs {
 // ---- activations in the products' form ----------------------------------------------
 // A group's 64 inputs, two a lane (2 lane and 2 lane + 1), to its place in a record:
 // scaled, the odd ones of each word of eight divided by 16, a word's in the order 0 4 1
-// 5 2 6 3 7 of the widened nibbles.  kParts 2: what the fp16 values leave goes to the
+// 5 2 6 3 7 of the masked nibbles.  kParts 2: what the fp16 values leave goes to the
 // record `low` bytes further, the same way.  By a whole warp.
 template <int kParts>
 __device__ __forceinline__ void put_group(uint8_t *record, size_t low, int group, float2 v) {
@@ -175,10 +176,10 @@ __device__ __forceinline__ void put_group(uint8_t *record, size_t low, int group
     __half *h = reinterpret_cast<__half *>(to + (group & 3) * 128) + (lane >> 2) * 8 + place;
     h[0] = a;
     h[2] = b;
-    const float sum = warp_sum(fa + 16.f * fb), start = warp_sum(fa + fb);
+    const float sum = warp_sum(fa + 16.f * fb);
     if (lane == 0)
-      *reinterpret_cast<float4 *>(to + kGroupsOf * 128 + (group & 3) * sizeof(Group)) =
-          make_float4(f, -1024.f * start, f * sum, 0.f);
+      *reinterpret_cast<float2 *>(to + kGroupsOf * 128 + (group & 3) * sizeof(Group)) =
+          make_float2(f, f * sum);
     rest.x -= fa;
     rest.y -= 16.f * fb;
   }
@@ -439,6 +440,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ float2 lds64(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -452,7 +458,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 template <int kParts>
 __device__ __forceinline__ void group_f16(float (&d)[2][4], const uint32_t (&w)[2][4], const uint4 (&x)[2],
                                           const uint4 (&low)[2]) {
-  constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u, k1024 = 0x64006400u;
+  constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -462,10 +468,10 @@ __device__ __forceinline__ void group_f16(float (&d)[2][4], const uint32_t (&w)[
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile) {
         const uint32_t a = w[tile][2 * i] >> (8 * step), b = w[tile][2 * i + 1] >> (8 * step);
-        q[tile][0] = and_or(a, kEven, k1024);
-        q[tile][1] = and_or(b, kEven, k1024);
-        q[tile][2] = and_or(a, kOdd, k1024);
-        q[tile][3] = and_or(b, kOdd, k1024);
+        q[tile][0] = a & kEven;
+        q[tile][1] = b & kEven;
+        q[tile][2] = a & kOdd;
+        q[tile][3] = b & kOdd;
         mma_f16(d[tile], q[tile][0], q[tile][1], q[tile][2], q[tile][3], b0, b1);
       }
       if constexpr (kParts == 2) {
@@ -482,7 +488,7 @@ __device__ __forceinline__ void group_f16(float (&d)[2][4], const uint32_t (&w)[
 // (row) g8; of the sums columns 2 t4 and 2 t4 + 1.  kBoth: a column a row, its two parts
 // one after the other; else down's second parts are columns of their own.
 template <bool kDown, bool kBoth>
-__device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint32_t full0,
+__device__ __forceinline__ bool multiply(float2 (&acc)[2][2], uint32_t base, uint32_t full0,
                                          uint32_t empty0, uint32_t sb_full0, uint32_t sb_empty0,
                                          int &st, int &ph, int &blocks, int s0, int s1, int groups,
                                          int n) {
@@ -497,6 +503,7 @@ __device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint
       kXOff + 2 * t4 * kRecord + kGroupsOf * 128 + half * 2 * (uint32_t)sizeof(Group);
   constexpr uint32_t kLow = kSlotRows * kRecord;  // to a row's second part
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const float2 none = make_float2(0.f, 0.f), unit = make_float2(0x1p24f, 0x1p24f);
   for (int c = s0; c < s1; ++c) {
     if ((c == s0 || c % kBlock == 0) && !warp_wait_stage(sb_full0 + 8u * (blocks & 1), (blocks >> 1) & 1))
       return false;
@@ -505,7 +512,8 @@ __device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint
     const uint32_t sb_at = base + R::kSbOff + (blocks & 1) * 2 * kSbBytes + (rows0 + g8) * kSbRow +
                            (c % kBlock) * 8 + half * 4;
     if (c * kGroupsOf + 2 * half < groups) {
-      uint4 x[2][2], r[2][2], low[2][2];
+      uint4 x[2][2], low[2][2];
+      float2 r[2][2];
       uint32_t w[2][2][4], sw[4], bw[4];
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
@@ -515,8 +523,8 @@ __device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint
                                        (((4 * half + 2 * gi + (lane >> 4)) ^ (lane & 7)) << 4));
         x[gi][0] = valid ? lds128(at + x_at + gi * 128) : zero;
         x[gi][1] = valid ? lds128(at + x_at + gi * 128 + 64) : zero;
-        r[gi][0] = real0 ? lds128(at + group_at + gi * 16) : zero;
-        r[gi][1] = real1 ? lds128(at + group_at + kRecord + gi * 16) : zero;
+        r[gi][0] = real0 ? lds64(at + group_at + gi * 16) : none;
+        r[gi][1] = real1 ? lds64(at + group_at + kRecord + gi * 16) : none;
         if constexpr (kBoth) {
           low[gi][0] = valid ? lds128(at + x_at + kLow + gi * 128) : zero;
           low[gi][1] = valid ? lds128(at + x_at + kLow + gi * 128 + 64) : zero;
@@ -529,29 +537,27 @@ __device__ __forceinline__ bool multiply(float (&acc)[2][4], uint32_t base, uint
       }
 #pragma unroll
       for (int gi = 0; gi < 2; ++gi) {
-        const float f0 = __uint_as_float(r[gi][0].x), f1 = __uint_as_float(r[gi][1].x);
-        float start0 = __uint_as_float(r[gi][0].y), start1 = __uint_as_float(r[gi][1].y);
-        float sum0 = __uint_as_float(r[gi][0].z), sum1 = __uint_as_float(r[gi][1].z);
+        const float2 f = make_float2(r[gi][0].x, r[gi][1].x);
+        float2 sum = make_float2(r[gi][0].y, r[gi][1].y);
         if constexpr (kBoth) {
-          const uint4 q0 = real0 ? lds128(at + group_at + kLow + gi * 16) : zero;
-          const uint4 q1 = real1 ? lds128(at + group_at + kLow + kRecord + gi * 16) : zero;
-          start0 += __uint_as_float(q0.y);
-          start1 += __uint_as_float(q1.y);
-          sum0 += __uint_as_float(q0.z);
-          sum1 += __uint_as_float(q1.z);
+          const float2 q0 = real0 ? lds64(at + group_at + kLow + gi * 16) : none;
+          const float2 q1 = real1 ? lds64(at + group_at + kLow + kRecord + gi * 16) : none;
+          sum.x += q0.y;
+          sum.y += q1.y;
         }
-        float d[2][4] = {{start0, start1, start0, start1}, {start0, start1, start0, start1}};
+        float d[2][4] = {};
         group_f16<kBoth ? 2 : 1>(d, w[gi], x[gi], kBoth ? low[gi] : x[gi]);
         auto of = [&](uint32_t word) { return __uint_as_float(gi ? word & 0xFFFF0000u : word << 16); };
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          const float s0r = of(sw[2 * tile]), s8r = of(sw[2 * tile + 1]);
-          const float b0r = of(bw[2 * tile]), b8r = of(bw[2 * tile + 1]);
-          acc[tile][0] = fmaf(s0r, f0 * d[tile][0], fmaf(b0r, sum0, acc[tile][0]));
-          acc[tile][1] = fmaf(s0r, f1 * d[tile][1], fmaf(b0r, sum1, acc[tile][1]));
-          acc[tile][2] = fmaf(s8r, f0 * d[tile][2], fmaf(b8r, sum0, acc[tile][2]));
-          acc[tile][3] = fmaf(s8r, f1 * d[tile][3], fmaf(b8r, sum1, acc[tile][3]));
-        }
+        for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // rows g8 and g8 + 8; columns 2 t4 and 2 t4 + 1
+            const float s = of(sw[2 * tile + i]), b = of(bw[2 * tile + i]);
+            // (the unit apart from 1 / scale, which alone may be 2^113)
+            const float2 v = __fmul2_rn(f, __fmul2_rn(unit, make_float2(d[tile][2 * i], d[tile][2 * i + 1])));
+            float2 &to = acc[tile][i];
+            to = __ffma2_rn(make_float2(s, s), v, __ffma2_rn(make_float2(b, b), sum, to));
+          }
       }
     }
     __syncwarp();
@@ -836,7 +842,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
     u += g.s1 - g.s0;
     if (g.slot != slot) n = __ldcg(&a.ws.slots[g.slot].n);
     slot = g.slot;
-    float acc[2][4] = {};
+    float2 acc[2][2] = {};
     if (kDown && n > 4)
       ok = multiply<kDown, kDown>(acc, base, full0, empty0, sb_full0, sb_empty0, st, ph, blocks, g.s0, g.s1,
                                    groups, n);
@@ -851,10 +857,10 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
                  2 * (lane & 3) * kRedPitch + rows0 + (lane >> 2);
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      red[16 * tile] = acc[tile][0];
-      red[16 * tile + kRedPitch] = acc[tile][1];
-      red[16 * tile + 8] = acc[tile][2];
-      red[16 * tile + 8 + kRedPitch] = acc[tile][3];
+      red[16 * tile] = acc[tile][0].x;
+      red[16 * tile + kRedPitch] = acc[tile][0].y;
+      red[16 * tile + 8] = acc[tile][1].x;
+      red[16 * tile + 8 + kRedPitch] = acc[tile][1].y;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive_u32(red_full0 + 8u * (k & 1));
