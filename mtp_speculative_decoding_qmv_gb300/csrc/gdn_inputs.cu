@@ -9,15 +9,18 @@
 // rows before a tile are read twice).  A warp takes one head (up to 128
 // channels, four a lane) of a tile of rows of one sequence and slides the
 // window along in registers, so the W taps cost no loads; four to eight rows' loads
-// are in flight a warp, 24 warps an SM.  The heads of a row are neighbouring warps, so
+// are in flight a warp, 24 warps an SM (16 for the widest windows, whose registers they
+// are).  The heads of a row are neighbouring warps, so
 // a CTA reads and writes runs of 1 KB.  The tiles begin at the sequences' first rows: a
 // sequence's first tile alone reads its window, and the same warp writes it, so
 // one launch needs no order among its CTAs.
 // Measured, 10240 channels and 48 heads, bf16, W = 4: three prompts of 7519 rows in all
 // 81 us (313 MB, 3.9 TB/s; ncu: issue 51 %, DRAM 43 %: a batch's loads, then its
 // arithmetic; with fewer warps and no batch ahead 236 us), 256 single tokens with
-// their windows 27 us (74 MB); four rows of one sequence 5 us, a launch and its
-// dependent loads.
+// their windows 23 us (74 MB); four rows of one sequence 5 us, a launch and its
+// dependent loads.  W = 2 .. 8, 7500 rows: 72, 77, 79, 85, 89, 95, 98 us; 256 tokens: 14,
+// 16, 18, 20, 22, 26, 30 (in a graph).  Each width has its kernel: one for all of them, W
+// known at run time, took 310 .. 323 and 58 .. 84.
 #include <cuda_runtime.h>
 
 #include "gdn_rows.cuh"
@@ -40,7 +43,7 @@ struct InputsArgs {
   void *q, *k, *v;
   float *alpha, *beta;
   float q_scale, eps;
-  int B, rows, slots, W, Hk, H, dk, dv, C, shift, update, heads, tasks;
+  int B, rows, slots, Hk, H, dk, dv, C, shift, update, heads, tasks;
 };
 
 // Four consecutive values.
@@ -71,10 +74,10 @@ __device__ __forceinline__ float silu(float y) {
   return y * r;
 }
 
+// CTAs an SM by what spills: at 6, 7500 bf16 rows take 79 us (W = 4; 83 at 5 or 4), 111 and
+// 153 (W = 7, 8; 95 and 98 at 4); at 5, fp32 rows of W = 6 take 116 (144 at 6, 120 at 4).
 template <class X, class Y, int kW>
-__global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel(const InputsArgs a) {
-  const int W = kW > 0 ? kW : a.W;
-  constexpr int kTaps = kW > 0 ? kW : kMaxW;
+__global__ void __launch_bounds__(kWarps * 32, kW <= 4 ? 6 : kW <= 6 ? 5 : 4) gdn_inputs_kernel(const InputsArgs a) {
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (unit >= a.tasks) return;
@@ -85,11 +88,11 @@ __global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel
   const int c0 = (kind == 2 ? 2 * a.Hk * a.dk + head * a.dv : unit * a.dk) + 4 * lane;
   const bool mine = 4 * lane < d && unit < a.heads;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 w[kTaps], h[kTaps];  // h[i]: the input W - 1 - i places back; h[W - 1] the newest
+  float4 w[kW], h[kW];  // h[i]: the input kW - 1 - i places back; h[kW - 1] the newest
 #pragma unroll
-  for (int i = 0; i < kTaps; ++i) {  // on their way while the tile is looked for
+  for (int i = 0; i < kW; ++i) {  // on their way while the tile is looked for
     w[i] = h[i] = zero;
-    if (i < W && mine) w[i] = load4(a.weight + (long long)i * a.C + c0);
+    if (mine) w[i] = load4(a.weight + (long long)i * a.C + c0);
   }
   int j;
   const int b = tile_owner(a.q_start, a.B, a.rows, a.shift, blockIdx.y, j);
@@ -136,28 +139,24 @@ __global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel
     return;
   }
   const X *x = static_cast<const X *>(a.x) + (s.start + t0) * a.x_stride + c0;
-  float *window = a.window + (long long)slot * (W - 1) * a.C + c0;
+  float *window = a.window + (long long)slot * (kW - 1) * a.C + c0;
 #pragma unroll
-  for (int i = 0; i < kTaps - 1; ++i)
-    if (i < W - 1 && mine)
+  for (int i = 0; i < kW - 1; ++i)
+    if (mine)
       h[i + 1] = t0 == 0 ? *reinterpret_cast<const float4 *>(window + (long long)i * a.C)
-                         : widen4(load4(x + (long long)(i - (W - 1)) * a.x_stride));
+                         : widen4(load4(x + (long long)(i - (kW - 1)) * a.x_stride));
   if (t0 == 0 && a.update && mine) {
-    // entry i of the next window: the input of row n - (W - 1) + i, or the old
+    // entry i of the next window: the input of row n - (kW - 1) + i, or the old
     // window's where that is before the first row
-    float4 next[kTaps];
+    float4 next[kW - 1];
 #pragma unroll
-    for (int i = 0; i < kTaps - 1; ++i) {
-      const int last = s.n - (W - 1) + i;
-      next[i] = zero;
-      if (i < W - 1 && last >= 0) next[i] = widen4(load4(x + (long long)last * a.x_stride));
-#pragma unroll
-      for (int o = 0; o < kTaps - 1; ++o)
-        if (o < W - 1 && last < 0 && o == last + W - 1) next[i] = h[o + 1];
+    for (int i = 0; i < kW - 1; ++i) {
+      const int last = s.n - (kW - 1) + i;
+      next[i] = last >= 0 ? widen4(load4(x + (long long)last * a.x_stride))
+                          : *reinterpret_cast<const float4 *>(window + (long long)(last + kW - 1) * a.C);
     }
 #pragma unroll
-    for (int i = 0; i < kTaps - 1; ++i)
-      if (i < W - 1) *reinterpret_cast<float4 *>(window + (long long)i * a.C) = next[i];
+    for (int i = 0; i < kW - 1; ++i) *reinterpret_cast<float4 *>(window + (long long)i * a.C) = next[i];
   }
   decltype(load4(x)) next[kBatch];
   auto load = [&](int t) {
@@ -177,19 +176,15 @@ __global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
 #pragma unroll
-      for (int o = 0; o < kTaps - 1; ++o) h[o] = h[o + 1];
-      const float4 now = t + i < n && mine ? widen4(raw[i]) : zero;
+      for (int o = 0; o < kW - 1; ++o) h[o] = h[o + 1];
+      h[kW - 1] = t + i < n && mine ? widen4(raw[i]) : zero;
       float4 sum = zero;
 #pragma unroll
-      for (int o = 0; o < kTaps; ++o) {
-        if (kW == 0 && o == W - 1) h[o] = now;
-        if (kW > 0 && o == kTaps - 1) h[o] = now;
-        if (o < W) {
-          sum.x = fmaf(w[o].x, h[o].x, sum.x);
-          sum.y = fmaf(w[o].y, h[o].y, sum.y);
-          sum.z = fmaf(w[o].z, h[o].z, sum.z);
-          sum.w = fmaf(w[o].w, h[o].w, sum.w);
-        }
+      for (int o = 0; o < kW; ++o) {
+        sum.x = fmaf(w[o].x, h[o].x, sum.x);
+        sum.y = fmaf(w[o].y, h[o].y, sum.y);
+        sum.z = fmaf(w[o].z, h[o].z, sum.z);
+        sum.w = fmaf(w[o].w, h[o].w, sum.w);
       }
       y[i] = make_float4(silu(sum.x), silu(sum.y), silu(sum.z), silu(sum.w));
     }
@@ -218,7 +213,11 @@ __global__ void __launch_bounds__(kWarps * 32, kW > 0 ? 6 : 4) gdn_inputs_kernel
 using Kernel = void (*)(InputsArgs);
 template <class X, class Y>
 Kernel pick(int W) {
-  return W == 4 ? gdn_inputs_kernel<X, Y, 4> : W == 2 ? gdn_inputs_kernel<X, Y, 2> : gdn_inputs_kernel<X, Y, 0>;
+  constexpr Kernel of[kMaxW - 1] = {gdn_inputs_kernel<X, Y, 2>, gdn_inputs_kernel<X, Y, 3>,
+                                    gdn_inputs_kernel<X, Y, 4>, gdn_inputs_kernel<X, Y, 5>,
+                                    gdn_inputs_kernel<X, Y, 6>, gdn_inputs_kernel<X, Y, 7>,
+                                    gdn_inputs_kernel<X, Y, 8>};
+  return of[W - 2];
 }
 
 }  // namespace
@@ -323,7 +322,6 @@ extern "C" sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_
   p.B = B;
   p.rows = rows;
   p.slots = slots;
-  p.W = W;
   p.Hk = Hk;
   p.H = Hv;
   p.dk = dk;
