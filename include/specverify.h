@@ -573,9 +573,10 @@ sv_status conv_window_replay(float *window, const float *x, const int32_t *n_rep
  *   alpha = exp(-exp(a_log[h]) log(1 + exp(a + dt_bias[h]))),
  *   beta  = 1 / (1 + exp(-b))
  * x, a and b are fp32 or bf16 with rows x_row_stride etc. elements apart; q, k
- * [rows][Hk][dk] and v [rows][Hv][dv] are fp32 or bf16 (fp32: what
- * gdn_tape_capture takes), alpha and beta fp32 [rows][Hv].  Arithmetic is fp32,
- * rounded once.  With update_window the window of every sequence with rows
+ * [rows][Hk][dk] and v [rows][Hv][dv] are fp32 or bf16, alpha and beta fp32
+ * [rows][Hv].  (Fp32 and Hk = Hv: what gdn_tape_capture takes.  It has no shared key
+ * heads: where Hk < Hv, repeat each q and k head for its Hv / Hk v heads first.)
+ * Arithmetic is fp32, rounded once.  With update_window the window of every sequence with rows
  * becomes its last W-1 inputs (an exact copy); without, it is read only, for a
  * verify block whose inputs conv_window_replay commits later.
  * Requires 2 <= W <= 8; x, weight, window, q, k, v 16-byte aligned, x's row

@@ -938,7 +938,9 @@ def gdn_inputs(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, weight: torch.
     Sequence s's rows are q_start[s]:q_start[s+1], its slot window_index[s] (s
     when omitted); rows past the last sequence are zero.  ``max_new``: a bound
     on a sequence's rows.  q, k and v are made in ``dtype`` for ``k_heads`` of
-    ``dk``, or are the first three of ``out``."""
+    ``dk``, or are the first three of ``out``.  (gdn_tape_capture takes them in
+    float32 with as many k heads as v heads: where there are fewer, repeat each
+    q and k head for its v heads first.)"""
     if x.dim() != 2 or a.dim() != 2 or weight.dim() != 2 or window.dim() != 3:
         raise ValueError("x and a must be [rows, width], weight [W, C], window [slots, W-1, C]")
     index = _on(x, "x")
