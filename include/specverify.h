@@ -331,12 +331,15 @@ sv_status qmv_wide(const uint32_t *w_packed, const uint16_t *scales, const uint1
  * [experts][inter][hidden / 64], down [experts][hidden][inter / 8] and
  * [experts][hidden][inter / 64].  y bf16 [rows][hidden], rounded once; ids int32
  * and weights fp32 [rows][top_k] receive the choice when not NULL.  Accuracy:
- * fp32 sums of exact products of x, whose 64 inputs of a group are scaled by one
+ * fp32 sums (on the tensor cores, where a sum of 64 products is cut off, not rounded,
+ * at every 16) of exact products of x, whose 64 inputs of a group are scaled by one
  * power of two (a value below 2^-28 of its group's largest keeps fewer bits than
  * bf16's); the activations between the products are fp32, split into two fp16 parts
  * (2^-22 of their group's largest).  An infinity or a NaN in x reaches its own row
  * alone.  A row depends on no other row up to the order of its fp32 sums, and
- * results do not depend on the run.
+ * results do not depend on the run; but that order changes with the other rows' choice,
+ * so a row of a verify block need not have the bits of the same row alone, as
+ * qmv_smallm's have.
  * Requires 0 <= rows <= 128 (0: no-op), 1 <= top_k <= 16, top_k <= experts <= 512,
  * hidden and inter multiples of 128, at most 65536; x, router, w_packed, scales
  * and biases 16-byte, y 8-byte aligned; no output overlaps an input or another output.
@@ -554,13 +557,13 @@ sv_status conv_window_replay(float *window, const float *x, const int32_t *n_rep
  * two take tokens that stand -- prompts, chunks of prompts, single tokens --
  * through such a layer: packed rows as in the attention layers below, sequence
  * b's at q_start[b] .. q_start[b+1] (int32 [B+1], ascending from 0, clamped to
- * [0, rows]), lengths mixed as they come, zero included.  The state and the
+ * [0, rows]), lengths as they come, zero included.  The state and the
  * window of sequence b are those of slot state_index[b] / window_index[b] (b
  * itself where the index is NULL); distinct sequences have distinct slots.  A
  * sequence whose slot is outside [0, slots) has zeros for its rows and touches
  * nothing else, and so have the rows from q_start[B] on.  max_new: the
- * caller's bound on a sequence's rows, which picks the kernel; a longer
- * sequence is still computed.  Hv is a multiple of Hk: v head h goes with q and
+ * caller's bound on a sequence's rows, which picks the kernel for all of the
+ * call's sequences; a longer sequence is still computed.  Hv is a multiple of Hk: v head h goes with q and
  * k head h / (Hv / Hk).  dk and dv are multiples of 8 in [8, 128].
  *
  * gdn_inputs: from a row x of C = 2 Hk dk + Hv dv channels (q heads, k heads,
@@ -576,7 +579,8 @@ sv_status conv_window_replay(float *window, const float *x, const int32_t *n_rep
  * [rows][Hk][dk] and v [rows][Hv][dv] are fp32 or bf16, alpha and beta fp32
  * [rows][Hv].  (Fp32 and Hk = Hv: what gdn_tape_capture takes.  It has no shared key
  * heads: where Hk < Hv, repeat each q and k head for its Hv / Hk v heads first.)
- * Arithmetic is fp32, rounded once.  With update_window the window of every sequence with rows
+ * Arithmetic is fp32, rounded once; silu is made of the approximate exponential
+ * and reciprocal, off by 2^-21 + 2^-23 |z| of its value, and is zero below z = -87.  With update_window the window of every sequence with rows
  * becomes its last W-1 inputs (an exact copy); without, it is read only, for a
  * verify block whose inputs conv_window_replay commits later.
  * Requires 2 <= W <= 8; x, weight, window, q, k, v 16-byte aligned, x's row
@@ -597,9 +601,14 @@ sv_status gdn_inputs(const void *x, const void *a, const void *b, sv_dtype x_dty
  * [rows][Hk][dk], v and out [rows][Hv][dv], all fp32 or all bf16, their rows
  * q_row_stride etc. elements apart; alpha, beta fp32 [rows][Hv].  States and
  * sums are fp32, out is rounded once.
- * bf16 rows with max_new from 32 on go 64 at a time: infinities and NaN among them
- * then reach all 64 rows of their sequence and head that go together, and what
- * follows; no other sequence.
+ * bf16 rows with max_new from 32 on go 64 at a time, on the tensor cores, every sequence
+ * of the call, whatever its length.  Sums are then cut off, not rounded, at every 16
+ * terms: the states after a prompt of thousands of rows are off by 7e-7 of their norm,
+ * row after row by 3e-7.  A row's bits depend on which way its call goes.
+ * Infinities and NaN reach all 64 rows of their sequence and head that go together, and
+ * what follows; no other sequence.  A sequence of one row costs what 64 rows cost: take
+ * single tokens and prompts in calls of their own (48 heads of 128 x 128, 64 single
+ * tokens and 512 rows of a prompt: 360 us in one call, 113 in two).
  * Requires q, k, v, state and out 16-byte aligned, row strides multiples of 8
  * elements; neither out nor state overlaps an input or the other.  Results do
  * not depend on the run.

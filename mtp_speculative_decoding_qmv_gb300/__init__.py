@@ -1001,7 +1001,9 @@ def gdn_advance(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.
     dk] in place: q, k [rows, k_heads, dk] and v [rows, v_heads, dv] fp32 or
     bf16, alpha, beta fp32 [rows, v_heads]; sequence s's rows are
     q_start[s]:q_start[s+1], its slot state_index[s] (s when omitted).
-    ``max_new``: a bound on a sequence's rows, which picks the kernel.
+    ``max_new``: a bound on a sequence's rows, which picks the kernel for all of
+    them: bf16 rows with ``max_new`` from 32 on go 64 at a time, a single token too,
+    so prompts and single tokens are faster in calls of their own.
     ``workspace``: uint8, gdn_advance_workspace_bytes of them, made per call when
     omitted and needed.  Returns out [rows, v_heads, dv] of q's dtype; rows past
     the last sequence are zero."""

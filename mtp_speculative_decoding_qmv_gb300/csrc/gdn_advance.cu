@@ -28,10 +28,12 @@ constexpr int kLanesPerRow = 8;
 constexpr int kRowsPerCta = 16;
 constexpr int kThreads = kRowsPerCta * kLanesPerRow;
 constexpr int kMaxDim = 128;
-// Rows of a sequence from which the chunks are taken (bf16).  In graphs, 48 heads of
-// 128 x 128, us of the row after row kernel and of the chunks at 24, 32 and 48 rows: one
-// sequence 14 and 15, 18 and 16, 26 and 15; 4 sequences 35 and 31, 46 and 30, 66 and
-// 32; 16 sequences 86 and 90, 113 and 91, 164 and 94.
+// The bound on a sequence's rows from which all of a call's go in chunks (bf16).  In
+// graphs, 48 heads of 128 x 128, us of the row after row kernel and of the chunks at 24,
+// 32 and 48 rows: one sequence 14 and 16, 18 and 16, 26 and 16; 4 sequences 35 and 31, 46
+// and 30, 66 and 32; 16 sequences 86 and 89, 113 and 91, 164 and 94.  A call that mixes
+// lengths pays for it: 64 single tokens beside a prompt of 512 rows take 360, as two
+// calls 113 (67 and 43).
 constexpr int kChunkFrom = 32;
 
 __device__ __forceinline__ float row_sum(float v) {
@@ -161,7 +163,10 @@ __global__ void __launch_bounds__(kThreads) gdn_recur_kernel(const AdvanceArgs a
 template <class T>
 sv_status recur_run(const AdvanceArgs &a, cudaStream_t stream) {
   // two rows a thread once the CTAs fill the device several times over: they share the
-  // loads and the widening of k and q
+  // loads and the widening of k and q.  (48 heads of 128 x 128, us with one and with two:
+  // single tokens of 1, 4, 7, 16 and 64 sequences 3.2 and 3.6, 5.9 and 6.0, 8.7 and 8.6,
+  // 16.2 and 15.4, 79 and 67; 8 rows each of 4, 16 and 64: 14.9 and 12.9, 46 and 36, 229
+  // and 171.  The rule changes at 7 sequences.)
   const long long one = (long long)((a.dv + kRowsPerCta - 1) / kRowsPerCta) * a.H * a.B;
   const int R = one > 16ll * device_sm_count() ? 2 : 1;
   const dim3 grid((unsigned)((a.dv + kRowsPerCta * R - 1) / (kRowsPerCta * R)), (unsigned)a.H,
