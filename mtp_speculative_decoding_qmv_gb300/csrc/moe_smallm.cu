@@ -25,7 +25,7 @@
 //  * the sum of a row's experts, in the order of choice.
 // Measured (us, in a graph): one row of 2048 inputs, 8 of 256 experts of 512, 27 (15
 // MB, 4 launches of 3 .. 9 us that wait for one another); 4 rows of 5120, 6 of 64
-// experts of 1024, 68 (2.7 TB/s: the later launches' first loads, the merge of the
+// experts of 1024, 67 .. 72 (2.6 TB/s: the later launches' first loads, the merge of the
 // split tiles and the launch itself are 8 .. 10 us each); 128 rows of
 // 2048, 6 of 96 experts of 1024, 153 .. 158 (2.2 TB/s: products and the masking of nibbles).
 //
